@@ -88,7 +88,9 @@ typedef enum {
   Q4_OP_GEMM_W4A16_MXFP4 = 6,
   Q4_OP_GEMM_FP8_BLOCKWISE = 7, /* needs none today: 0 */
   Q4_OP_GEMM_W4A8 = 8,          /* needs none today: 0 */
-  Q4_OP_GEMM_W4A4_MXFP4_FUSED = 9
+  Q4_OP_GEMM_W4A4_MXFP4_FUSED = 9,
+  Q4_OP_MOE_SORT = 10,          /* M = slots T * top_k, N = experts */
+  Q4_OP_GROUPED_WGRAD_FP8 = 11  /* M = rows of codes, N, K */
 } q4_op;
 
 /*
@@ -362,6 +364,122 @@ q4_status w4a8_weight_scales(const uint16_t* w_scales, int64_t N, int64_t K, flo
 q4_status gemm_w4a8(const uint8_t* qa, const float* sa, const uint8_t* w_codes,
                     const float* w_scales_kn, int64_t M, int64_t N, int64_t K, void* C,
                     int c_dtype, void* ws, size_t ws_bytes, q4_stream_t stream);
+
+/*
+ * Routing around grouped_gemm_moe, and its gradients.
+ *
+ * moe_route_topk: the top_k experts of every token by logit and their softmax
+ * weights.  logits: [T, E] of dtype, row pitch ld elements (ld >= E).  With V
+ * the token's experts whose logit is above -inf (a logit of -inf masks its
+ * expert), ids[t, :] are the first top_k of V by logit, ties to the lower
+ * index; a slot without an expert gets id -1 and weight 0.  weights[t, j] is
+ * the softmax over the chosen logits (Q4_ROUTE_TOPK: they sum to 1) or over
+ * all of V (Q4_ROUTE_ALL), in FP32.  A NaN or +inf latches Q4_ERR_NONFINITE
+ * and masks its expert.  ids: int32 [T, top_k]; weights: float [T, top_k].
+ * 1 <= top_k <= min(E, 32), E <= 1024.
+ * moe_route_topk_backward: d_logits [T, E] (dtype, contiguous) from d_weights
+ * [T, top_k], given the same logits and the ids of the forward call (distinct
+ * within a token; one outside [0, E) or of a masked expert is left out, its
+ * d_weights ignored).  Logits without a gradient get 0.
+ */
+typedef enum { Q4_ROUTE_TOPK = 0, Q4_ROUTE_ALL = 1 } q4_route_normalize;
+q4_status moe_route_topk(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, int top_k,
+                         int normalize, int32_t* ids, float* weights, q4_stream_t stream);
+q4_status moe_route_topk_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld,
+                                  int top_k, int normalize, const int32_t* ids,
+                                  const float* d_weights, void* d_logits, q4_stream_t stream);
+
+/*
+ * Slots (t, j) of ids [T, top_k] sorted by expert, then token, then j, as
+ * grouped_gemm_moe takes them:
+ *   expert_offsets int32 [E + 1]: expert e owns rows expert_offsets[e] ..
+ *                  expert_offsets[e + 1];
+ *   row_token      int32 [T * top_k]: the token of every row;
+ *   slot_row       int32 [T, top_k]: the row of every slot.
+ * An id outside [0, E) drops its slot: the dropped slots take the rows from
+ * expert_offsets[E] on, in slot order, and slot_row holds ~row (negative).
+ * 1 <= top_k <= 32, E <= 1024, T * top_k < 2^30.
+ * ws: q4_workspace_size(Q4_OP_MOE_SORT, T * top_k, E, 0) bytes.
+ */
+q4_status moe_sort_tokens(const int32_t* ids, int64_t T, int top_k, int E, int32_t* expert_offsets,
+                          int32_t* row_token, int32_t* slot_row, void* ws, size_t ws_bytes,
+                          q4_stream_t stream);
+
+/*
+ * Rows into expert order and back.  slot_row as moe_sort_tokens writes it
+ * (entries that name no row in [0, T * top_k) are left out).  All matrices
+ * are of one dtype; inputs have a row pitch (in elements, at least the
+ * width), outputs are contiguous.  Any width H >= 1; 16-byte aligned
+ * addresses and pitches take 128-bit accesses.
+ *  moe_dispatch            rows[row(t, j)] = x[t]; rows of dropped slots are 0.
+ *  moe_dispatch_backward   d_x[t] = sum_j d_rows[row(t, j)]
+ *  moe_combine             out[t] = sum_j weights[t, j] * rows[row(t, j)]
+ *  moe_combine_backward    d_rows[row(t, j)] = weights[t, j] * d_out[t] (0 for
+ *                          a dropped slot), d_weights[t, j] = <d_out[t],
+ *                          rows[row(t, j)]> (0 for a dropped slot).
+ * Sums are FP32, in ascending j, and leave dropped slots out whatever their
+ * rows and weights hold; results are rounded once to dtype (d_weights: FP32).
+ * moe_combine with weights NULL takes every weight as 1.  moe_combine_backward
+ * with d_weights NULL does not read rows.
+ */
+q4_status moe_dispatch(const void* x, int dtype, int64_t T, int64_t H, int64_t ldx,
+                       const int32_t* slot_row, int top_k, void* rows, q4_stream_t stream);
+q4_status moe_dispatch_backward(const void* d_rows, int dtype, int64_t T, int64_t H, int64_t ld,
+                                const int32_t* slot_row, int top_k, void* d_x, q4_stream_t stream);
+q4_status moe_combine(const void* rows, int dtype, int64_t T, int64_t H, int64_t ld,
+                      const int32_t* slot_row, const float* weights, int top_k, void* out,
+                      q4_stream_t stream);
+q4_status moe_combine_backward(const void* d_out, int dtype, int64_t T, int64_t H, int64_t ld_d_out,
+                               const void* rows, int64_t ld_rows, const int32_t* slot_row,
+                               const float* weights, int top_k, void* d_rows, float* d_weights,
+                               q4_stream_t stream);
+
+/*
+ * 8-bit activation checkpoints: x [rows, K] kept as E4M3 codes [rows, K] and
+ * one FP32 scale per row and 128 columns, scales [rows, ceil(K / 128)]:
+ *   s = the smallest power of two with max(amax, 1e-12) <= 448 s
+ *   code = e4m3_rne(x / s)
+ * (codes and scales are those of quantize_fp8_blockwise with block_rows 1 but
+ * for the power of two, so gemm_fp8_blockwise takes them too; code * s is a
+ * bf16 number.)  Any K >= 1; x has row pitch ld.  A non-finite input latches
+ * Q4_ERR_NONFINITE.
+ *
+ * swiglu_fp8: the gated activation of gate_up = [g | u] [rows, 2 I] (row pitch
+ * ld): h = silu(g) * u [rows, I] in dtype, and the checkpoint of gate_up taken
+ * in the same pass, each half in blocks of its own: codes [rows, 2 I], scales
+ * [rows, 2 ceil(I / 128)] (g's blocks, then u's).
+ * swiglu_fp8_backward: d_gate_up [rows, 2 I] from d_h [rows, I] (row pitch ld)
+ * and the checkpoint, at the restored g and u:
+ *   d_g = d_h u s (1 + g (1 - s)),  d_u = d_h g s,  s = 1 / (1 + exp(-g)).
+ */
+q4_status quantize_fp8_checkpoint(const void* x, int dtype, int64_t rows, int64_t K, int64_t ld,
+                                  uint8_t* codes, float* scales, q4_stream_t stream);
+q4_status swiglu_fp8(const void* gate_up, int dtype, int64_t rows, int64_t I, int64_t ld, void* h,
+                     uint8_t* codes, float* scales, q4_stream_t stream);
+q4_status swiglu_fp8_backward(const void* d_h, int dtype, int64_t rows, int64_t I, int64_t ld,
+                              const uint8_t* codes, const float* scales, void* d_gate_up,
+                              q4_stream_t stream);
+
+/*
+ * Weight gradient of the experts' products, read from an 8-bit checkpoint:
+ *   dW[e] = sum over r in [expert_offsets[e], expert_offsets[e + 1]) of
+ *           d_y[r]^T . x_hat[row_token[r]]
+ * d_y: bf16 [R, N], row pitch ldy.  codes [T, K], scales [T, ceil(K / 128)]:
+ * a checkpoint (quantize_fp8_checkpoint); x_hat = bf16(code * scale), which is
+ * exact for power-of-two scales (other scales round to nearest even).
+ * row_token int32 [R], values in [0, T), or NULL for row r = row r (T = R).
+ * expert_offsets int32 [E + 1], non-decreasing, in [0, R]; rows behind
+ * expert_offsets[E] take no part, an expert without rows gets 0.
+ * dW: [E, N, K] in w_dtype: Q4_F32, or Q4_BF16 (rounded once); accumulate != 0
+ * (Q4_F32 only) adds to what dW holds.  Sums are FP32.
+ * N % 8 == 0, ldy % 8 == 0, K % 16 == 0; d_y, codes and dW 16-byte aligned.
+ * ws: q4_workspace_size(Q4_OP_GROUPED_WGRAD_FP8, T, N, K) bytes.
+ */
+q4_status grouped_wgrad_fp8(const void* d_y_bf16, int64_t R, int64_t N, int64_t ldy,
+                            const uint8_t* codes, const float* scales, int64_t T, int64_t K,
+                            const int32_t* row_token, const int32_t* expert_offsets, int E,
+                            void* dW, int w_dtype, int accumulate, void* ws, size_t ws_bytes,
+                            q4_stream_t stream);
 
 /*
  * gemm_w4a4_nvfp4 without a workspace, for callers that cannot give the

@@ -26,9 +26,11 @@ OP_QUANTIZE_NVFP4, OP_GEMM_W4A4_NVFP4, OP_GEMM_W4A4_MXFP4, OP_GEMM_W4A16_INT4 = 
 OP_GROUPED_GEMM_MOE, OP_GEMM_W4A16_NVFP4, OP_GEMM_W4A16_MXFP4 = 4, 5, 6
 OP_GEMM_FP8_BLOCKWISE, OP_GEMM_W4A8 = 7, 8
 OP_GEMM_W4A4_MXFP4_FUSED = 9
+OP_MOE_SORT, OP_GROUPED_WGRAD_FP8 = 10, 11
 
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 _LAYOUT = {"rowmajor": ROWMAJOR, "mma": MMA}
+_NORMALIZE = {"topk": 0, "all": 1}  # q4_route_normalize: softmax over the chosen / over all logits
 _ROUNDING = {"pages": 0, "rne": 1}  # q4_rounding: E2M1 ties to the smaller magnitude / to even
 
 _lib: Optional[ctypes.CDLL] = None
@@ -84,6 +86,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     _sig(lib, "gemm_fp8_blockwise", I, P, P, P, P, I64, I64, I64, P, I, P, SZ, P)
     _sig(lib, "w4a8_weight_scales", I, P, I64, I64, P, P)
     _sig(lib, "gemm_w4a8", I, P, P, P, P, I64, I64, I64, P, I, P, SZ, P)
+    _sig(lib, "moe_route_topk", I, P, I, I64, I64, I64, I, I, P, P, P)
+    _sig(lib, "moe_route_topk_backward", I, P, I, I64, I64, I64, I, I, P, P, P, P)
+    _sig(lib, "moe_sort_tokens", I, P, I64, I, I, P, P, P, P, SZ, P)
+    _sig(lib, "moe_dispatch", I, P, I, I64, I64, I64, P, I, P, P)
+    _sig(lib, "moe_dispatch_backward", I, P, I, I64, I64, I64, P, I, P, P)
+    _sig(lib, "moe_combine", I, P, I, I64, I64, I64, P, P, I, P, P)
+    _sig(lib, "moe_combine_backward", I, P, I, I64, I64, I64, P, I64, P, P, I, P, P, P)
+    _sig(lib, "quantize_fp8_checkpoint", I, P, I, I64, I64, I64, P, P, P)
+    _sig(lib, "swiglu_fp8", I, P, I, I64, I64, I64, P, P, P, P)
+    _sig(lib, "swiglu_fp8_backward", I, P, I, I64, I64, I64, P, P, P, P)
+    _sig(lib, "grouped_wgrad_fp8", I, P, I64, I64, I64, P, P, I64, I64, P, P, I, P, I, I, P, SZ, P)
     _sig(lib, "q4_sync_status", I, P)
     _sig(lib, "q4_status_string", ctypes.c_char_p, I)
     _sig(lib, "q4_set_wait_timeout_ms", I, I)
@@ -437,6 +450,261 @@ def grouped_gemm_moe(tokens: torch.Tensor, expert_offsets: torch.Tensor, row_tok
         tokens.data_ptr(), T, K, expert_offsets.data_ptr(), row_token.data_ptr(), R, E,
         ctypes.byref(w), N, C.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
     return C
+
+
+# --------------------------------------------------------------------------- routed experts
+
+def _pitched(x: torch.Tensor, name: str) -> int:
+    """The row pitch of a 2-D CUDA matrix whose rows are contiguous and do not overlap."""
+    if not x.is_cuda or x.dim() != 2 or x.dtype not in _DTYPE:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor of float32, bfloat16 or float16")
+    rows, cols = x.shape
+    if cols > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1 or cols == 0:
+        return max(cols, 1)
+    if x.stride(0) < cols:
+        raise ValueError(f"{name} has overlapping rows")
+    return x.stride(0)
+
+
+def _on(stream, *tensors):
+    """Tensors allocated here for another stream's call: their memory is not
+    reused before that stream's work is done."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _exact(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device) -> torch.Tensor:
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _slots(slot_row: torch.Tensor, T: int, device) -> int:
+    if slot_row.dim() != 2:
+        raise ValueError("slot_row must be a [T, top_k] tensor")
+    _exact(slot_row, "slot_row", (T, slot_row.shape[1]), torch.int32, device)
+    return slot_row.shape[1]
+
+
+def moe_route_topk(logits: torch.Tensor, top_k: int, normalize: str = "topk", stream=None):
+    """The top_k experts of every token and their softmax weights.
+    logits [T, E] (f32 / bf16 / f16, any row pitch; -inf masks an expert) ->
+    (ids int32 [T, top_k], weights float32 [T, top_k]).  normalize: "topk"
+    (softmax over the chosen logits) or "all" (over every logit)."""
+    ld = _pitched(logits, "logits")
+    T, E = logits.shape
+    ids = torch.empty((T, max(top_k, 0)), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((T, max(top_k, 0)), dtype=torch.float32, device=logits.device)
+    _check("moe_route_topk", lib().moe_route_topk(
+        logits.data_ptr(), _DTYPE[logits.dtype], T, E, max(ld, E), top_k, _NORMALIZE[normalize],
+        ids.data_ptr(), weights.data_ptr(), _stream(stream)))
+    _on(stream, ids, weights)
+    return ids, weights
+
+
+def moe_route_topk_backward(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor,
+                            normalize: str = "topk", stream=None) -> torch.Tensor:
+    """d_logits [T, E] (logits' dtype) of moe_route_topk from d_weights float32 [T, top_k]."""
+    ld = _pitched(logits, "logits")
+    T, E = logits.shape
+    if ids.dim() != 2:
+        raise ValueError("ids must be a [T, top_k] tensor")
+    k = ids.shape[1]
+    _exact(ids, "ids", (T, k), torch.int32, logits.device)
+    _exact(d_weights, "d_weights", (T, k), torch.float32, logits.device)
+    d = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _check("moe_route_topk_backward", lib().moe_route_topk_backward(
+        logits.data_ptr(), _DTYPE[logits.dtype], T, E, max(ld, E), k, _NORMALIZE[normalize],
+        ids.data_ptr(), d_weights.data_ptr(), d.data_ptr(), _stream(stream)))
+    _on(stream, d)
+    return d
+
+
+def moe_sort_tokens(ids: torch.Tensor, E: int, ws: Optional[torch.Tensor] = None, stream=None):
+    """Slots of ids int32 [T, top_k] sorted by expert -> (expert_offsets int32
+    [E+1], row_token int32 [T*top_k], slot_row int32 [T, top_k]): the first two
+    are grouped_gemm_moe's; slot_row holds every slot's row, or ~row where the
+    id is outside [0, E) (dropped; those rows come last).  ``ws`` from
+    ``workspace(OP_MOE_SORT, T * top_k, E, 0, device)``."""
+    if not ids.is_cuda or ids.dim() != 2:
+        raise ValueError("ids must be a [T, top_k] CUDA tensor")
+    T, k = ids.shape
+    dev = ids.device
+    _exact(ids, "ids", (T, k), torch.int32, dev)
+    if E < 1:
+        raise ValueError("E must be positive")
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    row_token = torch.empty(T * k, dtype=torch.int32, device=dev)
+    slot_row = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if ws is None:
+        ws = workspace(OP_MOE_SORT, T * k, E, 0, dev)
+    _check("moe_sort_tokens", lib().moe_sort_tokens(
+        ids.data_ptr(), T, k, E, offsets.data_ptr(), row_token.data_ptr(), slot_row.data_ptr(),
+        ws.data_ptr(), ws.numel(), _stream(stream)))
+    _on(stream, offsets, row_token, slot_row, ws)
+    return offsets, row_token, slot_row
+
+
+def moe_dispatch(x: torch.Tensor, slot_row: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+    """rows [T*top_k, H]: x [T, H] copied to every slot's row; rows of dropped slots are zero."""
+    ld = _pitched(x, "x")
+    T, H = x.shape
+    k = _slots(slot_row, T, x.device)
+    rows = _out(out, T * k, H, x.dtype, x.device)
+    _check("moe_dispatch", lib().moe_dispatch(x.data_ptr(), _DTYPE[x.dtype], T, H, max(ld, H),
+                                              slot_row.data_ptr(), k, rows.data_ptr(), _stream(stream)))
+    _on(stream, rows)
+    return rows
+
+
+def moe_dispatch_backward(d_rows: torch.Tensor, slot_row: torch.Tensor, out=None,
+                          stream=None) -> torch.Tensor:
+    """d_x [T, H]: the sum of every token's rows of d_rows [T*top_k, H]."""
+    ld = _pitched(d_rows, "d_rows")
+    T, H = slot_row.shape[0], d_rows.shape[1]
+    k = _slots(slot_row, T, d_rows.device)
+    if d_rows.shape[0] != T * k:
+        raise ValueError(f"d_rows has {d_rows.shape[0]} rows, slot_row {T * k} slots")
+    d_x = _out(out, T, H, d_rows.dtype, d_rows.device)
+    _check("moe_dispatch_backward", lib().moe_dispatch_backward(
+        d_rows.data_ptr(), _DTYPE[d_rows.dtype], T, H, max(ld, H), slot_row.data_ptr(), k, d_x.data_ptr(),
+        _stream(stream)))
+    _on(stream, d_x)
+    return d_x
+
+
+def moe_combine(rows: torch.Tensor, slot_row: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                out=None, stream=None) -> torch.Tensor:
+    """out [T, H] = sum over a token's slots of weights * rows[slot_row]
+    (weights float32 [T, top_k]; None: all 1); dropped slots are left out."""
+    ld = _pitched(rows, "rows")
+    T, H = slot_row.shape[0], rows.shape[1]
+    k = _slots(slot_row, T, rows.device)
+    if rows.shape[0] != T * k:
+        raise ValueError(f"rows has {rows.shape[0]} rows, slot_row {T * k} slots")
+    if weights is not None:
+        _exact(weights, "weights", (T, k), torch.float32, rows.device)
+    C = _out(out, T, H, rows.dtype, rows.device)
+    _check("moe_combine", lib().moe_combine(rows.data_ptr(), _DTYPE[rows.dtype], T, H, max(ld, H),
+                                            slot_row.data_ptr(), _ptr(weights), k, C.data_ptr(),
+                                            _stream(stream)))
+    _on(stream, C)
+    return C
+
+
+def moe_combine_backward(d_out: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tensor,
+                         weights: torch.Tensor, need_d_weights: bool = True, out=None, stream=None):
+    """Gradients of moe_combine: (d_rows [T*top_k, H], d_weights float32 [T,
+    top_k], or None without ``need_d_weights``, when rows is not read)."""
+    ldd, ld = _pitched(d_out, "d_out"), _pitched(rows, "rows")
+    T, H = d_out.shape
+    k = _slots(slot_row, T, d_out.device)
+    if tuple(rows.shape) != (T * k, H) or rows.dtype != d_out.dtype or rows.device != d_out.device:
+        raise ValueError(f"rows must be a {d_out.dtype} tensor of shape ({T * k}, {H}) on {d_out.device}")
+    _exact(weights, "weights", (T, k), torch.float32, d_out.device)
+    d_rows = _out(out, T * k, H, d_out.dtype, d_out.device)
+    dw = torch.empty((T, k), dtype=torch.float32, device=d_out.device) if need_d_weights else None
+    _check("moe_combine_backward", lib().moe_combine_backward(
+        d_out.data_ptr(), _DTYPE[d_out.dtype], T, H, max(ldd, H), rows.data_ptr(), max(ld, H),
+        slot_row.data_ptr(), weights.data_ptr(), k, d_rows.data_ptr(), _ptr(dw), _stream(stream)))
+    _on(stream, d_rows, *(() if dw is None else (dw,)))
+    return d_rows, dw
+
+
+# --------------------------------------------------------------------------- 8-bit checkpoints
+
+def quantize_fp8_checkpoint(x: torch.Tensor, stream=None):
+    """8-bit checkpoint of x [rows, K] (any row pitch) -> (codes u8 [rows, K]
+    E4M3, scales float32 [rows, ceil(K/128)], powers of two)."""
+    ld = _pitched(x, "x")
+    rows, K = x.shape
+    codes = torch.empty((rows, K), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((rows, -(-K // 128)), dtype=torch.float32, device=x.device)
+    _check("quantize_fp8_checkpoint", lib().quantize_fp8_checkpoint(
+        x.data_ptr(), _DTYPE[x.dtype], rows, K, max(ld, K), codes.data_ptr(), scales.data_ptr(),
+        _stream(stream)))
+    _on(stream, codes, scales)
+    return codes, scales
+
+
+def swiglu_fp8(gate_up: torch.Tensor, out=None, stream=None):
+    """h = silu(gate) * up of gate_up = [gate | up] [rows, 2I], and gate_up's
+    8-bit checkpoint from the same pass -> (h [rows, I], codes u8 [rows, 2I],
+    scales float32 [rows, 2 ceil(I/128)])."""
+    ld = _pitched(gate_up, "gate_up")
+    rows, two = gate_up.shape
+    if two % 2:
+        raise ValueError("gate_up must have an even number of columns")
+    inner, dev = two // 2, gate_up.device
+    h = _out(out, rows, inner, gate_up.dtype, dev)
+    codes = torch.empty((rows, two), dtype=torch.uint8, device=dev)
+    scales = torch.empty((rows, 2 * -(-inner // 128)), dtype=torch.float32, device=dev)
+    _check("swiglu_fp8", lib().swiglu_fp8(
+        gate_up.data_ptr(), _DTYPE[gate_up.dtype], rows, inner, max(ld, two), h.data_ptr(),
+        codes.data_ptr(), scales.data_ptr(), _stream(stream)))
+    _on(stream, h, codes, scales)
+    return h, codes, scales
+
+
+def swiglu_fp8_backward(d_h: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, out=None,
+                        stream=None) -> torch.Tensor:
+    """d_gate_up [rows, 2I] from d_h [rows, I] and swiglu_fp8's checkpoint."""
+    ld = _pitched(d_h, "d_h")
+    rows, inner = d_h.shape
+    _exact(codes, "codes", (rows, 2 * inner), torch.uint8, d_h.device)
+    _exact(scales, "scales", (rows, 2 * -(-inner // 128)), torch.float32, d_h.device)
+    d = _out(out, rows, 2 * inner, d_h.dtype, d_h.device)
+    _check("swiglu_fp8_backward", lib().swiglu_fp8_backward(
+        d_h.data_ptr(), _DTYPE[d_h.dtype], rows, inner, max(ld, inner), codes.data_ptr(),
+        scales.data_ptr(), d.data_ptr(), _stream(stream)))
+    _on(stream, d)
+    return d
+
+
+def grouped_wgrad_fp8(d_y: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                      expert_offsets: torch.Tensor, row_token: Optional[torch.Tensor] = None,
+                      out_dtype=torch.float32, out=None, accumulate: bool = False,
+                      ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dW [E, N, K] = per expert, d_y[rows]^T . x[row_token[rows]] with x the
+    checkpoint (codes u8 [T, K], scales [T, ceil(K/128)]).  d_y bf16 [R, N] (any
+    row pitch that is a multiple of 8); row_token int32 [R], or None when the
+    checkpoint is in row order.  out_dtype float32 or bfloat16; ``accumulate``
+    (float32 ``out`` only) adds to ``out``.  ``ws`` from
+    ``workspace(OP_GROUPED_WGRAD_FP8, T, N, K, device)``."""
+    if d_y.dtype != torch.bfloat16:
+        raise ValueError("d_y must be bfloat16")
+    ldy = _pitched(d_y, "d_y")
+    R, N = d_y.shape
+    dev = d_y.device
+    _cuda2d(codes, "codes")
+    T, K = codes.shape
+    _exact(codes, "codes", (T, K), torch.uint8, dev)
+    _exact(scales, "scales", (T, -(-K // 128)), torch.float32, dev)
+    E = expert_offsets.numel() - 1
+    if E < 0:
+        raise ValueError("expert_offsets must hold E + 1 entries")
+    _exact(expert_offsets, "expert_offsets", (E + 1,), torch.int32, dev)
+    if row_token is not None:
+        _exact(row_token, "row_token", (R,), torch.int32, dev)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if out is None:
+        out = torch.empty((E, N, K), dtype=out_dtype, device=dev)
+    else:
+        _exact(out, "out", (E, N, K), out.dtype, dev)
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("the gradient is float32 or bfloat16")
+    if ws is None:
+        ws = workspace(OP_GROUPED_WGRAD_FP8, T, N, K, dev)
+    _check("grouped_wgrad_fp8", lib().grouped_wgrad_fp8(
+        d_y.data_ptr(), R, N, max(ldy, N), codes.data_ptr(), scales.data_ptr(), T, K, _ptr(row_token),
+        expert_offsets.data_ptr(), E, out.data_ptr(), _DTYPE[out.dtype], int(accumulate),
+        ws.data_ptr(), ws.numel(), _stream(stream)))
+    _on(stream, out, ws)
+    return out
 
 
 def sync_status(stream=None) -> int:

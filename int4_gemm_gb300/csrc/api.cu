@@ -311,6 +311,8 @@ size_t q4_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
     case Q4_OP_GROUPED_GEMM_MOE: return 0;  // needs E and R: q4_workspace_size_moe
     case Q4_OP_GEMM_FP8_BLOCKWISE:
     case Q4_OP_GEMM_W4A8: return 0;
+    case Q4_OP_MOE_SORT: return moe_sort_workspace_bytes(M, N);
+    case Q4_OP_GROUPED_WGRAD_FP8: return wgrad_workspace_bytes(M, N, K);
     default: return 0;
   }
 }
@@ -612,6 +614,183 @@ q4_status grouped_gemm_moe(const void* tokens_bf16, int64_t T, int64_t K,
   g.T = T; g.R = R; g.N = N; g.K = K; g.E = E;
   g.w_codes = W_codes; g.w_scales = W_scales; g.w_g = W_tensor_scales; g.C = C_bf16;
   return launch_grouped_gemm(g, s);
+}
+
+namespace {
+constexpr int kMaxTopK = 32, kMaxRouteExperts = 1024;
+constexpr int64_t kMaxSlots = INT32_MAX / 2;
+
+size_t elem_bytes(int dtype) { return dtype == Q4_F32 ? 4 : 2; }
+
+// Checks shared by the calls that move rows between token and expert order.
+q4_status check_rows(int dtype, int64_t T, int64_t H, int top_k) {
+  if (!valid_dtype(dtype) || T < 0 || H < 0 || top_k < 1) return Q4_ERR_INVALID_ARG;
+  if (top_k > kMaxTopK || T > kMaxSlots / top_k || H > INT32_MAX / 2) return Q4_ERR_UNSUPPORTED_SHAPE;
+  return Q4_OK;
+}
+bool elem_ptr(const void* p, int dtype) { return p && aligned(p, elem_bytes(dtype)); }
+bool word_ptr(const void* p) { return p && aligned(p, 4); }
+
+q4_status check_route(int dtype, int64_t T, int64_t E, int64_t ld, int top_k, int normalize) {
+  if (!valid_dtype(dtype) || T < 0 || E < 1 || ld < E || top_k < 1 || top_k > E) return Q4_ERR_INVALID_ARG;
+  if (normalize != Q4_ROUTE_TOPK && normalize != Q4_ROUTE_ALL) return Q4_ERR_INVALID_ARG;
+  if (top_k > kMaxTopK || E > kMaxRouteExperts || T > kMaxSlots / top_k) return Q4_ERR_UNSUPPORTED_SHAPE;
+  return Q4_OK;
+}
+
+q4_status check_checkpoint(int dtype, int64_t rows, int64_t width, int64_t ld, int64_t need) {
+  if (!valid_dtype(dtype) || rows < 0 || width < 1 || ld < need) return Q4_ERR_INVALID_ARG;
+  if (width > INT32_MAX / 4 || (rows && ceil_div(width, 128) > INT32_MAX / 2 / rows)) return Q4_ERR_UNSUPPORTED_SHAPE;
+  return Q4_OK;
+}
+}  // namespace
+
+q4_status moe_route_topk(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, int top_k,
+                         int normalize, int32_t* ids, float* weights, q4_stream_t stream) {
+  const q4_status st = check_route(dtype, T, E, ld, top_k, normalize);
+  if (st != Q4_OK || T == 0) return st;
+  if (!elem_ptr(logits, dtype) || !word_ptr(ids) || !word_ptr(weights)) return Q4_ERR_INVALID_ARG;
+  return launch_route(logits, dtype, T, (int)E, ld, top_k, normalize == Q4_ROUTE_ALL, ids, weights,
+                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+q4_status moe_route_topk_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld,
+                                  int top_k, int normalize, const int32_t* ids,
+                                  const float* d_weights, void* d_logits, q4_stream_t stream) {
+  const q4_status st = check_route(dtype, T, E, ld, top_k, normalize);
+  if (st != Q4_OK || T == 0) return st;
+  if (!elem_ptr(logits, dtype) || !word_ptr(ids) || !word_ptr(d_weights) || !elem_ptr(d_logits, dtype))
+    return Q4_ERR_INVALID_ARG;
+  return launch_route_backward(logits, dtype, T, (int)E, ld, top_k, normalize == Q4_ROUTE_ALL, ids,
+                               d_weights, d_logits, reinterpret_cast<cudaStream_t>(stream));
+}
+
+q4_status moe_sort_tokens(const int32_t* ids, int64_t T, int top_k, int E, int32_t* expert_offsets,
+                          int32_t* row_token, int32_t* slot_row, void* ws, size_t ws_bytes,
+                          q4_stream_t stream) {
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T < 0 || top_k < 1 || E < 1) return Q4_ERR_INVALID_ARG;
+  if (top_k > kMaxTopK || E > kMaxRouteExperts || T > kMaxSlots / top_k) return Q4_ERR_UNSUPPORTED_SHAPE;
+  if (!word_ptr(expert_offsets)) return Q4_ERR_INVALID_ARG;
+  if (T == 0) {
+    Q4_CUDA_TRY(cudaMemsetAsync(expert_offsets, 0, (size_t)(E + 1) * sizeof(int32_t), s));
+    return Q4_OK;
+  }
+  if (!word_ptr(ids) || !word_ptr(row_token) || !word_ptr(slot_row)) return Q4_ERR_INVALID_ARG;
+  const size_t need = moe_sort_workspace_bytes(T * top_k, E);
+  if (need && (!ws || !aligned(ws, 256) || ws_bytes < need)) return Q4_ERR_WORKSPACE;
+  return launch_moe_sort(ids, T * top_k, top_k, E, expert_offsets, row_token, slot_row, ws, s);
+}
+
+q4_status moe_dispatch(const void* x, int dtype, int64_t T, int64_t H, int64_t ldx,
+                       const int32_t* slot_row, int top_k, void* rows, q4_stream_t stream) {
+  const q4_status st = check_rows(dtype, T, H, top_k);
+  if (st != Q4_OK) return st;
+  if (ldx < H) return Q4_ERR_INVALID_ARG;
+  if (T == 0 || H == 0) return Q4_OK;
+  if (!elem_ptr(x, dtype) || !word_ptr(slot_row) || !elem_ptr(rows, dtype)) return Q4_ERR_INVALID_ARG;
+  return launch_dispatch(x, dtype, T, H, ldx, slot_row, top_k, rows, reinterpret_cast<cudaStream_t>(stream));
+}
+
+q4_status moe_combine(const void* rows, int dtype, int64_t T, int64_t H, int64_t ld,
+                      const int32_t* slot_row, const float* weights, int top_k, void* out,
+                      q4_stream_t stream) {
+  const q4_status st = check_rows(dtype, T, H, top_k);
+  if (st != Q4_OK) return st;
+  if (ld < H) return Q4_ERR_INVALID_ARG;
+  if (T == 0 || H == 0) return Q4_OK;
+  if (!elem_ptr(rows, dtype) || !word_ptr(slot_row) || !aligned(weights, 4) || !elem_ptr(out, dtype))
+    return Q4_ERR_INVALID_ARG;
+  return launch_combine(rows, dtype, T, H, ld, slot_row, weights, top_k, out,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+q4_status moe_dispatch_backward(const void* d_rows, int dtype, int64_t T, int64_t H, int64_t ld,
+                                const int32_t* slot_row, int top_k, void* d_x, q4_stream_t stream) {
+  return moe_combine(d_rows, dtype, T, H, ld, slot_row, nullptr, top_k, d_x, stream);
+}
+
+q4_status moe_combine_backward(const void* d_out, int dtype, int64_t T, int64_t H, int64_t ld_d_out,
+                               const void* rows, int64_t ld_rows, const int32_t* slot_row,
+                               const float* weights, int top_k, void* d_rows, float* d_weights,
+                               q4_stream_t stream) {
+  const q4_status st = check_rows(dtype, T, H, top_k);
+  if (st != Q4_OK) return st;
+  if (ld_d_out < H || (d_weights && ld_rows < H)) return Q4_ERR_INVALID_ARG;
+  if (T == 0) return Q4_OK;
+  if (H == 0) {  // sums over nothing
+    if (d_weights)
+      Q4_CUDA_TRY(cudaMemsetAsync(d_weights, 0, (size_t)T * top_k * sizeof(float),
+                                  reinterpret_cast<cudaStream_t>(stream)));
+    return Q4_OK;
+  }
+  if (!elem_ptr(d_out, dtype) || !word_ptr(slot_row) || !word_ptr(weights) || !elem_ptr(d_rows, dtype) ||
+      (d_weights && (!elem_ptr(rows, dtype) || !aligned(d_weights, 4))))
+    return Q4_ERR_INVALID_ARG;
+  return launch_combine_backward(d_out, dtype, T, H, ld_d_out, rows, ld_rows, slot_row, weights, top_k,
+                                 d_rows, d_weights, reinterpret_cast<cudaStream_t>(stream));
+}
+
+q4_status quantize_fp8_checkpoint(const void* x, int dtype, int64_t rows, int64_t K, int64_t ld,
+                                  uint8_t* codes, float* scales, q4_stream_t stream) {
+  const q4_status st = check_checkpoint(dtype, rows, K, ld, K);
+  if (st != Q4_OK || rows == 0) return st;
+  if (!elem_ptr(x, dtype) || !codes || !word_ptr(scales)) return Q4_ERR_INVALID_ARG;
+  return launch_checkpoint(x, dtype, rows, K, ld, codes, scales, reinterpret_cast<cudaStream_t>(stream));
+}
+
+q4_status swiglu_fp8(const void* gate_up, int dtype, int64_t rows, int64_t I, int64_t ld, void* h,
+                     uint8_t* codes, float* scales, q4_stream_t stream) {
+  const q4_status st = check_checkpoint(dtype, rows, I, ld, 2 * I);
+  if (st != Q4_OK || rows == 0) return st;
+  if (!elem_ptr(gate_up, dtype) || !elem_ptr(h, dtype) || !codes || !word_ptr(scales)) return Q4_ERR_INVALID_ARG;
+  return launch_swiglu(gate_up, dtype, rows, I, ld, h, codes, scales, reinterpret_cast<cudaStream_t>(stream));
+}
+
+q4_status swiglu_fp8_backward(const void* d_h, int dtype, int64_t rows, int64_t I, int64_t ld,
+                              const uint8_t* codes, const float* scales, void* d_gate_up,
+                              q4_stream_t stream) {
+  const q4_status st = check_checkpoint(dtype, rows, I, ld, I);
+  if (st != Q4_OK || rows == 0) return st;
+  if (!elem_ptr(d_h, dtype) || !codes || !word_ptr(scales) || !elem_ptr(d_gate_up, dtype))
+    return Q4_ERR_INVALID_ARG;
+  return launch_swiglu_backward(d_h, dtype, rows, I, ld, codes, scales, d_gate_up,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+q4_status grouped_wgrad_fp8(const void* d_y_bf16, int64_t R, int64_t N, int64_t ldy,
+                            const uint8_t* codes, const float* scales, int64_t T, int64_t K,
+                            const int32_t* row_token, const int32_t* expert_offsets, int E,
+                            void* dW, int w_dtype, int accumulate, void* ws, size_t ws_bytes,
+                            q4_stream_t stream) {
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (R < 0 || N < 0 || K < 0 || T < 0 || E < 0 || ldy < N) return Q4_ERR_INVALID_ARG;
+  if (w_dtype != Q4_F32 && w_dtype != Q4_BF16) return Q4_ERR_INVALID_ARG;
+  if (accumulate && w_dtype != Q4_F32) return Q4_ERR_INVALID_ARG;
+  if (N % 8 || ldy % 8 || K % 16) return Q4_ERR_UNSUPPORTED_SHAPE;
+  if (E > kMaxRouteExperts || R > kMaxSlots || T > kMaxSlots || N > INT32_MAX / 4 || K > INT32_MAX / 4 ||
+      ldy > INT32_MAX / 4)
+    return Q4_ERR_UNSUPPORTED_SHAPE;
+  if (E == 0 || N == 0 || K == 0) return Q4_OK;
+  if (!dW || !aligned(dW, 16)) return Q4_ERR_INVALID_ARG;
+  if (R == 0 || T == 0) {  // no rows at all: every expert's gradient is zero
+    if (R > 0) return Q4_ERR_INVALID_ARG;
+    if (!accumulate)
+      Q4_CUDA_TRY(cudaMemsetAsync(dW, 0, (size_t)E * N * K * elem_bytes(w_dtype), s));
+    return Q4_OK;
+  }
+  if (!row_token && T != R) return Q4_ERR_INVALID_ARG;
+  if (!d_y_bf16 || !aligned(d_y_bf16, 16) || !codes || !aligned(codes, 16) || !word_ptr(scales) ||
+      !aligned(row_token, 4) || !word_ptr(expert_offsets))
+    return Q4_ERR_INVALID_ARG;
+  const size_t need = wgrad_workspace_bytes(T, N, K);
+  if (need && (!ws || !aligned(ws, 256) || ws_bytes < need)) return Q4_ERR_WORKSPACE;
+  WgradArgs a = {};
+  a.dy = d_y_bf16; a.R = R; a.N = N; a.ldy = ldy;
+  a.codes = codes; a.scales = scales; a.tokens = T; a.K = K;
+  a.row_token = row_token; a.offsets = expert_offsets; a.E = E;
+  a.dw = dW; a.w_dtype = w_dtype; a.accumulate = accumulate != 0; a.ws = ws;
+  return launch_wgrad(a, s);
 }
 
 q4_status q4_sync_status(q4_stream_t stream) {

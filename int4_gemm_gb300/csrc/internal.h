@@ -111,6 +111,52 @@ q4_status launch_w4a8_gemm(const uint8_t* qa, const float* sa, const uint8_t* wq
                            int64_t M, int64_t N, int64_t K, void* C, int c_dtype,
                            cudaStream_t stream);
 
+// ---------------------------------------------------------------- routed experts
+q4_status launch_route(const void* logits, int dtype, int64_t tokens, int E, int64_t ld, int top_k,
+                       bool over_all, int32_t* ids, float* weights, cudaStream_t stream);
+q4_status launch_route_backward(const void* logits, int dtype, int64_t tokens, int E, int64_t ld,
+                                int top_k, bool over_all, const int32_t* ids,
+                                const float* d_weights, void* d_logits, cudaStream_t stream);
+size_t moe_sort_workspace_bytes(int64_t slots, int64_t E);
+q4_status launch_moe_sort(const int32_t* ids, int64_t slots, int top_k, int E, int32_t* offsets,
+                          int32_t* row_token, int32_t* slot_row, void* ws, cudaStream_t stream);
+q4_status launch_dispatch(const void* x, int dtype, int64_t tokens, int64_t H, int64_t ldx,
+                          const int32_t* slot_row, int top_k, void* rows, cudaStream_t stream);
+q4_status launch_combine(const void* rows, int dtype, int64_t tokens, int64_t H, int64_t ld,
+                         const int32_t* slot_row, const float* weights, int top_k, void* out,
+                         cudaStream_t stream);
+q4_status launch_combine_backward(const void* d_out, int dtype, int64_t tokens, int64_t H,
+                                  int64_t ldd, const void* rows, int64_t ld,
+                                  const int32_t* slot_row, const float* weights, int top_k,
+                                  void* d_rows, float* d_weights, cudaStream_t stream);
+
+// ---------------------------------------------------------------- 8-bit checkpoints
+q4_status launch_checkpoint(const void* x, int dtype, int64_t rows, int64_t K, int64_t ld,
+                            uint8_t* codes, float* scales, cudaStream_t stream);
+q4_status launch_swiglu(const void* gate_up, int dtype, int64_t rows, int64_t I, int64_t ld, void* h,
+                        uint8_t* codes, float* scales, cudaStream_t stream);
+q4_status launch_swiglu_backward(const void* d_h, int dtype, int64_t rows, int64_t I, int64_t ld,
+                                 const uint8_t* codes, const float* scales, void* d_gate_up,
+                                 cudaStream_t stream);
+
+// Weight gradient of the experts' products from a checkpoint.
+struct WgradArgs {
+  const void* dy;  // bf16 [R, N], row pitch ldy
+  int64_t R, N, ldy;
+  const uint8_t* codes;   // [tokens, K]
+  const float* scales;    // [tokens, ceil(K / 128)]
+  int64_t tokens, K;
+  const int32_t* row_token;  // [R] or nullptr
+  const int32_t* offsets;    // [E + 1]
+  int E;
+  void* dw;  // [E, N, K]
+  int w_dtype;
+  bool accumulate;
+  void* ws;
+};
+size_t wgrad_workspace_bytes(int64_t tokens, int64_t N, int64_t K);
+q4_status launch_wgrad(const WgradArgs& a, cudaStream_t stream);
+
 // TMA descriptor creation through the driver entry point.
 q4_status make_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner_bytes, uint64_t rows,
                           uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows,

@@ -1,0 +1,533 @@
+// Routing of tokens to experts around the grouped products: top-k with softmax
+// weights, tokens sorted by expert, rows brought into expert order and back,
+// and the gradients of these.
+//
+// With l the logits of a token, V its experts with l > -inf and C the top_k
+// of V by logit (ties to the lower index):
+//   weights   w_j = exp(l_j - m) / sum_{i in C or V} exp(l_i - m),  m = max l
+//   gradient  over C: dl_j = w_j (dw_j - sum_i dw_i w_i), zero elsewhere;
+//             over V: dl_e = p_e (g_e - sum_i dw_i p_i), g_e = dw_j for the
+//             chosen expert of slot j and 0 otherwise.
+// A slot (t, j) has a row in expert order; slot_row holds that row, or ~row
+// for a slot that was dropped (its row lies behind every expert's rows):
+//   dispatch  rows[row(t, j)] = x[t]                (zero for a dropped slot)
+//   combine   out[t] = sum_j w_tj rows[row(t, j)]   (dropped slots left out)
+//   gradient  d_rows[row(t, j)] = w_tj d_out[t],  dw_tj = <d_out[t], rows[row(t, j)]>
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace q4 {
+namespace {
+
+constexpr int kWarp = 32;
+constexpr unsigned kFull = 0xffffffffu;
+
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+// ------------------------------------------------------------------ routing
+// An unsigned key that orders logits as numbers do (-0 equal to +0); 0 for a
+// masked expert: -inf, or a NaN or +inf, which are latched as errors.
+__device__ __forceinline__ uint32_t order_key(float v, bool& bad) {
+  if (nonfinite(v)) {
+    bad |= !(v < 0.f);
+    return 0;
+  }
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+constexpr int kRouteWarps = 4;
+
+// One warp per token; lane l holds logits l, l + 32, ...  Every round takes
+// the warp's largest key, then the lowest index that has it.
+template <typename T, int NV>
+__global__ void __launch_bounds__(kRouteWarps * kWarp)
+    route_kernel(const T* __restrict__ logits, int64_t tokens, int E, int64_t ld, int top_k, int over_all,
+                 int32_t* __restrict__ ids, float* __restrict__ weights, int* status) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
+  if (t >= tokens) return;
+  const T* row = logits + t * ld;
+  uint32_t key[NV];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = e < E ? order_key(Elem<T>::to_f(row[e]), bad) : 0u;
+  }
+  if (__any_sync(kFull, bad) && lane == 0) latch_status(status, Q4_ERR_NONFINITE);
+  float top = 0.f, sum = 0.f, mine = 0.f;
+  int my_id = -1;
+  for (int j = 0; j < top_k; ++j) {
+    uint32_t best = 0;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (key[i] > best) best = key[i], at = i;
+    const uint32_t m = __reduce_max_sync(kFull, best);
+    if (m == 0) break;
+    const uint32_t id = __reduce_min_sync(kFull, best == m ? (uint32_t)(lane + 32 * at) : 0xffffffffu);
+    if (j == 0) {
+      top = key_value(m);
+      if (over_all) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (key[i]) sum += expf(key_value(key[i]) - top);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      }
+    }
+    const float w = expf(key_value(m) - top);
+    if (!over_all) sum += w;
+    if (lane == j) my_id = (int)id, mine = w;
+    if ((int)(id & 31u) == lane) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (i == (int)(id >> 5)) key[i] = 0;
+    }
+  }
+  if (lane < top_k) {
+    ids[t * top_k + lane] = my_id;
+    weights[t * top_k + lane] = my_id < 0 ? 0.f : mine / sum;
+  }
+}
+
+// The gradient; one warp per token, lane j also holds slot j.  The maximum
+// and sum are taken again from the logits, which have to be read anyway.
+template <typename T, int NV>
+__global__ void __launch_bounds__(kRouteWarps * kWarp)
+    route_backward_kernel(const T* __restrict__ logits, int64_t tokens, int E, int64_t ld, int top_k,
+                          int over_all, const int32_t* __restrict__ ids,
+                          const float* __restrict__ d_weights, T* __restrict__ d_logits) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
+  if (t >= tokens) return;
+  const T* row = logits + t * ld;
+  bool bad = false;
+  int id = lane < top_k ? ids[t * top_k + lane] : -1;
+  if (id >= E) id = -1;
+  const uint32_t kid = id >= 0 ? order_key(Elem<T>::to_f(row[id]), bad) : 0u;
+  const float dw = kid ? d_weights[t * top_k + lane] : 0.f;
+  uint32_t key[NV];
+  uint32_t best = over_all ? 0u : kid;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = e < E ? order_key(Elem<T>::to_f(row[e]), bad) : 0u;
+    if (over_all) best = max(best, key[i]);
+  }
+  const uint32_t m = __reduce_max_sync(kFull, best);
+  const float top = m ? key_value(m) : 0.f;
+  const float w = kid ? expf(key_value(kid) - top) : 0.f;
+  float p[NV];
+  float sum = over_all ? 0.f : w, dot = w * dw;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    p[i] = over_all && key[i] ? expf(key_value(key[i]) - top) : 0.f;
+    if (over_all) sum += p[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(kFull, sum, o);
+    dot += __shfl_xor_sync(kFull, dot, o);
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  dot *= inv;
+  float g[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) g[i] = over_all ? -p[i] * inv * dot : 0.f;
+  for (int j = 0; j < top_k; ++j) {
+    const int e = __shfl_sync(kFull, kid ? id : -1, j);
+    const float add = __shfl_sync(kFull, over_all ? w * inv * dw : w * inv * (dw - dot), j);
+    if (e >= 0 && (e & 31) == lane) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (i == (e >> 5)) g[i] += add;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + 32 * i;
+    if (e < E) d_logits[t * E + e] = from_f<T>(g[i]);
+  }
+}
+
+// ------------------------------------------------------------------ sort
+// A stable counting sort of the S = T top_k slots by expert (bucket E holds
+// the dropped ones): chunk histograms, one scan per expert over the chunks,
+// then every chunk places its slots.
+constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32;
+constexpr int kSortChunk = 2048, kSortPerWarp = kSortChunk / kSortWarps;
+
+__device__ __forceinline__ int sort_bucket(const int32_t* __restrict__ ids, int64_t i, int E) {
+  const int e = __ldg(ids + i);
+  return (unsigned)e < (unsigned)E ? e : E;
+}
+
+__global__ void __launch_bounds__(kSortThreads)
+    sort_count_kernel(const int32_t* __restrict__ ids, int64_t S, int E, int chunks, int32_t* __restrict__ hist) {
+  pdl_wait();
+  extern __shared__ int32_t cnt[];
+  for (int e = threadIdx.x; e <= E; e += kSortThreads) cnt[e] = 0;
+  __syncthreads();
+  const int64_t base = (int64_t)blockIdx.x * kSortChunk;
+  for (int i = threadIdx.x; i < kSortChunk && base + i < S; i += kSortThreads)
+    atomicAdd(cnt + sort_bucket(ids, base + i, E), 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= E; e += kSortThreads) hist[(int64_t)e * chunks + blockIdx.x] = cnt[e];
+}
+
+// Block e: exclusive prefix of expert e's chunk counts, and their total.
+__global__ void __launch_bounds__(kSortThreads)
+    sort_scan_kernel(int chunks, int32_t* __restrict__ hist, int32_t* __restrict__ total) {
+  pdl_wait();
+  __shared__ int32_t warp_sum[kSortWarps];
+  int32_t* h = hist + (int64_t)blockIdx.x * chunks;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int carry = 0;
+  for (int c0 = 0; c0 < chunks; c0 += kSortThreads) {
+    const int c = c0 + threadIdx.x;
+    const int v = c < chunks ? h[c] : 0;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int before = carry, all = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+      if (w < warp) before += warp_sum[w];
+      all += warp_sum[w];
+    }
+    if (c < chunks) h[c] = before + x - v;
+    carry += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) total[blockIdx.x] = carry;
+}
+
+__global__ void __launch_bounds__(kSortThreads)
+    sort_place_kernel(const int32_t* __restrict__ ids, int64_t S, int E, int top_k, int chunks,
+                      const int32_t* __restrict__ hist, const int32_t* __restrict__ total,
+                      int32_t* __restrict__ offsets, int32_t* __restrict__ row_token,
+                      int32_t* __restrict__ slot_row) {
+  pdl_wait();
+  extern __shared__ int32_t cnt[];  // [kSortWarps][E + 1], then [E + 1] first rows of the experts
+  __shared__ int32_t warp_sum[kSortWarps];
+  const int nb = E + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int32_t* first = cnt + kSortWarps * nb;
+  for (int i = threadIdx.x; i < kSortWarps * nb; i += kSortThreads) cnt[i] = 0;
+  // exclusive prefix of the experts' totals
+  int carry = 0;
+  for (int e0 = 0; e0 < nb; e0 += kSortThreads) {
+    const int e = e0 + threadIdx.x;
+    const int v = e < nb ? total[e] : 0;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int before = carry, all = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+      if (w < warp) before += warp_sum[w];
+      all += warp_sum[w];
+    }
+    if (e < nb) {
+      first[e] = before + x - v;
+      if (blockIdx.x == 0) offsets[e] = before + x - v;
+    }
+    carry += all;
+    __syncthreads();
+  }
+  const int64_t base = (int64_t)blockIdx.x * kSortChunk + warp * kSortPerWarp;
+  int32_t* mine = cnt + warp * nb;
+  for (int i = 0; i < kSortPerWarp; i += 32) {
+    const int64_t s = base + i + lane;
+    const int b = s < S ? sort_bucket(ids, s, E) : -1;
+    const unsigned peers = __match_any_sync(kFull, b);
+    if (b >= 0 && lane == __ffs(peers) - 1) mine[b] += __popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < nb; e += kSortThreads) {
+    int at = first[e] + hist[(int64_t)e * chunks + blockIdx.x];
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int c = cnt[w * nb + e];
+      cnt[w * nb + e] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  for (int i = 0; i < kSortPerWarp; i += 32) {
+    const int64_t s = base + i + lane;
+    const int b = s < S ? sort_bucket(ids, s, E) : -1;
+    const unsigned peers = __match_any_sync(kFull, b);
+    int row = 0;
+    if (b >= 0) row = mine[b] + __popc(peers & ((1u << lane) - 1u));
+    __syncwarp();
+    if (b >= 0 && lane == __ffs(peers) - 1) mine[b] += __popc(peers);
+    __syncwarp();
+    if (b >= 0) {
+      row_token[row] = (int32_t)(s / top_k);
+      slot_row[s] = b < E ? row : ~row;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ dispatch / combine
+// A row is cut into units: 16 bytes where the width, pitches and addresses
+// allow it, single elements otherwise.
+template <typename T, bool kVec>
+struct Unit {
+  static constexpr int n = kVec ? 16 / (int)sizeof(T) : 1;
+  T v[n];
+};
+template <typename T, bool kVec>
+__device__ __forceinline__ Unit<T, kVec> load_unit(const T* p) {
+  Unit<T, kVec> u;
+  if constexpr (kVec) {
+    *reinterpret_cast<uint4*>(u.v) = __ldg(reinterpret_cast<const uint4*>(p));
+  } else {
+    u.v[0] = p[0];
+  }
+  return u;
+}
+template <typename T, bool kVec>
+__device__ __forceinline__ void store_unit(T* p, const Unit<T, kVec>& u) {
+  if constexpr (kVec) {
+    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(u.v);
+  } else {
+    p[0] = u.v[0];
+  }
+}
+
+// blockIdx.x: token; the units of its row are spread over blockIdx.y.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(256)
+    dispatch_kernel(const T* __restrict__ x, int64_t ldx, int64_t H, const int32_t* __restrict__ slot_row,
+                    int top_k, uint32_t S, T* __restrict__ rows) {
+  pdl_wait();
+  constexpr int n = Unit<T, kVec>::n;
+  const int64_t t = blockIdx.x, units = H / n;
+  const int32_t* slots = slot_row + t * top_k;
+  for (int64_t u = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; u < units; u += (int64_t)gridDim.y * blockDim.x) {
+    const Unit<T, kVec> v = load_unit<T, kVec>(x + t * ldx + u * n);
+    Unit<T, kVec> zero;
+#pragma unroll
+    for (int i = 0; i < n; ++i) zero.v[i] = from_f<T>(0.f);
+    for (int j = 0; j < top_k; ++j) {
+      const int32_t s = __ldg(slots + j);
+      const uint32_t row = s < 0 ? ~s : s;
+      if (row < S) store_unit<T, kVec>(rows + (int64_t)row * H + u * n, s < 0 ? zero : v);
+    }
+  }
+}
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(256)
+    combine_kernel(const T* __restrict__ rows, int64_t ld, int64_t H, const int32_t* __restrict__ slot_row,
+                   const float* __restrict__ weights, int top_k, uint32_t S, T* __restrict__ out) {
+  pdl_wait();
+  constexpr int n = Unit<T, kVec>::n;
+  const int64_t t = blockIdx.x, units = H / n;
+  for (int64_t u = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; u < units; u += (int64_t)gridDim.y * blockDim.x) {
+    float acc[n];
+#pragma unroll
+    for (int i = 0; i < n; ++i) acc[i] = 0.f;
+    for (int j = 0; j < top_k; ++j) {
+      const int32_t s = __ldg(slot_row + t * top_k + j);
+      if ((uint32_t)s >= S) continue;
+      const float w = weights ? __ldg(weights + t * top_k + j) : 1.f;
+      const Unit<T, kVec> v = load_unit<T, kVec>(rows + (int64_t)s * ld + u * n);
+#pragma unroll
+      for (int i = 0; i < n; ++i) acc[i] = fmaf(w, Elem<T>::to_f(v.v[i]), acc[i]);
+    }
+    Unit<T, kVec> o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) o.v[i] = from_f<T>(acc[i]);
+    store_unit<T, kVec>(out + t * H + u * n, o);
+  }
+}
+
+constexpr int kGradThreads = 256;
+
+// One block per token; slot by slot, the row's dot product with d_out[t] is
+// summed over the block while w d_out[t] is written.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kGradThreads)
+    combine_backward_kernel(const T* __restrict__ d_out, int64_t ldd, const T* __restrict__ rows, int64_t ld,
+                            int64_t H, const int32_t* __restrict__ slot_row, const float* __restrict__ weights,
+                            int top_k, uint32_t S, T* __restrict__ d_rows, float* __restrict__ d_weights) {
+  pdl_wait();
+  constexpr int n = Unit<T, kVec>::n;
+  __shared__ float part[kGradThreads / 32];
+  const int64_t t = blockIdx.x, units = H / n;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int j = 0; j < top_k; ++j) {
+    const int32_t s = __ldg(slot_row + t * top_k + j);
+    const uint32_t row = s < 0 ? ~s : s;
+    const bool live = s >= 0 && row < S;
+    const float w = live ? __ldg(weights + t * top_k + j) : 0.f;
+    float dot = 0.f;
+    if (row < S) {
+      for (int64_t u = threadIdx.x; u < units; u += kGradThreads) {
+        const Unit<T, kVec> d = load_unit<T, kVec>(d_out + t * ldd + u * n);
+        Unit<T, kVec> o;
+        if (live && d_weights) {
+          const Unit<T, kVec> y = load_unit<T, kVec>(rows + (int64_t)row * ld + u * n);
+#pragma unroll
+          for (int i = 0; i < n; ++i) dot = fmaf(Elem<T>::to_f(d.v[i]), Elem<T>::to_f(y.v[i]), dot);
+        }
+#pragma unroll
+        for (int i = 0; i < n; ++i) o.v[i] = live ? from_f<T>(w * Elem<T>::to_f(d.v[i])) : from_f<T>(0.f);
+        store_unit<T, kVec>(d_rows + (int64_t)row * H + u * n, o);
+      }
+    }
+    if (d_weights) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+      if (lane == 0) part[warp] = dot;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        float sum = 0.f;
+        for (int i = 0; i < kGradThreads / 32; ++i) sum += part[i];
+        d_weights[t * top_k + j] = sum;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ------------------------------------------------------------------ launches
+template <typename F>
+q4_status by_dtype(int dtype, F&& f) {
+  if (dtype == Q4_F32) return f(float());
+  if (dtype == Q4_BF16) return f(__nv_bfloat16());
+  return f(__half());
+}
+
+inline bool vec16(const void* p, int64_t pitch, size_t elem) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (pitch * elem) % 16 == 0;
+}
+
+// Threads and y blocks for one row of `units` per token: enough blocks to
+// fill the GPU when there are few tokens.
+inline void row_grid(int64_t tokens, int64_t units, dim3& grid, dim3& block) {
+  const int64_t threads = std::min<int64_t>(256, ceil_div(units, 32) * 32);
+  const int64_t want = ceil_div((int64_t)num_sms() * 4, tokens);
+  const int64_t y = std::max<int64_t>(1, std::min<int64_t>(want, ceil_div(units, threads)));
+  grid = dim3((unsigned)tokens, (unsigned)std::min<int64_t>(y, 65535));
+  block = dim3((unsigned)threads);
+}
+
+}  // namespace
+
+#define Q4_ROUTE_NV(KERNEL, ...)                                                                  \
+  (E <= 32 ? launch_pdl(KERNEL<T, 1>, grid, block, 0, stream, __VA_ARGS__)                        \
+   : E <= 64 ? launch_pdl(KERNEL<T, 2>, grid, block, 0, stream, __VA_ARGS__)                      \
+   : E <= 128 ? launch_pdl(KERNEL<T, 4>, grid, block, 0, stream, __VA_ARGS__)                     \
+   : E <= 256 ? launch_pdl(KERNEL<T, 8>, grid, block, 0, stream, __VA_ARGS__)                     \
+   : E <= 512 ? launch_pdl(KERNEL<T, 16>, grid, block, 0, stream, __VA_ARGS__)                    \
+              : launch_pdl(KERNEL<T, 32>, grid, block, 0, stream, __VA_ARGS__))
+
+q4_status launch_route(const void* logits, int dtype, int64_t tokens, int E, int64_t ld, int top_k, bool over_all,
+                       int32_t* ids, float* weights, cudaStream_t stream) {
+  const dim3 grid((unsigned)ceil_div(tokens, kRouteWarps)), block(kRouteWarps * kWarp);
+  return by_dtype(dtype, [&](auto tag) {
+    using T = decltype(tag);
+    return Q4_ROUTE_NV(route_kernel, static_cast<const T*>(logits), tokens, E, ld, top_k, (int)over_all, ids,
+                       weights, device_status_ptr());
+  });
+}
+
+q4_status launch_route_backward(const void* logits, int dtype, int64_t tokens, int E, int64_t ld, int top_k,
+                                bool over_all, const int32_t* ids, const float* d_weights, void* d_logits,
+                                cudaStream_t stream) {
+  const dim3 grid((unsigned)ceil_div(tokens, kRouteWarps)), block(kRouteWarps * kWarp);
+  return by_dtype(dtype, [&](auto tag) {
+    using T = decltype(tag);
+    return Q4_ROUTE_NV(route_backward_kernel, static_cast<const T*>(logits), tokens, E, ld, top_k, (int)over_all,
+                       ids, d_weights, static_cast<T*>(d_logits));
+  });
+}
+
+// Counts per expert and chunk, then the experts' totals.
+size_t moe_sort_workspace_bytes(int64_t S, int64_t E) {
+  return (size_t)(E + 1) * (size_t)(ceil_div(S, kSortChunk) + 1) * sizeof(int32_t);
+}
+
+q4_status launch_moe_sort(const int32_t* ids, int64_t S, int top_k, int E, int32_t* offsets, int32_t* row_token,
+                          int32_t* slot_row, void* ws, cudaStream_t stream) {
+  const int chunks = (int)ceil_div(S, kSortChunk);
+  int32_t* hist = static_cast<int32_t*>(ws);
+  int32_t* total = hist + (int64_t)(E + 1) * chunks;
+  const size_t row = (size_t)(E + 1) * sizeof(int32_t);
+  q4_status st = launch_pdl(sort_count_kernel, chunks, kSortThreads, row, stream, ids, S, E, chunks, hist);
+  if (st != Q4_OK) return st;
+  st = launch_pdl(sort_scan_kernel, E + 1, kSortThreads, 0, stream, chunks, hist, total);
+  if (st != Q4_OK) return st;
+  return launch_pdl(sort_place_kernel, chunks, kSortThreads, (kSortWarps + 1) * row, stream, ids, S, E, top_k,
+                    chunks, hist, total, offsets, row_token, slot_row);
+}
+
+q4_status launch_dispatch(const void* x, int dtype, int64_t tokens, int64_t H, int64_t ldx, const int32_t* slot_row,
+                          int top_k, void* rows, cudaStream_t stream) {
+  return by_dtype(dtype, [&](auto tag) {
+    using T = decltype(tag);
+    const bool vec = vec16(x, ldx, sizeof(T)) && vec16(rows, H, sizeof(T));
+    dim3 grid, block;
+    row_grid(tokens, vec ? H * (int64_t)sizeof(T) / 16 : H, grid, block);
+    return launch_pdl(vec ? dispatch_kernel<T, true> : dispatch_kernel<T, false>, grid, block, 0, stream,
+                      static_cast<const T*>(x), ldx, H, slot_row, top_k, (uint32_t)(tokens * top_k),
+                      static_cast<T*>(rows));
+  });
+}
+
+q4_status launch_combine(const void* rows, int dtype, int64_t tokens, int64_t H, int64_t ld, const int32_t* slot_row,
+                         const float* weights, int top_k, void* out, cudaStream_t stream) {
+  return by_dtype(dtype, [&](auto tag) {
+    using T = decltype(tag);
+    const bool vec = vec16(rows, ld, sizeof(T)) && vec16(out, H, sizeof(T));
+    dim3 grid, block;
+    row_grid(tokens, vec ? H * (int64_t)sizeof(T) / 16 : H, grid, block);
+    return launch_pdl(vec ? combine_kernel<T, true> : combine_kernel<T, false>, grid, block, 0, stream,
+                      static_cast<const T*>(rows), ld, H, slot_row, weights, top_k, (uint32_t)(tokens * top_k),
+                      static_cast<T*>(out));
+  });
+}
+
+q4_status launch_combine_backward(const void* d_out, int dtype, int64_t tokens, int64_t H, int64_t ldd,
+                                  const void* rows, int64_t ld, const int32_t* slot_row, const float* weights,
+                                  int top_k, void* d_rows, float* d_weights, cudaStream_t stream) {
+  return by_dtype(dtype, [&](auto tag) {
+    using T = decltype(tag);
+    const bool vec = vec16(d_out, ldd, sizeof(T)) && vec16(d_rows, H, sizeof(T)) &&
+                     (!d_weights || vec16(rows, ld, sizeof(T)));
+    return launch_pdl(vec ? combine_backward_kernel<T, true> : combine_backward_kernel<T, false>, (unsigned)tokens,
+                      kGradThreads, 0, stream, static_cast<const T*>(d_out), ldd, static_cast<const T*>(rows), ld, H,
+                      slot_row, weights, top_k, (uint32_t)(tokens * top_k), static_cast<T*>(d_rows), d_weights);
+  });
+}
+
+}  // namespace q4

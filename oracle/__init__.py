@@ -49,7 +49,7 @@ by special cases (identity operand, equal blocks); no page prints a GEMM
 output, so beyond that their parity rests on the FP64 definition.
 """
 
-from . import formats, quantize, gemm, fp8  # noqa: F401
+from . import formats, quantize, gemm, fp8, moe  # noqa: F401
 from .quantize import (  # noqa: F401
     nvfp4_tensor_scale, quantize_nvfp4, quantize_mxfp4, quantize_int4_g128,
     dequantize_nvfp4, dequantize_mxfp4, dequantize_int4_g128,
