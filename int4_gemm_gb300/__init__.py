@@ -673,7 +673,7 @@ def grouped_wgrad_fp8(d_y: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
     row pitch that is a multiple of 8); row_token int32 [R], or None when the
     checkpoint is in row order.  out_dtype float32 or bfloat16; ``accumulate``
     (float32 ``out`` only) adds to ``out``.  ``ws`` from
-    ``workspace(OP_GROUPED_WGRAD_FP8, T, N, K, device)``."""
+    ``workspace(OP_GROUPED_WGRAD_FP8, R, N, K, device)``."""
     if d_y.dtype != torch.bfloat16:
         raise ValueError("d_y must be bfloat16")
     ldy = _pitched(d_y, "d_y")
@@ -698,7 +698,7 @@ def grouped_wgrad_fp8(d_y: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
     if out.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("the gradient is float32 or bfloat16")
     if ws is None:
-        ws = workspace(OP_GROUPED_WGRAD_FP8, T, N, K, dev)
+        ws = workspace(OP_GROUPED_WGRAD_FP8, R, N, K, dev)
     _check("grouped_wgrad_fp8", lib().grouped_wgrad_fp8(
         d_y.data_ptr(), R, N, max(ldy, N), codes.data_ptr(), scales.data_ptr(), T, K, _ptr(row_token),
         expert_offsets.data_ptr(), E, out.data_ptr(), _DTYPE[out.dtype], int(accumulate),

@@ -117,6 +117,26 @@ q4_status make_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t d0, uint6
   return r == CUDA_SUCCESS ? Q4_OK : Q4_ERR_CUDA;
 }
 
+// A tensor of FP32 or bf16 elements viewed as [d2][d1][d0] (s1, s2: the
+// pitches of d1 and d2 in elements), boxes of b0 x b1 x b2 elements.
+q4_status make_tmap_3d(CUtensorMap* map, int dtype, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                       uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2, bool swizzle128) {
+  CUtensorMap dummy;
+  q4_status st = make_tmap_2d_u8(&dummy, base, 16, 1, 16, 16, 1, false);  // loads the encoder
+  if (st != Q4_OK) return st;
+  const uint64_t size = dtype == Q4_F32 ? 4 : 2;
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {s1 * size, s2 * size};
+  const cuuint32_t box[3] = {b0, b1, b2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(
+      map, dtype == Q4_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+      const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? Q4_OK : Q4_ERR_CUDA;
+}
+
 namespace {
 
 // Workspace plan of one FP4 GEMM operand given raw or with row-major scales.
@@ -783,7 +803,7 @@ q4_status grouped_wgrad_fp8(const void* d_y_bf16, int64_t R, int64_t N, int64_t 
   if (!d_y_bf16 || !aligned(d_y_bf16, 16) || !codes || !aligned(codes, 16) || !word_ptr(scales) ||
       !aligned(row_token, 4) || !word_ptr(expert_offsets))
     return Q4_ERR_INVALID_ARG;
-  const size_t need = wgrad_workspace_bytes(T, N, K);
+  const size_t need = wgrad_workspace_bytes(R, N, K);
   if (need && (!ws || !aligned(ws, 256) || ws_bytes < need)) return Q4_ERR_WORKSPACE;
   WgradArgs a = {};
   a.dy = d_y_bf16; a.R = R; a.N = N; a.ldy = ldy;

@@ -154,7 +154,7 @@ struct WgradArgs {
   bool accumulate;
   void* ws;
 };
-size_t wgrad_workspace_bytes(int64_t tokens, int64_t N, int64_t K);
+size_t wgrad_workspace_bytes(int64_t R, int64_t N, int64_t K);
 q4_status launch_wgrad(const WgradArgs& a, cudaStream_t stream);
 
 // TMA descriptor creation through the driver entry point.
@@ -167,6 +167,11 @@ q4_status make_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner_byt
 q4_status make_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1,
                           uint64_t d2, uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1,
                           uint32_t b2, bool swizzle128);
+
+// The same for FP32 or bf16 elements: sizes, pitches and boxes in elements.
+q4_status make_tmap_3d(CUtensorMap* map, int dtype, const void* base, uint64_t d0, uint64_t d1,
+                       uint64_t d2, uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2,
+                       bool swizzle128);
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

@@ -5,20 +5,22 @@
 //
 // The contraction runs over rows, along which neither operand is contiguous:
 // d_y is [r][n] and x is [r][k], so both enter the tensor cores MN-major, as
-// they lie.  A first kernel restores x once per token into the workspace (the
-// codes are read once, not once per 256 columns of N and per routed copy);
-// the second is a grouped bf16 GEMM on CTA pairs:
+// they lie.  A first kernel restores x into the workspace in the order of the
+// routed rows; the second is a grouped bf16 GEMM on CTA pairs:
 //   tile     256 (n) x 256 (k) per pair, 128 n rows and 128 k columns of the
 //            operands per CTA, 64 rows r per stage (32 KB per CTA);
-//   warp 0   TMA producer: two 64 x 64 boxes of d_y, and of x sixteen
-//            four-row gathers per 64 columns through row_token (or two boxes
-//            when the checkpoint is in row order);
+//   warp 0   TMA producer: two 64 x 64 boxes of each operand per stage;
 //   warp 1   even CTA: four tcgen05.mma kind::f16 (256 x 256 x 16) per stage
 //            into one of two 256-column TMEM slots; odd CTA: tells the even
 //            one that its half of the stage has landed.  In a group's last
 //            stage both first clear the rows behind the group (they belong to
 //            the next expert, whose values may be infinite);
-//   warps 2..9  epilogue: TMEM to dW.
+//   warps 2..9  epilogue: TMEM through 128-byte swizzled rows in shared memory
+//            to dW by TMA stores (adds, when accumulating), clipped at the
+//            edges of the expert's matrix.
+// Restoring once per token and letting the producer gather rows (four-row TMA
+// gathers, 32 per stage) moved 0.4 GB less and was slower: 2453 us against
+// 1087 us with rows in order (64 experts of 2048 x 7168, 32768 rows).
 #include <algorithm>
 
 #include "common.cuh"
@@ -30,31 +32,33 @@ namespace {
 // ------------------------------------------------------------------ restore
 constexpr int kRestoreThreads = 256;
 
-// 16 codes per thread: x[t, c .. c + 16) = bf16(code * scale), row pitch KP.
+// 16 codes per thread: x[r, c .. c + 16) = bf16(code * scale) of token
+// row_token[r], for the rows that belong to an expert.
 __global__ void __launch_bounds__(kRestoreThreads)
     wgrad_restore_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales, int64_t tokens,
-                         int64_t K, int64_t KP, __nv_bfloat16* __restrict__ x) {
+                         int64_t K, const int32_t* __restrict__ row_token, const int32_t* __restrict__ last, int64_t R,
+                         __nv_bfloat16* __restrict__ x) {
   pdl_wait();
-  const uint32_t per_row = (uint32_t)(K / 16);
-  const int64_t KB = (K + 127) / 128;
-  for (int64_t t = blockIdx.y; t < tokens; t += gridDim.y) {
-    for (uint32_t v = blockIdx.x * kRestoreThreads + threadIdx.x; v < per_row; v += gridDim.x * kRestoreThreads) {
-      const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes + t * K) + v);
-      const float s = __ldg(scales + t * KB + v / 8);
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-      uint32_t o[8];
+  const uint32_t v = blockIdx.x * kRestoreThreads + threadIdx.x;
+  if (v >= (uint32_t)(K / 16)) return;
+  const int64_t KB = (K + 127) / 128, rows = min((int64_t)__ldg(last), R);
+  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+    const int64_t t = row_token ? min(max((int64_t)__ldg(row_token + r), (int64_t)0), tokens - 1) : r;
+    const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes + t * K) + v);
+    const float s = __ldg(scales + t * KB + v / 8);
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint32_t o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t h;  // two E4M3 codes as f16 (exact)
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[i / 2] >> (16 * (i & 1)))));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
-        o[i] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-      uint4* out = reinterpret_cast<uint4*>(x + t * KP + (int64_t)v * 16);
-      out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    for (int i = 0; i < 8; ++i) {
+      uint32_t h;  // two E4M3 codes as f16 (exact)
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[i / 2] >> (16 * (i & 1)))));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
+      o[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
+    uint4* out = reinterpret_cast<uint4*>(x + r * K + (int64_t)v * 16);
+    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
@@ -62,14 +66,16 @@ __global__ void __launch_bounds__(kRestoreThreads)
 constexpr int kRows = 64;                          // rows r per stage
 constexpr int kHalf = 128;                         // n rows, and k columns, of one CTA's operands
 constexpr int kTile = 256;                         // pair tile, both ways
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr uint32_t kPanelBytes = kRows * 128;      // 64 rows x 64 bf16, 128-byte swizzle
 constexpr uint32_t kOperandBytes = 2 * kPanelBytes;
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
 constexpr int kSlots = 2;
 constexpr int kEpiWarp0 = 2, kEpiWarps = 8;
 constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
-constexpr uint32_t kSmemBytes = kStages * kStageBytes + 1024 /*align*/ + 256 /*barriers*/;
+constexpr uint32_t kOutBytes = 32 * 128;           // 32 rows of 128 bytes: one TMA store of an epilogue warp
+constexpr uint32_t kOutTotal = 2 * kEpiWarps * kOutBytes;
+constexpr uint32_t kSmemBytes = kStages * kStageBytes + kOutTotal + 1024 /*align*/ + 256 /*barriers*/;
 static_assert(kSmemBytes <= 232448, "shared memory");
 static_assert(kSlots * kTile <= 512, "TMEM columns");
 
@@ -86,11 +92,9 @@ struct Smem {
 static_assert(sizeof(Smem) <= 256, "barrier block");
 
 struct Params {
-  int64_t R, N, K, tokens;
-  const int32_t* row_token;
+  int64_t R, N, K;
   const int32_t* offsets;
-  void* dw;
-  int num_n, num_k, tiles, bf16, accumulate;
+  int num_n, num_k, tiles, accumulate;
   KernelCtl ctl;
 };
 
@@ -116,17 +120,32 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t s) {
   return smem_desc(addr + s * 16 * 128, kPanelBytes, 1024, 2);
 }
 
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int32_t x, const int32_t (&r)[4],
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
-      : "memory");
+// A 32-row box of 128-byte rows from shared memory to dW[z], or added to it
+// (each element by one box, so sums do not depend on an order).
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y, int32_t z,
+                                             bool add) {
+  if (add)
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// At most kLeft of this thread's store groups still read their shared memory.
+template <int kLeft>
+__device__ __forceinline__ void tma_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
 }
 
 // Arrive on a peer's mbarrier with everything this thread has seen visible to
-// the cluster (the cleared rows of the odd CTA's stage among it).
+// the cluster: the cleared rows of the odd CTA's stage.  Only after a clear:
+// as the arrival of every stage it cost 1.1 us a stage and held the whole
+// kernel there (64 x 2048 x 7168, 32768 rows in order: 1764 us).
 __device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -167,13 +186,15 @@ __device__ __forceinline__ Tile tile_of(const Params& p, int t) {
   return o;
 }
 
+template <typename W>
 __global__ void __launch_bounds__(kThreads, 1)
     wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmap_y, const __grid_constant__ CUtensorMap tmap_x,
-                      const Params p) {
+                      const __grid_constant__ CUtensorMap tmap_w, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   pdl_wait();  // operands may come from the previous kernel
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Smem* sm = reinterpret_cast<Smem*>(smem + kStages * kStageBytes);
+  uint8_t* out_smem = smem + kStages * kStageBytes;
+  Smem* sm = reinterpret_cast<Smem*>(out_smem + kOutTotal);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();  // 0: issues the pair's MMAs
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
@@ -193,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     prefetch_tmap(&tmap_y);
     prefetch_tmap(&tmap_x);
+    prefetch_tmap(&tmap_w);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(&sm->tmem_base), kSlots * kTile);
@@ -215,16 +237,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = cid; t < p.tiles && alive; t += ncl) {
       const Tile w = tile_of(p, t);
       for (int r0 = 0; r0 < w.rows; r0 += kRows) {
-        // lane l gathers rows 4 (l % 16) .. of panel l / 16; rows behind the
-        // group repeat its last one (cleared before use)
-        int32_t tok[4];
-        if (p.row_token) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = min(r0 + (lane & 15) * 4 + i, w.rows - 1);
-            tok[i] = min(max(__ldg(p.row_token + w.lo + r), 0), (int32_t)(p.tokens - 1));
-          }
-        }
         if (!warp_wait(smem_u32(&sm->empty[stage]), phase ^ 1, p.ctl, abort_flag)) {
           alive = false;
           break;
@@ -235,16 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           mbar_arrive_expect_tx(full, kStageBytes);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i) {
             tma_load_2d(y + i * kPanelBytes, &tmap_y, (w.n0 + rank * kHalf + i * 64) * 2, row, full);
-        }
-        __syncwarp();
-        const int x0 = (w.k0 + rank * kHalf) * 2;
-        if (p.row_token) {
-          const int i = lane >> 4;
-          tma_gather4(x + i * kPanelBytes + (lane & 15) * 512, &tmap_x, x0 + i * 128, tok, full);
-        } else if (lane < 2) {
-          tma_load_2d(x + lane * kPanelBytes, &tmap_x, x0 + lane * 128, row, full);
+            tma_load_2d(x + i * kPanelBytes, &tmap_x, (w.k0 + rank * kHalf + i * 64) * 2, row, full);
+          }
         }
         issued[stage] = 1;
         issued_phase[stage] = phase;
@@ -313,8 +319,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             alive = false;
             break;
           }
-          if (w.rows - r0 < kRows) clear_rows(smem + stage * kStageBytes, w.rows - r0, lane);
-          if (lane == 0) mbar_arrive_cluster_release(leader_pair_full + stage * 8);
+          const bool part = w.rows - r0 < kRows;
+          if (part) clear_rows(smem + stage * kStageBytes, w.rows - r0, lane);
+          if (lane == 0) {
+            if (part)
+              mbar_arrive_cluster_release(leader_pair_full + stage * 8);
+            else
+              mbar_arrive_cluster(leader_pair_full + stage * 8);
+          }
           if (++stage == kStages) stage = 0, phase ^= 1;
         }
       }
@@ -326,11 +338,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h = (warp - kEpiWarp0) >> 2;   // column half of the slot
     const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + h * 128;
     const uint32_t leader_slot_empty = mapa_shared(smem_u32(&sm->slot_empty[0]), 0);
-    uint32_t done = 0;
+    uint8_t* buf = out_smem + (warp - kEpiWarp0) * 2 * kOutBytes;
+    constexpr int kCols = 128 / (int)sizeof(W);  // columns of one store
+    uint32_t done = 0, stores = 0;
     for (int t = cid; t < p.tiles; t += ncl) {
       const Tile w = tile_of(p, t);
-      const int64_t n = w.n0 + rank * kHalf + q * 32 + lane;
-      const int64_t k0 = w.k0 + h * 128;
+      const int n0 = w.n0 + rank * kHalf + q * 32;
+      const int k0 = w.k0 + h * 128;
       const uint32_t slot = done % kSlots, sphase = (done / kSlots) & 1;
       if (w.rows) {
         ++done;
@@ -340,49 +354,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {  // 16 columns at a time
-        uint32_t r[16];
-        if (w.rows) {
-          __syncwarp();
-          tmem_ld_32x32b_x16(t_lane + slot * kTile + c * 16, r);
-          tmem_ld_wait();
-          if (c == 7) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(leader_slot_empty + slot * 8);
+      for (int c = 0; c < 128 / kCols; ++c, ++stores) {
+        uint8_t* line = buf + (stores & 1) * kOutBytes;
+        if (lane == 0) tma_store_wait_read<1>();  // the store before the last has read this buffer
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kCols / 16; ++i) {  // 16 columns at a time
+          uint32_t r[16];
+          if (w.rows) {
+            tmem_ld_32x32b_x16(t_lane + slot * kTile + c * kCols + i * 16, r);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r[j] = 0u;
           }
-        } else {
+          constexpr int kWords = (int)sizeof(W);  // 16-byte words of 16 columns
 #pragma unroll
-          for (int j = 0; j < 16; ++j) r[j] = 0u;
-        }
-        const int64_t k = k0 + c * 16;
-        if (n >= p.N || k >= p.K) continue;  // K is a multiple of 16
-        const int64_t at = ((int64_t)w.e * p.N + n) * p.K + k;
-        if (p.bf16) {
-          uint32_t o[8];
+          for (int j = 0; j < kWords; ++j) {
+            uint4 o;
+            if constexpr (sizeof(W) == 4) {
+              o = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+            } else {
+              uint32_t b[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-            o[j] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-          uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dw) + at);
-          out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-          out[1] = make_uint4(o[4], o[5], o[6], o[7]);
-        } else {
-          float4* out = reinterpret_cast<float4*>(static_cast<float*>(p.dw) + at);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float4 v = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                                   __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-            if (p.accumulate) {
-              const float4 old = out[j];
-              v.x += old.x, v.y += old.y, v.z += old.z, v.w += old.w;
+              for (int m = 0; m < 4; ++m) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[8 * j + 2 * m]),
+                                                               __uint_as_float(r[8 * j + 2 * m + 1]));
+                b[m] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+              o = make_uint4(b[0], b[1], b[2], b[3]);
             }
-            out[j] = v;
+            *reinterpret_cast<uint4*>(line + lane * 128 + (((i * kWords + j) ^ (lane & 7)) << 4)) = o;
           }
+        }
+        if (w.rows && c == 128 / kCols - 1) {  // the slot's columns of this warp are all read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(leader_slot_empty + slot * 8);
+        }
+        fence_proxy_async_smem();  // the TMA store reads what these threads wrote
+        __syncwarp();
+        const int k = k0 + c * kCols;
+        if (lane == 0) {
+          if (n0 < p.N && k < p.K) tma_store_3d(&tmap_w, smem_u32(line), k, n0, w.e, p.accumulate != 0);
+          tma_store_commit();  // a group per buffer use, empty past the edge: the wait above counts groups
         }
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // written before the CTA exits
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -396,34 +416,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_barrier_sync();
 }
 
-// The restored rows are padded to whole tiles of columns, so that no gather
-// reaches past them; what the padding holds only meets columns that are not
-// stored.
-int64_t padded_k(int64_t K) { return ceil_div(K, kTile) * kTile; }
-
 }  // namespace
 
-size_t wgrad_workspace_bytes(int64_t tokens, int64_t N, int64_t K) {
+// The restored rows.
+size_t wgrad_workspace_bytes(int64_t R, int64_t N, int64_t K) {
   (void)N;
-  return (size_t)tokens * (size_t)padded_k(K) * sizeof(__nv_bfloat16);
+  return (size_t)R * (size_t)K * sizeof(__nv_bfloat16);
 }
 
-q4_status launch_wgrad(const WgradArgs& a, cudaStream_t stream) {
-  const int64_t KP = padded_k(a.K);
+namespace {
+
+template <typename W>
+q4_status launch_typed(const WgradArgs& a, cudaStream_t stream) {
   __nv_bfloat16* x = static_cast<__nv_bfloat16*>(a.ws);
   Params p = {};
-  p.R = a.R, p.N = a.N, p.K = a.K, p.tokens = a.tokens;
-  p.row_token = a.row_token, p.offsets = a.offsets;
-  p.dw = a.dw, p.bf16 = a.w_dtype == Q4_BF16, p.accumulate = a.accumulate;
+  p.R = a.R, p.N = a.N, p.K = a.K;
+  p.offsets = a.offsets;
+  p.accumulate = a.accumulate;
   const int64_t num_n = ceil_div(a.N, kTile), num_k = ceil_div(a.K, kTile);
   if (num_n * num_k > INT32_MAX / 2 / a.E) return Q4_ERR_UNSUPPORTED_SHAPE;
   p.num_n = (int)num_n, p.num_k = (int)num_k, p.tiles = (int)(a.E * num_n * num_k);
   p.ctl = KernelCtl{device_status_ptr(), wait_budget_ns()};
 
-  CUtensorMap ty, tx;
+  CUtensorMap ty, tx, tw;
   q4_status st = make_tmap_2d_u8(&ty, a.dy, a.N * 2, a.R, a.ldy * 2, 128, kRows, true);
   if (st != Q4_OK) return st;
-  st = make_tmap_2d_u8(&tx, x, KP * 2, a.tokens, KP * 2, 128, a.row_token ? 1 : kRows, true);
+  st = make_tmap_2d_u8(&tx, x, a.K * 2, a.R, a.K * 2, 128, kRows, true);
+  if (st != Q4_OK) return st;
+  st = make_tmap_3d(&tw, sizeof(W) == 4 ? Q4_F32 : Q4_BF16, a.dw, a.K, a.N, a.E, a.K, a.N * a.K, 128 / sizeof(W), 32,
+                    1, true);
   if (st != Q4_OK) return st;
 
   int dev = 0;
@@ -443,21 +464,27 @@ q4_status launch_wgrad(const WgradArgs& a, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   if (!max_pairs[dev]) {  // persistent: as many pairs as are resident at once
-    Q4_CUDA_TRY(cudaFuncSetAttribute(wgrad_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes));
+    Q4_CUDA_TRY(cudaFuncSetAttribute(wgrad_pair_kernel<W>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes));
     int n = 0;
     cfg.gridDim = dim3((unsigned)(num_sms() / 2 * 2), 1, 1);
-    if (cudaOccupancyMaxActiveClusters(&n, wgrad_pair_kernel, &cfg) != cudaSuccess || n <= 0) n = num_sms() / 2;
+    if (cudaOccupancyMaxActiveClusters(&n, wgrad_pair_kernel<W>, &cfg) != cudaSuccess || n <= 0) n = num_sms() / 2;
     max_pairs[dev] = std::min(n, num_sms() / 2);
   }
 
-  const unsigned gx = (unsigned)ceil_div(a.K / 16, kRestoreThreads);
-  const unsigned gy = (unsigned)std::min<int64_t>(a.tokens, 65535);
-  st = launch_pdl(wgrad_restore_kernel, dim3(gx, gy), kRestoreThreads, 0, stream, a.codes, a.scales, a.tokens, a.K,
-                  KP, x);
+  const int64_t gx = ceil_div(a.K / 16, kRestoreThreads);
+  const int64_t gy = std::max<int64_t>(1, std::min<int64_t>(a.R, (int64_t)num_sms() * 16 / gx));
+  st = launch_pdl(wgrad_restore_kernel, dim3((unsigned)gx, (unsigned)gy), kRestoreThreads, 0, stream, a.codes,
+                  a.scales, a.tokens, a.K, a.row_token, a.offsets + a.E, a.R, x);
   if (st != Q4_OK) return st;
   cfg.gridDim = dim3(2u * (unsigned)std::min(p.tiles, max_pairs[dev]), 1, 1);
-  Q4_CUDA_TRY(cudaLaunchKernelEx(&cfg, wgrad_pair_kernel, ty, tx, p));
+  Q4_CUDA_TRY(cudaLaunchKernelEx(&cfg, wgrad_pair_kernel<W>, ty, tx, tw, p));
   return Q4_OK;
+}
+
+}  // namespace
+
+q4_status launch_wgrad(const WgradArgs& a, cudaStream_t stream) {
+  return a.w_dtype == Q4_F32 ? launch_typed<float>(a, stream) : launch_typed<__nv_bfloat16>(a, stream);
 }
 
 }  // namespace q4
