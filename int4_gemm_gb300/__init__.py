@@ -455,17 +455,18 @@ def grouped_gemm_moe(tokens: torch.Tensor, expert_offsets: torch.Tensor, row_tok
 # --------------------------------------------------------------------------- routed experts
 
 def _pitched(x: torch.Tensor, name: str) -> int:
-    """The row pitch of a 2-D CUDA matrix whose rows are contiguous and do not overlap."""
-    if not x.is_cuda or x.dim() != 2 or x.dtype not in _DTYPE:
+    """The row pitch (at least the width) of a 2-D CUDA matrix whose rows are
+    contiguous and do not overlap."""
+    if not x.is_cuda or x.dtype not in _DTYPE or x.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor of float32, bfloat16 or float16")
-    rows, cols = x.shape
-    if cols > 1 and x.stride(1) != 1:
+    (rows, cols), (pitch, step) = x.shape, x.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if rows <= 1 or cols == 0:
-        return max(cols, 1)
-    if x.stride(0) < cols:
+    if pitch >= cols > 0:
+        return pitch
+    if rows > 1 and cols > 0:
         raise ValueError(f"{name} has overlapping rows")
-    return x.stride(0)
+    return max(cols, 1)
 
 
 def _on(stream, *tensors):
@@ -477,8 +478,8 @@ def _on(stream, *tensors):
 
 
 def _exact(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device) -> torch.Tensor:
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
     return t
 
 
@@ -499,7 +500,7 @@ def moe_route_topk(logits: torch.Tensor, top_k: int, normalize: str = "topk", st
     ids = torch.empty((T, max(top_k, 0)), dtype=torch.int32, device=logits.device)
     weights = torch.empty((T, max(top_k, 0)), dtype=torch.float32, device=logits.device)
     _check("moe_route_topk", lib().moe_route_topk(
-        logits.data_ptr(), _DTYPE[logits.dtype], T, E, max(ld, E), top_k, _NORMALIZE[normalize],
+        logits.data_ptr(), _DTYPE[logits.dtype], T, E, ld, top_k, _NORMALIZE[normalize],
         ids.data_ptr(), weights.data_ptr(), _stream(stream)))
     _on(stream, ids, weights)
     return ids, weights
@@ -517,7 +518,7 @@ def moe_route_topk_backward(logits: torch.Tensor, ids: torch.Tensor, d_weights: 
     _exact(d_weights, "d_weights", (T, k), torch.float32, logits.device)
     d = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
     _check("moe_route_topk_backward", lib().moe_route_topk_backward(
-        logits.data_ptr(), _DTYPE[logits.dtype], T, E, max(ld, E), k, _NORMALIZE[normalize],
+        logits.data_ptr(), _DTYPE[logits.dtype], T, E, ld, k, _NORMALIZE[normalize],
         ids.data_ptr(), d_weights.data_ptr(), d.data_ptr(), _stream(stream)))
     _on(stream, d)
     return d
@@ -539,12 +540,15 @@ def moe_sort_tokens(ids: torch.Tensor, E: int, ws: Optional[torch.Tensor] = None
     offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
     row_token = torch.empty(T * k, dtype=torch.int32, device=dev)
     slot_row = torch.empty((T, k), dtype=torch.int32, device=dev)
+    L = lib()
     if ws is None:
-        ws = workspace(OP_MOE_SORT, T * k, E, 0, dev)
-    _check("moe_sort_tokens", lib().moe_sort_tokens(
+        n = L.q4_workspace_size(OP_MOE_SORT, T * k, E, 0)
+        ws = _empty(n, dev) if n else None
+    _check("moe_sort_tokens", L.moe_sort_tokens(
         ids.data_ptr(), T, k, E, offsets.data_ptr(), row_token.data_ptr(), slot_row.data_ptr(),
-        ws.data_ptr(), ws.numel(), _stream(stream)))
-    _on(stream, offsets, row_token, slot_row, ws)
+        _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+    if stream is not None:
+        _on(stream, offsets, row_token, slot_row, *(() if ws is None else (ws,)))
     return offsets, row_token, slot_row
 
 
@@ -554,7 +558,7 @@ def moe_dispatch(x: torch.Tensor, slot_row: torch.Tensor, out=None, stream=None)
     T, H = x.shape
     k = _slots(slot_row, T, x.device)
     rows = _out(out, T * k, H, x.dtype, x.device)
-    _check("moe_dispatch", lib().moe_dispatch(x.data_ptr(), _DTYPE[x.dtype], T, H, max(ld, H),
+    _check("moe_dispatch", lib().moe_dispatch(x.data_ptr(), _DTYPE[x.dtype], T, H, ld,
                                               slot_row.data_ptr(), k, rows.data_ptr(), _stream(stream)))
     _on(stream, rows)
     return rows
@@ -570,7 +574,7 @@ def moe_dispatch_backward(d_rows: torch.Tensor, slot_row: torch.Tensor, out=None
         raise ValueError(f"d_rows has {d_rows.shape[0]} rows, slot_row {T * k} slots")
     d_x = _out(out, T, H, d_rows.dtype, d_rows.device)
     _check("moe_dispatch_backward", lib().moe_dispatch_backward(
-        d_rows.data_ptr(), _DTYPE[d_rows.dtype], T, H, max(ld, H), slot_row.data_ptr(), k, d_x.data_ptr(),
+        d_rows.data_ptr(), _DTYPE[d_rows.dtype], T, H, ld, slot_row.data_ptr(), k, d_x.data_ptr(),
         _stream(stream)))
     _on(stream, d_x)
     return d_x
@@ -588,7 +592,7 @@ def moe_combine(rows: torch.Tensor, slot_row: torch.Tensor, weights: Optional[to
     if weights is not None:
         _exact(weights, "weights", (T, k), torch.float32, rows.device)
     C = _out(out, T, H, rows.dtype, rows.device)
-    _check("moe_combine", lib().moe_combine(rows.data_ptr(), _DTYPE[rows.dtype], T, H, max(ld, H),
+    _check("moe_combine", lib().moe_combine(rows.data_ptr(), _DTYPE[rows.dtype], T, H, ld,
                                             slot_row.data_ptr(), _ptr(weights), k, C.data_ptr(),
                                             _stream(stream)))
     _on(stream, C)
@@ -608,7 +612,7 @@ def moe_combine_backward(d_out: torch.Tensor, rows: torch.Tensor, slot_row: torc
     d_rows = _out(out, T * k, H, d_out.dtype, d_out.device)
     dw = torch.empty((T, k), dtype=torch.float32, device=d_out.device) if need_d_weights else None
     _check("moe_combine_backward", lib().moe_combine_backward(
-        d_out.data_ptr(), _DTYPE[d_out.dtype], T, H, max(ldd, H), rows.data_ptr(), max(ld, H),
+        d_out.data_ptr(), _DTYPE[d_out.dtype], T, H, ldd, rows.data_ptr(), ld,
         slot_row.data_ptr(), weights.data_ptr(), k, d_rows.data_ptr(), _ptr(dw), _stream(stream)))
     _on(stream, d_rows, *(() if dw is None else (dw,)))
     return d_rows, dw
@@ -624,7 +628,7 @@ def quantize_fp8_checkpoint(x: torch.Tensor, stream=None):
     codes = torch.empty((rows, K), dtype=torch.uint8, device=x.device)
     scales = torch.empty((rows, -(-K // 128)), dtype=torch.float32, device=x.device)
     _check("quantize_fp8_checkpoint", lib().quantize_fp8_checkpoint(
-        x.data_ptr(), _DTYPE[x.dtype], rows, K, max(ld, K), codes.data_ptr(), scales.data_ptr(),
+        x.data_ptr(), _DTYPE[x.dtype], rows, K, ld, codes.data_ptr(), scales.data_ptr(),
         _stream(stream)))
     _on(stream, codes, scales)
     return codes, scales
@@ -643,7 +647,7 @@ def swiglu_fp8(gate_up: torch.Tensor, out=None, stream=None):
     codes = torch.empty((rows, two), dtype=torch.uint8, device=dev)
     scales = torch.empty((rows, 2 * -(-inner // 128)), dtype=torch.float32, device=dev)
     _check("swiglu_fp8", lib().swiglu_fp8(
-        gate_up.data_ptr(), _DTYPE[gate_up.dtype], rows, inner, max(ld, two), h.data_ptr(),
+        gate_up.data_ptr(), _DTYPE[gate_up.dtype], rows, inner, ld, h.data_ptr(),
         codes.data_ptr(), scales.data_ptr(), _stream(stream)))
     _on(stream, h, codes, scales)
     return h, codes, scales
@@ -658,7 +662,7 @@ def swiglu_fp8_backward(d_h: torch.Tensor, codes: torch.Tensor, scales: torch.Te
     _exact(scales, "scales", (rows, 2 * -(-inner // 128)), torch.float32, d_h.device)
     d = _out(out, rows, 2 * inner, d_h.dtype, d_h.device)
     _check("swiglu_fp8_backward", lib().swiglu_fp8_backward(
-        d_h.data_ptr(), _DTYPE[d_h.dtype], rows, inner, max(ld, inner), codes.data_ptr(),
+        d_h.data_ptr(), _DTYPE[d_h.dtype], rows, inner, ld, codes.data_ptr(),
         scales.data_ptr(), d.data_ptr(), _stream(stream)))
     _on(stream, d)
     return d
@@ -700,7 +704,7 @@ def grouped_wgrad_fp8(d_y: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
     if ws is None:
         ws = workspace(OP_GROUPED_WGRAD_FP8, R, N, K, dev)
     _check("grouped_wgrad_fp8", lib().grouped_wgrad_fp8(
-        d_y.data_ptr(), R, N, max(ldy, N), codes.data_ptr(), scales.data_ptr(), T, K, _ptr(row_token),
+        d_y.data_ptr(), R, N, ldy, codes.data_ptr(), scales.data_ptr(), T, K, _ptr(row_token),
         expert_offsets.data_ptr(), E, out.data_ptr(), _DTYPE[out.dtype], int(accumulate),
         ws.data_ptr(), ws.numel(), _stream(stream)))
     _on(stream, out, ws)

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kRouteWarps * kWarp)
 // the dropped ones): chunk histograms, one scan per expert over the chunks,
 // then every chunk places its slots.
 constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32;
-constexpr int kSortChunk = 2048, kSortPerWarp = kSortChunk / kSortWarps;
+constexpr int kSortChunk = 1024, kSortPerWarp = kSortChunk / kSortWarps;
 
 __device__ __forceinline__ int sort_bucket(const int32_t* __restrict__ ids, int64_t i, int E) {
   const int e = __ldg(ids + i);
@@ -293,6 +293,105 @@ __global__ void __launch_bounds__(kSortThreads)
       slot_row[s] = b < E ? row : ~row;
     }
   }
+}
+
+// The whole sort in one launch of one cluster: every block takes a contiguous
+// share of the slots, every warp of it a contiguous part of that.  The blocks'
+// histograms meet in distributed shared memory, and each block computes the
+// first row of its own slots of every expert from them.
+constexpr int kClusterThreads = 512, kClusterWarps = kClusterThreads / 32, kMaxCluster = 8;
+
+__device__ __forceinline__ int32_t load_peer(uint32_t addr, uint32_t rank) {
+  int32_t v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(addr, rank)) : "memory");
+  return v;
+}
+
+// smem: [warps][E + 1] counts of the warps, then [E + 1] of the block.
+__global__ void __launch_bounds__(kClusterThreads)
+    sort_cluster_kernel(const int32_t* __restrict__ ids, int S, int E, int top_k, int per_warp,
+                        int32_t* __restrict__ offsets, int32_t* __restrict__ row_token,
+                        int32_t* __restrict__ slot_row) {
+  pdl_wait();
+  extern __shared__ int32_t cnt[];
+  __shared__ int32_t warp_sum[kClusterWarps];
+  const int nb = E + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int rank = blockIdx.x, blocks = gridDim.x;
+  int32_t* own = cnt + warps * nb;
+  for (int i = threadIdx.x; i < warps * nb; i += blockDim.x) cnt[i] = 0;
+  __syncthreads();
+  const int base = (rank * warps + warp) * per_warp;
+  const int end = min(base + per_warp, S);
+  int32_t* mine = cnt + warp * nb;
+  for (int s0 = base; s0 < end; s0 += 32) {
+    const int b = s0 + lane < end ? sort_bucket(ids, s0 + lane, E) : -1;
+    const unsigned peers = __match_any_sync(kFull, b);
+    if (b >= 0 && lane == __ffs(peers) - 1) mine[b] += __popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < nb; e += blockDim.x) {
+    int sum = 0;
+    for (int w = 0; w < warps; ++w) sum += cnt[w * nb + e];
+    own[e] = sum;
+  }
+  if (blocks > 1)
+    cluster_barrier_sync();  // every block's histogram is there
+  else
+    __syncthreads();
+  // first row of expert e: the totals of the experts before it; of this
+  // block's slots of e: plus the counts of the blocks before this one
+  int carry = 0;
+  for (int e0 = 0; e0 < nb; e0 += blockDim.x) {
+    const int e = e0 + threadIdx.x;
+    int total = 0, before = 0;
+    if (e < nb)
+      for (int r = 0; r < blocks; ++r) {
+        const int c = r == rank ? own[e] : load_peer(smem_u32(own + e), r);
+        total += c;
+        if (r < rank) before += c;
+      }
+    int x = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int prefix = carry, all = 0;
+    for (int w = 0; w < warps; ++w) {
+      if (w < warp) prefix += warp_sum[w];
+      all += warp_sum[w];
+    }
+    if (e < nb) {
+      const int first = prefix + x - total;
+      if (rank == 0) offsets[e] = first;
+      int at = first + before;
+      for (int w = 0; w < warps; ++w) {
+        const int c = cnt[w * nb + e];
+        cnt[w * nb + e] = at;
+        at += c;
+      }
+    }
+    carry += all;
+    __syncthreads();
+  }
+  for (int s0 = base; s0 < end; s0 += 32) {
+    const int s = s0 + lane;
+    const int b = s < end ? sort_bucket(ids, s, E) : -1;
+    const unsigned peers = __match_any_sync(kFull, b);
+    int row = 0;
+    if (b >= 0) row = mine[b] + __popc(peers & ((1u << lane) - 1u));
+    __syncwarp();
+    if (b >= 0 && lane == __ffs(peers) - 1) mine[b] += __popc(peers);
+    __syncwarp();
+    if (b >= 0) {
+      row_token[row] = s / top_k;
+      slot_row[s] = b < E ? row : ~row;
+    }
+  }
+  if (blocks > 1) cluster_barrier_sync();  // no block leaves while a peer reads its histogram
 }
 
 // ------------------------------------------------------------------ dispatch / combine
@@ -569,13 +668,73 @@ q4_status launch_route_backward(const void* logits, int dtype, int64_t tokens, i
   });
 }
 
-// Counts per expert and chunk, then the experts' totals.
+namespace {
+// The cluster sort's shape: a warp per 32 slots, up to 16 per block and as many
+// as the counts leave room for, then more blocks, then longer parts (device
+// time at 256 experts, 16 / 32 warps per block: 1024 slots 4.8 / 6.0 us, 4096
+// 5.2 / 7.2, 16384 7.8 / 8.6).  Above kClusterSortSlots the three launches over
+// all SMs are faster: 32768 slots 8.2 us against 11.7, 131072 9.9 against 37;
+// below it they are slower (4096: 8.4 us) and cost the host two launches more.
+struct ClusterSort {
+  int warps, blocks, per_warp;
+  size_t smem;
+};
+constexpr size_t kClusterSortSmem = 200 * 1024;
+constexpr int64_t kClusterSortSlots = 16384;
+
+ClusterSort cluster_sort(int64_t S, int E) {
+  ClusterSort c;
+  const int64_t room = (int64_t)(kClusterSortSmem / 4) / (E + 1) - 1;
+  const int64_t want = ceil_div(S, 128);  // warps of at least four turns
+  c.warps = (int)std::max<int64_t>(1, std::min<int64_t>({kClusterWarps, room, want}));
+  c.blocks = 1;
+  while (c.blocks < kMaxCluster && (int64_t)c.blocks * c.warps < want) c.blocks *= 2;
+  c.per_warp = (int)(ceil_div(ceil_div(S, (int64_t)c.blocks * c.warps), 32) * 32);
+  c.smem = (size_t)(c.warps + 1) * (E + 1) * sizeof(int32_t);
+  return c;
+}
+
+q4_status launch_cluster_sort(const ClusterSort& c, const int32_t* ids, int64_t S, int top_k, int E, int32_t* offsets,
+                              int32_t* row_token, int32_t* slot_row, cudaStream_t stream) {
+  static int attr_done[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return Q4_ERR_CUDA;
+  if (!attr_done[dev]) {
+    Q4_CUDA_TRY(cudaFuncSetAttribute(sort_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)kClusterSortSmem));
+    attr_done[dev] = 1;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)c.blocks);
+  cfg.blockDim = dim3((unsigned)c.warps * 32);
+  cfg.dynamicSmemBytes = c.smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)c.blocks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  Q4_CUDA_TRY(cudaLaunchKernelEx(&cfg, sort_cluster_kernel, ids, (int)S, E, top_k, c.per_warp, offsets, row_token,
+                                 slot_row));
+  return Q4_OK;
+}
+}  // namespace
+
+// Counts per expert and chunk, then the experts' totals; none where one
+// cluster sorts.
 size_t moe_sort_workspace_bytes(int64_t S, int64_t E) {
+  if (S <= kClusterSortSlots) return 0;
   return (size_t)(E + 1) * (size_t)(ceil_div(S, kSortChunk) + 1) * sizeof(int32_t);
 }
 
 q4_status launch_moe_sort(const int32_t* ids, int64_t S, int top_k, int E, int32_t* offsets, int32_t* row_token,
                           int32_t* slot_row, void* ws, cudaStream_t stream) {
+  if (S <= kClusterSortSlots)
+    return launch_cluster_sort(cluster_sort(S, E), ids, S, top_k, E, offsets, row_token, slot_row, stream);
   const int chunks = (int)ceil_div(S, kSortChunk);
   int32_t* hist = static_cast<int32_t*>(ws);
   int32_t* total = hist + (int64_t)(E + 1) * chunks;

@@ -346,5 +346,5 @@ def test_refusals(lib):
         lib.moe_route_topk(torch.zeros((1, 1025), **f), 2)
     assert e.value.status == -2
     with pytest.raises(lib.Q4Error) as e:
-        lib.moe_sort_tokens(slot, 4, ws=torch.empty(0, dtype=torch.uint8, **f))
+        lib.moe_sort_tokens(torch.zeros((20000, 2), **i), 4, ws=torch.empty(0, dtype=torch.uint8, **f))
     assert e.value.status == -6
