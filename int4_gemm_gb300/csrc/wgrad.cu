@@ -32,33 +32,43 @@ namespace {
 // ------------------------------------------------------------------ restore
 constexpr int kRestoreThreads = 256;
 
-// 16 codes per thread: x[r, c .. c + 16) = bf16(code * scale) of token
-// row_token[r], for the rows that belong to an expert.
+// 8 codes per thread and row: x[r, c .. c + 8) = bf16(code * scale) of token
+// row_token[r], for the rows that belong to an expert; kRestoreRows rows at a
+// time, their loads in flight together.
+constexpr int kRestoreRows = 4;
+
 __global__ void __launch_bounds__(kRestoreThreads)
     wgrad_restore_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales, int64_t tokens,
                          int64_t K, const int32_t* __restrict__ row_token, const int32_t* __restrict__ last, int64_t R,
                          __nv_bfloat16* __restrict__ x) {
   pdl_wait();
   const uint32_t v = blockIdx.x * kRestoreThreads + threadIdx.x;
-  if (v >= (uint32_t)(K / 16)) return;
+  if (v >= (uint32_t)(K / 8)) return;
   const int64_t KB = (K + 127) / 128, rows = min((int64_t)__ldg(last), R);
-  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
-    const int64_t t = row_token ? min(max((int64_t)__ldg(row_token + r), (int64_t)0), tokens - 1) : r;
-    const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes + t * K) + v);
-    const float s = __ldg(scales + t * KB + v / 8);
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t o[8];
+  for (int64_t r0 = (int64_t)blockIdx.y * kRestoreRows; r0 < rows; r0 += (int64_t)gridDim.y * kRestoreRows) {
+    uint2 c[kRestoreRows];
+    float s[kRestoreRows];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t h;  // two E4M3 codes as f16 (exact)
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[i / 2] >> (16 * (i & 1)))));
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
-      o[i] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int i = 0; i < kRestoreRows; ++i) {
+      const int64_t r = min(r0 + i, rows - 1);
+      const int64_t t = row_token ? min(max((int64_t)__ldg(row_token + r), (int64_t)0), tokens - 1) : r;
+      c[i] = __ldg(reinterpret_cast<const uint2*>(codes + t * K) + v);
+      s[i] = __ldg(scales + t * KB + v / 16);
     }
-    uint4* out = reinterpret_cast<uint4*>(x + r * K + (int64_t)v * 16);
-    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+    for (int i = 0; i < kRestoreRows; ++i) {
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t h;  // two E4M3 codes as f16 (exact)
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)((j < 2 ? c[i].x : c[i].y) >> (16 * (j & 1)))));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s[i], f.y * s[i]);
+        o[j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      if (r0 + i < rows)
+        reinterpret_cast<uint4*>(x + (r0 + i) * K)[v] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
   }
 }
 
@@ -471,8 +481,8 @@ q4_status launch_typed(const WgradArgs& a, cudaStream_t stream) {
     max_pairs[dev] = std::min(n, num_sms() / 2);
   }
 
-  const int64_t gx = ceil_div(a.K / 16, kRestoreThreads);
-  const int64_t gy = std::max<int64_t>(1, std::min<int64_t>(a.R, (int64_t)num_sms() * 16 / gx));
+  const int64_t gx = ceil_div(a.K / 8, kRestoreThreads);
+  const int64_t gy = std::min<int64_t>(ceil_div(a.R, kRestoreRows), 65535);
   st = launch_pdl(wgrad_restore_kernel, dim3((unsigned)gx, (unsigned)gy), kRestoreThreads, 0, stream, a.codes,
                   a.scales, a.tokens, a.K, a.row_token, a.offsets + a.E, a.R, x);
   if (st != Q4_OK) return st;
