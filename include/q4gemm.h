@@ -90,7 +90,7 @@ typedef enum {
   Q4_OP_GEMM_W4A8 = 8,          /* needs none today: 0 */
   Q4_OP_GEMM_W4A4_MXFP4_FUSED = 9,
   Q4_OP_MOE_SORT = 10,          /* M = slots T * top_k, N = experts */
-  Q4_OP_GROUPED_WGRAD_FP8 = 11  /* M = routed rows R, N, K */
+  Q4_OP_GROUPED_WGRAD_FP8 = 11  /* R, N, K and E via q4_workspace_size_wgrad */
 } q4_op;
 
 /*
@@ -115,6 +115,7 @@ typedef struct {
 /* Bytes of workspace the operation needs for these sizes (0 if none). */
 size_t q4_workspace_size(int op, int64_t M, int64_t N, int64_t K);
 size_t q4_workspace_size_moe(int64_t T, int64_t N, int64_t K, int E, int64_t R);
+size_t q4_workspace_size_wgrad(int64_t R, int64_t N, int64_t K, int E);
 
 /* Size in bytes of a Q4_SCALES_MMA scale tensor for rows x nsf scales. */
 size_t q4_mma_scales_bytes(int64_t rows, int64_t nsf);
@@ -473,8 +474,8 @@ q4_status swiglu_fp8_backward(const void* d_h, int dtype, int64_t rows, int64_t 
  * dW: [E, N, K] in w_dtype: Q4_F32, or Q4_BF16 (rounded once); accumulate != 0
  * (Q4_F32 only) adds to what dW holds.  Sums are FP32.
  * N % 8 == 0, ldy % 8 == 0, K % 16 == 0; d_y, codes and dW 16-byte aligned.
- * ws: q4_workspace_size(Q4_OP_GROUPED_WGRAD_FP8, R, N, K) bytes (x_hat in the
- * order of the rows).
+ * ws: q4_workspace_size_wgrad(R, N, K, E) bytes (x_hat in the order of the
+ * rows, and every expert's last rows padded to 64 with zeros).
  */
 q4_status grouped_wgrad_fp8(const void* d_y_bf16, int64_t R, int64_t N, int64_t ldy,
                             const uint8_t* codes, const float* scales, int64_t T, int64_t K,

@@ -67,6 +67,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     P, I, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
     _sig(lib, "q4_workspace_size", SZ, I, I64, I64, I64)
     _sig(lib, "q4_workspace_size_moe", SZ, I64, I64, I64, I, I64)
+    _sig(lib, "q4_workspace_size_wgrad", SZ, I64, I64, I64, I)
     _sig(lib, "q4_mma_scales_bytes", SZ, I64, I64)
     _sig(lib, "quantize_nvfp4", I, P, I, I64, I64, P, P, I, P, P, SZ, P)
     _sig(lib, "quantize_mxfp4", I, P, I, I64, I64, P, P, I, P)
@@ -668,6 +669,10 @@ def swiglu_fp8_backward(d_h: torch.Tensor, codes: torch.Tensor, scales: torch.Te
     return d
 
 
+def wgrad_workspace(R: int, N: int, K: int, E: int, device) -> torch.Tensor:
+    return _empty(max(int(lib().q4_workspace_size_wgrad(R, N, K, E)), 256), device)
+
+
 def grouped_wgrad_fp8(d_y: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
                       expert_offsets: torch.Tensor, row_token: Optional[torch.Tensor] = None,
                       out_dtype=torch.float32, out=None, accumulate: bool = False,
@@ -677,7 +682,7 @@ def grouped_wgrad_fp8(d_y: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
     row pitch that is a multiple of 8); row_token int32 [R], or None when the
     checkpoint is in row order.  out_dtype float32 or bfloat16; ``accumulate``
     (float32 ``out`` only) adds to ``out``.  ``ws`` from
-    ``workspace(OP_GROUPED_WGRAD_FP8, R, N, K, device)``."""
+    ``wgrad_workspace(R, N, K, E, device)``."""
     if d_y.dtype != torch.bfloat16:
         raise ValueError("d_y must be bfloat16")
     ldy = _pitched(d_y, "d_y")
@@ -702,7 +707,7 @@ def grouped_wgrad_fp8(d_y: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
     if out.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("the gradient is float32 or bfloat16")
     if ws is None:
-        ws = workspace(OP_GROUPED_WGRAD_FP8, R, N, K, dev)
+        ws = wgrad_workspace(R, N, K, E, dev)
     _check("grouped_wgrad_fp8", lib().grouped_wgrad_fp8(
         d_y.data_ptr(), R, N, ldy, codes.data_ptr(), scales.data_ptr(), T, K, _ptr(row_token),
         expert_offsets.data_ptr(), E, out.data_ptr(), _DTYPE[out.dtype], int(accumulate),

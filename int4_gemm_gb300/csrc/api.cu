@@ -332,7 +332,7 @@ size_t q4_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
     case Q4_OP_GEMM_FP8_BLOCKWISE:
     case Q4_OP_GEMM_W4A8: return 0;
     case Q4_OP_MOE_SORT: return moe_sort_workspace_bytes(M, N);
-    case Q4_OP_GROUPED_WGRAD_FP8: return wgrad_workspace_bytes(M, N, K);
+    case Q4_OP_GROUPED_WGRAD_FP8: return 0;  // needs E: q4_workspace_size_wgrad
     default: return 0;
   }
 }
@@ -343,6 +343,11 @@ size_t q4_workspace_size_moe(int64_t T, int64_t N, int64_t K, int E, int64_t R) 
   Carver c{nullptr, 0, 0};
   plan_moe(c, T, K, E, R);
   return c.used;
+}
+
+size_t q4_workspace_size_wgrad(int64_t R, int64_t N, int64_t K, int E) {
+  if (R < 0 || N < 0 || K < 0 || E < 0) return 0;
+  return wgrad_workspace_bytes(R, N, K, E);
 }
 
 q4_status quantize_nvfp4_ex(const void* x, int x_dtype, int64_t rows, int64_t K, uint8_t* codes,
@@ -803,7 +808,7 @@ q4_status grouped_wgrad_fp8(const void* d_y_bf16, int64_t R, int64_t N, int64_t 
   if (!d_y_bf16 || !aligned(d_y_bf16, 16) || !codes || !aligned(codes, 16) || !word_ptr(scales) ||
       !aligned(row_token, 4) || !word_ptr(expert_offsets))
     return Q4_ERR_INVALID_ARG;
-  const size_t need = wgrad_workspace_bytes(R, N, K);
+  const size_t need = wgrad_workspace_bytes(R, N, K, E);
   if (need && (!ws || !aligned(ws, 256) || ws_bytes < need)) return Q4_ERR_WORKSPACE;
   WgradArgs a = {};
   a.dy = d_y_bf16; a.R = R; a.N = N; a.ldy = ldy;

@@ -154,7 +154,7 @@ struct WgradArgs {
   bool accumulate;
   void* ws;
 };
-size_t wgrad_workspace_bytes(int64_t R, int64_t N, int64_t K);
+size_t wgrad_workspace_bytes(int64_t R, int64_t N, int64_t K, int E);
 q4_status launch_wgrad(const WgradArgs& a, cudaStream_t stream);
 
 // TMA descriptor creation through the driver entry point.

@@ -6,21 +6,27 @@
 // The contraction runs over rows, along which neither operand is contiguous:
 // d_y is [r][n] and x is [r][k], so both enter the tensor cores MN-major, as
 // they lie.  A first kernel restores x into the workspace in the order of the
-// routed rows; the second is a grouped bf16 GEMM on CTA pairs:
+// routed rows, and there lays out each expert's last rows, those behind its
+// last multiple of 64, once more with zeros behind them, x's and d_y's: the
+// rows that follow belong to the next expert, whose values may be infinite.
+// The second is a grouped bf16 GEMM on CTA pairs:
 //   tile     256 (n) x 256 (k) per pair, 128 n rows and 128 k columns of the
 //            operands per CTA, 64 rows r per stage (32 KB per CTA);
 //   warp 0   TMA producer: two 64 x 64 boxes of each operand per stage;
 //   warp 1   even CTA: four tcgen05.mma kind::f16 (256 x 256 x 16) per stage
 //            into one of two 256-column TMEM slots; odd CTA: tells the even
-//            one that its half of the stage has landed.  In a group's last
-//            stage both first clear the rows behind the group (they belong to
-//            the next expert, whose values may be infinite);
+//            one that its half of the stage has landed;
 //   warps 2..9  epilogue: TMEM through 128-byte swizzled rows in shared memory
 //            to dW by TMA stores (adds, when accumulating), clipped at the
 //            edges of the expert's matrix.
-// Restoring once per token and letting the producer gather rows (four-row TMA
-// gathers, 32 per stage) moved 0.4 GB less and was slower: 2453 us against
-// 1087 us with rows in order (64 experts of 2048 x 7168, 32768 rows).
+// 64 experts of 2048 x 7168, bf16 dW: 760 us with 512 rows each (1265 TFLOP/s);
+// 2 experts of 16384 rows, where few outputs are written: 635 us (1515).
+// Measured and not kept, same sizes: restoring once per token and gathering
+// rows in the producer (four-row TMA gathers, 32 per stage), 2453 us; codes
+// converted on their way into the stage by eight or sixteen more warps, 1636
+// and 1244 us; clusters of two pairs that share d_y by multicast, 795 us (and
+// 744 instead of 635); clearing the rows behind a group in shared memory, which
+// the odd CTA has to release to the cluster, 0.5 us per expert and tile.
 #include <algorithm>
 
 #include "common.cuh"
@@ -32,51 +38,99 @@ namespace {
 // ------------------------------------------------------------------ restore
 constexpr int kRestoreThreads = 256;
 
-// 8 codes per thread and row: x[r, c .. c + 8) = bf16(code * scale) of token
-// row_token[r], for the rows that belong to an expert; kRestoreRows rows at a
-// time, their loads in flight together.
-constexpr int kRestoreRows = 4;
+constexpr int kRows = 64;         // rows r per stage of the GEMM
+constexpr int kRestoreRows = 4;   // rows of a thread whose loads are in flight together
 
+// 8 codes (two words) as bf16(code * s).
+__device__ __forceinline__ uint4 restore8(uint2 c, float s) {
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t h;  // two E4M3 codes as f16 (exact)
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)((j < 2 ? c.x : c.y) >> (16 * (j & 1)))));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
+    o[j] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+struct RestoreArgs {
+  const uint8_t* codes;
+  const float* scales;
+  int64_t tokens, K;
+  const int32_t* row_token;
+  const int32_t* offsets;
+  int64_t R;
+  int E;
+  const __nv_bfloat16* dy;
+  int64_t N, ldy;
+  __nv_bfloat16 *x, *x_tail, *y_tail;  // [R, K], [E * kRows, K], [E * kRows, N]
+};
+
+// First row and number of rows of expert e.
+__device__ __forceinline__ void expert_rows(const int32_t* offsets, int64_t R, int e, int64_t& lo, int& rows) {
+  lo = min(max((int64_t)__ldg(offsets + e), (int64_t)0), R);
+  const int64_t hi = min((int64_t)__ldg(offsets + e + 1), R);
+  rows = hi > lo ? (int)(hi - lo) : 0;
+}
+
+// Thread: 8 columns; block y: kRestoreRows rows, those of every expert first,
+// then each expert's kRows tail rows.
 __global__ void __launch_bounds__(kRestoreThreads)
-    wgrad_restore_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales, int64_t tokens,
-                         int64_t K, const int32_t* __restrict__ row_token, const int32_t* __restrict__ last, int64_t R,
-                         __nv_bfloat16* __restrict__ x) {
+    wgrad_restore_kernel(const RestoreArgs a, int64_t main_blocks, int64_t blocks) {
   pdl_wait();
   const uint32_t v = blockIdx.x * kRestoreThreads + threadIdx.x;
-  if (v >= (uint32_t)(K / 8)) return;
-  const int64_t KB = (K + 127) / 128, rows = min((int64_t)__ldg(last), R);
-  for (int64_t r0 = (int64_t)blockIdx.y * kRestoreRows; r0 < rows; r0 += (int64_t)gridDim.y * kRestoreRows) {
-    uint2 c[kRestoreRows];
-    float s[kRestoreRows];
-#pragma unroll
-    for (int i = 0; i < kRestoreRows; ++i) {
-      const int64_t r = min(r0 + i, rows - 1);
-      const int64_t t = row_token ? min(max((int64_t)__ldg(row_token + r), (int64_t)0), tokens - 1) : r;
-      c[i] = __ldg(reinterpret_cast<const uint2*>(codes + t * K) + v);
-      s[i] = __ldg(scales + t * KB + v / 16);
+  const bool has_x = v < (uint32_t)(a.K / 8), has_y = v < (uint32_t)(a.N / 8);
+  const int64_t KB = (a.K + 127) / 128;
+  for (int64_t b = blockIdx.y; b < blocks; b += gridDim.y) {
+    const bool tail = b >= main_blocks;
+    int64_t from = b * kRestoreRows, to = from;  // source row and row written
+    int64_t end = min((int64_t)__ldg(a.offsets + a.E), a.R);
+    if (tail) {
+      to = (b - main_blocks) * kRestoreRows;
+      int64_t lo;
+      int rows;
+      expert_rows(a.offsets, a.R, (int)(to / kRows), lo, rows);
+      if (rows % kRows == 0) continue;  // no tail (the same for the whole block)
+      from = lo + rows / kRows * kRows + to % kRows;
+      end = lo + rows;
     }
+    if (has_x) {
+      uint2 c[kRestoreRows];
+      float s[kRestoreRows];
 #pragma unroll
-    for (int i = 0; i < kRestoreRows; ++i) {
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t h;  // two E4M3 codes as f16 (exact)
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)((j < 2 ? c[i].x : c[i].y) >> (16 * (j & 1)))));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s[i], f.y * s[i]);
-        o[j] = *reinterpret_cast<const uint32_t*>(&b);
+      for (int i = 0; i < kRestoreRows; ++i) {
+        c[i] = make_uint2(0u, 0u);
+        s[i] = 0.f;
+        if (from + i >= end) continue;
+        const int64_t r = from + i;
+        const int64_t t = a.row_token ? min(max((int64_t)__ldg(a.row_token + r), (int64_t)0), a.tokens - 1) : r;
+        c[i] = __ldg(reinterpret_cast<const uint2*>(a.codes + t * a.K) + v);
+        s[i] = __ldg(a.scales + t * KB + v / 16);
       }
-      if (r0 + i < rows)
-        reinterpret_cast<uint4*>(x + (r0 + i) * K)[v] = make_uint4(o[0], o[1], o[2], o[3]);
+      __nv_bfloat16* x = tail ? a.x_tail : a.x;
+#pragma unroll
+      for (int i = 0; i < kRestoreRows; ++i)
+        if (tail || from + i < end) reinterpret_cast<uint4*>(x + (to + i) * a.K)[v] = restore8(c[i], s[i]);
+    }
+    if (tail && has_y) {
+#pragma unroll
+      for (int i = 0; i < kRestoreRows; ++i) {
+        uint4 d = make_uint4(0u, 0u, 0u, 0u);
+        if (from + i < end) d = __ldg(reinterpret_cast<const uint4*>(a.dy + (from + i) * a.ldy) + v);
+        reinterpret_cast<uint4*>(a.y_tail + (to + i) * a.N)[v] = d;
+      }
     }
   }
 }
 
 // ------------------------------------------------------------------ GEMM
-constexpr int kRows = 64;                          // rows r per stage
 constexpr int kHalf = 128;                         // n rows, and k columns, of one CTA's operands
 constexpr int kTile = 256;                         // pair tile, both ways
-constexpr int kStages = 5;
+// Six stages and one store buffer per epilogue warp: with five and two, 835 us
+// for 760 (64 experts of 2048 x 7168, 512 rows each, bf16; FP32: 1095 for 904).
+constexpr int kStages = 6;
 constexpr uint32_t kPanelBytes = kRows * 128;      // 64 rows x 64 bf16, 128-byte swizzle
 constexpr uint32_t kOperandBytes = 2 * kPanelBytes;
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
@@ -84,14 +138,14 @@ constexpr int kSlots = 2;
 constexpr int kEpiWarp0 = 2, kEpiWarps = 8;
 constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
 constexpr uint32_t kOutBytes = 32 * 128;           // 32 rows of 128 bytes: one TMA store of an epilogue warp
-constexpr uint32_t kOutTotal = 2 * kEpiWarps * kOutBytes;
+constexpr uint32_t kOutTotal = kEpiWarps * kOutBytes;
 constexpr uint32_t kSmemBytes = kStages * kStageBytes + kOutTotal + 1024 /*align*/ + 256 /*barriers*/;
 static_assert(kSmemBytes <= 232448, "shared memory");
 static_assert(kSlots * kTile <= 512, "TMEM columns");
 
 struct Smem {
   uint64_t full[kStages];       // this CTA's copies of the stage landed
-  uint64_t pair_full[kStages];  // even CTA: the odd CTA's did, its rows behind the group are clear
+  uint64_t pair_full[kStages];  // even CTA: the odd CTA's did
   uint64_t empty[kStages];      // the stage's MMAs are done (both CTAs)
   uint64_t slot_full[kSlots];   // the slot holds a tile (both CTAs)
   uint64_t slot_empty[kSlots];  // even CTA: every epilogue warp of the pair has read it
@@ -146,29 +200,9 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
                  : "memory");
 }
 __device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// At most kLeft of this thread's store groups still read their shared memory.
-template <int kLeft>
+// This thread's stores have read their shared memory.
 __device__ __forceinline__ void tma_store_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
-}
-
-// Arrive on a peer's mbarrier with everything this thread has seen visible to
-// the cluster: the cleared rows of the odd CTA's stage.  Only after a clear:
-// as the arrival of every stage it cost 1.1 us a stage and held the whole
-// kernel there (64 x 2048 x 7168, 32768 rows in order: 1764 us).
-__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-// Clears rows [from, 64) of the stage's four panels (the whole warp).
-__device__ __forceinline__ void clear_rows(uint8_t* stage, int from, int lane) {
-  const int words = (kRows - from) * 8;  // 16-byte words per panel
-  for (int p = 0; p < 4; ++p) {
-    uint4* dst = reinterpret_cast<uint4*>(stage + p * kPanelBytes + from * 128);
-    for (int i = lane; i < words; i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
-  fence_proxy_async_smem();  // the tensor cores read what these threads wrote
-  __syncwarp();
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // The bounded wait, with one answer for the whole warp: a lane that gave up
@@ -190,15 +224,14 @@ __device__ __forceinline__ Tile tile_of(const Params& p, int t) {
   const int r = t - o.e * per;
   o.n0 = (r % p.num_n) * kTile;
   o.k0 = (r / p.num_n) * kTile;
-  o.lo = min(max((int64_t)__ldg(p.offsets + o.e), (int64_t)0), p.R);
-  const int64_t hi = min((int64_t)__ldg(p.offsets + o.e + 1), p.R);
-  o.rows = hi > o.lo ? (int)(hi - o.lo) : 0;
+  expert_rows(p.offsets, p.R, o.e, o.lo, o.rows);
   return o;
 }
 
 template <typename W>
 __global__ void __launch_bounds__(kThreads, 1)
     wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmap_y, const __grid_constant__ CUtensorMap tmap_x,
+                      const __grid_constant__ CUtensorMap tmap_yt, const __grid_constant__ CUtensorMap tmap_xt,
                       const __grid_constant__ CUtensorMap tmap_w, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   pdl_wait();  // operands may come from the previous kernel
@@ -224,6 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     prefetch_tmap(&tmap_y);
     prefetch_tmap(&tmap_x);
+    prefetch_tmap(&tmap_yt);
+    prefetch_tmap(&tmap_xt);
     prefetch_tmap(&tmap_w);
   }
   if (warp == 1) {
@@ -253,13 +288,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t y = smem_u32(smem + stage * kStageBytes), x = y + kOperandBytes;
         const uint32_t full = smem_u32(&sm->full[stage]);
-        const int32_t row = (int32_t)w.lo + r0;
+        const bool tail = w.rows - r0 < kRows;
+        const int32_t row = tail ? w.e * kRows : (int32_t)w.lo + r0;
+        const CUtensorMap* ym = tail ? &tmap_yt : &tmap_y;
+        const CUtensorMap* xm = tail ? &tmap_xt : &tmap_x;
         if (lane == 0) {
           mbar_arrive_expect_tx(full, kStageBytes);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            tma_load_2d(y + i * kPanelBytes, &tmap_y, (w.n0 + rank * kHalf + i * 64) * 2, row, full);
-            tma_load_2d(x + i * kPanelBytes, &tmap_x, (w.k0 + rank * kHalf + i * 64) * 2, row, full);
+            tma_load_2d(y + i * kPanelBytes, ym, (w.n0 + rank * kHalf + i * 64) * 2, row, full);
+            tma_load_2d(x + i * kPanelBytes, xm, (w.k0 + rank * kHalf + i * 64) * 2, row, full);
           }
         }
         issued[stage] = 1;
@@ -288,20 +326,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++done;
         const uint32_t d = tmem + slot * kTile;
         for (int r0 = 0; r0 < w.rows; r0 += kRows) {
-          if (!warp_wait(smem_u32(&sm->full[stage]), phase, p.ctl, abort_flag)) {
+          if (!warp_wait(smem_u32(&sm->full[stage]), phase, p.ctl, abort_flag) ||
+              !warp_wait<true>(smem_u32(&sm->pair_full[stage]), phase, p.ctl, abort_flag)) {
             alive = false;
             break;
           }
-          uint8_t* st = smem + stage * kStageBytes;
-          if (w.rows - r0 < kRows) clear_rows(st, w.rows - r0, lane);
-          if (!warp_wait<true>(smem_u32(&sm->pair_full[stage]), phase, p.ctl, abort_flag)) {
-            alive = false;
-            break;
-          }
-          __syncwarp();
           tc_fence_after();
           if (lane == 0) {
-            const uint32_t y = smem_u32(st), x = y + kOperandBytes;
+            const uint32_t y = smem_u32(smem + stage * kStageBytes), x = y + kOperandBytes;
 #pragma unroll
             for (uint32_t s = 0; s < kRows / 16; ++s)
               mma_bf16_pair(d, operand_desc(y, s), operand_desc(x, s), r0 != 0 || s != 0 ? 1u : 0u);
@@ -329,14 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             alive = false;
             break;
           }
-          const bool part = w.rows - r0 < kRows;
-          if (part) clear_rows(smem + stage * kStageBytes, w.rows - r0, lane);
-          if (lane == 0) {
-            if (part)
-              mbar_arrive_cluster_release(leader_pair_full + stage * 8);
-            else
-              mbar_arrive_cluster(leader_pair_full + stage * 8);
-          }
+          if (lane == 0) mbar_arrive_cluster(leader_pair_full + stage * 8);
           if (++stage == kStages) stage = 0, phase ^= 1;
         }
       }
@@ -348,9 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h = (warp - kEpiWarp0) >> 2;   // column half of the slot
     const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16) + h * 128;
     const uint32_t leader_slot_empty = mapa_shared(smem_u32(&sm->slot_empty[0]), 0);
-    uint8_t* buf = out_smem + (warp - kEpiWarp0) * 2 * kOutBytes;
+    uint8_t* line = out_smem + (warp - kEpiWarp0) * kOutBytes;
     constexpr int kCols = 128 / (int)sizeof(W);  // columns of one store
-    uint32_t done = 0, stores = 0;
+    uint32_t done = 0;
     for (int t = cid; t < p.tiles; t += ncl) {
       const Tile w = tile_of(p, t);
       const int n0 = w.n0 + rank * kHalf + q * 32;
@@ -364,9 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
 #pragma unroll
-      for (int c = 0; c < 128 / kCols; ++c, ++stores) {
-        uint8_t* line = buf + (stores & 1) * kOutBytes;
-        if (lane == 0) tma_store_wait_read<1>();  // the store before the last has read this buffer
+      for (int c = 0; c < 128 / kCols; ++c) {
+        if (lane == 0) tma_store_wait_read();  // the last store has read the buffer
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < kCols / 16; ++i) {  // 16 columns at a time
@@ -407,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int k = k0 + c * kCols;
         if (lane == 0) {
           if (n0 < p.N && k < p.K) tma_store_3d(&tmap_w, smem_u32(line), k, n0, w.e, p.accumulate != 0);
-          tma_store_commit();  // a group per buffer use, empty past the edge: the wait above counts groups
+          tma_store_commit();
         }
       }
     }
@@ -428,17 +452,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-// The restored rows.
-size_t wgrad_workspace_bytes(int64_t R, int64_t N, int64_t K) {
-  (void)N;
-  return (size_t)R * (size_t)K * sizeof(__nv_bfloat16);
+namespace {
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+}  // namespace
+
+// The restored rows, then the tails of x and d_y.
+size_t wgrad_workspace_bytes(int64_t R, int64_t N, int64_t K, int E) {
+  return align256((size_t)R * K * 2) + align256((size_t)E * kRows * K * 2) + align256((size_t)E * kRows * N * 2);
 }
 
 namespace {
 
 template <typename W>
 q4_status launch_typed(const WgradArgs& a, cudaStream_t stream) {
-  __nv_bfloat16* x = static_cast<__nv_bfloat16*>(a.ws);
+  RestoreArgs r = {a.codes, a.scales, a.tokens, a.K, a.row_token, a.offsets, a.R, a.E};
+  r.dy = static_cast<const __nv_bfloat16*>(a.dy), r.N = a.N, r.ldy = a.ldy;
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  r.x = reinterpret_cast<__nv_bfloat16*>(ws);
+  ws += align256((size_t)a.R * a.K * 2);
+  r.x_tail = reinterpret_cast<__nv_bfloat16*>(ws);
+  ws += align256((size_t)a.E * kRows * a.K * 2);
+  r.y_tail = reinterpret_cast<__nv_bfloat16*>(ws);
   Params p = {};
   p.R = a.R, p.N = a.N, p.K = a.K;
   p.offsets = a.offsets;
@@ -448,10 +482,14 @@ q4_status launch_typed(const WgradArgs& a, cudaStream_t stream) {
   p.num_n = (int)num_n, p.num_k = (int)num_k, p.tiles = (int)(a.E * num_n * num_k);
   p.ctl = KernelCtl{device_status_ptr(), wait_budget_ns()};
 
-  CUtensorMap ty, tx, tw;
+  CUtensorMap ty, tx, yt, xt, tw;
   q4_status st = make_tmap_2d_u8(&ty, a.dy, a.N * 2, a.R, a.ldy * 2, 128, kRows, true);
   if (st != Q4_OK) return st;
-  st = make_tmap_2d_u8(&tx, x, a.K * 2, a.R, a.K * 2, 128, kRows, true);
+  st = make_tmap_2d_u8(&tx, r.x, a.K * 2, a.R, a.K * 2, 128, kRows, true);
+  if (st != Q4_OK) return st;
+  st = make_tmap_2d_u8(&yt, r.y_tail, a.N * 2, (uint64_t)a.E * kRows, a.N * 2, 128, kRows, true);
+  if (st != Q4_OK) return st;
+  st = make_tmap_2d_u8(&xt, r.x_tail, a.K * 2, (uint64_t)a.E * kRows, a.K * 2, 128, kRows, true);
   if (st != Q4_OK) return st;
   st = make_tmap_3d(&tw, sizeof(W) == 4 ? Q4_F32 : Q4_BF16, a.dw, a.K, a.N, a.E, a.K, a.N * a.K, 128 / sizeof(W), 32,
                     1, true);
@@ -481,13 +519,14 @@ q4_status launch_typed(const WgradArgs& a, cudaStream_t stream) {
     max_pairs[dev] = std::min(n, num_sms() / 2);
   }
 
-  const int64_t gx = ceil_div(a.K / 8, kRestoreThreads);
-  const int64_t gy = std::min<int64_t>(ceil_div(a.R, kRestoreRows), 65535);
-  st = launch_pdl(wgrad_restore_kernel, dim3((unsigned)gx, (unsigned)gy), kRestoreThreads, 0, stream, a.codes,
-                  a.scales, a.tokens, a.K, a.row_token, a.offsets + a.E, a.R, x);
+  const int64_t gx = ceil_div(std::max(a.K, a.N) / 8, kRestoreThreads);
+  const int64_t main_blocks = ceil_div(a.R, kRestoreRows);
+  const int64_t blocks = main_blocks + (int64_t)a.E * (kRows / kRestoreRows);
+  st = launch_pdl(wgrad_restore_kernel, dim3((unsigned)gx, (unsigned)std::min<int64_t>(blocks, 65535)),
+                  kRestoreThreads, 0, stream, r, main_blocks, blocks);
   if (st != Q4_OK) return st;
   cfg.gridDim = dim3(2u * (unsigned)std::min(p.tiles, max_pairs[dev]), 1, 1);
-  Q4_CUDA_TRY(cudaLaunchKernelEx(&cfg, wgrad_pair_kernel<W>, ty, tx, tw, p));
+  Q4_CUDA_TRY(cudaLaunchKernelEx(&cfg, wgrad_pair_kernel<W>, ty, tx, yt, xt, tw, p));
   return Q4_OK;
 }
 

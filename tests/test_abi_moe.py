@@ -96,7 +96,7 @@ def test_wgrad(clib):
         assert wgrad(**bad) == -2, bad
     for none in (dict(E=0), dict(N=0, ldy=0), dict(K=0)):
         assert wgrad(w=None, **none) == 0, none
-    need = clib.q4_workspace_size(11, 64, 16, 32)
-    if need:
-        for ws, nb in ((None, need), (FAKE + 16, need), (FAKE, need - 1)):
-            assert wgrad(ws=ws, nb=nb) == -6
+    need = clib.q4_workspace_size_wgrad(64, 16, 32, 2)
+    assert need >= 64 * 32 * 2 and clib.q4_workspace_size_wgrad(-1, 16, 32, 2) == 0
+    for ws, nb in ((None, need), (FAKE + 16, need), (FAKE, need - 1)):
+        assert wgrad(ws=ws, nb=nb) == -6
