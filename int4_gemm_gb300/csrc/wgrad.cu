@@ -12,21 +12,24 @@
 // The second is a grouped bf16 GEMM on CTA pairs:
 //   tile     256 (n) x 256 (k) per pair, 128 n rows and 128 k columns of the
 //            operands per CTA, 64 rows r per stage (32 KB per CTA);
-//   warp 0   TMA producer: two 64 x 64 boxes of each operand per stage;
+//   warp 0   TMA producer: two 64 x 64 boxes of each operand per stage; the
+//            bytes of both CTAs are counted on the even one's mbarrier;
 //   warp 1   even CTA: four tcgen05.mma kind::f16 (256 x 256 x 16) per stage
-//            into one of two 256-column TMEM slots; odd CTA: tells the even
-//            one that its half of the stage has landed;
+//            into one of two 256-column TMEM slots;
 //   warps 2..9  epilogue: TMEM through 128-byte swizzled rows in shared memory
 //            to dW by TMA stores (adds, when accumulating), clipped at the
 //            edges of the expert's matrix.
-// 64 experts of 2048 x 7168, bf16 dW: 760 us with 512 rows each (1265 TFLOP/s);
-// 2 experts of 16384 rows, where few outputs are written: 635 us (1515).
+// 64 experts of 2048 x 7168, bf16 dW, the restoring included: 732 us with 512
+// rows each (1313 TFLOP/s; 645 without the stores), 762 us with 27 to 1933; 2
+// experts of 16384 rows, where few outputs are written: 570 us (1688).
 // Measured and not kept, same sizes: restoring once per token and gathering
 // rows in the producer (four-row TMA gathers, 32 per stage), 2453 us; codes
 // converted on their way into the stage by eight or sixteen more warps, 1636
 // and 1244 us; clusters of two pairs that share d_y by multicast, 795 us (and
 // 744 instead of 635); clearing the rows behind a group in shared memory, which
-// the odd CTA has to release to the cluster, 0.5 us per expert and tile.
+// the odd CTA has to release to the cluster, 0.5 us per expert and tile; the odd
+// CTA's arrival passed on by a warp of it, 738 us (and 625 instead of 570); a
+// warp's whole part of a slot in registers before its first store, 762 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -144,8 +147,7 @@ static_assert(kSmemBytes <= 232448, "shared memory");
 static_assert(kSlots * kTile <= 512, "TMEM columns");
 
 struct Smem {
-  uint64_t full[kStages];       // this CTA's copies of the stage landed
-  uint64_t pair_full[kStages];  // even CTA: the odd CTA's did
+  uint64_t full[kStages];       // even CTA: both CTAs' copies of the stage landed
   uint64_t empty[kStages];      // the stage's MMAs are done (both CTAs)
   uint64_t slot_full[kSlots];   // the slot holds a tile (both CTAs)
   uint64_t slot_empty[kSlots];  // even CTA: every epilogue warp of the pair has read it
@@ -212,6 +214,17 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const K
   return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, ctl, abort_flag)) != 0;
 }
 
+// A box into this CTA's shared memory whose bytes are counted on an mbarrier of
+// the pair, given by its shared::cluster address.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                                 uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(cluster_bar)
+      : "memory");
+}
+
 struct Tile {
   int e, n0, k0;
   int64_t lo;
@@ -245,7 +258,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&sm->full[s]), 1);
-      mbar_init(smem_u32(&sm->pair_full[s]), 1);
       mbar_init(smem_u32(&sm->empty[s]), 1);
     }
     for (int s = 0; s < kSlots; ++s) {
@@ -274,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
+    const uint32_t leader_full = mapa_shared(smem_u32(&sm->full[0]), 0);
     uint32_t stage = 0, phase = 0;
     int issued[kStages];
     uint32_t issued_phase[kStages];
@@ -287,17 +300,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const uint32_t y = smem_u32(smem + stage * kStageBytes), x = y + kOperandBytes;
-        const uint32_t full = smem_u32(&sm->full[stage]);
+        const uint32_t full = leader_full + stage * 8;
         const bool tail = w.rows - r0 < kRows;
         const int32_t row = tail ? w.e * kRows : (int32_t)w.lo + r0;
         const CUtensorMap* ym = tail ? &tmap_yt : &tmap_y;
         const CUtensorMap* xm = tail ? &tmap_xt : &tmap_x;
         if (lane == 0) {
-          mbar_arrive_expect_tx(full, kStageBytes);
+          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sm->full[stage]), 2 * kStageBytes);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            tma_load_2d(y + i * kPanelBytes, ym, (w.n0 + rank * kHalf + i * 64) * 2, row, full);
-            tma_load_2d(x + i * kPanelBytes, xm, (w.k0 + rank * kHalf + i * 64) * 2, row, full);
+            tma_load_2d_pair(y + i * kPanelBytes, ym, (w.n0 + rank * kHalf + i * 64) * 2, row, full);
+            tma_load_2d_pair(x + i * kPanelBytes, xm, (w.k0 + rank * kHalf + i * 64) * 2, row, full);
           }
         }
         issued[stage] = 1;
@@ -305,16 +318,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++stage == kStages) stage = 0, phase ^= 1;
       }
     }
-    // drain: every copy this warp issued has landed before the CTA exits
-    if (lane == 0) {
+    // drain: every copy of the pair has landed before its CTAs exit (they leave
+    // together).  The odd CTA sees no count of its own: where it gave up, it
+    // leaves its copies a time far beyond any copy's.
+    if (!alive) {
+      const unsigned long long t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 200000ull) __nanosleep(1000);
+    }
+    if (lane == 0 && rank == 0) {
       KernelCtl drain = p.ctl;
       for (int s = 0; s < kStages; ++s)
         if (issued[s]) mbar_wait(smem_u32(&sm->full[s]), issued_phase[s], drain, nullptr);
     }
     __syncwarp();
   } else if (warp == 1) {
-    uint32_t stage = 0, phase = 0;
     if (rank == 0) {
+      uint32_t stage = 0, phase = 0;
       // ---------------------------------------------------------- MMA issuer
       uint32_t done = 0;
       bool alive = true;
@@ -326,8 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++done;
         const uint32_t d = tmem + slot * kTile;
         for (int r0 = 0; r0 < w.rows; r0 += kRows) {
-          if (!warp_wait(smem_u32(&sm->full[stage]), phase, p.ctl, abort_flag) ||
-              !warp_wait<true>(smem_u32(&sm->pair_full[stage]), phase, p.ctl, abort_flag)) {
+          if (!warp_wait<true>(smem_u32(&sm->full[stage]), phase, p.ctl, abort_flag)) {
             alive = false;
             break;
           }
@@ -349,21 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_commit_pair_mc(smem_u32(&sm->mma_done), 1);
         KernelCtl drain = p.ctl;
         mbar_wait(smem_u32(&sm->mma_done), 0, drain, nullptr);
-      }
-    } else {
-      // ---------------------------------------------------------- relay (odd CTA)
-      const uint32_t leader_pair_full = mapa_shared(smem_u32(&sm->pair_full[0]), 0);
-      bool alive = true;
-      for (int t = cid; t < p.tiles && alive; t += ncl) {
-        const Tile w = tile_of(p, t);
-        for (int r0 = 0; r0 < w.rows; r0 += kRows) {
-          if (!warp_wait(smem_u32(&sm->full[stage]), phase, p.ctl, abort_flag)) {
-            alive = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_cluster(leader_pair_full + stage * 8);
-          if (++stage == kStages) stage = 0, phase ^= 1;
-        }
       }
     }
     __syncwarp();
