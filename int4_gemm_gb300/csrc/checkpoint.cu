@@ -82,22 +82,32 @@ __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
 // whole rest of the kernels.
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 
-// A block of 128 columns is held by 16 lanes, 8 columns each with 128-bit
-// accesses (kVec; two blocks per warp), or by a warp, lane l holding columns
-// l, l + 32, ... one by one; columns past the block's end are zero.  16-bit
-// elements stay packed in the words they were loaded as until they are used.
+// A block of 128 columns is held by `lanes` lanes, `n` columns each.  With
+// 128-bit accesses (kVec) a lane holds chunks of 8 columns, lanes * 8 apart: one
+// chunk of FP32 (16 lanes), two of 16-bit elements (8 lanes), so that two loads
+// are in flight either way (one chunk of bf16: swiglu_fp8 94 us instead of 79
+// at 32768 x 2 x 2048).  Otherwise lane l of a warp holds columns l, l + 32, ...
+// one by one (a path without tests for whole blocks took longer, 33 us instead
+// of 27 for the gradient at 9973 x 1411).  Columns past the block's end are zero; 16-bit elements stay
+// packed in the words they were loaded as until they are used.
 template <typename T, bool kVec>
 struct Held {
-  static constexpr int lanes = kVec ? 16 : 32, n = 128 / lanes;
+  static constexpr int lanes = !kVec ? 32 : sizeof(T) == 2 ? 8 : 16, n = 128 / lanes;
+  static constexpr int chunks = kVec ? n / 8 : 1;
+  static_assert(chunks * lanes * 8 == 128 || !kVec, "a block");
   static constexpr bool packed = kVec && sizeof(T) == 2;
   static constexpr int words = packed ? n / 2 : n;
   uint32_t w[words];
 
+  static __device__ __forceinline__ int chunk(int l, int c) { return 8 * (l + lanes * c); }
+
   __device__ __forceinline__ void load(const T* __restrict__ p, int l, int cols) {
     if constexpr (kVec) {
+      constexpr int per = words / chunks / 4;  // 128-bit words of a chunk
 #pragma unroll
       for (int i = 0; i < words / 4; ++i) {
-        const uint4 v = n * l < cols ? __ldg(reinterpret_cast<const uint4*>(p + n * l) + i) : make_uint4(0u, 0u, 0u, 0u);
+        const int at = chunk(l, i / per);
+        const uint4 v = at < cols ? __ldg(reinterpret_cast<const uint4*>(p + at) + i % per) : make_uint4(0u, 0u, 0u, 0u);
         w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
       }
     } else {
@@ -140,14 +150,19 @@ struct Held {
 
 template <typename T, bool kVec, int n>
 __device__ __forceinline__ void store_block(T* __restrict__ p, int l, int cols, const float (&v)[n]) {
+  using H = Held<T, kVec>;
   if constexpr (kVec) {
-    if (n * l < cols) {
-      uint4* out = reinterpret_cast<uint4*>(p + n * l);
+#pragma unroll
+    for (int c = 0; c < H::chunks; ++c) {
+      const int at = H::chunk(l, c);
+      if (at >= cols) continue;
+      uint4* out = reinterpret_cast<uint4*>(p + at);
+      const float* f = v + 8 * c;
       if constexpr (sizeof(T) == 4) {
-        out[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-        out[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+        out[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        out[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
       } else {
-        out[0] = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+        out[0] = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
       }
     }
   } else {
@@ -158,15 +173,18 @@ __device__ __forceinline__ void store_block(T* __restrict__ p, int l, int cols, 
 }
 
 // Codes of the held columns f under the scale 2^e.
-template <bool kVec, int n>
+template <typename T, bool kVec, int n>
 __device__ __forceinline__ void encode_block(uint8_t* __restrict__ codes, int l, int cols, const float (&f)[n], int e) {
+  using H = Held<T, kVec>;
   const float inv = pow2f(-e);
   uint32_t w[n / 4];
 #pragma unroll
   for (int i = 0; i < n / 4; ++i)
     w[i] = e4m3x2(f[4 * i] * inv, f[4 * i + 1] * inv) | e4m3x2(f[4 * i + 2] * inv, f[4 * i + 3] * inv) << 16;
   if constexpr (kVec) {
-    if (n * l < cols) *reinterpret_cast<uint2*>(codes + n * l) = make_uint2(w[0], w[1]);
+#pragma unroll
+    for (int c = 0; c < H::chunks; ++c)
+      if (H::chunk(l, c) < cols) *reinterpret_cast<uint2*>(codes + H::chunk(l, c)) = make_uint2(w[2 * c], w[2 * c + 1]);
   } else {
 #pragma unroll
     for (int i = 0; i < n; ++i)
@@ -174,11 +192,16 @@ __device__ __forceinline__ void encode_block(uint8_t* __restrict__ codes, int l,
   }
 }
 
-template <bool kVec, int n>
+template <typename T, bool kVec, int n>
 __device__ __forceinline__ void load_codes(const uint8_t* __restrict__ codes, int l, int cols, uint32_t (&w)[n / 4]) {
+  using H = Held<T, kVec>;
   if constexpr (kVec) {
-    const uint2 c = n * l < cols ? __ldg(reinterpret_cast<const uint2*>(codes + n * l)) : make_uint2(0u, 0u);
-    w[0] = c.x, w[1] = c.y;
+#pragma unroll
+    for (int c = 0; c < H::chunks; ++c) {
+      const int at = H::chunk(l, c);
+      const uint2 v = at < cols ? __ldg(reinterpret_cast<const uint2*>(codes + at)) : make_uint2(0u, 0u);
+      w[2 * c] = v.x, w[2 * c + 1] = v.y;
+    }
   } else {
     uint32_t c[n];
 #pragma unroll
@@ -239,7 +262,7 @@ __global__ void __launch_bounds__(kThreads)
   const int e = scale_exponent(top);
   float f[H::n];
   v.floats(f);
-  encode_block<kVec>(codes + k.row * K + c, l, k.n, f, e);
+  encode_block<T, kVec>(codes + k.row * K + c, l, k.n, f, e);
   if (l == 0 && k.n > 0) {
     scales[b] = pow2f(e);
     if (nonfinite(top)) latch_status(status, Q4_ERR_NONFINITE);
@@ -263,8 +286,8 @@ __global__ void __launch_bounds__(kThreads)
   float g[H::n], u[H::n];
   hg.floats(g);
   hu.floats(u);
-  encode_block<kVec>(codes + k.row * 2 * I + c, l, k.n, g, eg);
-  encode_block<kVec>(codes + k.row * 2 * I + I + c, l, k.n, u, eu);
+  encode_block<T, kVec>(codes + k.row * 2 * I + c, l, k.n, g, eg);
+  encode_block<T, kVec>(codes + k.row * 2 * I + I + c, l, k.n, u, eu);
   if (l == 0 && k.n > 0) {
     scales[k.row * 2 * blk.per_row + k.i] = pow2f(eg);
     scales[k.row * 2 * blk.per_row + blk.per_row + k.i] = pow2f(eu);
@@ -291,8 +314,8 @@ __global__ void __launch_bounds__(kThreads)
   uint32_t wg[H::n / 4], wu[H::n / 4];
   H hd;
   hd.load(d_h + k.row * ld + c, l, k.n);
-  load_codes<kVec, H::n>(codes + k.row * 2 * I + c, l, k.n, wg);
-  load_codes<kVec, H::n>(codes + k.row * 2 * I + I + c, l, k.n, wu);
+  load_codes<T, kVec, H::n>(codes + k.row * 2 * I + c, l, k.n, wg);
+  load_codes<T, kVec, H::n>(codes + k.row * 2 * I + I + c, l, k.n, wu);
   const float sg = __ldg(sc), su = __ldg(sc + blk.per_row);
   float g[H::n], u[H::n], d[H::n];
   decode<H::n>(wg, sg, g);
@@ -321,7 +344,10 @@ inline bool mult(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p
 // One turn per thread: the blocks of threads are many and alike, and the
 // hardware keeps the SMs full of them (a grid of 8 per SM that loops left the
 // SMs 62% occupied at the end: 119 us instead of 93 at 32768 x 2 x 2048 bf16).
-unsigned block_grid(const Blocks& blk, bool vec) { return (unsigned)ceil_div(blk.total, kThreads / (vec ? 16 : 32)); }
+template <typename T>
+unsigned block_grid(const Blocks& blk, bool vec) {
+  return (unsigned)ceil_div(blk.total, kThreads / (vec ? Held<T, true>::lanes : Held<T, false>::lanes));
+}
 
 }  // namespace
 
@@ -331,7 +357,7 @@ q4_status launch_checkpoint(const void* x, int dtype, int64_t rows, int64_t K, i
   return by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
     const bool vec = K % 8 == 0 && ld * sizeof(T) % 16 == 0 && mult(x, 16) && mult(codes, 8);
-    return launch_pdl(vec ? checkpoint_kernel<T, true> : checkpoint_kernel<T, false>, block_grid(blk, vec), kThreads, 0,
+    return launch_pdl(vec ? checkpoint_kernel<T, true> : checkpoint_kernel<T, false>, block_grid<T>(blk, vec), kThreads, 0,
                       stream, static_cast<const T*>(x), blk, K, ld, codes, scales, device_status_ptr());
   });
 }
@@ -342,7 +368,7 @@ q4_status launch_swiglu(const void* gate_up, int dtype, int64_t rows, int64_t I,
   return by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
     const bool vec = I % 8 == 0 && ld * sizeof(T) % 16 == 0 && mult(gate_up, 16) && mult(h, 16) && mult(codes, 8);
-    return launch_pdl(vec ? swiglu_kernel<T, true> : swiglu_kernel<T, false>, block_grid(blk, vec), kThreads, 0, stream,
+    return launch_pdl(vec ? swiglu_kernel<T, true> : swiglu_kernel<T, false>, block_grid<T>(blk, vec), kThreads, 0, stream,
                       static_cast<const T*>(gate_up), blk, I, ld, static_cast<T*>(h), codes, scales,
                       device_status_ptr());
   });
@@ -354,7 +380,7 @@ q4_status launch_swiglu_backward(const void* d_h, int dtype, int64_t rows, int64
   return by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
     const bool vec = I % 8 == 0 && ld * sizeof(T) % 16 == 0 && mult(d_h, 16) && mult(codes, 8) && mult(d_gate_up, 16);
-    return launch_pdl(vec ? swiglu_backward_kernel<T, true> : swiglu_backward_kernel<T, false>, block_grid(blk, vec),
+    return launch_pdl(vec ? swiglu_backward_kernel<T, true> : swiglu_backward_kernel<T, false>, block_grid<T>(blk, vec),
                       kThreads, 0, stream, static_cast<const T*>(d_h), blk, I, ld, codes, scales,
                       static_cast<T*>(d_gate_up));
   });
