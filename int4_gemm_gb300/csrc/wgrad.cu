@@ -160,7 +160,7 @@ static_assert(sizeof(Smem) <= 256, "barrier block");
 struct Params {
   int64_t R, N, K;
   const int32_t* offsets;
-  int num_n, num_k, tiles, accumulate;
+  int E, splits, num_n, num_k, tiles, accumulate;
   KernelCtl ctl;
 };
 
@@ -187,7 +187,8 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t s) {
 }
 
 // A 32-row box of 128-byte rows from shared memory to dW[z], or added to it
-// (each element by one box, so sums do not depend on an order).
+// (each element by one box, so sums do not depend on an order; this addition
+// takes subnormal numbers as zero).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y, int32_t z,
                                              bool add) {
   if (add)
@@ -226,18 +227,31 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
 }
 
 struct Tile {
-  int e, n0, k0;
-  int64_t lo;
-  int rows;
+  int e, z, n0, k0;  // expert, matrix of the output, first n and k
+  int64_t lo;        // the expert's first row
+  int rows;          // its rows, and the part [begin, end) of them to sum
+  int begin, end;
 };
 __device__ __forceinline__ Tile tile_of(const Params& p, int t) {
   Tile o;
   const int per = p.num_n * p.num_k;
-  o.e = t / per;
-  const int r = t - o.e * per;
+  o.z = t / per;
+  const int r = t - o.z * per;
   o.n0 = (r % p.num_n) * kTile;
   o.k0 = (r / p.num_n) * kTile;
-  expert_rows(p.offsets, p.R, o.e, o.lo, o.rows);
+  o.e = o.z;
+  if (p.splits > 1) {
+    const int split = o.z / p.E;
+    o.e = o.z - split * p.E;
+    expert_rows(p.offsets, p.R, o.e, o.lo, o.rows);
+    const int stages = (o.rows + kRows - 1) / kRows;
+    o.begin = (int)((int64_t)stages * split / p.splits) * kRows;
+    o.end = min((int)((int64_t)stages * (split + 1) / p.splits) * kRows, o.rows);
+  } else {
+    expert_rows(p.offsets, p.R, o.e, o.lo, o.rows);
+    o.begin = 0;
+    o.end = o.rows;
+  }
   return o;
 }
 
@@ -294,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool alive = true;
     for (int t = cid; t < p.tiles && alive; t += ncl) {
       const Tile w = tile_of(p, t);
-      for (int r0 = 0; r0 < w.rows; r0 += kRows) {
+      for (int r0 = w.begin; r0 < w.end; r0 += kRows) {
         if (!warp_wait(smem_u32(&sm->empty[stage]), phase ^ 1, p.ctl, abort_flag)) {
           alive = false;
           break;
@@ -339,12 +353,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool alive = true;
       for (int t = cid; t < p.tiles && alive; t += ncl) {
         const Tile w = tile_of(p, t);
-        if (w.rows == 0) continue;
+        if (w.begin >= w.end) continue;
         const uint32_t slot = done % kSlots, sphase = (done / kSlots) & 1;
         if (!warp_wait<true>(smem_u32(&sm->slot_empty[slot]), sphase ^ 1, p.ctl, abort_flag)) break;
         ++done;
         const uint32_t d = tmem + slot * kTile;
-        for (int r0 = 0; r0 < w.rows; r0 += kRows) {
+        for (int r0 = w.begin; r0 < w.end; r0 += kRows) {
           if (!warp_wait<true>(smem_u32(&sm->full[stage]), phase, p.ctl, abort_flag)) {
             alive = false;
             break;
@@ -354,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t y = smem_u32(smem + stage * kStageBytes), x = y + kOperandBytes;
 #pragma unroll
             for (uint32_t s = 0; s < kRows / 16; ++s)
-              mma_bf16_pair(d, operand_desc(y, s), operand_desc(x, s), r0 != 0 || s != 0 ? 1u : 0u);
+              mma_bf16_pair(d, operand_desc(y, s), operand_desc(x, s), r0 != w.begin || s != 0 ? 1u : 0u);
             tc_commit_pair_mc(smem_u32(&sm->empty[stage]), 3);  // the stage is free in both CTAs
           }
           if (++stage == kStages) stage = 0, phase ^= 1;
@@ -384,7 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n0 = w.n0 + rank * kHalf + q * 32;
       const int k0 = w.k0 + h * 128;
       const uint32_t slot = done % kSlots, sphase = (done / kSlots) & 1;
-      if (w.rows) {
+      const bool some = w.begin < w.end;
+      if (some) {
         ++done;
         if (!warp_wait(smem_u32(&sm->slot_full[slot]), sphase, p.ctl, abort_flag)) break;
         tc_fence_after();
@@ -398,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kCols / 16; ++i) {  // 16 columns at a time
           uint32_t r[16];
-          if (w.rows) {
+          if (some) {
             tmem_ld_32x32b_x16(t_lane + slot * kTile + c * kCols + i * 16, r);
             tmem_ld_wait();
           } else {
@@ -424,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(line + lane * 128 + (((i * kWords + j) ^ (lane & 7)) << 4)) = o;
           }
         }
-        if (w.rows && c == 128 / kCols - 1) {  // the slot's columns of this warp are all read
+        if (some && c == 128 / kCols - 1) {  // the slot's columns of this warp are all read
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(leader_slot_empty + slot * 8);
@@ -433,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         const int k = k0 + c * kCols;
         if (lane == 0) {
-          if (n0 < p.N && k < p.K) tma_store_3d(&tmap_w, smem_u32(line), k, n0, w.e, p.accumulate != 0);
+          if (n0 < p.N && k < p.K) tma_store_3d(&tmap_w, smem_u32(line), k, n0, w.z, p.accumulate != 0);
           tma_store_commit();
         }
       }
@@ -456,18 +471,59 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 namespace {
+
+// dW = the sum of its splits' parts in their order (added to what it holds,
+// when accumulating); 4 elements per thread.
+constexpr int kJoinThreads = 256;
+
+template <typename W>
+__global__ void __launch_bounds__(kJoinThreads)
+    wgrad_join_kernel(const float4* __restrict__ parts, int splits, int64_t n4, int accumulate, W* __restrict__ dw) {
+  pdl_wait();
+  const int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
+  if (i >= n4) return;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  if constexpr (sizeof(W) == 4)
+    if (accumulate) sum = reinterpret_cast<const float4*>(dw)[i];
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float4 v = __ldg(parts + s * n4 + i);
+    sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+  }
+  if constexpr (sizeof(W) == 4) {
+    reinterpret_cast<float4*>(dw)[i] = sum;
+  } else {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x, sum.y), hi = __floats2bfloat162_rn(sum.z, sum.w);
+    reinterpret_cast<uint2*>(dw)[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                 *reinterpret_cast<const uint32_t*>(&hi));
+  }
+}
+
+// Where the tiles leave more than half of the CTA pairs idle and the experts'
+// rows are many, the rows are split, so that tiles times splits fill the pairs,
+// and the parts are joined by another launch (about 5 us, worth 16 stages).
+int split_count(int64_t R, int64_t N, int64_t K, int E) {
+  if (E <= 0 || N <= 0 || K <= 0) return 1;
+  const int64_t tiles = E * ceil_div(N, kTile) * ceil_div(K, kTile), stages = R / E / kRows;
+  const int64_t splits = std::min<int64_t>({num_sms() / 2 / tiles, stages / 4, 64});
+  return splits >= 2 && stages - stages / splits >= 16 ? (int)splits : 1;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 }  // namespace
 
-// The restored rows, then the tails of x and d_y.
+// The restored rows, the tails of x and d_y, the parts of split sums.
 size_t wgrad_workspace_bytes(int64_t R, int64_t N, int64_t K, int E) {
-  return align256((size_t)R * K * 2) + align256((size_t)E * kRows * K * 2) + align256((size_t)E * kRows * N * 2);
+  const int splits = split_count(R, N, K, E);
+  return align256((size_t)R * K * 2) + align256((size_t)E * kRows * K * 2) + align256((size_t)E * kRows * N * 2) +
+         (splits > 1 ? (size_t)splits * E * N * K * sizeof(float) : 0);
 }
 
 namespace {
 
+// dw: [splits * E, N, K].
 template <typename W>
-q4_status launch_typed(const WgradArgs& a, cudaStream_t stream) {
+q4_status launch_typed(const WgradArgs& a, W* dw, int splits, cudaStream_t stream) {
   RestoreArgs r = {a.codes, a.scales, a.tokens, a.K, a.row_token, a.offsets, a.R, a.E};
   r.dy = static_cast<const __nv_bfloat16*>(a.dy), r.N = a.N, r.ldy = a.ldy;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
@@ -479,10 +535,11 @@ q4_status launch_typed(const WgradArgs& a, cudaStream_t stream) {
   Params p = {};
   p.R = a.R, p.N = a.N, p.K = a.K;
   p.offsets = a.offsets;
-  p.accumulate = a.accumulate;
+  p.E = a.E, p.splits = splits;
+  p.accumulate = splits == 1 && a.accumulate;
   const int64_t num_n = ceil_div(a.N, kTile), num_k = ceil_div(a.K, kTile);
-  if (num_n * num_k > INT32_MAX / 2 / a.E) return Q4_ERR_UNSUPPORTED_SHAPE;
-  p.num_n = (int)num_n, p.num_k = (int)num_k, p.tiles = (int)(a.E * num_n * num_k);
+  if (num_n * num_k > INT32_MAX / 2 / a.E / splits) return Q4_ERR_UNSUPPORTED_SHAPE;
+  p.num_n = (int)num_n, p.num_k = (int)num_k, p.tiles = (int)(splits * a.E * num_n * num_k);
   p.ctl = KernelCtl{device_status_ptr(), wait_budget_ns()};
 
   CUtensorMap ty, tx, yt, xt, tw;
@@ -494,7 +551,7 @@ q4_status launch_typed(const WgradArgs& a, cudaStream_t stream) {
   if (st != Q4_OK) return st;
   st = make_tmap_2d_u8(&xt, r.x_tail, a.K * 2, (uint64_t)a.E * kRows, a.K * 2, 128, kRows, true);
   if (st != Q4_OK) return st;
-  st = make_tmap_3d(&tw, sizeof(W) == 4 ? Q4_F32 : Q4_BF16, a.dw, a.K, a.N, a.E, a.K, a.N * a.K, 128 / sizeof(W), 32,
+  st = make_tmap_3d(&tw, sizeof(W) == 4 ? Q4_F32 : Q4_BF16, dw, a.K, a.N, (uint64_t)splits * a.E, a.K, a.N * a.K, 128 / sizeof(W), 32,
                     1, true);
   if (st != Q4_OK) return st;
 
@@ -536,7 +593,22 @@ q4_status launch_typed(const WgradArgs& a, cudaStream_t stream) {
 }  // namespace
 
 q4_status launch_wgrad(const WgradArgs& a, cudaStream_t stream) {
-  return a.w_dtype == Q4_F32 ? launch_typed<float>(a, stream) : launch_typed<__nv_bfloat16>(a, stream);
+  const int splits = split_count(a.R, a.N, a.K, a.E);
+  if (splits == 1)
+    return a.w_dtype == Q4_F32 ? launch_typed(a, static_cast<float*>(a.dw), 1, stream)
+                               : launch_typed(a, static_cast<__nv_bfloat16*>(a.dw), 1, stream);
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  float* parts = reinterpret_cast<float*>(ws + align256((size_t)a.R * a.K * 2) + align256((size_t)a.E * kRows * a.K * 2) +
+                                          align256((size_t)a.E * kRows * a.N * 2));
+  q4_status st = launch_typed(a, parts, splits, stream);
+  if (st != Q4_OK) return st;
+  const int64_t n4 = a.E * a.N * a.K / 4;
+  const unsigned grid = (unsigned)ceil_div(n4, kJoinThreads);
+  if (a.w_dtype == Q4_F32)
+    return launch_pdl(wgrad_join_kernel<float>, grid, kJoinThreads, 0, stream, reinterpret_cast<const float4*>(parts),
+                      splits, n4, (int)a.accumulate, static_cast<float*>(a.dw));
+  return launch_pdl(wgrad_join_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, stream,
+                    reinterpret_cast<const float4*>(parts), splits, n4, 0, static_cast<__nv_bfloat16*>(a.dw));
 }
 
 }  // namespace q4

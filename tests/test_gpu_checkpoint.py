@@ -224,6 +224,68 @@ def test_wgrad_of_scales_that_are_no_powers_of_two(lib):
     _near(got, want, 90 * 2.0 ** -23 * size)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sizes", [[6000], [5000, 0, 2900], [1, 9000]])
+def test_wgrad_few_outputs_of_many_rows(lib, dtype, sizes):
+    """Rows split over the GPU and joined (float64 on the GPU)."""
+    g = torch.Generator("cuda").manual_seed(len(sizes))
+    N, K, E = 264, 272, len(sizes)
+    offsets, R = _groups(sizes, tail=3)
+    codes, scales = lib.quantize_fp8_checkpoint(torch.randn((700, K), device="cuda", generator=g))
+    token = torch.randint(0, 700, (R,), device="cuda", generator=g, dtype=torch.int32)
+    d = torch.randn((R, N), device="cuda", generator=g).bfloat16()
+    off = torch.from_numpy(offsets).cuda()
+    x = codes.view(torch.float8_e4m3fn).double() * scales.double().repeat_interleave(128, 1)[:, :K]
+    start = torch.randn((E, N, K), device="cuda", generator=g)
+    added = lib.grouped_wgrad_fp8(d, codes, scales, off, row_token=token, out=start.clone(), accumulate=True)
+    got = lib.grouped_wgrad_fp8(d, codes, scales, off, row_token=token, out_dtype=dtype)
+    assert torch.equal(got, lib.grouped_wgrad_fp8(d, codes, scales, off, row_token=token, out_dtype=dtype))
+    for e in range(E):
+        dd, xx = d[offsets[e]:offsets[e + 1]].double(), x[token[offsets[e]:offsets[e + 1]].long()]
+        want, size = dd.t() @ xx, dd.abs().t() @ xx.abs()
+        bound = (sizes[e] + 64) * 2.0 ** -23 * size
+        assert bool(((got[e].double() - want).abs() <= bound + U[dtype] * want.abs()).all())
+        want = want + start[e].double()
+        bound = bound + 2.0 ** -23 * start[e].double().abs()
+        assert bool(((added[e].double() - want).abs() <= bound + U[torch.float32] * want.abs()).all())
+    assert lib.sync_status() == 0
+
+
+def test_offsets_beyond_32_bits(lib):
+    """More than 2^31 elements in the rows, the checkpoint and the gradient."""
+    T, k, H = 40000, 8, 7168
+    x = torch.randn((T, H), device="cuda").bfloat16()
+    ids = torch.arange(T * k, device="cuda", dtype=torch.int32).reshape(T, k) % 97
+    _, token, slot = lib.moe_sort_tokens(ids, 97)
+    rows = lib.moe_dispatch(x, slot)
+    assert rows.numel() > 2 ** 31
+    assert torch.equal(rows[-1000:], x[token[-1000:].long()])
+    back = lib.moe_combine(rows, slot, torch.full((T, k), 0.125, device="cuda"))
+    assert torch.equal(back, x)
+    d_rows, dw = lib.moe_combine_backward(x, rows, slot, torch.ones((T, k), device="cuda"), out=rows)
+    assert torch.equal(d_rows[-1000:], x[token[-1000:].long()])
+    want = x[-100:].double().square().sum(1, keepdim=True).expand(100, k)
+    assert bool(((dw[-100:].double() - want).abs() <= 100 * 2.0 ** -24 * want).all())
+    codes, scales = lib.quantize_fp8_checkpoint(rows)
+    tail = moe.quantize_fp8_checkpoint(rows[-3:].float().cpu().numpy())
+    assert np.array_equal(codes[-3:].cpu().numpy(), tail[0]) and np.array_equal(scales[-3:].cpu().numpy(), tail[1])
+    del rows, d_rows, back
+    h, c2, s2 = lib.swiglu_fp8(x.reshape(-1, 2 * 3584).repeat(8, 1))
+    assert c2.numel() > 2 ** 31 and torch.equal(h[-40000:], h[:40000])
+    g = lib.swiglu_fp8_backward(h, c2, s2)
+    assert torch.equal(g[-40000:], g[:40000])
+    del h, c2, s2, g
+    E, N, K = 160, 2048, 7168
+    off = torch.arange(E + 1, device="cuda", dtype=torch.int32) * 3
+    d = torch.randn((3 * E, N), device="cuda").bfloat16()
+    dw = lib.grouped_wgrad_fp8(d, codes[:3 * E].contiguous(), scales[:3 * E].contiguous(), off, out_dtype=torch.bfloat16)
+    assert dw.numel() > 2 ** 31
+    xx = moe.restore_fp8_checkpoint(codes[3 * E - 3:3 * E].cpu().numpy(), scales[3 * E - 3:3 * E].cpu().numpy())
+    want = d[-3:].double().cpu().numpy().T @ xx
+    size = np.abs(d[-3:].double().cpu().numpy()).T @ np.abs(xx)
+    _near(dw[-1], want, 3 * 2.0 ** -23 * size, torch.bfloat16)
+
+
 def test_wgrad_large_groups(lib):
     """More tiles than SMs, groups of hundreds of rows, gathered tokens (float64 on the GPU)."""
     g = torch.Generator("cuda").manual_seed(4)
