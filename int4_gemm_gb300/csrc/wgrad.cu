@@ -19,9 +19,10 @@
 //   warps 2..9  epilogue: TMEM through 128-byte swizzled rows in shared memory
 //            to dW by TMA stores (adds, when accumulating), clipped at the
 //            edges of the expert's matrix.
-// 64 experts of 2048 x 7168, bf16 dW, the restoring included: 732 us with 512
-// rows each (1313 TFLOP/s; 645 without the stores), 762 us with 27 to 1933; 2
-// experts of 16384 rows, where few outputs are written: 570 us (1688).
+// 64 experts of 2048 x 7168, bf16 dW, the restoring (about 90 us) included: 726
+// us with 512 rows each (1326 TFLOP/s), 756 us with 27 to 1933; 2 experts of
+// 16384 rows, where few outputs are written: 551 us (1747).  Between the two
+// stand the stores: without them the first takes 645 us.
 // Measured and not kept, same sizes: restoring once per token and gathering
 // rows in the producer (four-row TMA gathers, 32 per stage), 2453 us; codes
 // converted on their way into the stage by eight or sixteen more warps, 1636
@@ -42,7 +43,7 @@ namespace {
 constexpr int kRestoreThreads = 256;
 
 constexpr int kRows = 64;         // rows r per stage of the GEMM
-constexpr int kRestoreRows = 4;   // rows of a thread whose loads are in flight together
+constexpr int kRestoreUnits = 4;  // groups of 8 columns of a thread, whose loads are in flight together
 
 // 8 codes (two words) as bf16(code * s).
 __device__ __forceinline__ uint4 restore8(uint2 c, float s) {
@@ -78,53 +79,59 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int64_t R, i
   rows = hi > lo ? (int)(hi - lo) : 0;
 }
 
-// Thread: 8 columns; block y: kRestoreRows rows, those of every expert first,
-// then each expert's kRows tail rows.
-__global__ void __launch_bounds__(kRestoreThreads)
-    wgrad_restore_kernel(const RestoreArgs a, int64_t main_blocks, int64_t blocks) {
+// Rows (blockIdx.y, threadIdx.y): those of every expert first, then each
+// expert's kRows tail rows.  A thread takes kRestoreUnits groups of 8 columns of it, threads apart,
+// so that finding the row costs little beside the conversions (one group of
+// four rows: 31 us instead of 25 for 8192 rows of 7168).
+__global__ void __launch_bounds__(kRestoreThreads, 8)
+    wgrad_restore_kernel(const RestoreArgs a, int64_t rows_out) {
   pdl_wait();
-  const uint32_t v = blockIdx.x * kRestoreThreads + threadIdx.x;
-  const bool has_x = v < (uint32_t)(a.K / 8), has_y = v < (uint32_t)(a.N / 8);
+  const uint32_t v0 = blockIdx.x * blockDim.x * kRestoreUnits + threadIdx.x;
+  const uint32_t xu = (uint32_t)(a.K / 8), yu = (uint32_t)(a.N / 8);
   const int64_t KB = (a.K + 127) / 128;
-  for (int64_t b = blockIdx.y; b < blocks; b += gridDim.y) {
-    const bool tail = b >= main_blocks;
-    int64_t from = b * kRestoreRows, to = from;  // source row and row written
+  for (int64_t b = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; b < rows_out; b += (int64_t)gridDim.y * blockDim.y) {
+    const bool tail = b >= a.R;
+    int64_t from = b, to = b;  // source row and row written
     int64_t end = min((int64_t)__ldg(a.offsets + a.E), a.R);
     if (tail) {
-      to = (b - main_blocks) * kRestoreRows;
+      to = b - a.R;
       int64_t lo;
       int rows;
       expert_rows(a.offsets, a.R, (int)(to / kRows), lo, rows);
-      if (rows % kRows == 0) continue;  // no tail (the same for the whole block)
+      if (rows % kRows == 0) continue;  // no tail
       from = lo + rows / kRows * kRows + to % kRows;
       end = lo + rows;
+    } else if (from >= end) {
+      continue;
     }
-    if (has_x) {
-      uint2 c[kRestoreRows];
-      float s[kRestoreRows];
+    const bool have = from < end;
+    int64_t t = 0;
+    if (have) t = a.row_token ? min(max((int64_t)__ldg(a.row_token + from), (int64_t)0), a.tokens - 1) : from;
+    const uint2* src = reinterpret_cast<const uint2*>(a.codes + t * a.K);
+    const float* scale = a.scales + t * KB;
+    uint4* dst = reinterpret_cast<uint4*>((tail ? a.x_tail : a.x) + to * a.K);
+    uint2 c[kRestoreUnits];
+    float s[kRestoreUnits];
 #pragma unroll
-      for (int i = 0; i < kRestoreRows; ++i) {
-        c[i] = make_uint2(0u, 0u);
-        s[i] = 0.f;
-        if (from + i >= end) continue;
-        const int64_t r = from + i;
-        const int64_t t = a.row_token ? min(max((int64_t)__ldg(a.row_token + r), (int64_t)0), a.tokens - 1) : r;
-        c[i] = __ldg(reinterpret_cast<const uint2*>(a.codes + t * a.K) + v);
-        s[i] = __ldg(a.scales + t * KB + v / 16);
-      }
-      __nv_bfloat16* x = tail ? a.x_tail : a.x;
-#pragma unroll
-      for (int i = 0; i < kRestoreRows; ++i)
-        if (tail || from + i < end) reinterpret_cast<uint4*>(x + (to + i) * a.K)[v] = restore8(c[i], s[i]);
-    }
-    if (tail && has_y) {
-#pragma unroll
-      for (int i = 0; i < kRestoreRows; ++i) {
-        uint4 d = make_uint4(0u, 0u, 0u, 0u);
-        if (from + i < end) d = __ldg(reinterpret_cast<const uint4*>(a.dy + (from + i) * a.ldy) + v);
-        reinterpret_cast<uint4*>(a.y_tail + (to + i) * a.N)[v] = d;
+    for (int i = 0; i < kRestoreUnits; ++i) {
+      const uint32_t v = v0 + i * blockDim.x;
+      c[i] = make_uint2(0u, 0u);
+      s[i] = 0.f;
+      if (have && v < xu) {
+        c[i] = __ldg(src + v);
+        s[i] = __ldg(scale + v / 16);
       }
     }
+#pragma unroll
+    for (int i = 0; i < kRestoreUnits; ++i) {
+      const uint32_t v = v0 + i * blockDim.x;
+      if (v < xu) dst[v] = restore8(c[i], s[i]);
+    }
+    if (!tail) continue;
+    const uint4* ysrc = reinterpret_cast<const uint4*>(a.dy + from * a.ldy);
+    uint4* ydst = reinterpret_cast<uint4*>(a.y_tail + to * a.N);
+    for (uint32_t v = blockIdx.x * blockDim.x + threadIdx.x; v < yu; v += gridDim.x * blockDim.x)
+      ydst[v] = have ? __ldg(ysrc + v) : make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -579,11 +586,13 @@ q4_status launch_typed(const WgradArgs& a, W* dw, int splits, cudaStream_t strea
     max_pairs[dev] = std::min(n, num_sms() / 2);
   }
 
-  const int64_t gx = ceil_div(std::max(a.K, a.N) / 8, kRestoreThreads);
-  const int64_t main_blocks = ceil_div(a.R, kRestoreRows);
-  const int64_t blocks = main_blocks + (int64_t)a.E * (kRows / kRestoreRows);
-  st = launch_pdl(wgrad_restore_kernel, dim3((unsigned)gx, (unsigned)std::min<int64_t>(blocks, 65535)),
-                  kRestoreThreads, 0, stream, r, main_blocks, blocks);
+  const int64_t rows_out = a.R + (int64_t)a.E * kRows, units = a.K / 8;
+  const int64_t per_row = std::min<int64_t>(kRestoreThreads, ceil_div(ceil_div(units, kRestoreUnits), 32) * 32);
+  const int64_t rows_per = kRestoreThreads / per_row;
+  st = launch_pdl(wgrad_restore_kernel,
+                  dim3((unsigned)ceil_div(units, per_row * kRestoreUnits),
+                       (unsigned)std::min<int64_t>(ceil_div(rows_out, rows_per), 65535)),
+                  dim3((unsigned)per_row, (unsigned)rows_per), 0, stream, r, rows_out);
   if (st != Q4_OK) return st;
   cfg.gridDim = dim3(2u * (unsigned)std::min(p.tiles, max_pairs[dev]), 1, 1);
   Q4_CUDA_TRY(cudaLaunchKernelEx(&cfg, wgrad_pair_kernel<W>, ty, tx, yt, xt, tw, p));
