@@ -404,6 +404,7 @@ __global__ void __launch_bounds__(kClusterThreads)
   __syncthreads();
   for (int e = threadIdx.x; e < nb; e += blockDim.x) {
     int sum = 0;
+#pragma unroll 8
     for (int w = 0; w < warps; ++w) sum += cnt[w * nb + e];
     own[e] = sum;
   }
@@ -440,10 +441,15 @@ __global__ void __launch_bounds__(kClusterThreads)
       const int first = prefix + x - total;
       if (rank == 0) offsets[e] = first;
       int at = first + before;
-      for (int w = 0; w < warps; ++w) {
-        const int c = cnt[w * nb + e];
-        cnt[w * nb + e] = at;
-        at += c;
+      for (int w0 = 0; w0 < warps; w0 += 8) {  // eight loads in flight
+        int c[8];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) c[w] = w0 + w < warps ? cnt[(w0 + w) * nb + e] : 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          if (w0 + w < warps) cnt[(w0 + w) * nb + e] = at;
+          at += c[w];
+        }
       }
     }
     carry += all;
@@ -757,7 +763,7 @@ constexpr int64_t kClusterSortSlots = 16384;
 ClusterSort cluster_sort(int64_t S, int E) {
   ClusterSort c;
   const int64_t room = (int64_t)(kClusterSortSmem / 4) / (E + 1) - 1;
-  const int64_t want = ceil_div(S, 128);  // warps of at least four turns
+  const int64_t want = ceil_div(S, 32);
   c.warps = (int)std::max<int64_t>(1, std::min<int64_t>({kClusterWarps, room, want}));
   c.blocks = 1;
   while (c.blocks < kMaxCluster && (int64_t)c.blocks * c.warps < want) c.blocks *= 2;
