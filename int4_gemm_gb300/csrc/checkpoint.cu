@@ -88,8 +88,9 @@ __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f +
 // are in flight either way (one chunk of bf16: swiglu_fp8 94 us instead of 79
 // at 32768 x 2 x 2048).  Otherwise lane l of a warp holds columns l, l + 32, ...
 // one by one (a path without tests for whole blocks took longer, 33 us instead
-// of 27 for the gradient at 9973 x 1411).  Columns past the block's end are zero; 16-bit elements stay
-// packed in the words they were loaded as until they are used.
+// of 27 for the gradient at 9973 x 1411).  Columns past the block's end are
+// zero; 16-bit elements of chunks stay packed in the words they were loaded as
+// until they are used.
 template <typename T, bool kVec>
 struct Held {
   static constexpr int lanes = !kVec ? 32 : sizeof(T) == 2 ? 8 : 16, n = 128 / lanes;

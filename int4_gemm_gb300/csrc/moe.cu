@@ -14,6 +14,8 @@
 //   combine   out[t] = sum_j w_tj rows[row(t, j)]   (dropped slots left out)
 //   gradient  d_rows[row(t, j)] = w_tj d_out[t],  dw_tj = <d_out[t], rows[row(t, j)]>
 #include <algorithm>
+#include <initializer_list>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -473,10 +475,13 @@ __global__ void __launch_bounds__(kClusterThreads)
 }
 
 // ------------------------------------------------------------------ dispatch / combine
-// A row is cut into units: 16 bytes where the width, pitches and addresses
-// allow it, single elements otherwise.  A unit stays the four words that it was
-// loaded as: an array of 16-bit elements takes a register for each of them
-// (107 registers instead of 64 in combine_backward_kernel, and half its rate).
+// A row is cut into units of kBytes: 16 where the width, pitches and addresses
+// allow it, else 4 (two 16-bit elements), else single elements.  A unit stays
+// the words that it was loaded as: an array of 16-bit elements takes a register
+// for each of them (107 registers instead of 64 in combine_backward_kernel, and
+// half its rate), and loads into half a register wait for one another (single
+// bf16 elements, 2048 x 4097, top-8: combine 49 us instead of 85, its gradient
+// 89 instead of 286; in units of 4 bytes at 4098: 36 and 60).
 template <typename T>
 __device__ __forceinline__ float2 unpack(uint32_t w);
 template <>
@@ -500,41 +505,50 @@ __device__ __forceinline__ uint32_t pack<__half>(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-template <typename T, bool kVec>
+template <typename T, int kBytes>
 struct Unit {
-  static constexpr int n = kVec ? 16 / (int)sizeof(T) : 1;
-  uint32_t w[kVec ? 4 : 1];  // a single 16-bit element is kept as the float it stands for
+  static constexpr int n = kBytes / (int)sizeof(T), words = kBytes < 4 ? 1 : kBytes / 4;
+  static constexpr bool packed = sizeof(T) == 2 && kBytes >= 4;
+  uint32_t w[words];  // a single 16-bit element: in the low half, the high one zero
 
   __device__ __forceinline__ void load(const T* p) {
-    if constexpr (kVec) {
+    if constexpr (kBytes == 16) {
       const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
       w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (kBytes == 4) {
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
     } else {
-      w[0] = __float_as_uint(Elem<T>::to_f(p[0]));
+      w[0] = __ldg(reinterpret_cast<const unsigned short*>(p));
     }
   }
   __device__ __forceinline__ void store(T* p) const {
-    if constexpr (kVec)
+    if constexpr (kBytes == 16)
       *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (kBytes == 4)
+      *reinterpret_cast<uint32_t*>(p) = w[0];
     else
-      p[0] = from_f<T>(__uint_as_float(w[0]));
+      *reinterpret_cast<unsigned short*>(p) = (unsigned short)w[0];
   }
   __device__ __forceinline__ void floats(float (&f)[n]) const {
-    if constexpr (kVec && sizeof(T) == 2) {
+    if constexpr (packed) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < words; ++i) {
         const float2 v = unpack<T>(w[i]);
         f[2 * i] = v.x, f[2 * i + 1] = v.y;
       }
+    } else if constexpr (sizeof(T) == 2) {
+      f[0] = unpack<T>(w[0]).x;
     } else {
 #pragma unroll
       for (int i = 0; i < n; ++i) f[i] = __uint_as_float(w[i]);
     }
   }
   __device__ __forceinline__ void round(const float (&f)[n]) {
-    if constexpr (kVec && sizeof(T) == 2) {
+    if constexpr (packed) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = pack<T>(f[2 * i], f[2 * i + 1]);
+      for (int i = 0; i < words; ++i) w[i] = pack<T>(f[2 * i], f[2 * i + 1]);
+    } else if constexpr (sizeof(T) == 2) {
+      w[0] = pack<T>(f[0], 0.f);
     } else {
 #pragma unroll
       for (int i = 0; i < n; ++i) w[i] = __float_as_uint(f[i]);
@@ -542,21 +556,21 @@ struct Unit {
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < (kVec ? 4 : 1); ++i) w[i] = 0u;
+    for (int i = 0; i < words; ++i) w[i] = 0u;
   }
 };
 
 // blockIdx.x: token; the units of its row are spread over blockIdx.y.
-template <typename T, bool kVec>
+template <typename T, int kBytes>
 __global__ void __launch_bounds__(256)
     dispatch_kernel(const T* __restrict__ x, int64_t ldx, int64_t H, const int32_t* __restrict__ slot_row,
                     int top_k, uint32_t S, T* __restrict__ rows) {
   pdl_wait();
-  constexpr int n = Unit<T, kVec>::n;
+  constexpr int n = Unit<T, kBytes>::n;
   const int64_t t = blockIdx.x, units = H / n;
   const int32_t* slots = slot_row + t * top_k;
   for (int64_t u = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; u < units; u += (int64_t)gridDim.y * blockDim.x) {
-    Unit<T, kVec> v, none;
+    Unit<T, kBytes> v, none;
     v.load(x + t * ldx + u * n);
     none.zero();
     for (int j = 0; j < top_k; ++j) {
@@ -571,12 +585,12 @@ __global__ void __launch_bounds__(256)
 // in groups of kJ whose loads are all in flight before the first is used.
 // 4096 x 7168 bf16, top-8: 83 us (6.4 TB/s; kJ = 8: 88 us); 3001 x 2047 f32,
 // top-4, single elements: 21.4 us (one unit and one slot at a time: 53.7 us).
-template <typename T, bool kVec, int kU, int kJ>
+template <typename T, int kBytes, int kU, int kJ>
 __global__ void __launch_bounds__(256)
     combine_kernel(const T* __restrict__ rows, int64_t ld, int64_t H, const int32_t* __restrict__ slot_row,
                    const float* __restrict__ weights, int top_k, uint32_t S, T* __restrict__ out) {
   pdl_wait();
-  constexpr int n = Unit<T, kVec>::n;
+  constexpr int n = Unit<T, kBytes>::n;
   const int64_t t = blockIdx.x, units = H / n;
   for (int64_t u0 = (int64_t)blockIdx.y * blockDim.x * kU + threadIdx.x; u0 - threadIdx.x < units;
        u0 += (int64_t)gridDim.y * blockDim.x * kU) {
@@ -595,7 +609,7 @@ __global__ void __launch_bounds__(256)
         row[j] = live ? rows + (int64_t)s * ld : nullptr;
         w[j] = live && weights ? __ldg(weights + t * top_k + j0 + j) : 1.f;
       }
-      Unit<T, kVec> v[kU][kJ];
+      Unit<T, kBytes> v[kU][kJ];
 #pragma unroll
       for (int a = 0; a < kU; ++a)
 #pragma unroll
@@ -618,7 +632,7 @@ __global__ void __launch_bounds__(256)
     for (int a = 0; a < kU; ++a) {
       const int64_t u = u0 + (int64_t)a * blockDim.x;
       if (u >= units) continue;
-      Unit<T, kVec> o;
+      Unit<T, kBytes> o;
       o.round(acc[a]);
       o.store(out + t * H + u * n);
     }
@@ -628,18 +642,18 @@ __global__ void __launch_bounds__(256)
 constexpr int kGradThreads = 256;
 
 // One warp per slot: the slot's row is read once, w d_out[t] written once, and
-// the dot product stays in the warp's registers until the end of the row; no
-// barrier, kU loads of the row in flight per lane.  The token's other slots
+// the dot product stays in the warp's registers, as 32 kU partial sums, until
+// the end of the row; no barrier, kU loads of the row in flight per lane.  The token's other slots
 // are the neighbouring warps', so d_out[t] comes from L1 for all but one.
 // 4096 x 7168 bf16, top-8: 149 us (6.7 TB/s, the copy rate; one block per
 // token: 182 to 207 us).
-template <typename T, bool kVec, int kU>
+template <typename T, int kBytes, int kU>
 __global__ void __launch_bounds__(kGradThreads)
     combine_backward_kernel(const T* __restrict__ d_out, int64_t ldd, const T* __restrict__ rows, int64_t ld,
                             int64_t H, const int32_t* __restrict__ slot_row, const float* __restrict__ weights,
                             int top_k, uint32_t S, T* __restrict__ d_rows, float* __restrict__ d_weights) {
   pdl_wait();
-  constexpr int n = Unit<T, kVec>::n;
+  constexpr int n = Unit<T, kBytes>::n;
   const uint32_t slot = blockIdx.x * (kGradThreads / 32) + (threadIdx.x >> 5);
   if (slot >= S) return;
   const int lane = threadIdx.x & 31;
@@ -649,10 +663,12 @@ __global__ void __launch_bounds__(kGradThreads)
   const bool live = s >= 0 && row < S, read = live && d_weights;
   const float w = live ? __ldg(weights + slot) : 0.f;
   const T* d_row = d_out + (int64_t)(slot / top_k) * ldd;
-  float dot = 0.f;
+  float part[kU];
+#pragma unroll
+  for (int a = 0; a < kU; ++a) part[a] = 0.f;
   if (row < S) {
     for (int64_t u0 = lane; u0 - lane < units; u0 += 32 * kU) {
-      Unit<T, kVec> d[kU], y[kU];
+      Unit<T, kBytes> d[kU], y[kU];
 #pragma unroll
       for (int a = 0; a < kU; ++a) {
         const int64_t u = u0 + 32 * a;
@@ -674,7 +690,7 @@ __global__ void __launch_bounds__(kGradThreads)
             float g[n];
             y[a].floats(g);
 #pragma unroll
-            for (int i = 0; i < n; ++i) dot = fmaf(f[i], g[i], dot);
+            for (int i = 0; i < n; ++i) part[a] = fmaf(f[i], g[i], part[a]);
           }
 #pragma unroll
           for (int i = 0; i < n; ++i) f[i] *= w;
@@ -687,6 +703,9 @@ __global__ void __launch_bounds__(kGradThreads)
     }
   }
   if (d_weights) {
+    float dot = 0.f;
+#pragma unroll
+    for (int a = 0; a < kU; ++a) dot += part[a];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
     if (lane == 0) d_weights[slot] = dot;
@@ -701,8 +720,24 @@ q4_status by_dtype(int dtype, F&& f) {
   return f(__half());
 }
 
-inline bool vec16(const void* p, int64_t pitch, size_t elem) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (pitch * elem) % 16 == 0;
+// The unit that every row of these matrices can be cut into: their addresses
+// and row pitches, and the width H, are multiples of it.
+struct Matrix {
+  const void* p;
+  int64_t pitch;
+};
+template <typename T>
+int unit_bytes(int64_t H, std::initializer_list<Matrix> all) {
+  uintptr_t bits = (uintptr_t)(H * sizeof(T));
+  for (const Matrix& m : all) bits |= reinterpret_cast<uintptr_t>(m.p) | (uintptr_t)(m.pitch * sizeof(T));
+  return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : (int)sizeof(T);
+}
+// f with the unit's size as a constant.
+template <typename T, typename F>
+q4_status by_unit(int bytes, F&& f) {
+  if (bytes == 16) return f(std::integral_constant<int, 16>());
+  if (bytes == 4) return f(std::integral_constant<int, 4>());
+  return f(std::integral_constant<int, (int)sizeof(T)>());
 }
 
 // Threads and y blocks for one row of `units` per token: enough blocks to
@@ -829,12 +864,13 @@ q4_status launch_dispatch(const void* x, int dtype, int64_t tokens, int64_t H, i
                           int top_k, void* rows, cudaStream_t stream) {
   return by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
-    const bool vec = vec16(x, ldx, sizeof(T)) && vec16(rows, H, sizeof(T));
-    dim3 grid, block;
-    row_grid(tokens, vec ? H * (int64_t)sizeof(T) / 16 : H, grid, block);
-    return launch_pdl(vec ? dispatch_kernel<T, true> : dispatch_kernel<T, false>, grid, block, 0, stream,
-                      static_cast<const T*>(x), ldx, H, slot_row, top_k, (uint32_t)(tokens * top_k),
-                      static_cast<T*>(rows));
+    return by_unit<T>(unit_bytes<T>(H, {{x, ldx}, {rows, H}}), [&](auto bytes) {
+      constexpr int B = decltype(bytes)::value;
+      dim3 grid, block;
+      row_grid(tokens, H * (int64_t)sizeof(T) / B, grid, block);
+      return launch_pdl(dispatch_kernel<T, B>, grid, block, 0, stream, static_cast<const T*>(x), ldx, H, slot_row,
+                        top_k, (uint32_t)(tokens * top_k), static_cast<T*>(rows));
+    });
   });
 }
 
@@ -842,14 +878,15 @@ q4_status launch_combine(const void* rows, int dtype, int64_t tokens, int64_t H,
                          const float* weights, int top_k, void* out, cudaStream_t stream) {
   return by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
-    const bool vec = vec16(rows, ld, sizeof(T)) && vec16(out, H, sizeof(T));
-    const int64_t units = vec ? H * (int64_t)sizeof(T) / 16 : H;
-    const int64_t per = vec ? 1 : 4;  // units per thread
-    const int64_t threads = std::min<int64_t>(256, ceil_div(ceil_div(units, per), 32) * 32);
-    const dim3 grid((unsigned)tokens, (unsigned)std::min<int64_t>(65535, ceil_div(units, threads * per)));
-    return launch_pdl(vec ? combine_kernel<T, true, 1, 4> : combine_kernel<T, false, 4, 4>, grid, dim3(threads), 0,
-                      stream, static_cast<const T*>(rows), ld, H, slot_row, weights, top_k,
-                      (uint32_t)(tokens * top_k), static_cast<T*>(out));
+    return by_unit<T>(unit_bytes<T>(H, {{rows, ld}, {out, H}}), [&](auto bytes) {
+      constexpr int B = decltype(bytes)::value, per = B == 16 ? 1 : 4;  // units per thread
+      const int64_t units = H * (int64_t)sizeof(T) / B;
+      const int64_t threads = std::min<int64_t>(256, ceil_div(ceil_div(units, per), 32) * 32);
+      const dim3 grid((unsigned)tokens, (unsigned)std::min<int64_t>(65535, ceil_div(units, threads * per)));
+      return launch_pdl(combine_kernel<T, B, per, 4>, grid, dim3((unsigned)threads), 0, stream,
+                        static_cast<const T*>(rows), ld, H, slot_row, weights, top_k, (uint32_t)(tokens * top_k),
+                        static_cast<T*>(out));
+    });
   });
 }
 
@@ -858,13 +895,14 @@ q4_status launch_combine_backward(const void* d_out, int dtype, int64_t tokens, 
                                   int top_k, void* d_rows, float* d_weights, cudaStream_t stream) {
   return by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
-    const bool vec = vec16(d_out, ldd, sizeof(T)) && vec16(d_rows, H, sizeof(T)) &&
-                     (!d_weights || vec16(rows, ld, sizeof(T)));
-    const uint32_t S = (uint32_t)(tokens * top_k);
-    return launch_pdl(vec ? combine_backward_kernel<T, true, 4> : combine_backward_kernel<T, false, 8>,
-                      (unsigned)ceil_div(S, kGradThreads / 32), kGradThreads, 0, stream, static_cast<const T*>(d_out),
-                      ldd, static_cast<const T*>(rows), ld, H, slot_row, weights, top_k, S, static_cast<T*>(d_rows),
-                      d_weights);
+    const Matrix read = d_weights ? Matrix{rows, ld} : Matrix{d_out, ldd};
+    return by_unit<T>(unit_bytes<T>(H, {{d_out, ldd}, {d_rows, H}, read}), [&](auto bytes) {
+      constexpr int B = decltype(bytes)::value;
+      const uint32_t S = (uint32_t)(tokens * top_k);
+      return launch_pdl(combine_backward_kernel<T, B, B == 16 ? 4 : 8>, (unsigned)ceil_div(S, kGradThreads / 32),
+                        kGradThreads, 0, stream, static_cast<const T*>(d_out), ldd, static_cast<const T*>(rows), ld,
+                        H, slot_row, weights, top_k, S, static_cast<T*>(d_rows), d_weights);
+    });
   });
 }
 
