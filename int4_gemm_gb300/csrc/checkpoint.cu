@@ -86,14 +86,17 @@ __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f +
 // 128-bit accesses (kVec) a lane holds chunks of 8 columns, lanes * 8 apart: one
 // chunk of FP32 (16 lanes), two of 16-bit elements (8 lanes), so that two loads
 // are in flight either way (one chunk of bf16: swiglu_fp8 94 us instead of 79
-// at 32768 x 2 x 2048).  Otherwise lane l of a warp holds columns l, l + 32, ...
-// one by one (a path without tests for whole blocks took longer, 33 us instead
-// of 27 for the gradient at 9973 x 1411).  Columns past the block's end are
-// zero; 16-bit elements of chunks stay packed in the words they were loaded as
-// until they are used.
-template <typename T, bool kVec>
+// at 32768 x 2 x 2048).  Otherwise lane l of kSingle holds columns l, l +
+// kSingle, ... one by one, 16-bit elements by way of whole registers (loads into
+// half a register wait for one another); sixteen lanes suit the kernels that
+// reduce over the block (quantize_fp8_checkpoint of 9973 x 2822 bf16: 22 us
+// instead of 32 with a warp), a warp the gradient (27 us instead of 30 at 9973 x
+// 1411; with a path without tests for whole blocks 30).  Columns past the
+// block's end are zero; 16-bit elements of chunks stay packed in the words they
+// were loaded as until they are used.
+template <typename T, bool kVec, int kSingle>
 struct Held {
-  static constexpr int lanes = !kVec ? 32 : sizeof(T) == 2 ? 8 : 16, n = 128 / lanes;
+  static constexpr int lanes = !kVec ? kSingle : sizeof(T) == 2 ? 8 : 16, n = 128 / lanes;
   static constexpr int chunks = kVec ? n / 8 : 1;
   static_assert(chunks * lanes * 8 == 128 || !kVec, "a block");
   static constexpr bool packed = kVec && sizeof(T) == 2;
@@ -113,7 +116,13 @@ struct Held {
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < n; ++i) w[i] = l + lanes * i < cols ? __float_as_uint(Elem<T>::to_f(p[l + lanes * i])) : 0u;
+      for (int i = 0; i < n; ++i) {
+        const int at = l + lanes * i;
+        if constexpr (sizeof(T) == 2)
+          w[i] = at < cols ? __ldg(reinterpret_cast<const unsigned short*>(p) + at) : 0u;
+        else
+          w[i] = at < cols ? __float_as_uint(__ldg(p + at)) : 0u;
+      }
     }
   }
   __device__ __forceinline__ void floats(float (&f)[n]) const {
@@ -123,6 +132,9 @@ struct Held {
         const float2 v = unpack2<T>(w[i]);
         f[2 * i] = v.x, f[2 * i + 1] = v.y;
       }
+    } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < n; ++i) f[i] = unpack2<T>(w[i]).x;
     } else {
 #pragma unroll
       for (int i = 0; i < n; ++i) f[i] = __uint_as_float(w[i]);
@@ -140,86 +152,87 @@ struct Held {
       const float2 v = unpack2<T>(top);  // NaN compares false, so it is kept if either half has it
       return __float_as_uint(v.x) > __float_as_uint(v.y) ? v.x : v.y;
     } else {
+      constexpr uint32_t kMagnitude = sizeof(T) == 2 ? 0x7fffu : 0x7fffffffu;
 #pragma unroll
-      for (int i = 0; i < words; ++i) top = max(top, w[i] & 0x7fffffffu);
+      for (int i = 0; i < words; ++i) top = max(top, w[i] & kMagnitude);
 #pragma unroll
       for (int o = lanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      return __uint_as_float(top);
+      if constexpr (sizeof(T) == 2)
+        return unpack2<T>(top).x;
+      else
+        return __uint_as_float(top);
+    }
+  }
+
+  static __device__ __forceinline__ void store(T* __restrict__ p, int l, int cols, const float (&v)[n]) {
+    if constexpr (kVec) {
+#pragma unroll
+      for (int c = 0; c < chunks; ++c) {
+        const int at = chunk(l, c);
+        if (at >= cols) continue;
+        uint4* out = reinterpret_cast<uint4*>(p + at);
+        const float* f = v + 8 * c;
+        if constexpr (sizeof(T) == 4) {
+          out[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+          out[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+        } else {
+          out[0] = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < n; ++i)
+        if (l + lanes * i < cols) p[l + lanes * i] = to_elem<T>(v[i]);
+    }
+  }
+
+  // Codes of the held columns f under the scale 2^e.
+  static __device__ __forceinline__ void encode(uint8_t* __restrict__ codes, int l, int cols, const float (&f)[n], int e) {
+    const float inv = pow2f(-e);
+    uint32_t w[n / 4];
+#pragma unroll
+    for (int i = 0; i < n / 4; ++i)
+      w[i] = e4m3x2(f[4 * i] * inv, f[4 * i + 1] * inv) | e4m3x2(f[4 * i + 2] * inv, f[4 * i + 3] * inv) << 16;
+    if constexpr (kVec) {
+#pragma unroll
+      for (int c = 0; c < chunks; ++c)
+        if (chunk(l, c) < cols) *reinterpret_cast<uint2*>(codes + chunk(l, c)) = make_uint2(w[2 * c], w[2 * c + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < n; ++i)
+        if (l + lanes * i < cols) codes[l + lanes * i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+    }
+  }
+
+  static __device__ __forceinline__ void load_codes(const uint8_t* __restrict__ codes, int l, int cols, uint32_t (&w)[n / 4]) {
+    if constexpr (kVec) {
+#pragma unroll
+      for (int c = 0; c < chunks; ++c) {
+        const int at = chunk(l, c);
+        const uint2 v = at < cols ? __ldg(reinterpret_cast<const uint2*>(codes + at)) : make_uint2(0u, 0u);
+        w[2 * c] = v.x, w[2 * c + 1] = v.y;
+      }
+    } else {
+      uint32_t c[n];
+#pragma unroll
+      for (int i = 0; i < n; ++i) c[i] = l + lanes * i < cols ? __ldg(codes + l + lanes * i) : 0u;
+#pragma unroll
+      for (int i = 0; i < n / 4; ++i) w[i] = c[4 * i] | c[4 * i + 1] << 8 | c[4 * i + 2] << 16 | c[4 * i + 3] << 24;
+    }
+  }
+
+  static __device__ __forceinline__ void decode(const uint32_t (&w)[n / 4], float scale, float (&v)[n]) {
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float2 f = e4m3x2_values(w[i / 2] >> (16 * (i & 1)));
+      v[2 * i] = f.x * scale;
+      v[2 * i + 1] = f.y * scale;
     }
   }
 };
 
-template <typename T, bool kVec, int n>
-__device__ __forceinline__ void store_block(T* __restrict__ p, int l, int cols, const float (&v)[n]) {
-  using H = Held<T, kVec>;
-  if constexpr (kVec) {
-#pragma unroll
-    for (int c = 0; c < H::chunks; ++c) {
-      const int at = H::chunk(l, c);
-      if (at >= cols) continue;
-      uint4* out = reinterpret_cast<uint4*>(p + at);
-      const float* f = v + 8 * c;
-      if constexpr (sizeof(T) == 4) {
-        out[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-        out[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
-      } else {
-        out[0] = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < n; ++i)
-      if (l + 32 * i < cols) p[l + 32 * i] = to_elem<T>(v[i]);
-  }
-}
-
-// Codes of the held columns f under the scale 2^e.
-template <typename T, bool kVec, int n>
-__device__ __forceinline__ void encode_block(uint8_t* __restrict__ codes, int l, int cols, const float (&f)[n], int e) {
-  using H = Held<T, kVec>;
-  const float inv = pow2f(-e);
-  uint32_t w[n / 4];
-#pragma unroll
-  for (int i = 0; i < n / 4; ++i)
-    w[i] = e4m3x2(f[4 * i] * inv, f[4 * i + 1] * inv) | e4m3x2(f[4 * i + 2] * inv, f[4 * i + 3] * inv) << 16;
-  if constexpr (kVec) {
-#pragma unroll
-    for (int c = 0; c < H::chunks; ++c)
-      if (H::chunk(l, c) < cols) *reinterpret_cast<uint2*>(codes + H::chunk(l, c)) = make_uint2(w[2 * c], w[2 * c + 1]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < n; ++i)
-      if (l + 32 * i < cols) codes[l + 32 * i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
-  }
-}
-
-template <typename T, bool kVec, int n>
-__device__ __forceinline__ void load_codes(const uint8_t* __restrict__ codes, int l, int cols, uint32_t (&w)[n / 4]) {
-  using H = Held<T, kVec>;
-  if constexpr (kVec) {
-#pragma unroll
-    for (int c = 0; c < H::chunks; ++c) {
-      const int at = H::chunk(l, c);
-      const uint2 v = at < cols ? __ldg(reinterpret_cast<const uint2*>(codes + at)) : make_uint2(0u, 0u);
-      w[2 * c] = v.x, w[2 * c + 1] = v.y;
-    }
-  } else {
-    uint32_t c[n];
-#pragma unroll
-    for (int i = 0; i < n; ++i) c[i] = l + 32 * i < cols ? codes[l + 32 * i] : 0u;
-#pragma unroll
-    for (int i = 0; i < n / 4; ++i) w[i] = c[4 * i] | c[4 * i + 1] << 8 | c[4 * i + 2] << 16 | c[4 * i + 3] << 24;
-  }
-}
-template <int n>
-__device__ __forceinline__ void decode(const uint32_t (&w)[n / 4], float scale, float (&v)[n]) {
-#pragma unroll
-  for (int i = 0; i < n / 2; ++i) {
-    const float2 f = e4m3x2_values(w[i / 2] >> (16 * (i & 1)));
-    v[2 * i] = f.x * scale;
-    v[2 * i + 1] = f.y * scale;
-  }
-}
+// Lanes per block where columns are taken one by one.
+constexpr int kForwardLanes = 16, kBackwardLanes = 32;
 
 // One block of a matrix with per_row blocks of 128 columns per row and `total`
 // blocks in all (below 2^30, so that 32-bit divisions find it).
@@ -252,7 +265,7 @@ __global__ void __launch_bounds__(kThreads)
     checkpoint_kernel(const T* __restrict__ x, Blocks blk, int64_t K, int64_t ld, uint8_t* __restrict__ codes,
                       float* __restrict__ scales, int* status) {
   pdl_wait();
-  using H = Held<T, kVec>;
+  using H = Held<T, kVec, kForwardLanes>;
   const int l = threadIdx.x & (H::lanes - 1);
   const uint32_t b = own_block<H::lanes>();
   const Block k = block_at(blk, b, K);
@@ -263,7 +276,7 @@ __global__ void __launch_bounds__(kThreads)
   const int e = scale_exponent(top);
   float f[H::n];
   v.floats(f);
-  encode_block<T, kVec>(codes + k.row * K + c, l, k.n, f, e);
+  H::encode(codes + k.row * K + c, l, k.n, f, e);
   if (l == 0 && k.n > 0) {
     scales[b] = pow2f(e);
     if (nonfinite(top)) latch_status(status, Q4_ERR_NONFINITE);
@@ -275,7 +288,7 @@ __global__ void __launch_bounds__(kThreads)
     swiglu_kernel(const T* __restrict__ gate_up, Blocks blk, int64_t I, int64_t ld, T* __restrict__ h,
                   uint8_t* __restrict__ codes, float* __restrict__ scales, int* status) {
   pdl_wait();
-  using H = Held<T, kVec>;
+  using H = Held<T, kVec, kForwardLanes>;
   const int l = threadIdx.x & (H::lanes - 1);
   const Block k = block_at(blk, own_block<H::lanes>(), I);
   const int64_t c = (int64_t)k.i * 128;
@@ -287,8 +300,8 @@ __global__ void __launch_bounds__(kThreads)
   float g[H::n], u[H::n];
   hg.floats(g);
   hu.floats(u);
-  encode_block<T, kVec>(codes + k.row * 2 * I + c, l, k.n, g, eg);
-  encode_block<T, kVec>(codes + k.row * 2 * I + I + c, l, k.n, u, eu);
+  H::encode(codes + k.row * 2 * I + c, l, k.n, g, eg);
+  H::encode(codes + k.row * 2 * I + I + c, l, k.n, u, eu);
   if (l == 0 && k.n > 0) {
     scales[k.row * 2 * blk.per_row + k.i] = pow2f(eg);
     scales[k.row * 2 * blk.per_row + blk.per_row + k.i] = pow2f(eu);
@@ -296,7 +309,7 @@ __global__ void __launch_bounds__(kThreads)
   }
 #pragma unroll
   for (int j = 0; j < H::n; ++j) g[j] = g[j] * sigmoid(g[j]) * u[j];
-  store_block<T, kVec>(h + k.row * I + c, l, k.n, g);
+  H::store(h + k.row * I + c, l, k.n, g);
 }
 
 template <typename T, bool kVec>
@@ -305,7 +318,7 @@ __global__ void __launch_bounds__(kThreads)
                            const uint8_t* __restrict__ codes, const float* __restrict__ scales,
                            T* __restrict__ d_gate_up) {
   pdl_wait();
-  using H = Held<T, kVec>;
+  using H = Held<T, kVec, kBackwardLanes>;
   const int l = threadIdx.x & (H::lanes - 1);
   const uint32_t b = own_block<H::lanes>();
   if (b >= blk.total) return;
@@ -315,12 +328,12 @@ __global__ void __launch_bounds__(kThreads)
   uint32_t wg[H::n / 4], wu[H::n / 4];
   H hd;
   hd.load(d_h + k.row * ld + c, l, k.n);
-  load_codes<T, kVec, H::n>(codes + k.row * 2 * I + c, l, k.n, wg);
-  load_codes<T, kVec, H::n>(codes + k.row * 2 * I + I + c, l, k.n, wu);
+  H::load_codes(codes + k.row * 2 * I + c, l, k.n, wg);
+  H::load_codes(codes + k.row * 2 * I + I + c, l, k.n, wu);
   const float sg = __ldg(sc), su = __ldg(sc + blk.per_row);
   float g[H::n], u[H::n], d[H::n];
-  decode<H::n>(wg, sg, g);
-  decode<H::n>(wu, su, u);
+  H::decode(wg, sg, g);
+  H::decode(wu, su, u);
   hd.floats(d);
 #pragma unroll
   for (int j = 0; j < H::n; ++j) {
@@ -329,8 +342,8 @@ __global__ void __launch_bounds__(kThreads)
     g[j] = ds * u[j] * fmaf(g[j], 1.f - s, 1.f);
     u[j] = du;
   }
-  store_block<T, kVec>(d_gate_up + k.row * 2 * I + c, l, k.n, g);
-  store_block<T, kVec>(d_gate_up + k.row * 2 * I + I + c, l, k.n, u);
+  H::store(d_gate_up + k.row * 2 * I + c, l, k.n, g);
+  H::store(d_gate_up + k.row * 2 * I + I + c, l, k.n, u);
 }
 
 template <typename F>
@@ -345,9 +358,9 @@ inline bool mult(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p
 // One turn per thread: the blocks of threads are many and alike, and the
 // hardware keeps the SMs full of them (a grid of 8 per SM that loops left the
 // SMs 62% occupied at the end: 119 us instead of 93 at 32768 x 2 x 2048 bf16).
-template <typename T>
+template <typename T, int kSingle>
 unsigned block_grid(const Blocks& blk, bool vec) {
-  return (unsigned)ceil_div(blk.total, kThreads / (vec ? Held<T, true>::lanes : Held<T, false>::lanes));
+  return (unsigned)ceil_div(blk.total, kThreads / (vec ? Held<T, true, kSingle>::lanes : kSingle));
 }
 
 }  // namespace
@@ -358,7 +371,7 @@ q4_status launch_checkpoint(const void* x, int dtype, int64_t rows, int64_t K, i
   return by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
     const bool vec = K % 8 == 0 && ld * sizeof(T) % 16 == 0 && mult(x, 16) && mult(codes, 8);
-    return launch_pdl(vec ? checkpoint_kernel<T, true> : checkpoint_kernel<T, false>, block_grid<T>(blk, vec), kThreads, 0,
+    return launch_pdl(vec ? checkpoint_kernel<T, true> : checkpoint_kernel<T, false>, block_grid<T, kForwardLanes>(blk, vec), kThreads, 0,
                       stream, static_cast<const T*>(x), blk, K, ld, codes, scales, device_status_ptr());
   });
 }
@@ -369,7 +382,7 @@ q4_status launch_swiglu(const void* gate_up, int dtype, int64_t rows, int64_t I,
   return by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
     const bool vec = I % 8 == 0 && ld * sizeof(T) % 16 == 0 && mult(gate_up, 16) && mult(h, 16) && mult(codes, 8);
-    return launch_pdl(vec ? swiglu_kernel<T, true> : swiglu_kernel<T, false>, block_grid<T>(blk, vec), kThreads, 0, stream,
+    return launch_pdl(vec ? swiglu_kernel<T, true> : swiglu_kernel<T, false>, block_grid<T, kForwardLanes>(blk, vec), kThreads, 0, stream,
                       static_cast<const T*>(gate_up), blk, I, ld, static_cast<T*>(h), codes, scales,
                       device_status_ptr());
   });
@@ -381,7 +394,7 @@ q4_status launch_swiglu_backward(const void* d_h, int dtype, int64_t rows, int64
   return by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
     const bool vec = I % 8 == 0 && ld * sizeof(T) % 16 == 0 && mult(d_h, 16) && mult(codes, 8) && mult(d_gate_up, 16);
-    return launch_pdl(vec ? swiglu_backward_kernel<T, true> : swiglu_backward_kernel<T, false>, block_grid<T>(blk, vec),
+    return launch_pdl(vec ? swiglu_backward_kernel<T, true> : swiglu_backward_kernel<T, false>, block_grid<T, kBackwardLanes>(blk, vec),
                       kThreads, 0, stream, static_cast<const T*>(d_h), blk, I, ld, codes, scales,
                       static_cast<T*>(d_gate_up));
   });
