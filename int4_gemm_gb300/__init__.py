@@ -123,13 +123,14 @@ def _check(fn: str, status: int):
 # The current stream's handle without building a Stream object (a few us per
 # call otherwise); the public route where this build of torch lacks it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream=None) -> int:
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -479,16 +480,18 @@ def _on(stream, *tensors):
 
 
 def _exact(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device) -> torch.Tensor:
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
-    return t
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+        return t
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
 
 
 def _slots(slot_row: torch.Tensor, T: int, device) -> int:
-    if slot_row.dim() != 2:
+    shape = slot_row.shape
+    if len(shape) != 2:
         raise ValueError("slot_row must be a [T, top_k] tensor")
-    _exact(slot_row, "slot_row", (T, slot_row.shape[1]), torch.int32, device)
-    return slot_row.shape[1]
+    k = shape[1]
+    _exact(slot_row, "slot_row", (T, k), torch.int32, device)
+    return k
 
 
 def moe_route_topk(logits: torch.Tensor, top_k: int, normalize: str = "topk", stream=None):
