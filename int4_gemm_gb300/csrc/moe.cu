@@ -243,7 +243,8 @@ __global__ void __launch_bounds__(kRouteWarps * kWarp)
 // ------------------------------------------------------------------ sort
 // A stable counting sort of the S = T top_k slots by expert (bucket E holds
 // the dropped ones): chunk histograms, one scan per expert over the chunks,
-// then every chunk places its slots.
+// then every chunk places its slots.  524288 slots of 256 experts take 17 us, of
+// which little is traffic (6 MB): three kernels that depend on one another.
 constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32;
 constexpr int kSortChunk = 1024, kSortPerWarp = kSortChunk / kSortWarps;
 
@@ -560,7 +561,8 @@ struct Unit {
   }
 };
 
-// blockIdx.x: token; the units of its row are spread over blockIdx.y.
+// blockIdx.x: token; the units of its row are spread over blockIdx.y.  Bound by
+// the writes: 4096 x 7168 bf16, top-8, 83 us (6.4 TB/s; a warp per slot the same).
 template <typename T, int kBytes>
 __global__ void __launch_bounds__(256)
     dispatch_kernel(const T* __restrict__ x, int64_t ldx, int64_t H, const int32_t* __restrict__ slot_row,
@@ -641,22 +643,26 @@ __global__ void __launch_bounds__(256)
 
 constexpr int kGradThreads = 256;
 
-// One warp per slot: the slot's row is read once, w d_out[t] written once, and
-// the dot product stays in the warp's registers, as 32 kU partial sums, until
-// the end of the row; no barrier, kU loads of the row in flight per lane.  The token's other slots
-// are the neighbouring warps', so d_out[t] comes from L1 for all but one.
+// kWarps warps per slot: the slot's row is read once, w d_out[t] written once,
+// and the dot product stays in registers, as 32 kU kWarps partial sums, until
+// the end of the row; kU loads of the row in flight per lane.  One warp, which
+// needs no barrier, where the slots fill the GPU: the token's other slots are
+// the neighbouring warps', so d_out[t] comes from L1 for all but one.  Eight,
+// joined in order of the warps, where they do not.
 // 4096 x 7168 bf16, top-8: 149 us (6.7 TB/s, the copy rate; one block per
 // token: 182 to 207 us).
-template <typename T, int kBytes, int kU>
+template <typename T, int kBytes, int kU, int kWarps>
 __global__ void __launch_bounds__(kGradThreads)
     combine_backward_kernel(const T* __restrict__ d_out, int64_t ldd, const T* __restrict__ rows, int64_t ld,
                             int64_t H, const int32_t* __restrict__ slot_row, const float* __restrict__ weights,
                             int top_k, uint32_t S, T* __restrict__ d_rows, float* __restrict__ d_weights) {
   pdl_wait();
-  constexpr int n = Unit<T, kBytes>::n;
-  const uint32_t slot = blockIdx.x * (kGradThreads / 32) + (threadIdx.x >> 5);
-  if (slot >= S) return;
-  const int lane = threadIdx.x & 31;
+  constexpr int n = Unit<T, kBytes>::n, kSlots = kGradThreads / 32 / kWarps;  // slots per block
+  __shared__ float joined[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t slot = blockIdx.x * kSlots + warp / kWarps;
+  if (slot >= S) return;  // with kWarps = 8 the same for the whole block
+  const int first = (warp % kWarps) * 32 + lane, step = 32 * kWarps;
   const int64_t units = H / n;
   const int32_t s = __ldg(slot_row + slot);
   const uint32_t row = s < 0 ? ~s : s;
@@ -667,21 +673,21 @@ __global__ void __launch_bounds__(kGradThreads)
 #pragma unroll
   for (int a = 0; a < kU; ++a) part[a] = 0.f;
   if (row < S) {
-    for (int64_t u0 = lane; u0 - lane < units; u0 += 32 * kU) {
+    for (int64_t u0 = first; u0 < units; u0 += step * kU) {
       Unit<T, kBytes> d[kU], y[kU];
 #pragma unroll
       for (int a = 0; a < kU; ++a) {
-        const int64_t u = u0 + 32 * a;
+        const int64_t u = u0 + step * a;
         if (read && u < units) y[a].load(rows + (int64_t)row * ld + u * n);
       }
 #pragma unroll
       for (int a = 0; a < kU; ++a) {
-        const int64_t u = u0 + 32 * a;
+        const int64_t u = u0 + step * a;
         if (live && u < units) d[a].load(d_row + u * n);
       }
 #pragma unroll
       for (int a = 0; a < kU; ++a) {
-        const int64_t u = u0 + 32 * a;
+        const int64_t u = u0 + step * a;
         if (u >= units) continue;
         float f[n];
         if (live) {
@@ -708,7 +714,16 @@ __global__ void __launch_bounds__(kGradThreads)
     for (int a = 0; a < kU; ++a) dot += part[a];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-    if (lane == 0) d_weights[slot] = dot;
+    if constexpr (kWarps > 1) {
+      if (lane == 0) joined[warp] = dot;
+      __syncthreads();
+      if (warp == 0) {
+        dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) dot += joined[i];
+      }
+    }
+    if (lane == 0 && warp % kWarps == 0) d_weights[slot] = dot;
   }
 }
 
@@ -898,10 +913,15 @@ q4_status launch_combine_backward(const void* d_out, int dtype, int64_t tokens, 
     const Matrix read = d_weights ? Matrix{rows, ld} : Matrix{d_out, ldd};
     return by_unit<T>(unit_bytes<T>(H, {{d_out, ldd}, {d_rows, H}, read}), [&](auto bytes) {
       constexpr int B = decltype(bytes)::value;
+      constexpr int U = B == 16 ? 4 : 8;
       const uint32_t S = (uint32_t)(tokens * top_k);
-      return launch_pdl(combine_backward_kernel<T, B, B == 16 ? 4 : 8>, (unsigned)ceil_div(S, kGradThreads / 32),
-                        kGradThreads, 0, stream, static_cast<const T*>(d_out), ldd, static_cast<const T*>(rows), ld,
-                        H, slot_row, weights, top_k, S, static_cast<T*>(d_rows), d_weights);
+      // warps per slot; 8 against 1 at 7168 wide: 128 slots 2.1 / 5.9 us, 512 3.1 / 6.0, 1024 5.1 / 6.1 (at
+      // 2048 wide 3.5 / 2.8), 2048 8.2 / 7.5
+      const int warps = S <= 4u * (uint32_t)num_sms() ? 8 : 1;
+      return launch_pdl(warps == 8 ? combine_backward_kernel<T, B, U, 8> : combine_backward_kernel<T, B, U, 1>,
+                        (unsigned)ceil_div((int64_t)S * warps, kGradThreads / 32), kGradThreads, 0, stream,
+                        static_cast<const T*>(d_out), ldd, static_cast<const T*>(rows), ld, H, slot_row, weights, top_k,
+                        S, static_cast<T*>(d_rows), d_weights);
     });
   });
 }
