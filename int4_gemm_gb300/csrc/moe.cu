@@ -36,30 +36,36 @@ template <>
 __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
 
 // ------------------------------------------------------------------ routing
+// One element as a float.  16-bit elements come through a whole register: loads
+// into half a register wait for one another.
+template <typename T>
+__device__ __forceinline__ float load_float(const T* p) {
+  if constexpr (sizeof(T) == 4) {
+    return __ldg(p);
+  } else {
+    const unsigned short b = __ldg(reinterpret_cast<const unsigned short*>(p));
+    return Elem<T>::to_f(*reinterpret_cast<const T*>(&b));
+  }
+}
+
 // The weights' exponential: within 2 + 1.2 |x| ulp, x = l - m <= 0, so the
 // relative error grows only where the weight itself is small.
 __device__ __forceinline__ float weight_exp(float x) { return __expf(x); }
 
-// An unsigned key that orders logits as numbers do (-0 equal to +0); 0 for a
-// masked expert: -inf, or a NaN or +inf, which are latched as errors.
-__device__ __forceinline__ uint32_t order_key(float v, bool& bad) {
-  if (nonfinite(v)) {
-    bad |= !(v < 0.f);
-    return 0;
-  }
-  const uint32_t b = __float_as_uint(v + 0.f);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
+// The logit of an FP32 key (Keys below).
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// A lane's experts, lane + 32 i.  The key of a 16-bit logit fits in 16 bits
+// A lane's experts, lane + 32 i, by an unsigned key that orders logits as
+// numbers do (-0 equal to +0); 0 for a masked expert: -inf, or a NaN or +inf,
+// which are latched as errors.  The key of a 16-bit logit fits in 16 bits
 // beside its expert (0xffff - e: the lower index wins a tie), which makes a
 // round one maximum over the warp; FP32 keys need the index found after it.
 // The keys stand in groups with their maxima kept, so that a round looks at
 // the maxima and at one group, the same for the whole warp, instead of at all
-// keys (16384 x 1024, top-8: 72 -> 47 us in FP32, 49 -> 42 us in bf16).
+// keys (16384 x 1024, top-8: 72 -> 47 us in FP32, 49 -> 42 us in bf16; with all
+// loads ahead of the first key 29 and 26).
 template <typename T, int NV>
 struct Keys {
   static constexpr bool kPacked = sizeof(T) == 2;
@@ -67,22 +73,29 @@ struct Keys {
   uint32_t key[NV], top[kGroups];
 
   __device__ __forceinline__ void load(const T* row, int E, int lane, bool& bad) {
+    // 16-bit elements by way of whole registers, so that no load waits for another
+    constexpr uint32_t kInf = kPacked ? (std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u) : 0x7f800000u;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = lane + 32 * i;
-      key[i] = 0u;
-      if (e >= E) continue;
-      if constexpr (kPacked) {
-        const T v = row[e];
-        const uint32_t b = *reinterpret_cast<const uint16_t*>(&v);
-        const uint32_t k = (b & 0x8000u ? ~(b - (b == 0x8000u)) : b | 0x8000u) & 0xffffu;  // -0: the key of +0
-        if (nonfinite(Elem<T>::to_f(v)))
-          bad |= !(Elem<T>::to_f(v) < 0.f);
-        else
-          key[i] = k << 16 | (0xffffu - e);
-      } else {
-        key[i] = order_key(row[e], bad);
-      }
+      if constexpr (kPacked)
+        key[i] = e < E ? (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(row) + e) : 0x8000u | kInf;
+      else
+        key[i] = e < E ? __float_as_uint(__ldg(row + e)) : 0x80000000u | kInf;  // -inf
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      constexpr uint32_t kSign = kPacked ? 0x8000u : 0x80000000u;
+      const uint32_t b = key[i];
+      // NaN and +inf are errors; they and -inf are masked
+      const bool masked = (b & ~kSign) >= kInf;
+      bad |= masked && b != (kSign | kInf);
+      // positive numbers above negative ones, the order of those turned; -0 as +0
+      const uint32_t k = b & kSign && b != kSign ? ~b : b | kSign;
+      if constexpr (kPacked)
+        key[i] = masked ? 0u : k << 16 | (0xffffu - (lane + 32 * i));
+      else
+        key[i] = masked ? 0u : k;
     }
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) top_of(g);
@@ -196,7 +209,7 @@ __global__ void __launch_bounds__(kRouteWarps * kWarp)
   const T* row = logits + t * ld;
   int id = lane < top_k ? ids[t * top_k + lane] : -1;
   if ((unsigned)id >= (unsigned)E) id = -1;
-  const float mine = id >= 0 ? Elem<T>::to_f(row[id]) : 0.f;
+  const float mine = id >= 0 ? load_float(row + id) : 0.f;
   const bool live = id >= 0 && !nonfinite(mine);
   const float dw = live ? d_weights[t * top_k + lane] : 0.f;
   const float kLow = -__int_as_float(0x7f800000);
@@ -206,7 +219,10 @@ __global__ void __launch_bounds__(kRouteWarps * kWarp)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = lane + 32 * i;
-      p[i] = e < E ? Elem<T>::to_f(row[e]) : kLow;
+      p[i] = e < E ? load_float(row + e) : kLow;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
       if (nonfinite(p[i])) p[i] = kLow;
       top = fmaxf(top, p[i]);
     }

@@ -19,7 +19,7 @@
 //   warps 2..9  epilogue: TMEM through 128-byte swizzled rows in shared memory
 //            to dW by TMA stores (adds, when accumulating), clipped at the
 //            edges of the expert's matrix.
-// 64 experts of 2048 x 7168, bf16 dW, the restoring (about 90 us) included: 726
+// 64 experts of 2048 x 7168, bf16 dW, the restoring (98 us) included: 726
 // us with 512 rows each (1326 TFLOP/s), 756 us with 27 to 1933; 2 experts of
 // 16384 rows, where few outputs are written: 551 us (1747).  Between the two
 // stand the stores: without them the first takes 645 us.
