@@ -260,7 +260,8 @@ __global__ void __launch_bounds__(kRouteWarps * kWarp)
 // A stable counting sort of the S = T top_k slots by expert (bucket E holds
 // the dropped ones): chunk histograms, one scan per expert over the chunks,
 // then every chunk places its slots.  524288 slots of 256 experts take 17 us, of
-// which little is traffic (6 MB): three kernels that depend on one another.
+// which little is traffic (6 MB): three kernels that depend on one another
+// (started early, to wait beside the one before, 26 us).
 constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32;
 constexpr int kSortChunk = 1024, kSortPerWarp = kSortChunk / kSortWarps;
 

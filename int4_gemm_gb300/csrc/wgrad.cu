@@ -41,6 +41,10 @@
 namespace q4 {
 namespace {
 
+// Lets the next kernel in the stream start once every block of this one has come
+// here or exited.
+__device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------------ restore
 constexpr int kRestoreThreads = 256;
 
@@ -88,6 +92,10 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int64_t R, i
 __global__ void __launch_bounds__(kRestoreThreads, 8)
     wgrad_restore_kernel(const RestoreArgs a, int64_t rows_out) {
   pdl_wait();
+  // the product may set up its barriers and tensor memory beside this kernel's
+  // last blocks; it waits for them before it reads (16 of 520 x 1024, 2000 rows:
+  // 16.4 -> 15.5 us)
+  pdl_release();
   const uint32_t v0 = blockIdx.x * blockDim.x * kRestoreUnits + threadIdx.x;
   const uint32_t xu = (uint32_t)(a.K / 8), yu = (uint32_t)(a.N / 8);
   const int64_t KB = (a.K + 127) / 128;
@@ -270,7 +278,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tmap_yt, const __grid_constant__ CUtensorMap tmap_xt,
                       const __grid_constant__ CUtensorMap tmap_w, const Params p) {
   extern __shared__ uint8_t smem_raw[];
-  pdl_wait();  // operands may come from the previous kernel
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* out_smem = smem + kStages * kStageBytes;
   Smem* sm = reinterpret_cast<Smem*>(out_smem + kOutTotal);
@@ -304,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_barrier_sync();  // the peer's barriers exist before any remote arrival
   tc_fence_after();
+  pdl_wait();  // from here on global memory: operands come from the previous kernel
   const uint32_t tmem = sm->tmem_base;
   volatile int* abort_flag = &sm->abort;
 
