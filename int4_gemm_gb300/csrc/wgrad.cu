@@ -47,7 +47,6 @@ __device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.lau
 
 // ------------------------------------------------------------------ restore
 constexpr int kRestoreThreads = 256;
-
 constexpr int kRows = 64;         // rows r per stage of the GEMM
 constexpr int kRestoreUnits = 4;  // groups of 8 columns of a thread, whose loads are in flight together
 
@@ -86,9 +85,10 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int64_t R, i
 }
 
 // Rows (blockIdx.y, threadIdx.y): those of every expert first, then each
-// expert's kRows tail rows.  A thread takes kRestoreUnits groups of 8 columns of it, threads apart,
-// so that finding the row costs little beside the conversions (one group of
-// four rows: 31 us instead of 25 for 8192 rows of 7168).
+// expert's kRows tail rows.  A thread takes kRestoreUnits groups of 8 columns of
+// its row, threads apart, so that finding the row costs little beside the
+// conversions (one group of four rows: 31 us instead of 25 for 8192 rows of
+// 7168).  Bound by the writes: 32768 rows of 7168 and 64 tails in 98 us, 5.6 TB/s.
 __global__ void __launch_bounds__(kRestoreThreads, 8)
     wgrad_restore_kernel(const RestoreArgs a, int64_t rows_out) {
   pdl_wait();
