@@ -58,9 +58,12 @@ class MoeLayer:
         self.w1 = QuantizedExperts(experts, 2 * inner, hidden, device, hidden ** -0.5)
         self.w2 = QuantizedExperts(experts, hidden, inner, device, inner ** -0.5)
 
-    def forward(self, x):
-        """x bf16 [T, hidden] -> (out bf16 [T, hidden], what backward needs)."""
+    def forward(self, x, allowed=None):
+        """x bf16 [T, hidden] -> (out bf16 [T, hidden], what backward needs).
+        allowed: bool [T, experts], the experts that a token may go to."""
         logits = x.float() @ self.router.t()
+        if allowed is not None:
+            logits = logits.masked_fill(~allowed, -float("inf"))
         ids, weights = q4.moe_route_topk(logits, self.k)
         offsets, row_token, slot_row = q4.moe_sort_tokens(ids, self.E)
         rows = torch.arange(row_token.numel(), dtype=torch.int32, device=x.device)

@@ -291,7 +291,9 @@ q4_status gemm_w4a16_mxfp4(const void* A_bf16, const uint8_t* Wq, const uint8_t*
  *   C[r, :] = A_hat[row_token[r], :] . W_hat_e^T   for r in
  *   [expert_offsets[e], expert_offsets[e+1])
  * expert_offsets: device int32 [E+1], non-decreasing, expert_offsets[0] = 0,
- * expert_offsets[E] = R.  row_token: device int32 [R], values in [0, T).
+ * expert_offsets[E] <= R.  row_token: device int32 [R], values in [0, T).
+ * Rows of C from expert_offsets[E] on (of slots that moe_sort_tokens dropped)
+ * are written as zeros, and so is all of C where E = 0.
  * W: the E experts' NVFP4 weights as one operand (raw must be NULL): codes
  * [E, N, K/2]; scales in W->scale_layout, either E consecutive
  * Q4_SCALES_MMA tensors of q4_mma_scales_bytes(N, K/16) bytes each or

@@ -435,7 +435,8 @@ def grouped_gemm_moe(tokens: torch.Tensor, expert_offsets: torch.Tensor, row_tok
                      w_codes: torch.Tensor, w_scales: torch.Tensor, w_tensor_scales: torch.Tensor,
                      N: int, ws: Optional[torch.Tensor] = None, out=None, stream=None,
                      w_scale_layout: str = "mma") -> torch.Tensor:
-    """C [R, N] bf16: routed rows times their expert's NVFP4 weights.
+    """C [R, N] bf16: routed rows times their expert's NVFP4 weights; rows from
+    expert_offsets[E] on (dropped slots) are zero.
     w_codes [E, N, K/2]; w_scales: E stacked MMA-layout scale tensors, or
     [E, N, K/16] row-major bytes with ``w_scale_layout="rowmajor"``;
     w_tensor_scales [E] float32; expert_offsets [E+1] / row_token [R] int32."""

@@ -596,7 +596,12 @@ q4_status grouped_gemm_moe(const void* tokens_bf16, int64_t T, int64_t K,
   if (K % 256) return Q4_ERR_UNSUPPORTED_SHAPE;
   if (E > 1024 || T > INT32_MAX / 2 || R > INT32_MAX / 2 || (int64_t)E * N > INT32_MAX / 2)
     return Q4_ERR_UNSUPPORTED_SHAPE;
-  if (R == 0 || N == 0 || E == 0) return Q4_OK;
+  if (R == 0 || N == 0) return Q4_OK;
+  if (E == 0) {  // no expert owns a row: all are zero
+    if (!C_bf16 || !aligned(C_bf16, 16)) return Q4_ERR_INVALID_ARG;
+    Q4_CUDA_TRY(cudaMemsetAsync(C_bf16, 0, (size_t)R * N * 2, s));
+    return Q4_OK;
+  }
   if (T == 0) return Q4_ERR_INVALID_ARG;  // routed rows need tokens
   if (!tokens_bf16 || !expert_offsets || !row_token || !W_codes || !W_scales ||
       !W_tensor_scales || !C_bf16)
@@ -631,7 +636,8 @@ q4_status grouped_gemm_moe(const void* tokens_bf16, int64_t T, int64_t K,
   if ((st = launch_grouped_prep(expert_offsets, row_token, E, pl.tok_sf, K / 16, pl.sched,
                                 pl.routed_sf, pl.cap_rows, s)) != Q4_OK)
     return st;
-  if ((st = launch_gather_rows(pl.tok_codes, row_token, R, K / 2, pl.routed_codes, s)) != Q4_OK)
+  if ((st = launch_gather_rows(pl.tok_codes, row_token, R, K / 2, pl.routed_codes, expert_offsets + E, C_bf16, N,
+                               s)) != Q4_OK)
     return st;
   GroupedArgs g = {};
   g.a_routed = pl.routed_codes; g.a_sf_rows = pl.routed_sf; g.a_g = pl.g;

@@ -82,7 +82,8 @@ q4_status launch_grouped_prep(const int32_t* offsets, const int32_t* row_token, 
                               const uint8_t* tok_scales_rowmajor, int64_t nsf, int32_t* sched,
                               uint8_t* a_sf_routed, int64_t sf_rows_cap, cudaStream_t stream);
 q4_status launch_gather_rows(const uint8_t* codes, const int32_t* row_token, int64_t R,
-                             int64_t row_bytes, uint8_t* out, cudaStream_t stream);
+                             int64_t row_bytes, uint8_t* out, const int32_t* rows_end, void* C, int64_t N,
+                             cudaStream_t stream);
 q4_status launch_grouped_gemm(const GroupedArgs& a, cudaStream_t stream);
 
 // W4A16 decode GEMMs (w4a16_workspace_bytes is 0: they need no workspace).

@@ -929,11 +929,25 @@ namespace {
 
 // Routed copy of the token codes: out[r] = codes[row_token[r]], r < R, so that
 // each expert's routed rows are consecutive and reach the GEMM by TMA.
-// 16-byte vectors, grid-stride; row_bytes is a multiple of 16.
+// 16-byte vectors, grid-stride; row_bytes is a multiple of 16.  C [R, N] (16-byte
+// aligned) is cleared from row *rows_end on.
 __global__ void __launch_bounds__(256)
     gather_rows_kernel(const uint8_t* __restrict__ codes, const int32_t* __restrict__ row_token,
-                       int64_t R, int64_t row_bytes, uint8_t* __restrict__ out) {
+                       int64_t R, int64_t row_bytes, uint8_t* __restrict__ out,
+                       const int32_t* __restrict__ rows_end, __nv_bfloat16* __restrict__ C, int64_t N) {
   pdl_wait();
+  // the rows of C behind the last expert's belong to no product: zero, so that
+  // whatever reads all R rows (the next product's tensor scale among it) meets no
+  // old memory
+  const int64_t begin = min(max((int64_t)__ldg(rows_end), (int64_t)0), R) * N, end = R * N;
+  for (int64_t u = begin / 8 + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < (end + 7) / 8;
+       u += (int64_t)gridDim.x * blockDim.x) {
+    if (u * 8 >= begin && u * 8 + 8 <= end) {
+      reinterpret_cast<uint4*>(C)[u] = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      for (int64_t i = max(u * 8, begin); i < min(u * 8 + 8, end); ++i) C[i] = __float2bfloat16_rn(0.f);
+    }
+  }
   const int64_t vpr = row_bytes / 16, total = R * vpr;
   for (int64_t v = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; v < total;
        v += (int64_t)gridDim.x * blockDim.x) {
@@ -1181,11 +1195,13 @@ q4_status launch_grouped_prep(const int32_t* offsets, const int32_t* row_token, 
 }
 
 q4_status launch_gather_rows(const uint8_t* codes, const int32_t* row_token, int64_t R,
-                             int64_t row_bytes, uint8_t* out, cudaStream_t stream) {
+                             int64_t row_bytes, uint8_t* out, const int32_t* rows_end, void* C, int64_t N,
+                             cudaStream_t stream) {
   if (R == 0) return Q4_OK;
   const int64_t total = R * (row_bytes / 16);
   const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(total, 256), (int64_t)num_sms() * 8);
-  return launch_pdl(gather_rows_kernel, grid, 256, 0, stream, codes, row_token, R, row_bytes, out);
+  return launch_pdl(gather_rows_kernel, grid, 256, 0, stream, codes, row_token, R, row_bytes, out, rows_end,
+                    static_cast<__nv_bfloat16*>(C), N);
 }
 
 q4_status launch_grouped_gemm(const GroupedArgs& a, cudaStream_t stream) {

@@ -58,13 +58,14 @@ def grouped_gemm_moe(tokens, expert_offsets, row_token, experts_q):
     """Routed NVFP4 MoE product.
 
     tokens: float32 [T, K] (bf16 values); expert_offsets: [E+1]; row_token:
-    [R] token id of each routed row, rows grouped by expert; experts_q: list of
-    (codes, scales, g) per expert.  Returns float64 C [R, N].
+    [R] token id of each routed row, rows grouped by expert, those behind the
+    last expert's end zero in C; experts_q: list of (codes, scales, g) per
+    expert.  Returns float64 C [R, N].
     """
     a_codes, a_scales, a_g = quantize_nvfp4(tokens)
     a_hat = dequantize_nvfp4(a_codes, a_scales, a_g)
     E = len(expert_offsets) - 1
-    R = int(expert_offsets[-1])
+    R = len(row_token)
     N = experts_q[0][0].shape[0] if E else 0
     out = np.zeros((R, N), dtype=np.float64)
     for e in range(E):
