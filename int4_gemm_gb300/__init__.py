@@ -6,6 +6,12 @@ PyTorch provides device memory (outputs and workspaces are torch tensors
 allocated here, on the caller's side of the ABI) and streams.  There is no
 fallback: if ``libq4gemm.so`` is missing or a call fails, an exception is
 raised.
+
+A call runs on the current stream, or on ``stream``, whose memory its own outputs
+and workspaces then are: work that is pending elsewhere does not touch them, and
+the current stream may read them (after waiting for ``stream``) and let them go.
+Ordering ``stream`` with the inputs, and with an ``out`` or ``ws`` that is given,
+is the caller's part, as under ``torch.cuda.stream``.
 """
 from __future__ import annotations
 
@@ -144,25 +150,48 @@ def _cuda2d(x: torch.Tensor, name: str) -> torch.Tensor:
     return x
 
 
-def _out(out: Optional[torch.Tensor], M: int, N: int, dtype: torch.dtype, device) -> torch.Tensor:
+def _new(shape, dtype: torch.dtype, device, stream=None, result: bool = True) -> torch.Tensor:
+    """New memory for a call on ``stream``.  Recycled memory is safe on the stream
+    that it is allocated for only (kernels of another may still be about to
+    write it), so it is allocated for the call's; the current stream is recorded as
+    a user of the results."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _given(t: torch.Tensor, stream) -> torch.Tensor:
+    """The caller's tensor, not reused before ``stream`` is done with it."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _out(out: Optional[torch.Tensor], M: int, N: int, dtype: torch.dtype, device, stream=None) -> torch.Tensor:
     """A new [M, N] output, or the caller's, checked against the call."""
     if out is None:
-        return torch.empty((M, N), dtype=dtype, device=device)
+        return _new((M, N), dtype, device, stream)
     if (tuple(out.shape) != (M, N) or out.dtype != dtype or out.device != torch.device(device)
             or not out.is_contiguous()):
         raise ValueError(f"out must be a contiguous {dtype} tensor of shape ({M}, {N}) on {device}")
-    return out
+    return _given(out, stream)
 
 
-def _empty(nbytes: int, device) -> torch.Tensor:
-    return torch.empty(max(int(nbytes), 0), dtype=torch.uint8, device=device)
+def _empty(nbytes: int, device, stream=None) -> torch.Tensor:
+    """A workspace."""
+    return _new(max(int(nbytes), 0), torch.uint8, device, stream, result=False)
 
 
-def workspace(op: int, M: int, N: int, K: int, device) -> torch.Tensor:
+def workspace(op: int, M: int, N: int, K: int, device, stream=None) -> torch.Tensor:
     n = lib().q4_workspace_size(op, M, N, K)
-    ws = _empty(max(n, 256), device)
-    if op == OP_GEMM_W4A4_MXFP4_FUSED:
-        ws[:256].zero_()  # the grid gate's counters start at zero
+    ws = _empty(max(n, 256), device, stream)
+    if op == OP_GEMM_W4A4_MXFP4_FUSED:  # the grid gate's counters start at zero
+        with torch.cuda.stream(stream):  # None: the current one
+            ws[:256].zero_()
     return ws
 
 
@@ -179,14 +208,14 @@ def quantize_nvfp4(x: torch.Tensor, scale_layout: str = "rowmajor", rounding: st
     _cuda2d(x, "x")
     rows, K = x.shape
     dev = x.device
-    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
+    codes = _new((rows, K // 2), torch.uint8, dev, stream)
     lay = _LAYOUT[scale_layout]
     if lay == ROWMAJOR:
-        scales = torch.empty((rows, K // 16), dtype=torch.uint8, device=dev)
+        scales = _new((rows, K // 16), torch.uint8, dev, stream)
     else:
-        scales = _empty(mma_scales_bytes(rows, K // 16), dev)
-    ts = torch.empty(1, dtype=torch.float32, device=dev)
-    ws = workspace(OP_QUANTIZE_NVFP4, rows, 0, K, dev)
+        scales = _new(mma_scales_bytes(rows, K // 16), torch.uint8, dev, stream)
+    ts = _new(1, torch.float32, dev, stream)
+    ws = workspace(OP_QUANTIZE_NVFP4, rows, 0, K, dev, stream)
     _check("quantize_nvfp4", lib().quantize_nvfp4_ex(
         x.data_ptr(), _DTYPE[x.dtype], rows, K, codes.data_ptr(), scales.data_ptr(), lay,
         _ROUNDING[rounding], ts.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
@@ -200,12 +229,12 @@ def quantize_mxfp4(x: torch.Tensor, scale_layout: str = "rowmajor", rounding: st
     _cuda2d(x, "x")
     rows, K = x.shape
     dev = x.device
-    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
+    codes = _new((rows, K // 2), torch.uint8, dev, stream)
     lay = _LAYOUT[scale_layout]
     if lay == ROWMAJOR:
-        scales = torch.empty((rows, K // 32), dtype=torch.uint8, device=dev)
+        scales = _new((rows, K // 32), torch.uint8, dev, stream)
     else:
-        scales = _empty(mma_scales_bytes(rows, K // 32), dev)
+        scales = _new(mma_scales_bytes(rows, K // 32), torch.uint8, dev, stream)
     _check("quantize_mxfp4", lib().quantize_mxfp4_ex(
         x.data_ptr(), _DTYPE[x.dtype], rows, K, codes.data_ptr(), scales.data_ptr(), lay,
         _ROUNDING[rounding], _stream(stream)))
@@ -216,8 +245,8 @@ def quantize_int4_g128(x: torch.Tensor, stream=None):
     """-> (codes u8 [rows, K/2], scales int16 [rows, K/128] holding FP16 bits)."""
     _cuda2d(x, "x")
     rows, K = x.shape
-    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((rows, K // 128), dtype=torch.int16, device=x.device)
+    codes = _new((rows, K // 2), torch.uint8, x.device, stream)
+    scales = _new((rows, K // 128), torch.int16, x.device, stream)
     _check("quantize_int4_g128", lib().quantize_int4_g128(
         x.data_ptr(), _DTYPE[x.dtype], rows, K, codes.data_ptr(), scales.data_ptr(),
         _stream(stream)))
@@ -227,7 +256,7 @@ def quantize_int4_g128(x: torch.Tensor, stream=None):
 def scales_to_mma(src: torch.Tensor, stream=None) -> torch.Tensor:
     _cuda2d(src, "src")
     rows, nsf = src.shape
-    dst = _empty(mma_scales_bytes(rows, nsf), src.device)
+    dst = _new(mma_scales_bytes(rows, nsf), torch.uint8, src.device, stream)
     _check("q4_scales_to_mma", lib().q4_scales_to_mma(src.data_ptr(), rows, nsf, dst.data_ptr(),
                                                       _stream(stream)))
     return dst
@@ -262,9 +291,9 @@ def _gemm_fp4(fn: str, op: int, A, B, K: int, out_dtype: torch.dtype, stream=Non
     a, M = _operand(A, K)
     b, N = _operand(B, K)
     dev = (A.codes if isinstance(A, Fp4Operand) else A).device
-    C = _out(out, M, N, out_dtype, dev)
+    C = _out(out, M, N, out_dtype, dev, stream)
     if ws is None:
-        ws = workspace(op, M, N, K, dev)
+        ws = workspace(op, M, N, K, dev, stream)
     _check(fn, getattr(lib(), fn)(ctypes.byref(a), ctypes.byref(b), M, N, K, C.data_ptr(),
                                   _DTYPE[out_dtype], ws.data_ptr(), ws.numel(), _stream(stream)))
     return C
@@ -294,9 +323,9 @@ def gemm_w4a4_mxfp4_fused(A: torch.Tensor, B, K: int, out_dtype=torch.bfloat16, 
         raise ValueError(f"A has K = {A.shape[1]}, not {K}")
     b, N = _operand(B, K)
     M = A.shape[0]
-    C = _out(out, M, N, out_dtype, A.device)
+    C = _out(out, M, N, out_dtype, A.device, stream)
     if ws is None:
-        ws = workspace(OP_GEMM_W4A4_MXFP4_FUSED, M, N, K, A.device)
+        ws = workspace(OP_GEMM_W4A4_MXFP4_FUSED, M, N, K, A.device, stream)
     _check("gemm_w4a4_mxfp4_fused",
            lib().gemm_w4a4_mxfp4_fused(A.data_ptr(), _DTYPE[A.dtype], ctypes.byref(b), M, N, K,
                                        C.data_ptr(), _DTYPE[out_dtype], ws.data_ptr(), ws.numel(),
@@ -314,7 +343,7 @@ def gemm_w4a4_nvfp4_noalloc(A: torch.Tensor, B: Fp4Operand, K: int, out_dtype=to
         raise ValueError("A must be the raw activation tensor")
     _, M = _operand(A, K)
     b, N = _operand(B, K)
-    C = _out(out, M, N, out_dtype, A.device)
+    C = _out(out, M, N, out_dtype, A.device, stream)
     _check("gemm_w4a4_nvfp4_noalloc", lib().gemm_w4a4_nvfp4_noalloc(
         A.data_ptr(), _DTYPE[A.dtype], ctypes.byref(b), M, N, K, C.data_ptr(), _DTYPE[out_dtype],
         _stream(stream)))
@@ -328,7 +357,7 @@ def gemm_w4a16_int4(A: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor, out=Non
     _cuda2d(A, "A")
     M, K = A.shape
     N = Wq.shape[0]
-    C = _out(out, M, N, torch.bfloat16, A.device)
+    C = _out(out, M, N, torch.bfloat16, A.device, stream)
     _check("gemm_w4a16_int4", lib().gemm_w4a16_int4(A.data_ptr(), Wq.data_ptr(), Ws.data_ptr(), M,
                                                      N, K, C.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
                                                      _stream(stream)))
@@ -342,7 +371,7 @@ def gemm_w4a16_nvfp4(A: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor, Wg: to
     _cuda2d(A, "A")
     M, K = A.shape
     N = Wq.shape[0]
-    C = _out(out, M, N, torch.bfloat16, A.device)
+    C = _out(out, M, N, torch.bfloat16, A.device, stream)
     _check("gemm_w4a16_nvfp4", lib().gemm_w4a16_nvfp4(A.data_ptr(), Wq.data_ptr(), Ws.data_ptr(),
                                                        Wg.data_ptr(), M, N, K, C.data_ptr(),
                                                        _ptr(ws), 0 if ws is None else ws.numel(),
@@ -357,7 +386,7 @@ def gemm_w4a16_mxfp4(A: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor, out=No
     _cuda2d(A, "A")
     M, K = A.shape
     N = Wq.shape[0]
-    C = _out(out, M, N, torch.bfloat16, A.device)
+    C = _out(out, M, N, torch.bfloat16, A.device, stream)
     _check("gemm_w4a16_mxfp4", lib().gemm_w4a16_mxfp4(A.data_ptr(), Wq.data_ptr(), Ws.data_ptr(),
                                                        M, N, K, C.data_ptr(), _ptr(ws),
                                                        0 if ws is None else ws.numel(),
@@ -373,10 +402,9 @@ def quantize_fp8_blockwise(x: torch.Tensor, block_rows: int, codes=None, scales=
     _cuda2d(x, "x")
     rows, K = x.shape
     if codes is None:
-        codes = torch.empty((rows, K), dtype=torch.uint8, device=x.device)
+        codes = _new((rows, K), torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty((rows // max(block_rows, 1), K // 128), dtype=torch.float32,
-                             device=x.device)
+        scales = _new((rows // max(block_rows, 1), K // 128), torch.float32, x.device, stream)
     _check("quantize_fp8_blockwise", lib().quantize_fp8_blockwise(
         x.data_ptr(), _DTYPE[x.dtype], rows, K, block_rows, codes.data_ptr(), scales.data_ptr(),
         _stream(stream)))
@@ -390,7 +418,7 @@ def gemm_fp8_blockwise(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb:
     _cuda2d(qa, "qa")
     M, K = qa.shape
     N = qb.shape[0]
-    C = _out(out, M, N, out_dtype if out is None else out.dtype, qa.device)
+    C = _out(out, M, N, out_dtype if out is None else out.dtype, qa.device, stream)
     _check("gemm_fp8_blockwise", lib().gemm_fp8_blockwise(
         qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), M, N, K, C.data_ptr(),
         _DTYPE[C.dtype], None, 0, _stream(stream)))
@@ -402,7 +430,7 @@ def w4a8_weight_scales(w_scales: torch.Tensor, stream=None) -> torch.Tensor:
     int16 bits) -> float32 [K/128, N], the layout gemm_w4a8 reads."""
     _cuda2d(w_scales, "w_scales")
     N, KB = w_scales.shape
-    out = torch.empty((KB, N), dtype=torch.float32, device=w_scales.device)
+    out = _new((KB, N), torch.float32, w_scales.device, stream)
     _check("w4a8_weight_scales", lib().w4a8_weight_scales(
         w_scales.data_ptr(), N, KB * 128, out.data_ptr(), _stream(stream)))
     return out
@@ -416,7 +444,7 @@ def gemm_w4a8(qa: torch.Tensor, sa: torch.Tensor, w_codes: torch.Tensor, w_scale
     _cuda2d(qa, "qa")
     M, K = qa.shape
     N = w_codes.shape[0]
-    C = _out(out, M, N, out_dtype if out is None else out.dtype, qa.device)
+    C = _out(out, M, N, out_dtype if out is None else out.dtype, qa.device, stream)
     _check("gemm_w4a8", lib().gemm_w4a8(
         qa.data_ptr(), sa.data_ptr(), w_codes.data_ptr(), w_scales_kn.data_ptr(), M, N, K,
         C.data_ptr(), _DTYPE[C.dtype], None, 0, _stream(stream)))
@@ -424,11 +452,11 @@ def gemm_w4a8(qa: torch.Tensor, sa: torch.Tensor, w_codes: torch.Tensor, w_scale
 
 
 def moe_workspace(T: int, N: int, K: int, E: int, R: int, device,
-                  w_scale_layout: str = "mma") -> torch.Tensor:
+                  w_scale_layout: str = "mma", stream=None) -> torch.Tensor:
     n = int(lib().q4_workspace_size_moe(T, N, K, E, R))
     if w_scale_layout == "rowmajor":  # room for the weight scales in the tensor-core layout
         n += E * mma_scales_bytes(N, K // 16)
-    return _empty(max(n, 256), device)
+    return _empty(max(n, 256), device, stream)
 
 
 def grouped_gemm_moe(tokens: torch.Tensor, expert_offsets: torch.Tensor, row_token: torch.Tensor,
@@ -444,9 +472,9 @@ def grouped_gemm_moe(tokens: torch.Tensor, expert_offsets: torch.Tensor, row_tok
     T, K = tokens.shape
     E = expert_offsets.numel() - 1
     R = row_token.numel()
-    C = _out(out, R, N, torch.bfloat16, tokens.device)
+    C = _out(out, R, N, torch.bfloat16, tokens.device, stream)
     if ws is None:
-        ws = moe_workspace(T, N, K, E, R, tokens.device, w_scale_layout)
+        ws = moe_workspace(T, N, K, E, R, tokens.device, w_scale_layout, stream)
     w = _Operand(None, 0, w_codes.data_ptr(), w_scales.data_ptr(), _LAYOUT[w_scale_layout],
                  w_tensor_scales.data_ptr())
     _check("grouped_gemm_moe", lib().grouped_gemm_moe(
@@ -472,14 +500,6 @@ def _pitched(x: torch.Tensor, name: str) -> int:
     return max(cols, 1)
 
 
-def _on(stream, *tensors):
-    """Tensors allocated here for another stream's call: their memory is not
-    reused before that stream's work is done."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
-
-
 def _exact(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device) -> torch.Tensor:
     if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
         return t
@@ -502,12 +522,11 @@ def moe_route_topk(logits: torch.Tensor, top_k: int, normalize: str = "topk", st
     (softmax over the chosen logits) or "all" (over every logit)."""
     ld = _pitched(logits, "logits")
     T, E = logits.shape
-    ids = torch.empty((T, max(top_k, 0)), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((T, max(top_k, 0)), dtype=torch.float32, device=logits.device)
+    ids = _new((T, max(top_k, 0)), torch.int32, logits.device, stream)
+    weights = _new((T, max(top_k, 0)), torch.float32, logits.device, stream)
     _check("moe_route_topk", lib().moe_route_topk(
         logits.data_ptr(), _DTYPE[logits.dtype], T, E, ld, top_k, _NORMALIZE[normalize],
         ids.data_ptr(), weights.data_ptr(), _stream(stream)))
-    _on(stream, ids, weights)
     return ids, weights
 
 
@@ -521,11 +540,10 @@ def moe_route_topk_backward(logits: torch.Tensor, ids: torch.Tensor, d_weights: 
     k = ids.shape[1]
     _exact(ids, "ids", (T, k), torch.int32, logits.device)
     _exact(d_weights, "d_weights", (T, k), torch.float32, logits.device)
-    d = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    d = _new((T, E), logits.dtype, logits.device, stream)
     _check("moe_route_topk_backward", lib().moe_route_topk_backward(
         logits.data_ptr(), _DTYPE[logits.dtype], T, E, ld, k, _NORMALIZE[normalize],
         ids.data_ptr(), d_weights.data_ptr(), d.data_ptr(), _stream(stream)))
-    _on(stream, d)
     return d
 
 
@@ -542,18 +560,18 @@ def moe_sort_tokens(ids: torch.Tensor, E: int, ws: Optional[torch.Tensor] = None
     _exact(ids, "ids", (T, k), torch.int32, dev)
     if E < 1:
         raise ValueError("E must be positive")
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    row_token = torch.empty(T * k, dtype=torch.int32, device=dev)
-    slot_row = torch.empty((T, k), dtype=torch.int32, device=dev)
+    offsets = _new(E + 1, torch.int32, dev, stream)
+    row_token = _new(T * k, torch.int32, dev, stream)
+    slot_row = _new((T, k), torch.int32, dev, stream)
     L = lib()
     if ws is None:
         n = L.q4_workspace_size(OP_MOE_SORT, T * k, E, 0)
-        ws = _empty(n, dev) if n else None
+        ws = _empty(n, dev, stream) if n else None
+    else:
+        _given(ws, stream)
     _check("moe_sort_tokens", L.moe_sort_tokens(
         ids.data_ptr(), T, k, E, offsets.data_ptr(), row_token.data_ptr(), slot_row.data_ptr(),
         _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
-    if stream is not None:
-        _on(stream, offsets, row_token, slot_row, *(() if ws is None else (ws,)))
     return offsets, row_token, slot_row
 
 
@@ -562,10 +580,9 @@ def moe_dispatch(x: torch.Tensor, slot_row: torch.Tensor, out=None, stream=None)
     ld = _pitched(x, "x")
     T, H = x.shape
     k = _slots(slot_row, T, x.device)
-    rows = _out(out, T * k, H, x.dtype, x.device)
+    rows = _out(out, T * k, H, x.dtype, x.device, stream)
     _check("moe_dispatch", lib().moe_dispatch(x.data_ptr(), _DTYPE[x.dtype], T, H, ld,
                                               slot_row.data_ptr(), k, rows.data_ptr(), _stream(stream)))
-    _on(stream, rows)
     return rows
 
 
@@ -577,11 +594,10 @@ def moe_dispatch_backward(d_rows: torch.Tensor, slot_row: torch.Tensor, out=None
     k = _slots(slot_row, T, d_rows.device)
     if d_rows.shape[0] != T * k:
         raise ValueError(f"d_rows has {d_rows.shape[0]} rows, slot_row {T * k} slots")
-    d_x = _out(out, T, H, d_rows.dtype, d_rows.device)
+    d_x = _out(out, T, H, d_rows.dtype, d_rows.device, stream)
     _check("moe_dispatch_backward", lib().moe_dispatch_backward(
         d_rows.data_ptr(), _DTYPE[d_rows.dtype], T, H, ld, slot_row.data_ptr(), k, d_x.data_ptr(),
         _stream(stream)))
-    _on(stream, d_x)
     return d_x
 
 
@@ -596,11 +612,10 @@ def moe_combine(rows: torch.Tensor, slot_row: torch.Tensor, weights: Optional[to
         raise ValueError(f"rows has {rows.shape[0]} rows, slot_row {T * k} slots")
     if weights is not None:
         _exact(weights, "weights", (T, k), torch.float32, rows.device)
-    C = _out(out, T, H, rows.dtype, rows.device)
+    C = _out(out, T, H, rows.dtype, rows.device, stream)
     _check("moe_combine", lib().moe_combine(rows.data_ptr(), _DTYPE[rows.dtype], T, H, ld,
                                             slot_row.data_ptr(), _ptr(weights), k, C.data_ptr(),
                                             _stream(stream)))
-    _on(stream, C)
     return C
 
 
@@ -614,12 +629,11 @@ def moe_combine_backward(d_out: torch.Tensor, rows: torch.Tensor, slot_row: torc
     if tuple(rows.shape) != (T * k, H) or rows.dtype != d_out.dtype or rows.device != d_out.device:
         raise ValueError(f"rows must be a {d_out.dtype} tensor of shape ({T * k}, {H}) on {d_out.device}")
     _exact(weights, "weights", (T, k), torch.float32, d_out.device)
-    d_rows = _out(out, T * k, H, d_out.dtype, d_out.device)
-    dw = torch.empty((T, k), dtype=torch.float32, device=d_out.device) if need_d_weights else None
+    d_rows = _out(out, T * k, H, d_out.dtype, d_out.device, stream)
+    dw = _new((T, k), torch.float32, d_out.device, stream) if need_d_weights else None
     _check("moe_combine_backward", lib().moe_combine_backward(
         d_out.data_ptr(), _DTYPE[d_out.dtype], T, H, ldd, rows.data_ptr(), ld,
         slot_row.data_ptr(), weights.data_ptr(), k, d_rows.data_ptr(), _ptr(dw), _stream(stream)))
-    _on(stream, d_rows, *(() if dw is None else (dw,)))
     return d_rows, dw
 
 
@@ -630,12 +644,11 @@ def quantize_fp8_checkpoint(x: torch.Tensor, stream=None):
     E4M3, scales float32 [rows, ceil(K/128)], powers of two)."""
     ld = _pitched(x, "x")
     rows, K = x.shape
-    codes = torch.empty((rows, K), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((rows, -(-K // 128)), dtype=torch.float32, device=x.device)
+    codes = _new((rows, K), torch.uint8, x.device, stream)
+    scales = _new((rows, -(-K // 128)), torch.float32, x.device, stream)
     _check("quantize_fp8_checkpoint", lib().quantize_fp8_checkpoint(
         x.data_ptr(), _DTYPE[x.dtype], rows, K, ld, codes.data_ptr(), scales.data_ptr(),
         _stream(stream)))
-    _on(stream, codes, scales)
     return codes, scales
 
 
@@ -648,13 +661,12 @@ def swiglu_fp8(gate_up: torch.Tensor, out=None, stream=None):
     if two % 2:
         raise ValueError("gate_up must have an even number of columns")
     inner, dev = two // 2, gate_up.device
-    h = _out(out, rows, inner, gate_up.dtype, dev)
-    codes = torch.empty((rows, two), dtype=torch.uint8, device=dev)
-    scales = torch.empty((rows, 2 * -(-inner // 128)), dtype=torch.float32, device=dev)
+    h = _out(out, rows, inner, gate_up.dtype, dev, stream)
+    codes = _new((rows, two), torch.uint8, dev, stream)
+    scales = _new((rows, 2 * -(-inner // 128)), torch.float32, dev, stream)
     _check("swiglu_fp8", lib().swiglu_fp8(
         gate_up.data_ptr(), _DTYPE[gate_up.dtype], rows, inner, ld, h.data_ptr(),
         codes.data_ptr(), scales.data_ptr(), _stream(stream)))
-    _on(stream, h, codes, scales)
     return h, codes, scales
 
 
@@ -665,16 +677,15 @@ def swiglu_fp8_backward(d_h: torch.Tensor, codes: torch.Tensor, scales: torch.Te
     rows, inner = d_h.shape
     _exact(codes, "codes", (rows, 2 * inner), torch.uint8, d_h.device)
     _exact(scales, "scales", (rows, 2 * -(-inner // 128)), torch.float32, d_h.device)
-    d = _out(out, rows, 2 * inner, d_h.dtype, d_h.device)
+    d = _out(out, rows, 2 * inner, d_h.dtype, d_h.device, stream)
     _check("swiglu_fp8_backward", lib().swiglu_fp8_backward(
         d_h.data_ptr(), _DTYPE[d_h.dtype], rows, inner, ld, codes.data_ptr(),
         scales.data_ptr(), d.data_ptr(), _stream(stream)))
-    _on(stream, d)
     return d
 
 
-def wgrad_workspace(R: int, N: int, K: int, E: int, device) -> torch.Tensor:
-    return _empty(max(int(lib().q4_workspace_size_wgrad(R, N, K, E)), 256), device)
+def wgrad_workspace(R: int, N: int, K: int, E: int, device, stream=None) -> torch.Tensor:
+    return _empty(max(int(lib().q4_workspace_size_wgrad(R, N, K, E)), 256), device, stream)
 
 
 def grouped_wgrad_fp8(d_y: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
@@ -705,18 +716,19 @@ def grouped_wgrad_fp8(d_y: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     if out is None:
-        out = torch.empty((E, N, K), dtype=out_dtype, device=dev)
+        out = _new((E, N, K), out_dtype, dev, stream)
     else:
-        _exact(out, "out", (E, N, K), out.dtype, dev)
+        _given(_exact(out, "out", (E, N, K), out.dtype, dev), stream)
     if out.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("the gradient is float32 or bfloat16")
     if ws is None:
-        ws = wgrad_workspace(R, N, K, E, dev)
+        ws = wgrad_workspace(R, N, K, E, dev, stream)
+    else:
+        _given(ws, stream)
     _check("grouped_wgrad_fp8", lib().grouped_wgrad_fp8(
         d_y.data_ptr(), R, N, ldy, codes.data_ptr(), scales.data_ptr(), T, K, _ptr(row_token),
         expert_offsets.data_ptr(), E, out.data_ptr(), _DTYPE[out.dtype], int(accumulate),
         ws.data_ptr(), ws.numel(), _stream(stream)))
-    _on(stream, out, ws)
     return out
 
 
@@ -735,7 +747,9 @@ def read_probe(src: torch.Tensor, sink: Optional[torch.Tensor] = None, stream=No
     if not src.is_cuda or not src.is_contiguous():
         raise ValueError("src must be a contiguous CUDA tensor")
     if sink is None:
-        sink = torch.zeros(int(lib().q4_read_probe_sink_words()), dtype=torch.int32, device=src.device)
+        sink = _new(int(lib().q4_read_probe_sink_words()), torch.int32, src.device, stream)
+        with torch.cuda.stream(stream):
+            sink.zero_()
     _check("q4_read_probe", lib().q4_read_probe(src.data_ptr(), src.numel() * src.element_size(),
                                                 sink.data_ptr(), _stream(stream)))
     return sink
