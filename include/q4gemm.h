@@ -444,8 +444,9 @@ q4_status moe_combine_backward(const void* d_out, int dtype, int64_t T, int64_t 
  *   code = e4m3_rne(x / s)
  * (codes and scales are those of quantize_fp8_blockwise with block_rows 1 but
  * for the power of two, so gemm_fp8_blockwise takes them too; code * s is a
- * bf16 number.)  Any K >= 1; x has row pitch ld.  A non-finite input latches
- * Q4_ERR_NONFINITE.
+ * bf16 number.  At the largest scale, 2^120, finite numbers stop at the code 240,
+ * since 256 * 2^120 would not be one.)  Any K >= 1; x has row pitch ld.  A
+ * non-finite input latches Q4_ERR_NONFINITE.
  *
  * swiglu_fp8: the gated activation of gate_up = [g | u] [rows, 2 I] (row pitch
  * ld): h = silu(g) * u [rows, I] in dtype, and the checkpoint of gate_up taken

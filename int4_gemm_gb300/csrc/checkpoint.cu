@@ -8,7 +8,7 @@
 // feed it to the bf16 tensor cores without a second rounding, while against
 // s = amax / 448 at most one bit of E4M3's range (none of its precision) is
 // given up.  x / s is exact, so the only rounding is the E4M3 one (to nearest
-// even).
+// even; finite numbers of 248 * 2^120 and more stop at 240 * 2^120).
 //
 // swiglu of gate_up = [g | u]:  h = silu(g) u,  silu(g) = g / (1 + exp(-g));
 // its gradient at the restored g and u, with s = 1 / (1 + exp(-g)):
@@ -35,11 +35,16 @@ __device__ __forceinline__ float2 e4m3x2_values(uint32_t codes) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// The largest scale's exponent.  Numbers from 248 * 2^120 on round to the code 256,
+// which would stand for 2^128, beyond FP32 and bf16; they stop at 240.  (Greater
+// codes come from infinities only, and stay.)
+constexpr int kTopExponent = 120;
+
 // Exponent of the block's scale: 448 = 1.75 * 2^8, so the significand of amax
 // decides between its own exponent - 8 and - 7.
 __device__ __forceinline__ int scale_exponent(float amax) {
   const uint32_t b = max(__float_as_uint(amax), __float_as_uint(1e-12f));
-  return min((int)((b + 0x1fffffu) >> 23) - 127 - 8, 120);  // 120: a non-finite block
+  return min((int)((b + 0x1fffffu) >> 23) - 127 - 8, kTopExponent);  // a non-finite block has the top one, too
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
@@ -89,7 +94,7 @@ __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f +
 // at 32768 x 2 x 2048).  Otherwise lane l of kSingle holds columns l, l +
 // kSingle, ... one by one, 16-bit elements by way of whole registers (loads into
 // half a register wait for one another); sixteen lanes suit the kernels that
-// reduce over the block (quantize_fp8_checkpoint of 9973 x 2822 bf16: 22 us
+// reduce over the block (quantize_fp8_checkpoint of 9973 x 2822 bf16: 23 us
 // instead of 32 with a warp), a warp the gradient (27 us instead of 30 at 9973 x
 // 1411; with a path without tests for whole blocks 30).  Columns past the
 // block's end are zero; 16-bit elements of chunks stay packed in the words they
@@ -193,6 +198,10 @@ struct Held {
 #pragma unroll
     for (int i = 0; i < n / 4; ++i)
       w[i] = e4m3x2(f[4 * i] * inv, f[4 * i + 1] * inv) | e4m3x2(f[4 * i + 2] * inv, f[4 * i + 3] * inv) << 16;
+    if (e == kTopExponent) {  // 256 (0x78) becomes 240 (0x77), four codes at once
+#pragma unroll
+      for (int i = 0; i < n / 4; ++i) w[i] -= __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x78787878u) & 0x01010101u;
+    }
     if constexpr (kVec) {
 #pragma unroll
       for (int c = 0; c < chunks; ++c)

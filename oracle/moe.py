@@ -10,7 +10,8 @@ at a time, never called by the product path.
 * Order: slots (t, j) by expert, then token, then j; an id outside [0, E) drops
   its slot, which takes one of the last rows and is marked by ~row.
 * Checkpoint: E4M3 codes of x / s, one power-of-two scale per row and 128
-  columns, the smallest s with max(amax, 1e-12) <= 448 s.
+  columns, the smallest s with max(amax, 1e-12) <= 448 s.  Where s = 2^120 (the
+  largest), finite values stop at the code 240, so that code * s is finite.
 * SwiGLU: h = silu(g) u; gradient at the restored g and u.
 * Weight gradient: dW[e] = sum over the rows of expert e of d_y^T x_hat.
 """
@@ -136,7 +137,10 @@ def quantize_fp8_checkpoint(x):
         for _ in range(8):
             e = np.where(amax > E4M3_MAX * np.exp2(e.astype(float)), e + 1, e)
         s = np.exp2(e.astype(float))
-        codes[:, 128 * b:128 * b + 128] = e4m3_encode_signed((v / s[:, None]).astype(np.float32))
+        q = v / s[:, None]
+        # 256 * 2^120 would be beyond float32: finite values stop at the code before
+        q = np.where(np.isfinite(q) & (e == 120)[:, None], np.clip(q, -240.0, 240.0), q)
+        codes[:, 128 * b:128 * b + 128] = e4m3_encode_signed(q.astype(np.float32))
         scales[:, b] = s
     return codes, scales
 

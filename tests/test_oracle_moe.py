@@ -118,3 +118,13 @@ def test_wgrad_is_the_difference_quotient():
         return sum(float(d[i] @ v[e] @ x[row_token[i]]) for e in range(3) for i in range(offsets[e], offsets[e + 1]))
     got, _ = moe.grouped_wgrad(d, x, row_token, offsets)
     assert np.allclose(got, _differences(loss, w), atol=1e-7)
+
+
+def test_checkpoint_of_the_largest_values_restores_as_finite():
+    top = np.finfo(np.float32).max
+    x = np.array([[top, -top, 248 * 2.0 ** 120, 247 * 2.0 ** 120, 1.0]], np.float32)
+    codes, scales = moe.quantize_fp8_checkpoint(x)
+    assert scales[0, 0] == 2.0 ** 120
+    v = moe.restore_fp8_checkpoint(codes, scales)
+    assert np.all(np.isfinite(v.astype(np.float32)))
+    assert np.array_equal(v[0], np.array([240, -240, 240, 240, 0]) * 2.0 ** 120)
