@@ -371,6 +371,10 @@ q4_status gemm_w4a8(const uint8_t* qa, const float* sa, const uint8_t* w_codes,
 /*
  * Routing around grouped_gemm_moe, and its gradients.
  *
+ * Here and in the calls below down to grouped_wgrad_fp8, outputs and workspace
+ * overlap neither inputs nor one another (else Q4_ERR_INVALID_ARG), but for the
+ * in-place form of moe_combine_backward.
+ *
  * moe_route_topk: the top_k experts of every token by logit and their softmax
  * weights.  logits: [T, E] of dtype, row pitch ld elements (ld >= E).  With V
  * the token's experts whose logit is above -inf (a logit of -inf masks its
@@ -423,7 +427,8 @@ q4_status moe_sort_tokens(const int32_t* ids, int64_t T, int top_k, int E, int32
  * Sums are FP32, in ascending j, and leave dropped slots out whatever their
  * rows and weights hold; results are rounded once to dtype (d_weights: FP32).
  * moe_combine with weights NULL takes every weight as 1.  moe_combine_backward
- * with d_weights NULL does not read rows.
+ * with d_weights NULL does not read rows; otherwise d_rows may be rows itself
+ * (the same address, ld_rows = H, no row named twice by slot_row).
  */
 q4_status moe_dispatch(const void* x, int dtype, int64_t T, int64_t H, int64_t ldx,
                        const int32_t* slot_row, int top_k, void* rows, q4_stream_t stream);

@@ -622,7 +622,8 @@ def moe_combine(rows: torch.Tensor, slot_row: torch.Tensor, weights: Optional[to
 def moe_combine_backward(d_out: torch.Tensor, rows: torch.Tensor, slot_row: torch.Tensor,
                          weights: torch.Tensor, need_d_weights: bool = True, out=None, stream=None):
     """Gradients of moe_combine: (d_rows [T*top_k, H], d_weights float32 [T,
-    top_k], or None without ``need_d_weights``, when rows is not read)."""
+    top_k], or None without ``need_d_weights``, when rows is not read).  ``out``
+    may be rows itself."""
     ldd, ld = _pitched(d_out, "d_out"), _pitched(rows, "rows")
     T, H = d_out.shape
     k = _slots(slot_row, T, d_out.device)

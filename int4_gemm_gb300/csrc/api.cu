@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "common.cuh"
@@ -674,6 +675,35 @@ q4_status check_checkpoint(int dtype, int64_t rows, int64_t width, int64_t ld, i
   if (width > INT32_MAX / 4 || (rows && ceil_div(width, 128) > INT32_MAX / 2 / rows)) return Q4_ERR_UNSUPPORTED_SHAPE;
   return Q4_OK;
 }
+
+// Memory that a call reads or writes: rows of `width` bytes, `pitch` bytes apart.
+struct Extent {
+  const void* p;
+  int64_t rows, width, pitch;
+  Extent(const void* p_, int64_t bytes) : p(p_), rows(1), width(bytes), pitch(bytes) {}
+  Extent(const void* p_, int64_t rows_, int64_t width_, int64_t pitch_)
+      : p(p_), rows(rows_), width(width_), pitch(pitch_) {}
+};
+// Whether a contiguous extent shares a byte with another one.
+bool overlap(const Extent& flat, const Extent& m) {
+  if (!flat.p || !m.p || flat.width <= 0 || m.rows <= 0 || m.width <= 0) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(flat.p), b = reinterpret_cast<uintptr_t>(m.p);
+  const uintptr_t pitch = (uintptr_t)m.pitch, width = (uintptr_t)m.width, bytes = (uintptr_t)flat.width;
+  if (a + bytes <= b || a >= b + (uintptr_t)(m.rows - 1) * pitch + width) return false;
+  if (a < b) return true;
+  const uintptr_t at = (a - b) % pitch;  // behind the start of a row; behind its end a next row follows
+  return at < width || at + bytes > pitch;
+}
+// Whether the outputs (contiguous) overlap neither an input nor one another.
+bool apart(std::initializer_list<Extent> outputs, std::initializer_list<Extent> inputs) {
+  for (const Extent* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Extent& i : inputs)
+      if (overlap(*o, i)) return false;
+    for (const Extent* other = outputs.begin(); other != o; ++other)
+      if (overlap(*o, *other)) return false;
+  }
+  return true;
+}
 }  // namespace
 
 q4_status moe_route_topk(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, int top_k,
@@ -681,6 +711,8 @@ q4_status moe_route_topk(const void* logits, int dtype, int64_t T, int64_t E, in
   const q4_status st = check_route(dtype, T, E, ld, top_k, normalize);
   if (st != Q4_OK || T == 0) return st;
   if (!elem_ptr(logits, dtype) || !word_ptr(ids) || !word_ptr(weights)) return Q4_ERR_INVALID_ARG;
+  const int64_t b = elem_bytes(dtype);
+  if (!apart({{ids, T * top_k * 4}, {weights, T * top_k * 4}}, {{logits, T, E * b, ld * b}})) return Q4_ERR_INVALID_ARG;
   return launch_route(logits, dtype, T, (int)E, ld, top_k, normalize == Q4_ROUTE_ALL, ids, weights,
                       reinterpret_cast<cudaStream_t>(stream));
 }
@@ -691,6 +723,9 @@ q4_status moe_route_topk_backward(const void* logits, int dtype, int64_t T, int6
   const q4_status st = check_route(dtype, T, E, ld, top_k, normalize);
   if (st != Q4_OK || T == 0) return st;
   if (!elem_ptr(logits, dtype) || !word_ptr(ids) || !word_ptr(d_weights) || !elem_ptr(d_logits, dtype))
+    return Q4_ERR_INVALID_ARG;
+  const int64_t b = elem_bytes(dtype);
+  if (!apart({{d_logits, T * E * b}}, {{logits, T, E * b, ld * b}, {ids, T * top_k * 4}, {d_weights, T * top_k * 4}}))
     return Q4_ERR_INVALID_ARG;
   return launch_route_backward(logits, dtype, T, (int)E, ld, top_k, normalize == Q4_ROUTE_ALL, ids,
                                d_weights, d_logits, reinterpret_cast<cudaStream_t>(stream));
@@ -710,6 +745,10 @@ q4_status moe_sort_tokens(const int32_t* ids, int64_t T, int top_k, int E, int32
   if (!word_ptr(ids) || !word_ptr(row_token) || !word_ptr(slot_row)) return Q4_ERR_INVALID_ARG;
   const size_t need = moe_sort_workspace_bytes(T * top_k, E);
   if (need && (!ws || !aligned(ws, 256) || ws_bytes < need)) return Q4_ERR_WORKSPACE;
+  const int64_t slot_bytes = T * top_k * 4;
+  if (!apart({{expert_offsets, (E + 1) * (int64_t)4}, {row_token, slot_bytes}, {slot_row, slot_bytes}, {ws, (int64_t)need}},
+             {{ids, slot_bytes}}))
+    return Q4_ERR_INVALID_ARG;
   return launch_moe_sort(ids, T * top_k, top_k, E, expert_offsets, row_token, slot_row, ws, s);
 }
 
@@ -720,6 +759,8 @@ q4_status moe_dispatch(const void* x, int dtype, int64_t T, int64_t H, int64_t l
   if (ldx < H) return Q4_ERR_INVALID_ARG;
   if (T == 0 || H == 0) return Q4_OK;
   if (!elem_ptr(x, dtype) || !word_ptr(slot_row) || !elem_ptr(rows, dtype)) return Q4_ERR_INVALID_ARG;
+  const int64_t b = elem_bytes(dtype), S = T * top_k;
+  if (!apart({{rows, S * H * b}}, {{x, T, H * b, ldx * b}, {slot_row, S * 4}})) return Q4_ERR_INVALID_ARG;
   return launch_dispatch(x, dtype, T, H, ldx, slot_row, top_k, rows, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -732,6 +773,8 @@ q4_status moe_combine(const void* rows, int dtype, int64_t T, int64_t H, int64_t
   if (T == 0 || H == 0) return Q4_OK;
   if (!elem_ptr(rows, dtype) || !word_ptr(slot_row) || !aligned(weights, 4) || !elem_ptr(out, dtype))
     return Q4_ERR_INVALID_ARG;
+  const int64_t b = elem_bytes(dtype), S = T * top_k;
+  if (!apart({{out, T * H * b}}, {{rows, S, H * b, ld * b}, {slot_row, S * 4}, {weights, S * 4}})) return Q4_ERR_INVALID_ARG;
   return launch_combine(rows, dtype, T, H, ld, slot_row, weights, top_k, out,
                         reinterpret_cast<cudaStream_t>(stream));
 }
@@ -758,6 +801,13 @@ q4_status moe_combine_backward(const void* d_out, int dtype, int64_t T, int64_t 
   if (!elem_ptr(d_out, dtype) || !word_ptr(slot_row) || !word_ptr(weights) || !elem_ptr(d_rows, dtype) ||
       (d_weights && (!elem_ptr(rows, dtype) || !aligned(d_weights, 4))))
     return Q4_ERR_INVALID_ARG;
+  const int64_t b = elem_bytes(dtype), S = T * top_k;
+  // rows is read for d_weights only, and may be d_rows itself
+  const bool in_place = !d_weights || (rows == d_rows && ld_rows == H);
+  if (!apart({{d_rows, S * H * b}, {d_weights, S * 4}},
+             {{d_out, T, H * b, ld_d_out * b}, {in_place ? nullptr : rows, S, H * b, ld_rows * b}, {slot_row, S * 4},
+              {weights, S * 4}}))
+    return Q4_ERR_INVALID_ARG;
   return launch_combine_backward(d_out, dtype, T, H, ld_d_out, rows, ld_rows, slot_row, weights, top_k,
                                  d_rows, d_weights, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -767,6 +817,8 @@ q4_status quantize_fp8_checkpoint(const void* x, int dtype, int64_t rows, int64_
   const q4_status st = check_checkpoint(dtype, rows, K, ld, K);
   if (st != Q4_OK || rows == 0) return st;
   if (!elem_ptr(x, dtype) || !codes || !word_ptr(scales)) return Q4_ERR_INVALID_ARG;
+  const int64_t b = elem_bytes(dtype);
+  if (!apart({{codes, rows * K}, {scales, rows * ceil_div(K, 128) * 4}}, {{x, rows, K * b, ld * b}})) return Q4_ERR_INVALID_ARG;
   return launch_checkpoint(x, dtype, rows, K, ld, codes, scales, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -775,6 +827,10 @@ q4_status swiglu_fp8(const void* gate_up, int dtype, int64_t rows, int64_t I, in
   const q4_status st = check_checkpoint(dtype, rows, I, ld, 2 * I);
   if (st != Q4_OK || rows == 0) return st;
   if (!elem_ptr(gate_up, dtype) || !elem_ptr(h, dtype) || !codes || !word_ptr(scales)) return Q4_ERR_INVALID_ARG;
+  const int64_t b = elem_bytes(dtype);
+  if (!apart({{h, rows * I * b}, {codes, rows * 2 * I}, {scales, rows * 2 * ceil_div(I, 128) * 4}},
+             {{gate_up, rows, 2 * I * b, ld * b}}))
+    return Q4_ERR_INVALID_ARG;
   return launch_swiglu(gate_up, dtype, rows, I, ld, h, codes, scales, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -784,6 +840,10 @@ q4_status swiglu_fp8_backward(const void* d_h, int dtype, int64_t rows, int64_t 
   const q4_status st = check_checkpoint(dtype, rows, I, ld, I);
   if (st != Q4_OK || rows == 0) return st;
   if (!elem_ptr(d_h, dtype) || !codes || !word_ptr(scales) || !elem_ptr(d_gate_up, dtype))
+    return Q4_ERR_INVALID_ARG;
+  const int64_t b = elem_bytes(dtype);
+  if (!apart({{d_gate_up, rows * 2 * I * b}},
+             {{d_h, rows, I * b, ld * b}, {codes, rows * 2 * I}, {scales, rows * 2 * ceil_div(I, 128) * 4}}))
     return Q4_ERR_INVALID_ARG;
   return launch_swiglu_backward(d_h, dtype, rows, I, ld, codes, scales, d_gate_up,
                                 reinterpret_cast<cudaStream_t>(stream));
@@ -816,6 +876,10 @@ q4_status grouped_wgrad_fp8(const void* d_y_bf16, int64_t R, int64_t N, int64_t 
     return Q4_ERR_INVALID_ARG;
   const size_t need = wgrad_workspace_bytes(R, N, K, E);
   if (need && (!ws || !aligned(ws, 256) || ws_bytes < need)) return Q4_ERR_WORKSPACE;
+  if (!apart({{dW, (int64_t)E * N * K * (int64_t)elem_bytes(w_dtype)}, {ws, (int64_t)need}},
+             {{d_y_bf16, R, N * 2, ldy * 2}, {codes, T * K}, {scales, T * ceil_div(K, 128) * 4}, {row_token, R * 4},
+              {expert_offsets, (E + 1) * (int64_t)4}}))
+    return Q4_ERR_INVALID_ARG;
   WgradArgs a = {};
   a.dy = d_y_bf16; a.R = R; a.N = N; a.ldy = ldy;
   a.codes = codes; a.scales = scales; a.tokens = T; a.K = K;

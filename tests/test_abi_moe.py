@@ -100,3 +100,36 @@ def test_wgrad(clib):
     assert need >= 64 * 32 * 2 and clib.q4_workspace_size_wgrad(-1, 16, 32, 2) == 0
     for ws, nb in ((None, need), (FAKE + 16, need), (FAKE, need - 1)):
         assert wgrad(ws=ws, nb=nb) == -6
+
+
+def test_overlapping_memory(clib):
+    """Outputs that share memory with an input, with one another or with the
+    workspace (otherwise valid calls)."""
+    far = [FAKE + (i << 24) for i in range(8)]
+
+    def calls(x, y, z, u, v, ws):
+        return [("route", clib.moe_route_topk(x, 0, 4, 8, 8, 2, 0, y, z, None)),
+                ("route_backward", clib.moe_route_topk_backward(x, 0, 4, 8, 8, 2, 0, u, v, y, None)),
+                ("sort", clib.moe_sort_tokens(x, 4, 2, 8, y, z, u, None, 0, None)),
+                ("sort_long", clib.moe_sort_tokens(far[6], 1 << 15, 2, 8, y, far[5], far[7], x, 1 << 20, None)),
+                ("checkpoint", clib.quantize_fp8_checkpoint(x, 1, 4, 8, 8, y, z, None)),
+                ("swiglu", clib.swiglu_fp8(x, 1, 4, 8, 16, y, z, u, None)),
+                ("swiglu_backward", clib.swiglu_fp8_backward(x, 1, 4, 8, 8, z, u, y, None)),
+                ("dispatch", clib.moe_dispatch(x, 1, 4, 8, 8, z, 2, y, None)),
+                ("combine", clib.moe_combine(x, 1, 4, 8, 8, z, u, 2, y, None)),
+                ("combine_backward", clib.moe_combine_backward(x, 1, 4, 8, 8, z, 8, u, v, 2, y, far[7], None)),
+                ("wgrad", clib.grouped_wgrad_fp8(x, 4, 8, 8, z, u, 4, 16, None, v, 1, y, 0, 0, ws, 1 << 20, None))]
+    for name, status in calls(far[0], far[0] + 16, far[1], far[2], far[3], far[4]):
+        assert status == -1, name
+    # two outputs of one call
+    assert clib.moe_route_topk(far[0], 0, 4, 8, 8, 2, 0, far[1], far[1] + 16, None) == -1
+    assert clib.moe_sort_tokens(far[0], 4, 2, 8, far[1], far[2], far[2] + 4, None, 0, None) == -1
+    assert clib.swiglu_fp8(far[0], 1, 4, 8, 16, far[1], far[2], far[2] + 60, None) == -1
+    assert clib.quantize_fp8_checkpoint(far[0], 1, 4, 8, 8, far[1], far[1] + 28, None) == -1
+    assert clib.moe_combine_backward(far[0], 1, 4, 8, 8, far[1], 8, far[2], far[3], 2, far[4], far[4] + 124, None) == -1
+    # d_rows over rows: only the same matrix
+    assert clib.moe_combine_backward(far[0], 1, 4, 8, 8, far[1], 16, far[2], far[3], 2, far[1], far[4], None) == -1
+    assert clib.moe_combine_backward(far[0], 1, 4, 8, 8, far[1], 8, far[2], far[3], 2, far[1] + 16, far[4], None) == -1
+    # the workspace over an input, over dW
+    assert clib.grouped_wgrad_fp8(far[0], 4, 8, 8, far[1], far[2], 4, 16, None, far[3], 1, far[4], 0, 0, far[0], 1 << 20, None) == -1
+    assert clib.grouped_wgrad_fp8(far[0], 4, 8, 8, far[1], far[2], 4, 16, None, far[3], 1, far[4], 0, 0, far[4], 1 << 20, None) == -1
