@@ -493,11 +493,11 @@ def _pitched(x: torch.Tensor, name: str) -> int:
     (rows, cols), (pitch, step) = x.shape, x.stride()
     if cols > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if pitch >= cols > 0:
-        return pitch
-    if rows > 1 and cols > 0:
+    if rows <= 1 or cols == 0:  # no row has a next one, or no row has an element
+        return cols
+    if pitch < cols:
         raise ValueError(f"{name} has overlapping rows")
-    return max(cols, 1)
+    return pitch
 
 
 def _exact(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device) -> torch.Tensor:
