@@ -522,8 +522,11 @@ def moe_route_topk(logits: torch.Tensor, top_k: int, normalize: str = "topk", st
     (softmax over the chosen logits) or "all" (over every logit)."""
     ld = _pitched(logits, "logits")
     T, E = logits.shape
-    ids = _new((T, max(top_k, 0)), torch.int32, logits.device, stream)
-    weights = _new((T, max(top_k, 0)), torch.float32, logits.device, stream)
+    if abs(top_k) >= 1 << 31:
+        raise ValueError("top_k must fit in 32 bits")
+    slots = (T, top_k if 0 < top_k <= E else 0)  # none: refused below
+    ids = _new(slots, torch.int32, logits.device, stream)
+    weights = _new(slots, torch.float32, logits.device, stream)
     _check("moe_route_topk", lib().moe_route_topk(
         logits.data_ptr(), _DTYPE[logits.dtype], T, E, ld, top_k, _NORMALIZE[normalize],
         ids.data_ptr(), weights.data_ptr(), _stream(stream)))
@@ -558,8 +561,8 @@ def moe_sort_tokens(ids: torch.Tensor, E: int, ws: Optional[torch.Tensor] = None
     T, k = ids.shape
     dev = ids.device
     _exact(ids, "ids", (T, k), torch.int32, dev)
-    if E < 1:
-        raise ValueError("E must be positive")
+    if not 0 < E < 1 << 31:
+        raise ValueError("E must be positive and fit in 32 bits")
     offsets = _new(E + 1, torch.int32, dev, stream)
     row_token = _new(T * k, torch.int32, dev, stream)
     slot_row = _new((T, k), torch.int32, dev, stream)

@@ -1,5 +1,5 @@
 """Edges of the routed-expert calls' arguments: matrices of one row and of no
-columns.
+columns, counts beyond 32 bits.
 
 Tolerance of the weight gradient of one row: the product of two bf16 numbers is
 exact in float32: none.
@@ -38,3 +38,23 @@ def test_weight_gradient_of_no_outputs(lib):
     for d in (torch.empty((5, 0), dtype=torch.bfloat16, device="cuda"),
               torch.ones((5, 16), dtype=torch.bfloat16, device="cuda")[:, :0]):
         assert lib.grouped_wgrad_fp8(d, codes, scales, off).shape == (2, 0, 32)
+
+
+def test_refused_top_k_allocates_nothing(lib):
+    x = torch.zeros((1 << 20, 8), device="cuda")
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    with pytest.raises(lib.Q4Error) as e:
+        lib.moe_route_topk(x, 1 << 10)
+    assert e.value.status == -1
+    assert torch.cuda.max_memory_allocated() - before < 1 << 20
+
+
+def test_counts_beyond_32_bits_are_refused(lib):
+    """2^32 + n is not n."""
+    x = torch.zeros((1, 8), device="cuda")
+    ids = torch.zeros((1, 2), dtype=torch.int32, device="cuda")
+    for call in (lambda: lib.moe_route_topk(x, (1 << 32) + 2), lambda: lib.moe_sort_tokens(ids, (1 << 32) + 4),
+                 lambda: lib.moe_route_topk(x, 2 - (1 << 32))):
+        with pytest.raises(ValueError):
+            call()
