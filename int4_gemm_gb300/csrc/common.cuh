@@ -38,9 +38,11 @@ __device__ __forceinline__ unsigned long long globaltimer_ns() {
 // griddepcontrol.launch_dependents: the next kernel is released only as their
 // blocks exit.  Releasing it at kernel entry let its blocks occupy SM slots
 // while this kernel still ran and made the short MXFP4 step (quantize +
-// split-K GEMM) about 1 us slower, with no gain on the longer steps.  The
-// W4A16 GEMM does release its successor early, so that the next decode GEMM
-// streams its weights under this one's tail.
+// split-K GEMM) about 1 us slower, with no gain on the longer steps.  Two
+// kernels do release their successor early: the W4A16 GEMM, so that the next
+// decode GEMM streams its weights under this one's tail, and the weight
+// gradient's restore kernel, whose successor is always the product of the same
+// call, which sets up its barriers and tensor memory meanwhile.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------

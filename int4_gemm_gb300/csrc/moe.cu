@@ -153,9 +153,11 @@ struct Keys {
 
 constexpr int kRouteWarps = 4;
 
-// One warp per token.  Bound by the latency and issue of the rounds: 16384 x
-// 256 bf16, top-8 and softmax over all, takes 12.1 us (its gradient 6.2), where
-// reading the 8 MB takes 1.2 at the copy rate.
+// One warp per token.  Bound by the integer pipe in the rounds (69% of the issue
+// slots while the SMs run, 4.7 warps ready per cycle, the others waiting for that
+// pipe rather than for memory): 16384 x 256 bf16, top-8 and softmax over all, takes
+// 12.1 us (its gradient 6.2, waiting for its loads), where reading the 8 MB takes 1.2
+// at the copy rate.
 template <typename T, int NV>
 __global__ void __launch_bounds__(kRouteWarps * kWarp)
     route_kernel(const T* __restrict__ logits, int64_t tokens, int E, int64_t ld, int top_k, int over_all,
