@@ -19,6 +19,10 @@
  *  FP8     E4M3 bytes (one per element), one FP32 scale per 128 x 128 weight
  *          block or per (1, 128) activation block.  "Quantization in
  *          deployment", "Fake quantization" (fp8_blockwise) and exercise 2.
+ *  INT8    symmetric integers in [-127, 127], one FP32 scale amax / 127 per row
+ *          (per token of the activations, per output channel of the weights).
+ *          "LLM quantization", the eight-weight worked example (scale amax /
+ *          127).
  *
  * The E2M1 code of a value y = clamp(x / S, -6, 6) is the nearest of
  * 0, 0.5, 1, 1.5, 2, 3, 4, 6 with ties going to the smaller magnitude; its
@@ -90,7 +94,10 @@ typedef enum {
   Q4_OP_GEMM_W4A8 = 8,          /* needs none today: 0 */
   Q4_OP_GEMM_W4A4_MXFP4_FUSED = 9,
   Q4_OP_MOE_SORT = 10,          /* M = slots T * top_k, N = experts */
-  Q4_OP_GROUPED_WGRAD_FP8 = 11  /* R, N, K and E via q4_workspace_size_wgrad */
+  Q4_OP_GROUPED_WGRAD_FP8 = 11, /* R, N, K and E via q4_workspace_size_wgrad */
+  Q4_OP_GEMM_W8A8_INT8 = 12,
+  Q4_OP_RMS_NORM_BACKWARD = 13, /* M = rows, K = width H */
+  Q4_OP_MOE_BALANCE_LOSS = 14   /* M = tokens T, N = experts */
 } q4_op;
 
 /*
@@ -490,6 +497,100 @@ q4_status grouped_wgrad_fp8(const void* d_y_bf16, int64_t R, int64_t N, int64_t 
                             const int32_t* row_token, const int32_t* expert_offsets, int E,
                             void* dW, int w_dtype, int accumulate, void* ws, size_t ws_bytes,
                             q4_stream_t stream);
+
+/*
+ * 8-bit integers with one scale per row ("LLM quantization", the eight-weight
+ * worked example, whose INT8 scale is amax / 127): for every row of x [rows, K]
+ * (row pitch ld), in float32 with IEEE rounding,
+ *   s = max(amax, 1e-12) / 127;  q = rint(x / s), ties to even, in [-127, 127].
+ * codes: int8 [rows, K]; scales: float [rows].  Any K >= 1.  A non-finite input
+ * latches Q4_ERR_NONFINITE.  Weights [N, K] get one scale per output channel,
+ * activations [M, K] one per token.
+ *
+ * gemm_w8a8_int8: C[m, n] = sa[m] * sb[n] * sum_k qa[m, k] * qb[n, k].  The sum is
+ * the exact integer (any int8 codes, -128 included), which is rounded to FP32
+ * once, then multiplied by sa[m], then by sb[n]; C is FP32 or, rounded once
+ * more, bf16 (c_dtype Q4_F32 or Q4_BF16), 16-byte aligned, [M, N] contiguous.
+ * qa, qb: 16-byte aligned.  K % 16 == 0, K < 131072 (the sum fits in 32 bits);
+ * any M and N.  ws: q4_workspace_size(Q4_OP_GEMM_W8A8_INT8, M, N, K) bytes.
+ */
+q4_status quantize_int8(const void* x, int x_dtype, int64_t rows, int64_t K, int64_t ld, int8_t* codes,
+                        float* scales, q4_stream_t stream);
+q4_status gemm_w8a8_int8(const int8_t* qa, const float* sa, const int8_t* qb, const float* sb, int64_t M,
+                         int64_t N, int64_t K, void* C, int c_dtype, void* ws, size_t ws_bytes,
+                         q4_stream_t stream);
+
+/*
+ * Root-mean-square norm with the residual's addition.  For every row, in FP32:
+ *   h = x + residual;  rstd = 1 / sqrt(mean(h^2) + eps);  y = h * rstd * weight
+ * x, residual: [rows, H] of dtype with row pitches (in elements); residual NULL:
+ * h = x.  weight: [H] of w_dtype (dtype or Q4_F32), NULL: all 1.  eps > 0.
+ * 1 <= H <= 32768.  h and y are rounded once each to dtype (y and the 8-bit
+ * codes are taken from the unrounded h):
+ *   rms_norm       y [rows, H];
+ *   rms_norm_fp8   E4M3 codes [rows, H] of y, one FP32 scale per row and 128
+ *                  columns, max(amax, 1e-12) / 448, scales [rows, ceil(H / 128)]:
+ *                  the activations of gemm_fp8_blockwise and gemm_w4a8 (where
+ *                  H % 128 == 0) and an 8-bit checkpoint for grouped_wgrad_fp8;
+ *   rms_norm_int8  integers int8 [rows, H], one FP32 scale per row, max(amax,
+ *                  1e-12) / 127, scales [rows]: gemm_w8a8_int8's activations.
+ * The 8-bit forms write y too where y is not NULL.  h [rows, H] (NULL: not
+ * written) may be residual itself (the same address, ld_residual = H); rstd
+ * [rows] FP32 (NULL: not written) is what the gradient needs.  A row whose
+ * input, sum of squares or scale is not finite latches Q4_ERR_NONFINITE.
+ *
+ * rms_norm_backward: from d_y [rows, H] (the gradient of y), h and rstd, with
+ * g = d_y * weight,
+ *   d_x = rstd * (g - h * rstd^2 * mean(g * h)) + d_h      [rows, H], dtype
+ *   d_weight = sum over rows of d_y * h * rstd             [H], FP32
+ * d_x is the gradient of x and of residual alike.  d_h (NULL: none) is the
+ * gradient that reaches h by other ways (the residual stream); d_x may be d_h
+ * itself (the same address, ld_d_h = H).  d_weight NULL: not computed.  The sum
+ * over rows has a fixed order.  ws: q4_workspace_size(Q4_OP_RMS_NORM_BACKWARD,
+ * rows, 0, H) bytes (not needed without d_weight).
+ *
+ * But for those two in-place forms outputs and workspace overlap neither inputs
+ * nor one another (else Q4_ERR_INVALID_ARG); so it is for quantize_int8,
+ * gemm_w8a8_int8 and moe_balance_loss with its gradient, too.
+ */
+q4_status rms_norm(const void* x, int dtype, int64_t rows, int64_t H, int64_t ldx, const void* residual,
+                   int64_t ld_residual, const void* weight, int w_dtype, float eps, void* y, void* h,
+                   float* rstd, q4_stream_t stream);
+q4_status rms_norm_fp8(const void* x, int dtype, int64_t rows, int64_t H, int64_t ldx, const void* residual,
+                       int64_t ld_residual, const void* weight, int w_dtype, float eps, uint8_t* codes,
+                       float* scales, void* y, void* h, float* rstd, q4_stream_t stream);
+q4_status rms_norm_int8(const void* x, int dtype, int64_t rows, int64_t H, int64_t ldx, const void* residual,
+                        int64_t ld_residual, const void* weight, int w_dtype, float eps, int8_t* codes,
+                        float* scales, void* y, void* h, float* rstd, q4_stream_t stream);
+q4_status rms_norm_backward(const void* d_y, int dtype, int64_t rows, int64_t H, int64_t ld_d_y, const void* h,
+                            int64_t ld_h, const float* rstd, const void* weight, int w_dtype, const void* d_h,
+                            int64_t ld_d_h, void* d_x, float* d_weight, void* ws, size_t ws_bytes,
+                            q4_stream_t stream);
+
+/*
+ * Balance loss of the router, beside moe_route_topk: with p[t] the softmax of
+ * logits[t] over the experts above -inf (a logit of -inf masks its expert, as do
+ * NaN and +inf, which latch Q4_ERR_NONFINITE), n the tokens that have such an
+ * expert, and counts[e] the slots of ids [T, top_k] with id e (ids outside
+ * [0, E), dropped slots, count nowhere),
+ *   f[e] = counts[e] * E / (n * top_k),  mean[e] = sum_t p[t, e] / n,
+ *   loss = coeff * sum_e f[e] * mean[e]     (coeff where the load is uniform).
+ * counts: int32 [E + 1], the last entry n; mean: float [E]; loss: one float.
+ * Where n = 0, loss and mean are 0.  logits: [T, E] of dtype, row pitch ld.
+ * moe_balance_loss_backward: with the counts taken as constants,
+ *   d_logits[t, e] = *d_loss * coeff / n * p[t, e] * (f[e] - sum_j p[t, j] f[j])
+ * [T, E] of dtype, contiguous; accumulate != 0 adds it to what d_logits holds
+ * (moe_route_topk_backward's gradient) and rounds the sum once.  d_loss: one
+ * device float.  Softmax and sums are FP32, in a fixed order.
+ * 1 <= top_k <= min(E, 32), E <= 1024, T * top_k < 2^30; coeff finite.
+ * ws: q4_workspace_size(Q4_OP_MOE_BALANCE_LOSS, T, E, 0) bytes.
+ */
+q4_status moe_balance_loss(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const int32_t* ids,
+                           int top_k, float coeff, float* loss, int32_t* counts, float* mean, void* ws,
+                           size_t ws_bytes, q4_stream_t stream);
+q4_status moe_balance_loss_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld,
+                                    const int32_t* counts, int top_k, const float* d_loss, float coeff,
+                                    int accumulate, void* d_logits, q4_stream_t stream);
 
 /*
  * gemm_w4a4_nvfp4 without a workspace, for callers that cannot give the

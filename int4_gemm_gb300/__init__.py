@@ -33,6 +33,7 @@ OP_GROUPED_GEMM_MOE, OP_GEMM_W4A16_NVFP4, OP_GEMM_W4A16_MXFP4 = 4, 5, 6
 OP_GEMM_FP8_BLOCKWISE, OP_GEMM_W4A8 = 7, 8
 OP_GEMM_W4A4_MXFP4_FUSED = 9
 OP_MOE_SORT, OP_GROUPED_WGRAD_FP8 = 10, 11
+OP_GEMM_W8A8_INT8, OP_RMS_NORM_BACKWARD, OP_MOE_BALANCE_LOSS = 12, 13, 14
 
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 _LAYOUT = {"rowmajor": ROWMAJOR, "mma": MMA}
@@ -104,6 +105,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     _sig(lib, "swiglu_fp8", I, P, I, I64, I64, I64, P, P, P, P)
     _sig(lib, "swiglu_fp8_backward", I, P, I, I64, I64, I64, P, P, P, P)
     _sig(lib, "grouped_wgrad_fp8", I, P, I64, I64, I64, P, P, I64, I64, P, P, I, P, I, I, P, SZ, P)
+    F = ctypes.c_float
+    _sig(lib, "quantize_int8", I, P, I, I64, I64, I64, P, P, P)
+    _sig(lib, "gemm_w8a8_int8", I, P, P, P, P, I64, I64, I64, P, I, P, SZ, P)
+    _sig(lib, "rms_norm", I, P, I, I64, I64, I64, P, I64, P, I, F, P, P, P, P)
+    for name in ("rms_norm_fp8", "rms_norm_int8"):
+        _sig(lib, name, I, P, I, I64, I64, I64, P, I64, P, I, F, P, P, P, P, P, P)
+    _sig(lib, "rms_norm_backward", I, P, I, I64, I64, I64, P, I64, P, P, I, P, I64, P, P, P, SZ, P)
+    _sig(lib, "moe_balance_loss", I, P, I, I64, I64, I64, P, I, F, P, P, P, P, SZ, P)
+    _sig(lib, "moe_balance_loss_backward", I, P, I, I64, I64, I64, P, I, P, F, I, P, P)
     _sig(lib, "q4_sync_status", I, P)
     _sig(lib, "q4_status_string", ctypes.c_char_p, I)
     _sig(lib, "q4_set_wait_timeout_ms", I, I)
@@ -734,6 +744,189 @@ def grouped_wgrad_fp8(d_y: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
         expert_offsets.data_ptr(), E, out.data_ptr(), _DTYPE[out.dtype], int(accumulate),
         ws.data_ptr(), ws.numel(), _stream(stream)))
     return out
+
+
+# --------------------------------------------------------------------------- 8-bit integers
+
+def quantize_int8(x: torch.Tensor, stream=None):
+    """8-bit integers of x [rows, K] (any row pitch) -> (codes int8 [rows, K],
+    scales float32 [rows] = max(amax, 1e-12) / 127)."""
+    ld = _pitched(x, "x")
+    rows, K = x.shape
+    codes = _new((rows, K), torch.int8, x.device, stream)
+    scales = _new(rows, torch.float32, x.device, stream)
+    _check("quantize_int8", lib().quantize_int8(x.data_ptr(), _DTYPE[x.dtype], rows, K, ld, codes.data_ptr(),
+                                                scales.data_ptr(), _stream(stream)))
+    return codes, scales
+
+
+def gemm_w8a8_int8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Tensor, out_dtype=torch.bfloat16,
+                   out=None, stream=None) -> torch.Tensor:
+    """C [M, N] = sa * sb * (qa . qb^T) with exact integer sums: qa int8 [M, K]
+    with sa float32 [M], qb int8 [N, K] with sb float32 [N] (quantize_int8,
+    rms_norm_int8).  K % 16 == 0, K < 131072; out float32 or bfloat16."""
+    if qa.dim() != 2 or qb.dim() != 2 or not qa.is_cuda:
+        raise ValueError("qa and qb must be 2-D CUDA tensors")
+    (M, K), N, dev = qa.shape, qb.shape[0], qa.device
+    _exact(qa, "qa", (M, K), torch.int8, dev)
+    _exact(qb, "qb", (N, K), torch.int8, dev)
+    _exact(sa, "sa", (M,), torch.float32, dev)
+    _exact(sb, "sb", (N,), torch.float32, dev)
+    C = _out(out, M, N, out_dtype if out is None else out.dtype, dev, stream)
+    if C.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("the product is float32 or bfloat16")
+    _check("gemm_w8a8_int8", lib().gemm_w8a8_int8(qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), M, N, K,
+                                                  C.data_ptr(), _DTYPE[C.dtype], None, 0, _stream(stream)))
+    return C
+
+
+# --------------------------------------------------------------------------- norm
+
+def _norm_operands(x, weight, residual, h_out, stream):
+    """(row pitches of x and residual, weight's dtype code, h)."""
+    ldx, (rows, H), dev = _pitched(x, "x"), x.shape, x.device
+    ldr = 0
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype != x.dtype or residual.device != dev:
+            raise ValueError(f"residual must be a {x.dtype} tensor of shape ({rows}, {H}) on {dev}")
+        ldr = _pitched(residual, "residual")
+    elif h_out is not None:
+        raise ValueError("h_out needs a residual (without one h is x)")
+    h = None if residual is None else _out(h_out, rows, H, x.dtype, dev, stream)
+    return ldx, ldr, _norm_weight(weight, x), h
+
+
+def _norm_weight(weight, x) -> int:
+    if weight is None:
+        return F32
+    return _DTYPE[_exact(weight, "weight", (x.shape[1],), torch.float32 if weight.dtype == torch.float32 else x.dtype,
+                         x.device).dtype]
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+             eps: float = 1e-6, out=None, h_out=None, stream=None):
+    """Root-mean-square norm of h = x + residual ([rows, H], any row pitch; no
+    residual: h = x) -> (y [rows, H] = h * rstd * weight, h [rows, H] or None
+    without a residual, rstd float32 [rows]).  weight [H] in x's type or
+    float32, None: all 1.  ``h_out`` may be residual itself."""
+    ldx, ldr, wd, h = _norm_operands(x, weight, residual, h_out, stream)
+    rows, H = x.shape
+    y = _out(out, rows, H, x.dtype, x.device, stream)
+    rstd = _new(rows, torch.float32, x.device, stream)
+    _check("rms_norm", lib().rms_norm(x.data_ptr(), _DTYPE[x.dtype], rows, H, ldx, _ptr(residual), ldr, _ptr(weight), wd,
+                                      eps, y.data_ptr(), _ptr(h), rstd.data_ptr(), _stream(stream)))
+    return y, h, rstd
+
+
+def _norm_8bit(fn, code_dtype, scales_shape, x, weight, residual, eps, need_y, h_out, stream):
+    ldx, ldr, wd, h = _norm_operands(x, weight, residual, h_out, stream)
+    (rows, H), dev = x.shape, x.device
+    codes = _new((rows, H), code_dtype, dev, stream)
+    scales = _new(scales_shape, torch.float32, dev, stream)
+    y = _new((rows, H), x.dtype, dev, stream) if need_y else None
+    rstd = _new(rows, torch.float32, dev, stream)
+    _check(fn, getattr(lib(), fn)(x.data_ptr(), _DTYPE[x.dtype], rows, H, ldx, _ptr(residual), ldr, _ptr(weight), wd, eps,
+                                  codes.data_ptr(), scales.data_ptr(), _ptr(y), _ptr(h), rstd.data_ptr(), _stream(stream)))
+    return codes, scales, y, h, rstd
+
+
+def rms_norm_fp8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, need_y: bool = False, h_out=None, stream=None):
+    """rms_norm with its result in FP8 -> (codes u8 [rows, H] E4M3, scales
+    float32 [rows, ceil(H/128)], y or None without ``need_y``, h or None without
+    a residual, rstd): the activations of gemm_fp8_blockwise and gemm_w4a8, and
+    an 8-bit checkpoint for grouped_wgrad_fp8."""
+    return _norm_8bit("rms_norm_fp8", torch.uint8, (x.shape[0], -(-x.shape[-1] // 128)), x, weight, residual, eps, need_y,
+                      h_out, stream)
+
+
+def rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                  eps: float = 1e-6, need_y: bool = False, h_out=None, stream=None):
+    """rms_norm with its result in 8-bit integers -> (codes int8 [rows, H],
+    scales float32 [rows], y or None without ``need_y``, h or None without a
+    residual, rstd): gemm_w8a8_int8's activations."""
+    return _norm_8bit("rms_norm_int8", torch.int8, (x.shape[0],), x, weight, residual, eps, need_y, h_out, stream)
+
+
+def rms_norm_backward(d_y: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                      d_h: Optional[torch.Tensor] = None, need_d_weight: bool = True, out=None,
+                      ws: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of rms_norm: (d_x [rows, H], d_weight float32 [H] or None
+    without ``need_d_weight``) from d_y, h (x where there was no residual), rstd
+    and weight.  d_x is the gradient of x and of residual alike; d_h, the
+    gradient that reaches h by other ways, is added to it, and ``out`` may be
+    d_h itself.  ``ws`` from ``workspace(OP_RMS_NORM_BACKWARD, rows, 0, H, device)``."""
+    ldy, ldh = _pitched(d_y, "d_y"), _pitched(h, "h")
+    (rows, H), dev = d_y.shape, d_y.device
+    ldd = 0
+    for name, t in (("h", h), ("d_h", d_h)):
+        if t is not None and (t.shape != d_y.shape or t.dtype != d_y.dtype or t.device != dev):
+            raise ValueError(f"{name} must be a {d_y.dtype} tensor of shape ({rows}, {H}) on {dev}")
+    if d_h is not None:
+        ldd = _pitched(d_h, "d_h")
+    _exact(rstd, "rstd", (rows,), torch.float32, dev)
+    wd = _norm_weight(weight, d_y)
+    d_x = _out(out, rows, H, d_y.dtype, dev, stream)
+    dw = _new(H, torch.float32, dev, stream) if need_d_weight else None
+    L = lib()
+    if ws is None:
+        n = L.q4_workspace_size(OP_RMS_NORM_BACKWARD, rows, 0, H) if need_d_weight else 0
+        ws = _empty(n, dev, stream) if n else None
+    else:
+        _given(ws, stream)
+    _check("rms_norm_backward", L.rms_norm_backward(
+        d_y.data_ptr(), _DTYPE[d_y.dtype], rows, H, ldy, h.data_ptr(), ldh, rstd.data_ptr(), _ptr(weight), wd, _ptr(d_h), ldd,
+        d_x.data_ptr(), _ptr(dw), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+    return d_x, dw
+
+
+# --------------------------------------------------------------------------- balance loss
+
+def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, coeff: float = 1.0, ws: Optional[torch.Tensor] = None,
+                     stream=None):
+    """The router's balance loss from logits [T, E] (any row pitch) and ids int32
+    [T, top_k] (moe_route_topk's, or with dropped slots as -1) -> (loss float32
+    [1], counts int32 [E + 1]: slots per expert, then the tokens that took part,
+    mean float32 [E]: the experts' mean probabilities).  ``ws`` from
+    ``workspace(OP_MOE_BALANCE_LOSS, T, E, 0, device)``."""
+    ld = _pitched(logits, "logits")
+    (T, E), dev = logits.shape, logits.device
+    if ids.dim() != 2:
+        raise ValueError("ids must be a [T, top_k] tensor")
+    k = ids.shape[1]
+    _exact(ids, "ids", (T, k), torch.int32, dev)
+    loss = _new(1, torch.float32, dev, stream)
+    counts = _new(E + 1, torch.int32, dev, stream)
+    mean = _new(E, torch.float32, dev, stream)
+    L = lib()
+    if ws is None:
+        n = L.q4_workspace_size(OP_MOE_BALANCE_LOSS, T, E, 0)
+        ws = _empty(n, dev, stream) if n else None
+    else:
+        _given(ws, stream)
+    _check("moe_balance_loss", L.moe_balance_loss(
+        logits.data_ptr(), _DTYPE[logits.dtype], T, E, ld, ids.data_ptr(), k, coeff, loss.data_ptr(), counts.data_ptr(),
+        mean.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+    return loss, counts, mean
+
+
+def moe_balance_loss_backward(logits: torch.Tensor, counts: torch.Tensor, top_k: int, d_loss: torch.Tensor,
+                              coeff: float = 1.0, out=None, accumulate: bool = False, stream=None) -> torch.Tensor:
+    """d_logits [T, E] (logits' dtype) of moe_balance_loss from d_loss float32 [1]
+    and the counts of the forward call.  ``accumulate`` adds it to ``out``."""
+    ld = _pitched(logits, "logits")
+    (T, E), dev = logits.shape, logits.device
+    _exact(counts, "counts", (E + 1,), torch.int32, dev)
+    _exact(d_loss, "d_loss", (1,), torch.float32, dev)
+    if abs(top_k) >= 1 << 31:
+        raise ValueError("top_k must fit in 32 bits")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    d = _out(out, T, E, logits.dtype, dev, stream)
+    _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
+        logits.data_ptr(), _DTYPE[logits.dtype], T, E, ld, counts.data_ptr(), top_k, d_loss.data_ptr(), coeff,
+        int(accumulate), d.data_ptr(), _stream(stream)))
+    return d
 
 
 def sync_status(stream=None) -> int:

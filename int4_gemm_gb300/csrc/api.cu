@@ -312,6 +312,12 @@ __global__ void wait_probe_kernel(KernelCtl ctl) {
 
 using namespace q4;
 
+namespace {
+constexpr int kMaxTopK = 32, kMaxRouteExperts = 1024;
+constexpr int64_t kMaxSlots = INT32_MAX / 2;
+constexpr int64_t kMaxNormWidth = 32768, kMaxInt8K = 131071;  // 128 * 128 * K < 2^31
+}  // namespace
+
 extern "C" {
 
 size_t q4_mma_scales_bytes(int64_t rows, int64_t nsf) {
@@ -334,6 +340,9 @@ size_t q4_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
     case Q4_OP_GEMM_W4A8: return 0;
     case Q4_OP_MOE_SORT: return moe_sort_workspace_bytes(M, N);
     case Q4_OP_GROUPED_WGRAD_FP8: return 0;  // needs E: q4_workspace_size_wgrad
+    case Q4_OP_GEMM_W8A8_INT8: return 0;
+    case Q4_OP_RMS_NORM_BACKWARD: return K >= 1 && K <= kMaxNormWidth ? norm_backward_workspace_bytes(M, K) : 0;
+    case Q4_OP_MOE_BALANCE_LOSS: return M > 0 && N >= 1 && N <= kMaxRouteExperts ? balance_workspace_bytes(M, N) : 0;
     default: return 0;
   }
 }
@@ -649,9 +658,6 @@ q4_status grouped_gemm_moe(const void* tokens_bf16, int64_t T, int64_t K,
 }
 
 namespace {
-constexpr int kMaxTopK = 32, kMaxRouteExperts = 1024;
-constexpr int64_t kMaxSlots = INT32_MAX / 2;
-
 size_t elem_bytes(int dtype) { return dtype == Q4_F32 ? 4 : 2; }
 
 // Checks shared by the calls that move rows between token and expert order.
@@ -886,6 +892,153 @@ q4_status grouped_wgrad_fp8(const void* d_y_bf16, int64_t R, int64_t N, int64_t 
   a.row_token = row_token; a.offsets = expert_offsets; a.E = E;
   a.dw = dW; a.w_dtype = w_dtype; a.accumulate = accumulate != 0; a.ws = ws;
   return launch_wgrad(a, s);
+}
+
+q4_status quantize_int8(const void* x, int x_dtype, int64_t rows, int64_t K, int64_t ld, int8_t* codes, float* scales,
+                        q4_stream_t stream) {
+  if (!valid_dtype(x_dtype) || rows < 0 || K < 1 || ld < K) return Q4_ERR_INVALID_ARG;
+  if (rows > INT32_MAX / 2 || K > INT32_MAX / 4) return Q4_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0) return Q4_OK;
+  if (!elem_ptr(x, x_dtype) || !codes || !word_ptr(scales)) return Q4_ERR_INVALID_ARG;
+  const int64_t b = elem_bytes(x_dtype);
+  if (!apart({{codes, rows * K}, {scales, rows * 4}}, {{x, rows, K * b, ld * b}})) return Q4_ERR_INVALID_ARG;
+  return launch_quantize_int8(x, x_dtype, rows, K, ld, codes, scales, reinterpret_cast<cudaStream_t>(stream));
+}
+
+q4_status gemm_w8a8_int8(const int8_t* qa, const float* sa, const int8_t* qb, const float* sb, int64_t M, int64_t N, int64_t K,
+                         void* C, int c_dtype, void* ws, size_t ws_bytes, q4_stream_t stream) {
+  (void)ws;  // needs no workspace (q4_workspace_size gives 0)
+  (void)ws_bytes;
+  if (M < 0 || N < 0 || K <= 0 || (c_dtype != Q4_F32 && c_dtype != Q4_BF16)) return Q4_ERR_INVALID_ARG;
+  if (K % 16 || K > kMaxInt8K || M > INT32_MAX / 2 || N > INT32_MAX / 2 || ceil_div(M, 64) * ceil_div(N, 64) > INT32_MAX / 2)
+    return Q4_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0 || N == 0) return Q4_OK;
+  if (!qa || !aligned(qa, 16) || !qb || !aligned(qb, 16) || !word_ptr(sa) || !word_ptr(sb) || !C || !aligned(C, 16))
+    return Q4_ERR_INVALID_ARG;
+  if (!apart({{C, M * N * (int64_t)elem_bytes(c_dtype)}}, {{qa, M * K}, {sa, M * 4}, {qb, N * K}, {sb, N * 4}}))
+    return Q4_ERR_INVALID_ARG;
+  return launch_int8_gemm(qa, sa, qb, sb, M, N, K, C, c_dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+namespace {
+q4_status check_norm(int dtype, int64_t rows, int64_t H, const void* weight, int w_dtype) {
+  if (!valid_dtype(dtype) || rows < 0 || H < 1) return Q4_ERR_INVALID_ARG;
+  if (weight && w_dtype != dtype && w_dtype != Q4_F32) return Q4_ERR_INVALID_ARG;
+  if (H > kMaxNormWidth || rows > INT32_MAX / 2) return Q4_ERR_UNSUPPORTED_SHAPE;
+  return Q4_OK;
+}
+
+q4_status norm_common(int form, const void* x, int dtype, int64_t rows, int64_t H, int64_t ldx, const void* residual,
+                      int64_t ld_residual, const void* weight, int w_dtype, float eps, void* codes, float* scales, void* y,
+                      void* h, float* rstd, q4_stream_t stream) {
+  const q4_status st = check_norm(dtype, rows, H, weight, w_dtype);
+  if (st != Q4_OK) return st;
+  if (ldx < H || (residual && ld_residual < H) || !(eps > 0.f) || eps > 3.0e38f) return Q4_ERR_INVALID_ARG;
+  if (rows == 0) return Q4_OK;
+  if (!elem_ptr(x, dtype) || !aligned(residual, elem_bytes(dtype)) || !aligned(weight, elem_bytes(w_dtype)) ||
+      !aligned(y, elem_bytes(dtype)) || !aligned(h, elem_bytes(dtype)) || !aligned(rstd, 4))
+    return Q4_ERR_INVALID_ARG;
+  if (form == Q4_NORM_PLAIN ? !y : !codes || !word_ptr(scales)) return Q4_ERR_INVALID_ARG;
+  const int64_t b = elem_bytes(dtype), per_row = form == Q4_NORM_FP8 ? ceil_div(H, 128) : 1;
+  const bool in_place = residual && h == residual && ld_residual == H;
+  const Extent xs{x, rows, H * b, ldx * b}, rs{in_place ? nullptr : residual, rows, H * b, ld_residual * b};
+  const Extent ws{weight, H * (int64_t)elem_bytes(w_dtype)};
+  if (!apart({{y, rows * H * b}, {h, rows * H * b}, {codes, rows * H}, {scales, rows * per_row * 4}, {rstd, rows * 4}},
+             {xs, rs, ws}))
+    return Q4_ERR_INVALID_ARG;
+  NormArgs a = {};
+  a.x = x; a.residual = residual; a.weight = weight;
+  a.rows = rows; a.H = H; a.ldx = ldx; a.ld_residual = ld_residual;
+  a.w_fp32 = w_dtype == Q4_F32; a.eps = eps;
+  a.h = h; a.y = y; a.codes = static_cast<uint8_t*>(codes); a.scales = scales; a.rstd = rstd;
+  return launch_norm(a, dtype, form, reinterpret_cast<cudaStream_t>(stream));
+}
+}  // namespace
+
+q4_status rms_norm(const void* x, int dtype, int64_t rows, int64_t H, int64_t ldx, const void* residual, int64_t ld_residual,
+                   const void* weight, int w_dtype, float eps, void* y, void* h, float* rstd, q4_stream_t stream) {
+  return norm_common(Q4_NORM_PLAIN, x, dtype, rows, H, ldx, residual, ld_residual, weight, w_dtype, eps, nullptr, nullptr, y, h,
+                     rstd, stream);
+}
+
+q4_status rms_norm_fp8(const void* x, int dtype, int64_t rows, int64_t H, int64_t ldx, const void* residual,
+                       int64_t ld_residual, const void* weight, int w_dtype, float eps, uint8_t* codes, float* scales, void* y,
+                       void* h, float* rstd, q4_stream_t stream) {
+  return norm_common(Q4_NORM_FP8, x, dtype, rows, H, ldx, residual, ld_residual, weight, w_dtype, eps, codes, scales, y, h, rstd,
+                     stream);
+}
+
+q4_status rms_norm_int8(const void* x, int dtype, int64_t rows, int64_t H, int64_t ldx, const void* residual,
+                        int64_t ld_residual, const void* weight, int w_dtype, float eps, int8_t* codes, float* scales, void* y,
+                        void* h, float* rstd, q4_stream_t stream) {
+  return norm_common(Q4_NORM_INT8, x, dtype, rows, H, ldx, residual, ld_residual, weight, w_dtype, eps, codes, scales, y, h,
+                     rstd, stream);
+}
+
+q4_status rms_norm_backward(const void* d_y, int dtype, int64_t rows, int64_t H, int64_t ld_d_y, const void* h, int64_t ld_h,
+                            const float* rstd, const void* weight, int w_dtype, const void* d_h, int64_t ld_d_h, void* d_x,
+                            float* d_weight, void* ws, size_t ws_bytes, q4_stream_t stream) {
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const q4_status st = check_norm(dtype, rows, H, weight, w_dtype);
+  if (st != Q4_OK) return st;
+  if (ld_d_y < H || ld_h < H || (d_h && ld_d_h < H) || !aligned(d_weight, 4)) return Q4_ERR_INVALID_ARG;
+  if (rows == 0) {  // a sum over nothing
+    if (d_weight) Q4_CUDA_TRY(cudaMemsetAsync(d_weight, 0, (size_t)H * sizeof(float), s));
+    return Q4_OK;
+  }
+  if (!elem_ptr(d_y, dtype) || !elem_ptr(h, dtype) || !word_ptr(rstd) || !aligned(weight, elem_bytes(w_dtype)) ||
+      !aligned(d_h, elem_bytes(dtype)) || !elem_ptr(d_x, dtype))
+    return Q4_ERR_INVALID_ARG;
+  const size_t need = d_weight ? norm_backward_workspace_bytes(rows, H) : 0;
+  if (need && (!ws || !aligned(ws, 256) || ws_bytes < need)) return Q4_ERR_WORKSPACE;
+  const int64_t b = elem_bytes(dtype);
+  const bool in_place = d_h && d_x == d_h && ld_d_h == H;
+  if (!apart({{d_x, rows * H * b}, {d_weight, H * 4}, {need ? ws : nullptr, (int64_t)need}},
+             {{d_y, rows, H * b, ld_d_y * b}, {h, rows, H * b, ld_h * b}, {rstd, rows * 4},
+              {weight, H * (int64_t)elem_bytes(w_dtype)}, {in_place ? nullptr : d_h, rows, H * b, ld_d_h * b}}))
+    return Q4_ERR_INVALID_ARG;
+  NormBackwardArgs a = {};
+  a.d_y = d_y; a.h = h; a.d_h = d_h; a.weight = weight;
+  a.rows = rows; a.H = H; a.ld_d_y = ld_d_y; a.ld_h = ld_h; a.ld_d_h = ld_d_h;
+  a.rstd = rstd; a.w_fp32 = w_dtype == Q4_F32; a.d_x = d_x;
+  return launch_norm_backward(a, dtype, d_weight, ws, s);
+}
+
+q4_status moe_balance_loss(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const int32_t* ids, int top_k,
+                           float coeff, float* loss, int32_t* counts, float* mean, void* ws, size_t ws_bytes,
+                           q4_stream_t stream) {
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const q4_status st = check_route(dtype, T, E, ld, top_k, Q4_ROUTE_ALL);
+  if (st != Q4_OK) return st;
+  if (!(coeff - coeff == 0.f) || !word_ptr(loss) || !word_ptr(counts) || !word_ptr(mean)) return Q4_ERR_INVALID_ARG;
+  const size_t need = T ? balance_workspace_bytes(T, E) : 0;
+  if (T && (!elem_ptr(logits, dtype) || !word_ptr(ids))) return Q4_ERR_INVALID_ARG;
+  if (need && (!ws || !aligned(ws, 256) || ws_bytes < need)) return Q4_ERR_WORKSPACE;
+  const int64_t b = elem_bytes(dtype);
+  if (!apart({{loss, 4}, {counts, (E + 1) * 4}, {mean, E * 4}, {need ? ws : nullptr, (int64_t)need}},
+             {{logits, T, E * b, ld * b}, {ids, T * top_k * 4}}))
+    return Q4_ERR_INVALID_ARG;
+  if (T == 0) {
+    Q4_CUDA_TRY(cudaMemsetAsync(loss, 0, sizeof(float), s));
+    Q4_CUDA_TRY(cudaMemsetAsync(counts, 0, (size_t)(E + 1) * sizeof(int32_t), s));
+    Q4_CUDA_TRY(cudaMemsetAsync(mean, 0, (size_t)E * sizeof(float), s));
+    return Q4_OK;
+  }
+  return launch_balance(logits, dtype, T, (int)E, ld, ids, top_k, coeff, loss, counts, mean, ws, s);
+}
+
+q4_status moe_balance_loss_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const int32_t* counts,
+                                    int top_k, const float* d_loss, float coeff, int accumulate, void* d_logits,
+                                    q4_stream_t stream) {
+  const q4_status st = check_route(dtype, T, E, ld, top_k, Q4_ROUTE_ALL);
+  if (st != Q4_OK) return st;
+  if (!(coeff - coeff == 0.f)) return Q4_ERR_INVALID_ARG;
+  if (T == 0) return Q4_OK;
+  if (!elem_ptr(logits, dtype) || !word_ptr(counts) || !word_ptr(d_loss) || !elem_ptr(d_logits, dtype)) return Q4_ERR_INVALID_ARG;
+  const int64_t b = elem_bytes(dtype);
+  if (!apart({{d_logits, T * E * b}}, {{logits, T, E * b, ld * b}, {counts, (E + 1) * 4}, {d_loss, 4}})) return Q4_ERR_INVALID_ARG;
+  return launch_balance_backward(logits, dtype, T, (int)E, ld, counts, top_k, d_loss, coeff, accumulate != 0, d_logits,
+                                 reinterpret_cast<cudaStream_t>(stream));
 }
 
 q4_status q4_sync_status(q4_stream_t stream) {

@@ -16,6 +16,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "elem.cuh"
 #include "internal.h"
 
 namespace q4 {
@@ -23,11 +24,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // The values of the two codes in the low 16 bits.
 __device__ __forceinline__ float2 e4m3x2_values(uint32_t codes) {
   uint32_t h;
@@ -47,39 +43,6 @@ __device__ __forceinline__ int scale_exponent(float amax) {
   return min((int)((b + 0x1fffffu) >> 23) - 127 - 8, kTopExponent);  // a non-finite block has the top one, too
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
-template <typename T>
-__device__ __forceinline__ T to_elem(float v);
-template <>
-__device__ __forceinline__ float to_elem<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 to_elem<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half to_elem<__half>(float v) { return __float2half_rn(v); }
-
-// Two 16-bit elements in one word.
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-template <typename T>
-__device__ __forceinline__ float2 unpack2(uint32_t w);
-template <>
-__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-template <>
-__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
 
 // silu's factor 1 / (1 + exp(-g)) with the fast exponential and reciprocal
 // (below 2^-17 relative error for |g| <= 88; below g = -87.3 it is 0 instead
@@ -359,15 +322,6 @@ __global__ void __launch_bounds__(kThreads)
   H::store(d_gate_up + k.row * 2 * I + c, l, k.n, g);
   H::store(d_gate_up + k.row * 2 * I + I + c, l, k.n, u);
 }
-
-template <typename F>
-q4_status by_dtype(int dtype, F&& f) {
-  if (dtype == Q4_F32) return f(float());
-  if (dtype == Q4_BF16) return f(__nv_bfloat16());
-  return f(__half());
-}
-
-inline bool mult(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // One turn per thread: the blocks of threads are many and alike, and the
 // hardware keeps the SMs full of them (a grid of 8 per SM that loops left the

@@ -158,6 +158,43 @@ struct WgradArgs {
 size_t wgrad_workspace_bytes(int64_t R, int64_t N, int64_t K, int E);
 q4_status launch_wgrad(const WgradArgs& a, cudaStream_t stream);
 
+// ---------------------------------------------------------------- norm
+enum { Q4_NORM_PLAIN = 0, Q4_NORM_FP8 = 1, Q4_NORM_INT8 = 2 };
+struct NormArgs {
+  const void *x, *residual, *weight;  // residual, weight: may be null
+  int64_t rows, H, ldx, ld_residual;
+  bool w_fp32;
+  float eps;
+  void *h, *y;  // may be null
+  uint8_t* codes;
+  float *scales, *rstd;  // rstd may be null
+};
+q4_status launch_norm(const NormArgs& a, int dtype, int form, cudaStream_t stream);
+struct NormBackwardArgs {
+  const void *d_y, *h, *d_h, *weight;  // d_h, weight: may be null
+  int64_t rows, H, ld_d_y, ld_h, ld_d_h;
+  const float* rstd;
+  bool w_fp32;
+  void* d_x;
+  float* partial;  // [grid, H], set by the launcher
+};
+size_t norm_backward_workspace_bytes(int64_t rows, int64_t H);
+q4_status launch_norm_backward(NormBackwardArgs a, int dtype, float* d_weight, void* ws, cudaStream_t stream);
+
+// ---------------------------------------------------------------- INT8
+q4_status launch_quantize_int8(const void* x, int dtype, int64_t rows, int64_t K, int64_t ld, int8_t* codes, float* scales,
+                               cudaStream_t stream);
+q4_status launch_int8_gemm(const int8_t* qa, const float* sa, const int8_t* qb, const float* sb, int64_t M, int64_t N, int64_t K,
+                           void* C, int c_dtype, cudaStream_t stream);
+
+// ---------------------------------------------------------------- balance loss
+size_t balance_workspace_bytes(int64_t tokens, int64_t E);
+q4_status launch_balance(const void* logits, int dtype, int64_t tokens, int E, int64_t ld, const int32_t* ids, int top_k,
+                         float coeff, float* loss, int32_t* counts, float* mean, void* ws, cudaStream_t stream);
+q4_status launch_balance_backward(const void* logits, int dtype, int64_t tokens, int E, int64_t ld, const int32_t* counts,
+                                  int top_k, const float* d_loss, float coeff, bool accumulate, void* d_logits,
+                                  cudaStream_t stream);
+
 // TMA descriptor creation through the driver entry point.
 q4_status make_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner_bytes, uint64_t rows,
                           uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows,
