@@ -502,7 +502,8 @@ q4_status grouped_wgrad_fp8(const void* d_y_bf16, int64_t R, int64_t N, int64_t 
  * 8-bit integers with one scale per row ("LLM quantization", the eight-weight
  * worked example, whose INT8 scale is amax / 127): for every row of x [rows, K]
  * (row pitch ld), in float32 with IEEE rounding,
- *   s = max(amax, 1e-12) / 127;  q = rint(x / s), ties to even, in [-127, 127].
+ *   s = max(amax, 1e-12) * (1 / 127, rounded);  q = rint(x / s), ties to even, in
+ *   [-127, 127].
  * codes: int8 [rows, K]; scales: float [rows].  Any K >= 1.  A non-finite input
  * latches Q4_ERR_NONFINITE.  Weights [N, K] get one scale per output channel,
  * activations [M, K] one per token.

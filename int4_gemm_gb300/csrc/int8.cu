@@ -3,7 +3,31 @@
 // with exact 32-bit integer sums.
 //
 // The quantizer follows the oracle step by step in FP32 with IEEE rounding:
-//   s = max(amax, 1e-12) / 127,  q = rint(x / s)  (ties to even)
+//   s = max(amax, 1e-12) * RN(1 / 127),  q = rint(x / s)  (ties to even)
+//
+// The product on this GPU's f16 tensor cores, which are far faster than its
+// integer ones: an 8-bit integer is an f16 number, a product of two (at most
+// 2^14) and the FP32 sum of 1024 of them (at most 2^24) are exact, and every
+// 1024 columns the sum is added to a 32-bit integer.  The weights are the M
+// operand of the MMA, its rows the tensor memory's lanes:
+//   warp 0       TMA producer: 128 columns of the weight rows and of the tokens
+//                per stage, as 8-bit codes;
+//   warps 4..11  converters, two groups of four that take turns of 64 columns:
+//                a thread reads its weight row's 64 codes and stores them as f16
+//                in tensor memory, the MMA's A operand; the tokens' codes go to
+//                shared memory as f16, swizzled, the B operand.  (With both
+//                operands in shared memory its 128 bytes per clock would bound
+//                the product: 96 KB per 64 columns of a 256 x 256 tile instead of
+//                64 KB.)
+//   warp 1       MMA issuer: two halves of the tile's tokens one after another,
+//                each into one of three accumulator slots, so that a slot is read
+//                while the next ones are filled;
+//   warps 12..19 promotion: slot -> 32-bit integers in registers, then scales and
+//                stores.
+// Large products run on CTA pairs (256 weight rows x 256 tokens, cta_group::2),
+// the others on single CTAs (128 weight rows x up to 256 tokens) whose K range is
+// split over a cluster where there are few tiles; the integer sums then meet in
+// distributed shared memory.
 #include <algorithm>
 
 #include "common.cuh"
@@ -30,7 +54,7 @@ __global__ void __launch_bounds__(kQuantThreads)
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
   __syncthreads();
   for (int w = 0; w < kQuantThreads / 32; ++w) top = max(top, part[w]);
-  const float s = __fdiv_rn(fmaxf(__uint_as_float(top), 1e-12f), 127.f);
+  const float s = fmaxf(__uint_as_float(top), 1e-12f) * (1.f / 127.f);
   if (threadIdx.x == 0) {
     scales[blockIdx.x] = s;
     if (nonfinite(__uint_as_float(top))) latch_status(status, Q4_ERR_NONFINITE);
@@ -40,56 +64,499 @@ __global__ void __launch_bounds__(kQuantThreads)
 }
 
 // ------------------------------------------------------------------ product
-constexpr int kTile = 64, kStep = 64, kPitch = kStep + 16;  // C tile, K bytes per stage, row pitch in shared memory
+constexpr int kRows = 128;        // weight rows of a CTA
+constexpr int kStageK = 128;      // columns per TMA stage
+constexpr int kChunk = 64;        // columns per conversion: 128 bytes of f16
+constexpr int kRunStages = 8;     // stages whose sums are exact in FP32: 1024 columns
+constexpr int kConvSlots = 4;     // tensor-memory slots of converted weights, 32 columns each
+constexpr int kAccSlots = 3;      // accumulator slots of up to 128 tokens
+constexpr uint32_t kTmemA = kAccSlots * 128;  // first column of the converted weights
+constexpr int kMaxStages = 12;
+constexpr uint32_t kWeightBytes = kRows * kStageK;
+constexpr int kConvWarp0 = 4, kConvGroups = 2, kPromWarp0 = 12, kPromWarps = 8;
+constexpr int kThreads = (kPromWarp0 + kPromWarps) * 32;
+// Registers per thread: launched with 96, then 48 for the warps that issue copies and MMAs,
+// 56 for the converters, 160 for the promotion (48 + 2 * 56 + 2 * 160 = 5 * 96).
+constexpr int kIssueRegs = 48, kConvRegs = 56, kPromRegs = 160;
+constexpr uint32_t kSmemTotal = 232448;
+constexpr uint32_t kSmemRing = kSmemTotal - 1024 /*align*/ - 512 /*barriers*/;
+static_assert(kTmemA + kConvSlots * 32 <= 512, "TMEM columns");
 
-__device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+struct Smem {
+  uint64_t full[kMaxStages];        // the stage's codes landed
+  uint64_t empty[kMaxStages];       // the converters have read it
+  uint64_t conv_full[kConvSlots];   // converted (pair: on the even CTA, by both)
+  uint64_t conv_empty[kConvSlots];  // its MMAs are done
+  uint64_t acc_full[kAccSlots];
+  uint64_t acc_empty[kAccSlots];    // (pair: on the even CTA, by both)
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Smem) <= 512, "barrier block");
+
+struct Params {
+  int64_t M, N, K;
+  const float *sa, *sb;
+  void* C;
+  int c_dtype;
+  int half, halves;  // tokens per accumulator slot, slots per tile
+  int conv_slots, stages;
+  int num_m, num_n, splits;  // tiles of tokens and weight rows; K parts (cluster size, single CTAs)
+  KernelCtl ctl;
+};
+
+// tcgen05.mma kind::f16: FP32 accumulator (bits 4-5 = 1), f16 A and B (0), both
+// K-major, N / 8 in bits 17-22, M / 16 in bits 24-28.
+__host__ __device__ constexpr uint32_t mma_desc(uint32_t M, uint32_t N) { return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24); }
+
+template <bool kPair>
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
-template <typename C>
-__global__ void __launch_bounds__(128)
-    int8_gemm_kernel(const int8_t* __restrict__ qa, const float* __restrict__ sa, const int8_t* __restrict__ qb,
-                     const float* __restrict__ sb, int64_t M, int64_t N, int64_t K, C* __restrict__ out) {
-  pdl_wait();
-  __shared__ __align__(16) uint8_t ta[kTile * kPitch], tb[kTile * kPitch];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  const int64_t m0 = (int64_t)blockIdx.x * kTile, n0 = (int64_t)blockIdx.y * kTile;
-  int acc[8][4] = {};
-  for (int64_t k0 = 0; k0 < K; k0 += kStep) {
-    for (int i = threadIdx.x; i < kTile * kStep / 16; i += 128) {
-      const int r = i / (kStep / 16), c = i % (kStep / 16) * 16;
-      const bool in = k0 + c < K;
-      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-      *reinterpret_cast<uint4*>(ta + r * kPitch + c) =
-          in && m0 + r < M ? *reinterpret_cast<const uint4*>(qa + (m0 + r) * K + k0 + c) : zero;
-      *reinterpret_cast<uint4*>(tb + r * kPitch + c) =
-          in && n0 + r < N ? *reinterpret_cast<const uint4*>(qb + (n0 + r) * K + k0 + c) : zero;
+template <bool kPair>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (kPair)
+    tc_commit_pair_mc(bar, 3);
+  else
+    tc_commit(bar);
+}
+
+// The bounded wait, with one answer for the whole warp.
+template <bool kCluster>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const KernelCtl& ctl, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, ctl, abort_flag)) != 0;
+}
+
+// Arrives on a barrier of the even CTA after writes to this CTA's shared and
+// tensor memory that the even CTA's MMAs read.
+__device__ __forceinline__ void arrive_release_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+template <int kRegs>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// 16 consecutive TMEM columns of the warp's 32 lanes from registers
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Four 8-bit integers as f16, exactly: the byte b = q + 128 below the exponent of
+// 1024 is 1024 + b, and 1152 less is q.
+__device__ __forceinline__ uint2 int8x4_to_f16(uint32_t w) {
+  const uint32_t u = w ^ 0x80808080u;
+  const __half2 offset = __half2half2(__ushort_as_half(0x6480));
+  const uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), offset);
+  const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), offset);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+__device__ __forceinline__ void store_c(const Params& p, int64_t m, int64_t n, int v, float sb) {
+  const float f = (float)v * __ldg(p.sa + m) * sb;
+  if (p.c_dtype == Q4_BF16)
+    static_cast<__nv_bfloat16*>(p.C)[m * p.N + n] = __float2bfloat16_rn(f);
+  else
+    static_cast<float*>(p.C)[m * p.N + n] = f;
+}
+
+template <bool kPair>
+__global__ void __launch_bounds__(kThreads, 1)
+    int8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_t, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Smem* sm = reinterpret_cast<Smem*>(smem + kSmemRing);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  const int width = p.half * p.halves;                       // tokens of a tile
+  const int own = kPair ? width / 2 : width;                 // of which this CTA holds
+  const uint32_t token_bytes = (uint32_t)own * kStageK;      // codes per stage
+  const uint32_t stage_bytes = kWeightBytes + token_bytes;
+  const uint32_t f16_bytes = (uint32_t)own * kChunk * 2;     // converted tokens per slot
+  uint8_t* f16_smem = smem + p.stages * stage_bytes;
+  const int units = kPair ? gridDim.x >> 1 : gridDim.x / p.splits;
+  const int unit = kPair ? blockIdx.x >> 1 : blockIdx.x / p.splits;
+  const int tiles = p.num_m * p.num_n;
+  const int KB = (int)((p.K + kStageK - 1) / kStageK);
+  const int kb0 = kPair ? 0 : (int)((int64_t)KB * rank / p.splits);  // this CTA's stages
+  const int kb1 = kPair ? KB : (int)((int64_t)KB * (rank + 1) / p.splits);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(smem_u32(&sm->full[s]), 1);
+      mbar_init(smem_u32(&sm->empty[s]), 4 * kConvGroups);
     }
-    __syncthreads();
+    for (int s = 0; s < kConvSlots; ++s) {
+      mbar_init(smem_u32(&sm->conv_full[s]), kPair ? 8 : 4);
+      mbar_init(smem_u32(&sm->conv_empty[s]), 1);
+    }
+    for (int s = 0; s < kAccSlots; ++s) {
+      mbar_init(smem_u32(&sm->acc_full[s]), 1);
+      mbar_init(smem_u32(&sm->acc_empty[s]), kPair ? 8 : 4);
+    }
+    mbar_init(smem_u32(&sm->mma_done), 1);
+    sm->abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmap_w);
+    prefetch_tmap(&tmap_t);
+  }
+  if (warp == 1) {
+    if constexpr (kPair) {
+      tmem_alloc_pair(smem_u32(&sm->tmem_base), 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(&sm->tmem_base), 512);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (kPair) cluster_barrier_sync();  // the peer's barriers exist before any remote arrival
+  tc_fence_after();
+  pdl_wait();  // from here on global memory: operands come from the previous kernel
+  const uint32_t tmem = sm->tmem_base;
+  volatile int* abort_flag = &sm->abort;
+  // bands of 4096 tokens, whose codes stay in L2; within a band tokens first
+  auto tile_mn = [&](int t, int64_t& m0, int64_t& n0) {
+    const int band_m = 4096 / width, band_tiles = band_m * p.num_n;
+    const int band = t / band_tiles, r = t - band * band_tiles;
+    const int gm = min(band_m, p.num_m - band * band_m);
+    m0 = (int64_t)(band * band_m + r % gm) * width;
+    n0 = (int64_t)(r / gm) * (kPair ? 2 * kRows : kRows) + (kPair ? rank * kRows : 0);
+  };
+
+  if (warp < kConvWarp0) {
+    registers_down<kIssueRegs>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      uint32_t stage = 0, phase = 0, count = 0;
+      bool alive = true;
+      for (int t = unit; t < tiles && alive; t += units) {
+        int64_t m0, n0;
+        tile_mn(t, m0, n0);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!warp_wait<false>(smem_u32(&sm->empty[stage]), phase ^ 1, p.ctl, abort_flag)) {
+            alive = false;
+            break;
+          }
+          if (lane == 0) {
+            const uint32_t dst = smem_u32(smem + stage * stage_bytes), full = smem_u32(&sm->full[stage]);
+            mbar_arrive_expect_tx(full, stage_bytes);
+            tma_load_2d(dst, &tmap_w, kb * kStageK, (int32_t)n0, full);
+            const int box = kPair ? p.half / 2 : p.half;
+            for (int h = 0; h < p.halves; ++h)
+              tma_load_2d(dst + kWeightBytes + h * box * kStageK, &tmap_t, kb * kStageK,
+                          (int32_t)m0 + h * p.half + (kPair ? rank * box : 0), full);
+          }
+          ++count;
+          if (++stage == (uint32_t)p.stages) stage = 0, phase ^= 1;
+        }
+      }
+      // drain: every copy has landed before the CTA exits
+      if (lane == 0) {
+        KernelCtl drain = p.ctl;
+        const uint32_t S = (uint32_t)p.stages;
+        for (uint32_t g = count > S ? count - S : 0u; g < count; ++g) mbar_wait(smem_u32(&sm->full[g % S]), (g / S) & 1, drain, nullptr);
+      }
+      __syncwarp();
+    } else if (warp == 1 && (!kPair || rank == 0)) {
+      // ---------------------------------------------------------- MMA issuer
+      const uint32_t idesc = mma_desc(kPair ? 2 * kRows : kRows, (uint32_t)p.half);
+      const uint32_t half_bytes = f16_bytes / p.halves;
+      uint32_t slot = 0, phase = 0, acc = 0;  // acc: accumulator slots begun
+      bool alive = true;
+      for (int t = unit; t < tiles && alive; t += units) {
+        const int chunks = 2 * (kb1 - kb0);
+        for (int i = 0; i < chunks && alive; ++i) {
+          const int in_run = i % (2 * kRunStages);
+          const bool ends = in_run == 2 * kRunStages - 1 || i == chunks - 1;
+          if (!warp_wait<kPair>(smem_u32(&sm->conv_full[slot]), phase, p.ctl, abort_flag)) {
+            alive = false;
+            break;
+          }
+          for (int h = 0; h < p.halves; ++h) {
+            const uint32_t a = (acc + h) % kAccSlots;
+            if (in_run == 0 &&
+                !warp_wait<kPair>(smem_u32(&sm->acc_empty[a]), (((acc + h) / kAccSlots) & 1) ^ 1, p.ctl, abort_flag)) {
+              alive = false;
+              break;
+            }
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t b = smem_u32(f16_smem + slot * f16_bytes + h * half_bytes);
 #pragma unroll
-    for (int k = 0; k < kStep; k += 32) {
-      uint32_t a[4];
+              for (uint32_t k = 0; k < kChunk / 16; ++k)
+                mma_f16<kPair>(tmem + a * 128, tmem + kTmemA + slot * 32 + k * 8, smem_desc(b + 32 * k, 16, 1024, 2), idesc,
+                               in_run != 0 || k != 0 ? 1u : 0u);
+              if (h == p.halves - 1) commit<kPair>(smem_u32(&sm->conv_empty[slot]));
+              if (ends) commit<kPair>(smem_u32(&sm->acc_full[a]));
+            }
+            __syncwarp();
+          }
+          if (ends) acc += p.halves;
+          if (++slot == (uint32_t)p.conv_slots) slot = 0, phase ^= 1;
+        }
+      }
+      if (lane == 0) {  // every MMA is complete before TMEM is released
+        if constexpr (kPair)
+          tc_commit_pair_mc(smem_u32(&sm->mma_done), 1);
+        else
+          tc_commit(smem_u32(&sm->mma_done));
+        KernelCtl drain = p.ctl;
+        mbar_wait(smem_u32(&sm->mma_done), 0, drain, nullptr);
+      }
+      __syncwarp();
+    }
+  } else if (warp < kPromWarp0) {
+    // ------------------------------------------------------------ converters
+    registers_down<kConvRegs>();
+    const int group = (warp - kConvWarp0) >> 2, q = warp & 3;
+    const uint32_t leader_full = kPair ? mapa_shared(smem_u32(&sm->conv_full[0]), 0) : smem_u32(&sm->conv_full[0]);
+    uint32_t stage = 0, phase = 0;
+    uint32_t chunk = group;  // chunks of 64 columns since the start, of which this group takes every second
+    bool alive = true;
+    for (int t = unit; t < tiles && alive; t += units) {
+      for (int kb = kb0; kb < kb1; ++kb, chunk += kConvGroups) {
+        const uint32_t slot = chunk % p.conv_slots;
+        if (!warp_wait<false>(smem_u32(&sm->full[stage]), phase, p.ctl, abort_flag) ||
+            !warp_wait<kPair>(smem_u32(&sm->conv_empty[slot]), ((chunk / p.conv_slots) & 1) ^ 1, p.ctl, abort_flag)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        const uint8_t* raw = smem + stage * stage_bytes;
+        // this thread's weight row: 64 codes, two halves of 16 TMEM columns
+        {
+          const int r = q * 32 + lane;
+          const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + kTmemA + slot * 32;
+          uint4 v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        a[i] = *reinterpret_cast<const uint32_t*>(ta + (warp * 16 + g + (i & 1) * 8) * kPitch + k + 4 * q + (i >> 1) * 16);
+          for (int j = 0; j < 4; ++j)
+            v[j] = *reinterpret_cast<const uint4*>(raw + r * kStageK + (((group * 4 + j) ^ (r & 7)) << 4));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint8_t* b = tb + (j * 8 + g) * kPitch + k + 4 * q;
-        mma_s8(acc[j], a, *reinterpret_cast<const uint32_t*>(b), *reinterpret_cast<const uint32_t*>(b + 16));
+          for (int j = 0; j < 4; j += 2) {
+            uint32_t o[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4& x = v[j + i / 4];
+              const uint2 f = int8x4_to_f16((i & 3) == 0 ? x.x : (i & 3) == 1 ? x.y : (i & 3) == 2 ? x.z : x.w);
+              o[2 * i] = f.x;
+              o[2 * i + 1] = f.y;
+            }
+            tmem_st_x16(at + j * 8, o);
+          }
+        }
+        // tokens: a warp takes 8 rows of four 16-code pieces at a time
+        uint8_t* f16 = f16_smem + slot * f16_bytes;
+        for (int r0 = q * 8; r0 < own; r0 += 32) {
+          const int r = r0 + (lane & 7), j = lane >> 3;
+          const uint4 x = *reinterpret_cast<const uint4*>(raw + kWeightBytes + r * kStageK + (((group * 4 + j) ^ (r & 7)) << 4));
+          const uint2 f0 = int8x4_to_f16(x.x), f1 = int8x4_to_f16(x.y), f2 = int8x4_to_f16(x.z), f3 = int8x4_to_f16(x.w);
+          *reinterpret_cast<uint4*>(f16 + r * 128 + (((2 * j) ^ (r & 7)) << 4)) = make_uint4(f0.x, f0.y, f1.x, f1.y);
+          *reinterpret_cast<uint4*>(f16 + r * 128 + (((2 * j + 1) ^ (r & 7)) << 4)) = make_uint4(f2.x, f2.y, f3.x, f3.y);
+        }
+        tmem_st_wait();
+        fence_proxy_async_smem();  // the tensor cores read what these threads wrote
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sm->empty[stage]));
+          if (kPair)
+            arrive_release_cluster(leader_full + slot * 8);
+          else
+            mbar_arrive(leader_full + slot * 8);
+        }
+        if (++stage == (uint32_t)p.stages) stage = 0, phase ^= 1;
       }
     }
-    __syncthreads();
-  }
+  } else {
+    // ------------------------------------------------------------ promotion + store
+    registers_up<kPromRegs>();
+    const int q = warp & 3;                  // TMEM lane quarter this warp may access
+    const int h = (warp - kPromWarp0) >> 2;  // half of the tile's tokens
+    const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16);
+    const uint32_t leader_empty = kPair ? mapa_shared(smem_u32(&sm->acc_empty[0]), 0) : smem_u32(&sm->acc_empty[0]);
+    const int runs = (kb1 - kb0 + kRunStages - 1) / kRunStages;
+    uint32_t acc = h;
+    bool alive = h < p.halves;
+    int sum[128];
+    for (int t = unit; t < tiles && alive; t += units) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 128; ++j) sum[j] = 0;
+      for (int run = 0; run < runs; ++run, acc += p.halves) {
+        const uint32_t a = acc % kAccSlots;
+        if (!warp_wait<kPair>(smem_u32(&sm->acc_full[a]), (acc / kAccSlots) & 1, p.ctl, abort_flag)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t m = m0 + warp * 16 + g + (i >> 1) * 8, n = n0 + j * 8 + 2 * q + (i & 1);
-      if (m < M && n < N) out[m * N + n] = to_elem<C>((float)acc[j][i] * sa[m] * sb[n]);
+        for (int c = 0; c < 8; ++c) {
+          if (c * 16 >= p.half) continue;
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(t_lane + a * 128 + c * 16, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[c * 16 + j] += __float2int_rn(__uint_as_float(r[j]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (kPair)
+            mbar_arrive_cluster(leader_empty + a * 8);
+          else
+            mbar_arrive(leader_empty + a * 8);
+        }
+      }
+      if (!alive) break;
+      int64_t m0, n0;
+      tile_mn(t, m0, n0);
+      if (kPair || p.splits == 1) {
+        const int64_t n = n0 + q * 32 + lane;
+        const float sb = n < p.N ? __ldg(p.sb + n) : 0.f;
+        m0 += h * p.half;
+#pragma unroll
+        for (int j = 0; j < 128; ++j)
+          if (j < p.half && m0 + j < p.M && n < p.N) store_c(p, m0 + j, n, sum[j], sb);
+      }
     }
+    if (!kPair && p.splits > 1) {
+      // the cluster's parts of one tile: owner o adds weight rows [o per, (o + 1) per)
+      cluster_barrier_sync();  // no CTA of the cluster uses its stages any more
+      const int per = (kRows + p.splits - 1) / p.splits, pitch = width + 4;
+      const int row = q * 32 + lane, owner = row / per;
+      const uint32_t dst = mapa_shared(smem_u32(smem), (uint32_t)owner) +
+                           (uint32_t)(((rank * per + row - owner * per) * pitch + h * p.half) * 4);
+      if (h < p.halves) {
+#pragma unroll
+        for (int j = 0; j < 128; j += 4)
+          if (j < p.half)
+            asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + j * 4), "r"(sum[j]), "r"(sum[j + 1]),
+                         "r"(sum[j + 2]), "r"(sum[j + 3])
+                         : "memory");
+      }
+      cluster_barrier_sync();  // every part has landed
+      int64_t m0, n0;
+      tile_mn(unit, m0, n0);
+      const int rows = min(per, kRows - rank * per), cols = (int)min((int64_t)width, p.M - m0);
+      const int* part = reinterpret_cast<const int*>(smem);
+      for (int e = threadIdx.x - kPromWarp0 * 32; e < rows * cols && !*abort_flag; e += kPromWarps * 32) {
+        const int c = e / rows, r = e - c * rows;
+        const int64_t n = n0 + rank * per + r;
+        if (n >= p.N) continue;
+        int v = 0;
+        for (int s = 0; s < p.splits; ++s) v += part[(s * per + r) * pitch + c];
+        store_c(p, m0 + c, n, v, __ldg(p.sb + n));
+      }
+    }
+  }
+  // (the promotion warps of a split tile meet the cluster's others above; what
+  // follows is short enough for every warp's registers)
+  if (!kPair && p.splits > 1 && warp < kPromWarp0) {
+    cluster_barrier_sync();
+    cluster_barrier_sync();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (kPair) cluster_barrier_sync();  // the pair's MMAs are complete in both CTAs
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (kPair)
+      tmem_dealloc_pair(tmem, 512);
+    else
+      tmem_dealloc(tmem, 512);
+  }
+  if (kPair) cluster_barrier_sync();  // no CTA leaves while its peer may still arrive on its barriers
+}
+
+// How a product is cut.
+struct Shape {
+  bool pair;
+  int half, halves, conv_slots, stages, num_m, num_n, splits;
+};
+Shape shape_of(int64_t M, int64_t N, int64_t K) {
+  Shape s;
+  const int sms = num_sms();
+  const int64_t pair_tiles = ceil_div(M, 256) * ceil_div(N, 256);
+  s.pair = M > 256 && pair_tiles >= sms / 4;
+  if (s.pair) {
+    s.half = 128, s.halves = 2;
+    s.num_m = (int)ceil_div(M, 256), s.num_n = (int)ceil_div(N, 256), s.splits = 1;
+  } else {
+    s.num_m = (int)ceil_div(M, 256);
+    const int64_t per = ceil_div(M, s.num_m);
+    s.halves = per > 128 ? 2 : 1;
+    s.half = (int)(ceil_div(per, 16 * s.halves) * 16);
+    s.num_n = (int)ceil_div(N, kRows);
+    const int64_t tiles = (int64_t)s.num_m * s.num_n, KB = ceil_div(K, kStageK);
+    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({8, sms / tiles, KB}));
+  }
+  const uint32_t own = (uint32_t)(s.half * s.halves / (s.pair ? 2 : 1));
+  s.conv_slots = own > 128 ? 2 : kConvSlots;
+  s.stages = (int)std::min<uint32_t>(kMaxStages, (kSmemRing - s.conv_slots * own * kChunk * 2) / (kWeightBytes + own * kStageK));
+  return s;
+}
+
+template <bool kPair>
+q4_status launch_shape(const Shape& s, Params& p, const CUtensorMap& tw, const CUtensorMap& tt, cudaStream_t stream) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return Q4_ERR_CUDA;
+  static int max_pairs[64] = {0}, ready[64] = {0};
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemTotal;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)(kPair ? 2 : s.splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (!ready[dev]) {
+    Q4_CUDA_TRY(cudaFuncSetAttribute(int8_gemm_kernel<kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal));
+    if (kPair) {  // persistent: as many pairs as are resident at once
+      int n = 0;
+      cfg.gridDim = dim3((unsigned)(num_sms() / 2 * 2), 1, 1);
+      if (cudaOccupancyMaxActiveClusters(&n, int8_gemm_kernel<kPair>, &cfg) != cudaSuccess || n <= 0) n = num_sms() / 2;
+      max_pairs[dev] = std::min(n, num_sms() / 2);
+    }
+    ready[dev] = 1;
+  }
+  const int tiles = s.num_m * s.num_n;
+  const int grid = kPair ? 2 * std::min(tiles, max_pairs[dev]) : s.splits > 1 ? tiles * s.splits : std::min(tiles, num_sms());
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  Q4_CUDA_TRY(cudaLaunchKernelEx(&cfg, int8_gemm_kernel<kPair>, tw, tt, p));
+  return Q4_OK;
 }
 
 }  // namespace
@@ -105,10 +572,18 @@ q4_status launch_quantize_int8(const void* x, int dtype, int64_t rows, int64_t K
 
 q4_status launch_int8_gemm(const int8_t* qa, const float* sa, const int8_t* qb, const float* sb, int64_t M, int64_t N, int64_t K,
                            void* C, int c_dtype, cudaStream_t stream) {
-  const dim3 grid((unsigned)ceil_div(M, kTile), (unsigned)ceil_div(N, kTile));
-  if (c_dtype == Q4_F32)
-    return launch_pdl(int8_gemm_kernel<float>, grid, 128, 0, stream, qa, sa, qb, sb, M, N, K, static_cast<float*>(C));
-  return launch_pdl(int8_gemm_kernel<__nv_bfloat16>, grid, 128, 0, stream, qa, sa, qb, sb, M, N, K, static_cast<__nv_bfloat16*>(C));
+  const Shape s = shape_of(M, N, K);
+  CUtensorMap tw, tt;
+  q4_status st;
+  if ((st = make_tmap_2d_u8(&tw, qb, K, N, K, kStageK, kRows, true)) != Q4_OK) return st;
+  if ((st = make_tmap_2d_u8(&tt, qa, K, M, K, kStageK, s.pair ? s.half / 2 : s.half, true)) != Q4_OK) return st;
+  Params p = {};
+  p.M = M; p.N = N; p.K = K;
+  p.sa = sa; p.sb = sb; p.C = C; p.c_dtype = c_dtype;
+  p.half = s.half; p.halves = s.halves; p.conv_slots = s.conv_slots; p.stages = s.stages;
+  p.num_m = s.num_m; p.num_n = s.num_n; p.splits = s.splits;
+  p.ctl = KernelCtl{device_status_ptr(), wait_budget_ns()};
+  return s.pair ? launch_shape<true>(s, p, tw, tt, stream) : launch_shape<false>(s, p, tw, tt, stream);
 }
 
 }  // namespace q4

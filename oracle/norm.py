@@ -6,8 +6,8 @@ float64; quantize_int8 follows float32 steps with IEEE rounding, as the other
 quantizers do, and the integer product is exact.
 
 * Norm: h = x + residual, rstd = 1 / sqrt(mean(h^2) + eps), y = h rstd w.
-* INT8: s = max(amax, 1e-12) / 127 per row, q = rint(x / s), ties to even (the
-  scale of the worked example's INT8 row).
+* INT8: s = max(amax, 1e-12) * RN(1 / 127) per row, q = rint(x / s), ties to even
+  (the scale of the worked example's INT8 row).
 * Product: C = (the exact integer sum, rounded to float32) * sa * sb, each
   product rounded to float32.
 * Balance: p = softmax over the experts above -inf, n tokens with one,
@@ -44,7 +44,7 @@ def rms_norm_backward(d_y, h, rstd, weight=None, d_h=None):
 def quantize_int8(x):
     """-> (codes int8 [rows, K], scales float32 [rows])."""
     x = np.asarray(x, np.float32)
-    s = np.maximum(np.max(np.abs(x), axis=1), F32_1E_12) / np.float32(127.0)
+    s = np.maximum(np.max(np.abs(x), axis=1), F32_1E_12) * (np.float32(1.0) / np.float32(127.0))
     q = np.rint(x / s[:, None])
     return np.clip(q, -127, 127).astype(np.int8), s
 

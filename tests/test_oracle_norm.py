@@ -48,7 +48,7 @@ def test_int8_worked_row():
     gold = json.load(open(os.path.join(os.path.dirname(__file__), "golden", "pages_values.json")))["worked_row"]
     row = np.array([gold["weights"]], np.float32)
     q, s = norm.quantize_int8(row)
-    assert s[0] == np.float32(0.88) / np.float32(127) and abs(s[0] - gold["scale_int8"]) < 5e-6
+    assert s[0] == np.float32(0.88) * (np.float32(1) / np.float32(127)) and abs(s[0] - gold["scale_int8"]) < 5e-6
     assert q[0, 3] == 127 and np.all(np.abs(q * s[:, None] - row) <= s[0] / 2 * (1 + 1e-6))
 
 
@@ -56,7 +56,7 @@ def test_int8_ties_and_edges():
     x = np.array([[127.0, 0.5, 1.5, -2.5, -0.5, 126.5], [0, 0, 0, 0, 0, 0], [1e-20, 0, 0, 0, 0, -1e-20]], np.float32)
     q, s = norm.quantize_int8(x)
     assert s[0] == 1.0 and q[0].tolist() == [127, 0, 2, -2, 0, 126]
-    assert not q[1].any() and not q[2].any() and s[1] == np.float32(1e-12) / np.float32(127)
+    assert not q[1].any() and not q[2].any() and s[1] == np.float32(1e-12) * (np.float32(1) / np.float32(127))
 
 
 def test_int8_product_by_loops():
