@@ -76,8 +76,8 @@ constexpr uint32_t kWeightBytes = kRows * kStageK;
 constexpr int kConvWarp0 = 4, kConvGroups = 2, kPromWarp0 = 12, kPromWarps = 8;
 constexpr int kThreads = (kPromWarp0 + kPromWarps) * 32;
 // Registers per thread: launched with 96, then 48 for the warps that issue copies and MMAs,
-// 56 for the converters, 160 for the promotion (48 + 2 * 56 + 2 * 160 = 5 * 96).
-constexpr int kIssueRegs = 48, kConvRegs = 56, kPromRegs = 160;
+// 64 for the converters, 152 for the promotion (48 + 2 * 64 + 2 * 152 = 5 * 96).
+constexpr int kIssueRegs = 48, kConvRegs = 64, kPromRegs = 152;
 constexpr uint32_t kSmemTotal = 232448;
 constexpr uint32_t kSmemRing = kSmemTotal - 1024 /*align*/ - 512 /*barriers*/;
 static_assert(kTmemA + kConvSlots * 32 <= 512, "TMEM columns");
@@ -85,7 +85,8 @@ static_assert(kTmemA + kConvSlots * 32 <= 512, "TMEM columns");
 struct Smem {
   uint64_t full[kMaxStages];        // the stage's codes landed
   uint64_t empty[kMaxStages];       // the converters have read it
-  uint64_t conv_full[kConvSlots];   // converted (pair: on the even CTA, by both)
+  uint64_t conv_full[kConvSlots];   // this CTA's part is converted
+  uint64_t pair_full[kConvSlots];   // even CTA: so is the odd CTA's (relay)
   uint64_t conv_empty[kConvSlots];  // its MMAs are done
   uint64_t acc_full[kAccSlots];
   uint64_t acc_empty[kAccSlots];    // (pair: on the even CTA, by both)
@@ -100,8 +101,6 @@ struct Params {
   const float *sa, *sb;
   void* C;
   int c_dtype;
-  int half, halves;  // tokens per accumulator slot, slots per tile
-  int conv_slots, stages;
   int num_m, num_n, splits;  // tiles of tokens and weight rows; K parts (cluster size, single CTAs)
   KernelCtl ctl;
 };
@@ -142,10 +141,13 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const K
   return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, ctl, abort_flag)) != 0;
 }
 
-// Arrives on a barrier of the even CTA after writes to this CTA's shared and
-// tensor memory that the even CTA's MMAs read.
-__device__ __forceinline__ void arrive_release_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// One lane of a converged warp.  Its branch is known to be taken by one thread, so
+// that the operands of MMAs in it can stay in uniform registers: behind a test of
+// the lane number every MMA took 180 clocks to issue instead of 60.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 template <int kRegs>
@@ -186,20 +188,30 @@ __device__ __forceinline__ void store_c(const Params& p, int64_t m, int64_t n, i
     static_cast<float*>(p.C)[m * p.N + n] = f;
 }
 
-template <bool kPair>
+// What a CTA holds of a tile: kHalf tokens per accumulator slot, kHalves slots.
+template <bool kPair, int kHalf, int kHalves>
+struct Cut {
+  static constexpr int width = kHalf * kHalves;            // tokens of a tile
+  static constexpr int own = kPair ? width / 2 : width;    // of which this CTA holds
+  static constexpr int box = kPair ? kHalf / 2 : kHalf;    // tokens of one copy
+  static constexpr uint32_t stage_bytes = kWeightBytes + own * kStageK;
+  static constexpr uint32_t f16_bytes = own * kChunk * 2;  // converted tokens per slot
+  static constexpr int conv_slots = own > 128 ? 2 : kConvSlots;
+  static constexpr int fit = (kSmemRing - conv_slots * f16_bytes) / stage_bytes;
+  static constexpr int stages = fit < kMaxStages ? fit : kMaxStages;
+  static_assert(stages >= 3 && f16_bytes % 1024 == 0 && stage_bytes % 1024 == 0, "shared memory");
+};
+
+template <bool kPair, int kHalf, int kHalves>
 __global__ void __launch_bounds__(kThreads, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_t, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Smem* sm = reinterpret_cast<Smem*>(smem + kSmemRing);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
-  const int width = p.half * p.halves;                       // tokens of a tile
-  const int own = kPair ? width / 2 : width;                 // of which this CTA holds
-  const uint32_t token_bytes = (uint32_t)own * kStageK;      // codes per stage
-  const uint32_t stage_bytes = kWeightBytes + token_bytes;
-  const uint32_t f16_bytes = (uint32_t)own * kChunk * 2;     // converted tokens per slot
-  uint8_t* f16_smem = smem + p.stages * stage_bytes;
+  using T = Cut<kPair, kHalf, kHalves>;
+  uint8_t* f16_smem = smem + T::stages * T::stage_bytes;
   const int units = kPair ? gridDim.x >> 1 : gridDim.x / p.splits;
   const int unit = kPair ? blockIdx.x >> 1 : blockIdx.x / p.splits;
   const int tiles = p.num_m * p.num_n;
@@ -213,7 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sm->empty[s]), 4 * kConvGroups);
     }
     for (int s = 0; s < kConvSlots; ++s) {
-      mbar_init(smem_u32(&sm->conv_full[s]), kPair ? 8 : 4);
+      mbar_init(smem_u32(&sm->conv_full[s]), 4);
+      mbar_init(smem_u32(&sm->pair_full[s]), 1);
       mbar_init(smem_u32(&sm->conv_empty[s]), 1);
     }
     for (int s = 0; s < kAccSlots; ++s) {
@@ -244,10 +257,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &sm->abort;
   // bands of 4096 tokens, whose codes stay in L2; within a band tokens first
   auto tile_mn = [&](int t, int64_t& m0, int64_t& n0) {
-    const int band_m = 4096 / width, band_tiles = band_m * p.num_n;
+    constexpr int band_m = 4096 / T::width;
+    const int band_tiles = band_m * p.num_n;
     const int band = t / band_tiles, r = t - band * band_tiles;
     const int gm = min(band_m, p.num_m - band * band_m);
-    m0 = (int64_t)(band * band_m + r % gm) * width;
+    m0 = (int64_t)(band * band_m + r % gm) * T::width;
     n0 = (int64_t)(r / gm) * (kPair ? 2 * kRows : kRows) + (kPair ? rank * kRows : 0);
   };
 
@@ -266,29 +280,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           if (lane == 0) {
-            const uint32_t dst = smem_u32(smem + stage * stage_bytes), full = smem_u32(&sm->full[stage]);
-            mbar_arrive_expect_tx(full, stage_bytes);
+            const uint32_t dst = smem_u32(smem + stage * T::stage_bytes), full = smem_u32(&sm->full[stage]);
+            mbar_arrive_expect_tx(full, T::stage_bytes);
             tma_load_2d(dst, &tmap_w, kb * kStageK, (int32_t)n0, full);
-            const int box = kPair ? p.half / 2 : p.half;
-            for (int h = 0; h < p.halves; ++h)
-              tma_load_2d(dst + kWeightBytes + h * box * kStageK, &tmap_t, kb * kStageK,
-                          (int32_t)m0 + h * p.half + (kPair ? rank * box : 0), full);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+              tma_load_2d(dst + kWeightBytes + h * T::box * kStageK, &tmap_t, kb * kStageK,
+                          (int32_t)m0 + h * kHalf + (kPair ? rank * T::box : 0), full);
           }
           ++count;
-          if (++stage == (uint32_t)p.stages) stage = 0, phase ^= 1;
+          if (++stage == T::stages) stage = 0, phase ^= 1;
         }
       }
       // drain: every copy has landed before the CTA exits
       if (lane == 0) {
         KernelCtl drain = p.ctl;
-        const uint32_t S = (uint32_t)p.stages;
-        for (uint32_t g = count > S ? count - S : 0u; g < count; ++g) mbar_wait(smem_u32(&sm->full[g % S]), (g / S) & 1, drain, nullptr);
+        constexpr uint32_t S = T::stages;
+        for (uint32_t g = count > S ? count - S : 0u; g < count; ++g)
+          mbar_wait(smem_u32(&sm->full[g % S]), (g / S) & 1, drain, nullptr);
       }
       __syncwarp();
     } else if (warp == 1 && (!kPair || rank == 0)) {
       // ---------------------------------------------------------- MMA issuer
-      const uint32_t idesc = mma_desc(kPair ? 2 * kRows : kRows, (uint32_t)p.half);
-      const uint32_t half_bytes = f16_bytes / p.halves;
+      constexpr uint32_t idesc = mma_desc(kPair ? 2 * kRows : kRows, kHalf);
+      constexpr uint32_t half_bytes = T::f16_bytes / kHalves;
+      const uint64_t desc0 = smem_desc(smem_u32(f16_smem), 16, 1024, 2);  // 128-byte swizzle, 8-row groups 1024 bytes apart
+      const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
       uint32_t slot = 0, phase = 0, acc = 0;  // acc: accumulator slots begun
       bool alive = true;
       for (int t = unit; t < tiles && alive; t += units) {
@@ -296,11 +313,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < chunks && alive; ++i) {
           const int in_run = i % (2 * kRunStages);
           const bool ends = in_run == 2 * kRunStages - 1 || i == chunks - 1;
-          if (!warp_wait<kPair>(smem_u32(&sm->conv_full[slot]), phase, p.ctl, abort_flag)) {
+          if (!warp_wait<false>(smem_u32(&sm->conv_full[slot]), phase, p.ctl, abort_flag) ||
+              (kPair && !warp_wait<true>(smem_u32(&sm->pair_full[slot]), phase, p.ctl, abort_flag))) {
             alive = false;
             break;
           }
-          for (int h = 0; h < p.halves; ++h) {
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) {
             const uint32_t a = (acc + h) % kAccSlots;
             if (in_run == 0 &&
                 !warp_wait<kPair>(smem_u32(&sm->acc_empty[a]), (((acc + h) / kAccSlots) & 1) ^ 1, p.ctl, abort_flag)) {
@@ -308,28 +327,47 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             tc_fence_after();
-            if (lane == 0) {
-              const uint32_t b = smem_u32(f16_smem + slot * f16_bytes + h * half_bytes);
+            if (elect_one()) {
+              const uint64_t b = desc0 + ((slot * T::f16_bytes + h * half_bytes) >> 4);
 #pragma unroll
               for (uint32_t k = 0; k < kChunk / 16; ++k)
-                mma_f16<kPair>(tmem + a * 128, tmem + kTmemA + slot * 32 + k * 8, smem_desc(b + 32 * k, 16, 1024, 2), idesc,
+                mma_f16<kPair>(tmem_u + a * 128, tmem_u + kTmemA + slot * 32 + k * 8, b + 2 * k, idesc,
                                in_run != 0 || k != 0 ? 1u : 0u);
-              if (h == p.halves - 1) commit<kPair>(smem_u32(&sm->conv_empty[slot]));
+              if (h == kHalves - 1) commit<kPair>(smem_u32(&sm->conv_empty[slot]));
               if (ends) commit<kPair>(smem_u32(&sm->acc_full[a]));
             }
             __syncwarp();
           }
-          if (ends) acc += p.halves;
-          if (++slot == (uint32_t)p.conv_slots) slot = 0, phase ^= 1;
+          if (ends) acc += kHalves;
+          if (++slot == T::conv_slots) slot = 0, phase ^= 1;
         }
       }
-      if (lane == 0) {  // every MMA is complete before TMEM is released
+      // every MMA (of this thread, the same one throughout) is complete before TMEM
+      // is released
+      if (elect_one()) {
         if constexpr (kPair)
           tc_commit_pair_mc(smem_u32(&sm->mma_done), 1);
         else
           tc_commit(smem_u32(&sm->mma_done));
-        KernelCtl drain = p.ctl;
-        mbar_wait(smem_u32(&sm->mma_done), 0, drain, nullptr);
+      }
+      __syncwarp();
+      KernelCtl drain = p.ctl;
+      mbar_wait(smem_u32(&sm->mma_done), 0, drain, nullptr);
+      __syncwarp();
+    } else if (kPair && warp == 1) {
+      // ---------------------------------------------------------- relay (odd CTA)
+      const uint32_t leader_pair_full = mapa_shared(smem_u32(&sm->pair_full[0]), 0);
+      uint32_t slot = 0, phase = 0;
+      bool alive = true;
+      for (int t = unit; t < tiles && alive; t += units) {
+        for (int i = 0; i < 2 * (kb1 - kb0); ++i) {
+          if (!warp_wait<false>(smem_u32(&sm->conv_full[slot]), phase, p.ctl, abort_flag)) {
+            alive = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_cluster(leader_pair_full + slot * 8);
+          if (++slot == T::conv_slots) slot = 0, phase ^= 1;
+        }
       }
       __syncwarp();
     }
@@ -337,20 +375,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ converters
     registers_down<kConvRegs>();
     const int group = (warp - kConvWarp0) >> 2, q = warp & 3;
-    const uint32_t leader_full = kPair ? mapa_shared(smem_u32(&sm->conv_full[0]), 0) : smem_u32(&sm->conv_full[0]);
     uint32_t stage = 0, phase = 0;
     uint32_t chunk = group;  // chunks of 64 columns since the start, of which this group takes every second
     bool alive = true;
     for (int t = unit; t < tiles && alive; t += units) {
       for (int kb = kb0; kb < kb1; ++kb, chunk += kConvGroups) {
-        const uint32_t slot = chunk % p.conv_slots;
+        const uint32_t slot = chunk % T::conv_slots;
         if (!warp_wait<false>(smem_u32(&sm->full[stage]), phase, p.ctl, abort_flag) ||
-            !warp_wait<kPair>(smem_u32(&sm->conv_empty[slot]), ((chunk / p.conv_slots) & 1) ^ 1, p.ctl, abort_flag)) {
+            !warp_wait<kPair>(smem_u32(&sm->conv_empty[slot]), ((chunk / T::conv_slots) & 1) ^ 1, p.ctl, abort_flag)) {
           alive = false;
           break;
         }
         tc_fence_after();
-        const uint8_t* raw = smem + stage * stage_bytes;
+        const uint8_t* raw = smem + stage * T::stage_bytes;
         // this thread's weight row: 64 codes, two halves of 16 TMEM columns
         {
           const int r = q * 32 + lane;
@@ -372,14 +409,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_x16(at + j * 8, o);
           }
         }
-        // tokens: a warp takes 8 rows of four 16-code pieces at a time
-        uint8_t* f16 = f16_smem + slot * f16_bytes;
-        for (int r0 = q * 8; r0 < own; r0 += 32) {
-          const int r = r0 + (lane & 7), j = lane >> 3;
-          const uint4 x = *reinterpret_cast<const uint4*>(raw + kWeightBytes + r * kStageK + (((group * 4 + j) ^ (r & 7)) << 4));
-          const uint2 f0 = int8x4_to_f16(x.x), f1 = int8x4_to_f16(x.y), f2 = int8x4_to_f16(x.z), f3 = int8x4_to_f16(x.w);
-          *reinterpret_cast<uint4*>(f16 + r * 128 + (((2 * j) ^ (r & 7)) << 4)) = make_uint4(f0.x, f0.y, f1.x, f1.y);
-          *reinterpret_cast<uint4*>(f16 + r * 128 + (((2 * j + 1) ^ (r & 7)) << 4)) = make_uint4(f2.x, f2.y, f3.x, f3.y);
+        // tokens: a warp takes 8 rows of four 16-code pieces at a time, four times
+        // in flight
+        uint8_t* f16 = f16_smem + slot * T::f16_bytes;
+        const int r0 = q * 8 + (lane & 7), j = lane >> 3;
+        const uint8_t* from = raw + kWeightBytes + r0 * kStageK + (((group * 4 + j) ^ (lane & 7)) << 4);
+        uint8_t* to = f16 + r0 * 128;
+        constexpr int kTurns = (T::own + 31) / 32, kFlight = kTurns < 4 ? kTurns : 4;
+#pragma unroll
+        for (int u = 0; u < kTurns; u += kFlight) {
+          uint4 x[kFlight];
+#pragma unroll
+          for (int i = 0; i < kFlight; ++i)
+            if (T::own >= 32 || q * 8 < T::own) x[i] = *reinterpret_cast<const uint4*>(from + (u + i) * 32 * kStageK);
+#pragma unroll
+          for (int i = 0; i < kFlight; ++i) {
+            if (T::own < 32 && q * 8 >= T::own) continue;
+            const uint2 f0 = int8x4_to_f16(x[i].x), f1 = int8x4_to_f16(x[i].y), f2 = int8x4_to_f16(x[i].z), f3 = int8x4_to_f16(x[i].w);
+            *reinterpret_cast<uint4*>(to + (u + i) * 32 * 128 + (((2 * j) ^ (lane & 7)) << 4)) = make_uint4(f0.x, f0.y, f1.x, f1.y);
+            *reinterpret_cast<uint4*>(to + (u + i) * 32 * 128 + (((2 * j + 1) ^ (lane & 7)) << 4)) = make_uint4(f2.x, f2.y, f3.x, f3.y);
+          }
         }
         tmem_st_wait();
         fence_proxy_async_smem();  // the tensor cores read what these threads wrote
@@ -387,12 +436,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_u32(&sm->empty[stage]));
-          if (kPair)
-            arrive_release_cluster(leader_full + slot * 8);
-          else
-            mbar_arrive(leader_full + slot * 8);
+          mbar_arrive(smem_u32(&sm->conv_full[slot]));
         }
-        if (++stage == (uint32_t)p.stages) stage = 0, phase ^= 1;
+        if (++stage == T::stages) stage = 0, phase ^= 1;
       }
     }
   } else {
@@ -404,12 +450,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t leader_empty = kPair ? mapa_shared(smem_u32(&sm->acc_empty[0]), 0) : smem_u32(&sm->acc_empty[0]);
     const int runs = (kb1 - kb0 + kRunStages - 1) / kRunStages;
     uint32_t acc = h;
-    bool alive = h < p.halves;
+    bool alive = h < kHalves;
     int sum[128];
     for (int t = unit; t < tiles && alive; t += units) {
 #pragma unroll
       for (int j = 0; j < 128; ++j) sum[j] = 0;
-      for (int run = 0; run < runs; ++run, acc += p.halves) {
+      for (int run = 0; run < runs; ++run, acc += kHalves) {
         const uint32_t a = acc % kAccSlots;
         if (!warp_wait<kPair>(smem_u32(&sm->acc_full[a]), (acc / kAccSlots) & 1, p.ctl, abort_flag)) {
           alive = false;
@@ -418,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          if (c * 16 >= p.half) continue;
+          if (c * 16 >= kHalf) break;
           uint32_t r[16];
           tmem_ld_32x32b_x16(t_lane + a * 128 + c * 16, r);
           tmem_ld_wait();
@@ -440,23 +486,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kPair || p.splits == 1) {
         const int64_t n = n0 + q * 32 + lane;
         const float sb = n < p.N ? __ldg(p.sb + n) : 0.f;
-        m0 += h * p.half;
+        m0 += h * kHalf;
 #pragma unroll
         for (int j = 0; j < 128; ++j)
-          if (j < p.half && m0 + j < p.M && n < p.N) store_c(p, m0 + j, n, sum[j], sb);
+          if (j < kHalf && m0 + j < p.M && n < p.N) store_c(p, m0 + j, n, sum[j], sb);
       }
     }
     if (!kPair && p.splits > 1) {
       // the cluster's parts of one tile: owner o adds weight rows [o per, (o + 1) per)
       cluster_barrier_sync();  // no CTA of the cluster uses its stages any more
-      const int per = (kRows + p.splits - 1) / p.splits, pitch = width + 4;
+      const int per = (kRows + p.splits - 1) / p.splits, pitch = T::width + 4;
       const int row = q * 32 + lane, owner = row / per;
       const uint32_t dst = mapa_shared(smem_u32(smem), (uint32_t)owner) +
-                           (uint32_t)(((rank * per + row - owner * per) * pitch + h * p.half) * 4);
-      if (h < p.halves) {
+                           (uint32_t)(((rank * per + row - owner * per) * pitch + h * kHalf) * 4);
+      if (h < kHalves) {
 #pragma unroll
         for (int j = 0; j < 128; j += 4)
-          if (j < p.half)
+          if (j < kHalf)
             asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + j * 4), "r"(sum[j]), "r"(sum[j + 1]),
                          "r"(sum[j + 2]), "r"(sum[j + 3])
                          : "memory");
@@ -464,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cluster_barrier_sync();  // every part has landed
       int64_t m0, n0;
       tile_mn(unit, m0, n0);
-      const int rows = min(per, kRows - rank * per), cols = (int)min((int64_t)width, p.M - m0);
+      const int rows = min(per, kRows - rank * per), cols = (int)min((int64_t)T::width, p.M - m0);
       const int* part = reinterpret_cast<const int*>(smem);
       for (int e = threadIdx.x - kPromWarp0 * 32; e < rows * cols && !*abort_flag; e += kPromWarps * 32) {
         const int c = e / rows, r = e - c * rows;
@@ -496,36 +542,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (kPair) cluster_barrier_sync();  // no CTA leaves while its peer may still arrive on its barriers
 }
 
-// How a product is cut.
-struct Shape {
+// How a product is cut: the kernel's form, tiles and K parts.
+struct Plan {
   bool pair;
-  int half, halves, conv_slots, stages, num_m, num_n, splits;
+  int half, halves, num_m, num_n, splits;
 };
-Shape shape_of(int64_t M, int64_t N, int64_t K) {
-  Shape s;
+Plan plan_of(int64_t M, int64_t N, int64_t K) {
+  Plan s;
   const int sms = num_sms();
-  const int64_t pair_tiles = ceil_div(M, 256) * ceil_div(N, 256);
-  s.pair = M > 256 && pair_tiles >= sms / 4;
-  if (s.pair) {
-    s.half = 128, s.halves = 2;
-    s.num_m = (int)ceil_div(M, 256), s.num_n = (int)ceil_div(N, 256), s.splits = 1;
-  } else {
-    s.num_m = (int)ceil_div(M, 256);
-    const int64_t per = ceil_div(M, s.num_m);
-    s.halves = per > 128 ? 2 : 1;
-    s.half = (int)(ceil_div(per, 16 * s.halves) * 16);
-    s.num_n = (int)ceil_div(N, kRows);
-    const int64_t tiles = (int64_t)s.num_m * s.num_n, KB = ceil_div(K, kStageK);
-    s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({8, sms / tiles, KB}));
-  }
-  const uint32_t own = (uint32_t)(s.half * s.halves / (s.pair ? 2 : 1));
-  s.conv_slots = own > 128 ? 2 : kConvSlots;
-  s.stages = (int)std::min<uint32_t>(kMaxStages, (kSmemRing - s.conv_slots * own * kChunk * 2) / (kWeightBytes + own * kStageK));
+  s.pair = M > 256 && ceil_div(M, 256) * ceil_div(N, 256) >= sms / 4;
+  s.half = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  s.halves = M <= 128 ? 1 : 2;
+  s.num_m = (int)ceil_div(M, s.half * s.halves);
+  s.num_n = (int)ceil_div(N, s.pair ? 2 * kRows : kRows);
+  s.splits = 1;
+  if (!s.pair)
+    s.splits = (int)std::max<int64_t>(
+        1, std::min<int64_t>({8, sms / std::max<int64_t>(1, (int64_t)s.num_m * s.num_n), ceil_div(K, kStageK)}));
   return s;
 }
 
-template <bool kPair>
-q4_status launch_shape(const Shape& s, Params& p, const CUtensorMap& tw, const CUtensorMap& tt, cudaStream_t stream) {
+template <bool kPair, int kHalf, int kHalves>
+q4_status launch_plan(const Plan& s, const int8_t* qa, const int8_t* qb, const Params& p, cudaStream_t stream) {
+  using T = Cut<kPair, kHalf, kHalves>;
+  const auto kernel = int8_gemm_kernel<kPair, kHalf, kHalves>;
+  CUtensorMap tw, tt;
+  q4_status st;
+  if ((st = make_tmap_2d_u8(&tw, qb, p.K, p.N, p.K, kStageK, kRows, true)) != Q4_OK) return st;
+  if ((st = make_tmap_2d_u8(&tt, qa, p.K, p.M, p.K, kStageK, T::box, true)) != Q4_OK) return st;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return Q4_ERR_CUDA;
   static int max_pairs[64] = {0}, ready[64] = {0};
@@ -543,11 +587,11 @@ q4_status launch_shape(const Shape& s, Params& p, const CUtensorMap& tw, const C
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   if (!ready[dev]) {
-    Q4_CUDA_TRY(cudaFuncSetAttribute(int8_gemm_kernel<kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal));
+    Q4_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal));
     if (kPair) {  // persistent: as many pairs as are resident at once
       int n = 0;
       cfg.gridDim = dim3((unsigned)(num_sms() / 2 * 2), 1, 1);
-      if (cudaOccupancyMaxActiveClusters(&n, int8_gemm_kernel<kPair>, &cfg) != cudaSuccess || n <= 0) n = num_sms() / 2;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) n = num_sms() / 2;
       max_pairs[dev] = std::min(n, num_sms() / 2);
     }
     ready[dev] = 1;
@@ -555,7 +599,7 @@ q4_status launch_shape(const Shape& s, Params& p, const CUtensorMap& tw, const C
   const int tiles = s.num_m * s.num_n;
   const int grid = kPair ? 2 * std::min(tiles, max_pairs[dev]) : s.splits > 1 ? tiles * s.splits : std::min(tiles, num_sms());
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
-  Q4_CUDA_TRY(cudaLaunchKernelEx(&cfg, int8_gemm_kernel<kPair>, tw, tt, p));
+  Q4_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, tw, tt, p));
   return Q4_OK;
 }
 
@@ -572,18 +616,18 @@ q4_status launch_quantize_int8(const void* x, int dtype, int64_t rows, int64_t K
 
 q4_status launch_int8_gemm(const int8_t* qa, const float* sa, const int8_t* qb, const float* sb, int64_t M, int64_t N, int64_t K,
                            void* C, int c_dtype, cudaStream_t stream) {
-  const Shape s = shape_of(M, N, K);
-  CUtensorMap tw, tt;
-  q4_status st;
-  if ((st = make_tmap_2d_u8(&tw, qb, K, N, K, kStageK, kRows, true)) != Q4_OK) return st;
-  if ((st = make_tmap_2d_u8(&tt, qa, K, M, K, kStageK, s.pair ? s.half / 2 : s.half, true)) != Q4_OK) return st;
+  const Plan s = plan_of(M, N, K);
   Params p = {};
   p.M = M; p.N = N; p.K = K;
   p.sa = sa; p.sb = sb; p.C = C; p.c_dtype = c_dtype;
-  p.half = s.half; p.halves = s.halves; p.conv_slots = s.conv_slots; p.stages = s.stages;
   p.num_m = s.num_m; p.num_n = s.num_n; p.splits = s.splits;
   p.ctl = KernelCtl{device_status_ptr(), wait_budget_ns()};
-  return s.pair ? launch_shape<true>(s, p, tw, tt, stream) : launch_shape<false>(s, p, tw, tt, stream);
+  if (s.pair) return launch_plan<true, 128, 2>(s, qa, qb, p, stream);
+  if (s.half == 16) return launch_plan<false, 16, 1>(s, qa, qb, p, stream);
+  if (s.half == 32) return launch_plan<false, 32, 1>(s, qa, qb, p, stream);
+  if (s.half == 64) return launch_plan<false, 64, 1>(s, qa, qb, p, stream);
+  if (s.halves == 1) return launch_plan<false, 128, 1>(s, qa, qb, p, stream);
+  return launch_plan<false, 128, 2>(s, qa, qb, p, stream);
 }
 
 }  // namespace q4
