@@ -29,6 +29,7 @@
 // split over a cluster where there are few tiles; the integer sums then meet in
 // distributed shared memory.
 #include <algorithm>
+#include <cstddef>
 
 #include "common.cuh"
 #include "elem.cuh"
@@ -85,8 +86,7 @@ static_assert(kTmemA + kConvSlots * 32 <= 512, "TMEM columns");
 struct Smem {
   uint64_t full[kMaxStages];        // the stage's codes landed
   uint64_t empty[kMaxStages];       // the converters have read it
-  uint64_t conv_full[kConvSlots];   // this CTA's part is converted
-  uint64_t pair_full[kConvSlots];   // even CTA: so is the odd CTA's (relay)
+  uint64_t conv_full[kConvSlots];   // converted (on a pair's even CTA: the odd CTA's part too, by its relay)
   uint64_t conv_empty[kConvSlots];  // its MMAs are done
   uint64_t acc_full[kAccSlots];
   uint64_t acc_empty[kAccSlots];    // (pair: on the even CTA, by both)
@@ -225,8 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sm->empty[s]), 4 * kConvGroups);
     }
     for (int s = 0; s < kConvSlots; ++s) {
-      mbar_init(smem_u32(&sm->conv_full[s]), 4);
-      mbar_init(smem_u32(&sm->pair_full[s]), 1);
+      mbar_init(smem_u32(&sm->conv_full[s]), kPair && rank == 0 ? 5 : 4);
       mbar_init(smem_u32(&sm->conv_empty[s]), 1);
     }
     for (int s = 0; s < kAccSlots; ++s) {
@@ -305,41 +304,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc = mma_desc(kPair ? 2 * kRows : kRows, kHalf);
       constexpr uint32_t half_bytes = T::f16_bytes / kHalves;
       const uint64_t desc0 = smem_desc(smem_u32(f16_smem), 16, 1024, 2);  // 128-byte swizzle, 8-row groups 1024 bytes apart
-      const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
-      uint32_t slot = 0, phase = 0, acc = 0;  // acc: accumulator slots begun
+      const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0), bar0 = smem_u32(&sm->conv_full[0]);
+      const uint32_t acc_full0 = smem_u32(&sm->acc_full[0]), acc_empty0 = smem_u32(&sm->acc_empty[0]);
+      constexpr uint32_t kToEmpty = offsetof(Smem, conv_empty) - offsetof(Smem, conv_full);
+      // the issue path counts: a 64-column chunk's MMAs run for 512 clocks, and every
+      // uniform operation in front of them takes some ten
+      uint32_t slot = 0, phase = 0;
+      uint32_t acc[2] = {0, kHalves == 2 ? 1u : 0u}, acc_phase[2] = {1, 1};  // slot of each half, parity of its wait
       bool alive = true;
+      auto next_chunk = [&]() {
+        if (++slot == T::conv_slots) slot = 0, phase ^= 1;
+      };
+      // one half's MMAs of the chunk in `slot`; the first of a run overwrite
+      auto half = [&](int h, bool first) {
+        const uint64_t b = desc0 + (slot * T::f16_bytes + h * half_bytes) / 16;
+        const uint32_t d = tmem_u + acc[h] * 128, a = tmem_u + kTmemA + slot * 32;
+#pragma unroll
+        for (uint32_t k = 0; k < kChunk / 16; ++k) mma_f16<kPair>(d, a + k * 8, b + 2 * k, idesc, !first || k != 0 ? 1u : 0u);
+      };
       for (int t = unit; t < tiles && alive; t += units) {
-        const int chunks = 2 * (kb1 - kb0);
-        for (int i = 0; i < chunks && alive; ++i) {
-          const int in_run = i % (2 * kRunStages);
-          const bool ends = in_run == 2 * kRunStages - 1 || i == chunks - 1;
-          if (!warp_wait<false>(smem_u32(&sm->conv_full[slot]), phase, p.ctl, abort_flag) ||
-              (kPair && !warp_wait<true>(smem_u32(&sm->pair_full[slot]), phase, p.ctl, abort_flag))) {
+        for (int left = 2 * (kb1 - kb0); left > 0 && alive; left -= 2 * kRunStages) {
+          const int n = min(left, 2 * kRunStages);  // chunks of this run, an even number
+          if (!warp_wait<kPair>(bar0 + slot * 8, phase, p.ctl, abort_flag)) {
             alive = false;
             break;
           }
+          tc_fence_after();
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) {
-            const uint32_t a = (acc + h) % kAccSlots;
-            if (in_run == 0 &&
-                !warp_wait<kPair>(smem_u32(&sm->acc_empty[a]), (((acc + h) / kAccSlots) & 1) ^ 1, p.ctl, abort_flag)) {
+            if (!warp_wait<kPair>(acc_empty0 + acc[h] * 8, acc_phase[h], p.ctl, abort_flag)) {
               alive = false;
               break;
             }
             tc_fence_after();
             if (elect_one()) {
-              const uint64_t b = desc0 + ((slot * T::f16_bytes + h * half_bytes) >> 4);
-#pragma unroll
-              for (uint32_t k = 0; k < kChunk / 16; ++k)
-                mma_f16<kPair>(tmem_u + a * 128, tmem_u + kTmemA + slot * 32 + k * 8, b + 2 * k, idesc,
-                               in_run != 0 || k != 0 ? 1u : 0u);
-              if (h == kHalves - 1) commit<kPair>(smem_u32(&sm->conv_empty[slot]));
-              if (ends) commit<kPair>(smem_u32(&sm->acc_full[a]));
+              half(h, true);
+              if (h == kHalves - 1) commit<kPair>(bar0 + kToEmpty + slot * 8);
             }
             __syncwarp();
           }
-          if (ends) acc += kHalves;
-          if (++slot == T::conv_slots) slot = 0, phase ^= 1;
+          if (!alive) break;
+          next_chunk();
+#pragma unroll 1
+          for (int i = 1; i < n; ++i) {
+            if (!warp_wait<kPair>(bar0 + slot * 8, phase, p.ctl, abort_flag)) {
+              alive = false;
+              break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h) {
+                half(h, false);
+                if (i == n - 1) commit<kPair>(acc_full0 + acc[h] * 8);  // the run is complete
+              }
+              commit<kPair>(bar0 + kToEmpty + slot * 8);
+            }
+            __syncwarp();
+            next_chunk();
+          }
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) {
+            acc[h] += kHalves;
+            if (acc[h] >= kAccSlots) acc[h] -= kAccSlots, acc_phase[h] ^= 1;
+          }
         }
       }
       // every MMA (of this thread, the same one throughout) is complete before TMEM
@@ -356,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (kPair && warp == 1) {
       // ---------------------------------------------------------- relay (odd CTA)
-      const uint32_t leader_pair_full = mapa_shared(smem_u32(&sm->pair_full[0]), 0);
+      const uint32_t leader_full = mapa_shared(smem_u32(&sm->conv_full[0]), 0);
       uint32_t slot = 0, phase = 0;
       bool alive = true;
       for (int t = unit; t < tiles && alive; t += units) {
@@ -365,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             alive = false;
             break;
           }
-          if (lane == 0) mbar_arrive_cluster(leader_pair_full + slot * 8);
+          if (lane == 0) mbar_arrive_cluster(leader_full + slot * 8);
           if (++slot == T::conv_slots) slot = 0, phase ^= 1;
         }
       }
