@@ -180,12 +180,20 @@ __device__ __forceinline__ uint2 int8x4_to_f16(uint32_t w) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-__device__ __forceinline__ void store_c(const Params& p, int64_t m, int64_t n, int v, float sb) {
-  const float f = (float)v * __ldg(p.sa + m) * sb;
-  if (p.c_dtype == Q4_BF16)
-    static_cast<__nv_bfloat16*>(p.C)[m * p.N + n] = __float2bfloat16_rn(f);
-  else
-    static_cast<float*>(p.C)[m * p.N + n] = f;
+// Up to kCols tokens of one weight row per lane: 32 consecutive outputs of a token
+// per store.  The tokens' scales come from the lanes that loaded them.
+template <typename C, int kCols>
+__device__ __forceinline__ void store_columns(C* out, int64_t N, const float* sa, int cols, float sb, bool in, int lane,
+                                              const int (&v)[128]) {
+  float scale[(kCols + 31) / 32];
+#pragma unroll
+  for (int i = 0; i < (kCols + 31) / 32; ++i) scale[i] = i * 32 + lane < cols ? __ldg(sa + i * 32 + lane) : 0.f;
+#pragma unroll
+  for (int j = 0; j < kCols; ++j) {
+    const float s = __shfl_sync(0xffffffffu, scale[j / 32], j & 31);
+    if (in && j < cols) out[0] = to_elem<C>((float)v[j] * s * sb);
+    out += N;
+  }
 }
 
 // What a CTA holds of a tile: kHalf tokens per accumulator slot, kHalves slots.
@@ -515,9 +523,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t n = n0 + q * 32 + lane;
         const float sb = n < p.N ? __ldg(p.sb + n) : 0.f;
         m0 += h * kHalf;
-#pragma unroll
-        for (int j = 0; j < 128; ++j)
-          if (j < kHalf && m0 + j < p.M && n < p.N) store_c(p, m0 + j, n, sum[j], sb);
+        const int cols = (int)min((int64_t)kHalf, p.M - m0);
+        if (p.c_dtype == Q4_BF16)
+          store_columns<__nv_bfloat16, kHalf>(static_cast<__nv_bfloat16*>(p.C) + m0 * p.N + n, p.N, p.sa + m0, cols, sb, n < p.N,
+                                              lane, sum);
+        else
+          store_columns<float, kHalf>(static_cast<float*>(p.C) + m0 * p.N + n, p.N, p.sa + m0, cols, sb, n < p.N, lane, sum);
       }
     }
     if (!kPair && p.splits > 1) {
@@ -546,7 +557,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n >= p.N) continue;
         int v = 0;
         for (int s = 0; s < p.splits; ++s) v += part[(s * per + r) * pitch + c];
-        store_c(p, m0 + c, n, v, __ldg(p.sb + n));
+        const float f = (float)v * __ldg(p.sa + m0 + c) * __ldg(p.sb + n);
+        if (p.c_dtype == Q4_BF16)
+          static_cast<__nv_bfloat16*>(p.C)[(m0 + c) * p.N + n] = __float2bfloat16_rn(f);
+        else
+          static_cast<float*>(p.C)[(m0 + c) * p.N + n] = f;
       }
     }
   }
