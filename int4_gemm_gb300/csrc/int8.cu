@@ -12,7 +12,7 @@
 // operand of the MMA, its rows the tensor memory's lanes:
 //   warp 0       TMA producer: 128 columns of the weight rows and of the tokens
 //                per stage, as 8-bit codes;
-//   warps 4..11  converters, two groups of four that take turns of 64 columns:
+//   warps 4..    converters, groups of four that take turns of 64 columns:
 //                a thread reads its weight row's 64 codes and stores them as f16
 //                in tensor memory, the MMA's A operand; the tokens' codes go to
 //                shared memory as f16, swizzled, the B operand.  (With both
@@ -22,7 +22,7 @@
 //   warp 1       MMA issuer: two halves of the tile's tokens one after another,
 //                each into one of three accumulator slots, so that a slot is read
 //                while the next ones are filled;
-//   warps 12..19 promotion: slot -> 32-bit integers in registers, then scales and
+//   last eight   promotion: slot -> 32-bit integers in registers, then scales and
 //                stores.
 // Large products run on CTA pairs (256 weight rows x 256 tokens, cta_group::2),
 // the others on single CTAs (128 weight rows x up to 256 tokens) whose K range is
@@ -68,17 +68,16 @@ __global__ void __launch_bounds__(kQuantThreads)
 constexpr int kRows = 128;        // weight rows of a CTA
 constexpr int kStageK = 128;      // columns per TMA stage
 constexpr int kChunk = 64;        // columns per conversion: 128 bytes of f16
-constexpr int kRunStages = 8;     // stages whose sums are exact in FP32: 1024 columns
+constexpr int kSegment = 8;       // chunks of half a run: a run's sums, of 1024 columns, are exact in FP32
 constexpr int kConvSlots = 4;     // tensor-memory slots of converted weights, 32 columns each
 constexpr int kAccSlots = 3;      // accumulator slots of up to 128 tokens
 constexpr uint32_t kTmemA = kAccSlots * 128;  // first column of the converted weights
 constexpr int kMaxStages = 12;
 constexpr uint32_t kWeightBytes = kRows * kStageK;
-constexpr int kConvWarp0 = 4, kConvGroups = 2, kPromWarp0 = 12, kPromWarps = 8;
-constexpr int kThreads = (kPromWarp0 + kPromWarps) * 32;
-// Registers per thread: launched with 96, then 48 for the warps that issue copies and MMAs,
-// 64 for the converters, 152 for the promotion (48 + 2 * 64 + 2 * 152 = 5 * 96).
-constexpr int kIssueRegs = 48, kConvRegs = 64, kPromRegs = 152;
+constexpr int kConvWarp0 = 4, kPromWarps = 8;
+// Registers per thread after the launch, which gives every thread the same: the
+// warps that issue copies and MMAs, the converters, the promotion (Cut::prom_regs).
+constexpr int kIssueRegs = 48, kConvRegs = 64;
 constexpr uint32_t kSmemTotal = 232448;
 constexpr uint32_t kSmemRing = kSmemTotal - 1024 /*align*/ - 512 /*barriers*/;
 static_assert(kTmemA + kConvSlots * 32 <= 512, "TMEM columns");
@@ -184,7 +183,7 @@ __device__ __forceinline__ uint2 int8x4_to_f16(uint32_t w) {
 // per store.  The tokens' scales come from the lanes that loaded them.
 template <typename C, int kCols>
 __device__ __forceinline__ void store_columns(C* out, int64_t N, const float* sa, int cols, float sb, bool in, int lane,
-                                              const int (&v)[128]) {
+                                              const int (&v)[kCols]) {
   float scale[(kCols + 31) / 32];
 #pragma unroll
   for (int i = 0; i < (kCols + 31) / 32; ++i) scale[i] = i * 32 + lane < cols ? __ldg(sa + i * 32 + lane) : 0.f;
@@ -207,11 +206,20 @@ struct Cut {
   static constexpr int conv_slots = own > 128 ? 2 : kConvSlots;
   static constexpr int fit = (kSmemRing - conv_slots * f16_bytes) / stage_bytes;
   static constexpr int stages = fit < kMaxStages ? fit : kMaxStages;
+  // groups of four converter warps: four where few tokens leave registers for them,
+  // since the weights' way through a group takes 800 clocks per chunk whatever the
+  // tokens, and HBM brings a chunk in 350
+  static constexpr int groups = kHalf <= 64 ? 4 : 2;
+  static constexpr int prom_warp0 = kConvWarp0 + 4 * groups;
+  static constexpr int threads = (prom_warp0 + kPromWarps) * 32;
+  static constexpr int prom_regs = kHalf <= 64 ? 96 : 152;
+  static constexpr int launch_regs = 65536 / threads / 8 * 8;
+  static_assert(kIssueRegs + groups * kConvRegs + 2 * prom_regs <= (1 + groups + 2) * launch_regs, "registers");
   static_assert(stages >= 3 && f16_bytes % 1024 == 0 && stage_bytes % 1024 == 0, "shared memory");
 };
 
 template <bool kPair, int kHalf, int kHalves>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_t, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -230,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(smem_u32(&sm->full[s]), 1);
-      mbar_init(smem_u32(&sm->empty[s]), 4 * kConvGroups);
+      mbar_init(smem_u32(&sm->empty[s]), 8);
     }
     for (int s = 0; s < kConvSlots; ++s) {
       mbar_init(smem_u32(&sm->conv_full[s]), kPair && rank == 0 ? 5 : 4);
@@ -318,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the issue path counts: a 64-column chunk's MMAs run for 512 clocks, and every
       // uniform operation in front of them takes some ten
       uint32_t slot = 0, phase = 0;
-      uint32_t acc[2] = {0, kHalves == 2 ? 1u : 0u}, acc_phase[2] = {1, 1};  // slot of each half, parity of its wait
+      uint32_t acc[2] = {0, 0}, next_acc = 0, next_phase = 1;  // each half's slot; the next one, parity of its wait
       bool alive = true;
       auto next_chunk = [&]() {
         if (++slot == T::conv_slots) slot = 0, phase ^= 1;
@@ -331,8 +339,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t k = 0; k < kChunk / 16; ++k) mma_f16<kPair>(d, a + k * 8, b + 2 * k, idesc, !first || k != 0 ? 1u : 0u);
       };
       for (int t = unit; t < tiles && alive; t += units) {
-        for (int left = 2 * (kb1 - kb0); left > 0 && alive; left -= 2 * kRunStages) {
-          const int n = min(left, 2 * kRunStages);  // chunks of this run, an even number
+        int seg = 0;
+        for (int left = 2 * (kb1 - kb0); left > 0 && alive; left -= kSegment, ++seg) {
+          const int n = min(left, kSegment);  // chunks of this segment, an even number
+          // the second half's runs begin one segment apart from the first's, so
+          // that their slots are read at different times
+          const bool begins[2] = {seg % 2 == 0, seg % 2 == 1 || seg == 0};
+          const bool ends[2] = {seg % 2 == 1 || left <= kSegment, seg % 2 == 0 || left <= kSegment};
           if (!warp_wait<kPair>(bar0 + slot * 8, phase, p.ctl, abort_flag)) {
             alive = false;
             break;
@@ -340,13 +353,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) {
-            if (!warp_wait<kPair>(acc_empty0 + acc[h] * 8, acc_phase[h], p.ctl, abort_flag)) {
-              alive = false;
-              break;
+            if (begins[h]) {
+              if (!warp_wait<kPair>(acc_empty0 + next_acc * 8, next_phase, p.ctl, abort_flag)) {
+                alive = false;
+                break;
+              }
+              tc_fence_after();
+              acc[h] = next_acc;
+              if (++next_acc == kAccSlots) next_acc = 0, next_phase ^= 1;
             }
-            tc_fence_after();
             if (elect_one()) {
-              half(h, true);
+              half(h, begins[h]);
               if (h == kHalves - 1) commit<kPair>(bar0 + kToEmpty + slot * 8);
             }
             __syncwarp();
@@ -364,17 +381,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int h = 0; h < kHalves; ++h) {
                 half(h, false);
-                if (i == n - 1) commit<kPair>(acc_full0 + acc[h] * 8);  // the run is complete
+                if (i == n - 1 && ends[h]) commit<kPair>(acc_full0 + acc[h] * 8);  // the run is complete
               }
               commit<kPair>(bar0 + kToEmpty + slot * 8);
             }
             __syncwarp();
             next_chunk();
-          }
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h) {
-            acc[h] += kHalves;
-            if (acc[h] >= kAccSlots) acc[h] -= kAccSlots, acc_phase[h] ^= 1;
           }
         }
       }
@@ -407,15 +419,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-  } else if (warp < kPromWarp0) {
+  } else if (warp < T::prom_warp0) {
     // ------------------------------------------------------------ converters
     registers_down<kConvRegs>();
     const int group = (warp - kConvWarp0) >> 2, q = warp & 3;
-    uint32_t stage = 0, phase = 0;
-    uint32_t chunk = group;  // chunks of 64 columns since the start, of which this group takes every second
+    const int sub = group & 1;  // which 64 columns of a stage
+    uint32_t at_stage = group >> 1;  // stages since the start, of which this group takes every (groups / 2)-th
+    int tile = unit, kb = kb0 + (group >> 1);
     bool alive = true;
-    for (int t = unit; t < tiles && alive; t += units) {
-      for (int kb = kb0; kb < kb1; ++kb, chunk += kConvGroups) {
+    for (;;) {
+      while (kb >= kb1 && tile < tiles) kb -= kb1 - kb0, tile += units;
+      if (tile >= tiles || !alive) break;
+      {
+        const uint32_t stage = at_stage % T::stages, phase = (at_stage / T::stages) & 1, chunk = 2 * at_stage + sub;
         const uint32_t slot = chunk % T::conv_slots;
         if (!warp_wait<false>(smem_u32(&sm->full[stage]), phase, p.ctl, abort_flag) ||
             !warp_wait<kPair>(smem_u32(&sm->conv_empty[slot]), ((chunk / T::conv_slots) & 1) ^ 1, p.ctl, abort_flag)) {
@@ -431,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint4 v[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            v[j] = *reinterpret_cast<const uint4*>(raw + r * kStageK + (((group * 4 + j) ^ (r & 7)) << 4));
+            v[j] = *reinterpret_cast<const uint4*>(raw + r * kStageK + (((sub * 4 + j) ^ (r & 7)) << 4));
 #pragma unroll
           for (int j = 0; j < 4; j += 2) {
             uint32_t o[16];
@@ -449,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // in flight
         uint8_t* f16 = f16_smem + slot * T::f16_bytes;
         const int r0 = q * 8 + (lane & 7), j = lane >> 3;
-        const uint8_t* from = raw + kWeightBytes + r0 * kStageK + (((group * 4 + j) ^ (lane & 7)) << 4);
+        const uint8_t* from = raw + kWeightBytes + r0 * kStageK + (((sub * 4 + j) ^ (lane & 7)) << 4);
         uint8_t* to = f16 + r0 * 128;
         constexpr int kTurns = (T::own + 31) / 32, kFlight = kTurns < 4 ? kTurns : 4;
 #pragma unroll
@@ -474,33 +490,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(smem_u32(&sm->empty[stage]));
           mbar_arrive(smem_u32(&sm->conv_full[slot]));
         }
-        if (++stage == T::stages) stage = 0, phase ^= 1;
+        at_stage += T::groups / 2, kb += T::groups / 2;
       }
     }
   } else {
     // ------------------------------------------------------------ promotion + store
-    registers_up<kPromRegs>();
-    const int q = warp & 3;                  // TMEM lane quarter this warp may access
-    const int h = (warp - kPromWarp0) >> 2;  // half of the tile's tokens
+    registers_up<T::prom_regs>();
+    const int q = warp & 3;                     // TMEM lane quarter this warp may access
+    const int h = (warp - T::prom_warp0) >> 2;  // half of the tile's tokens
     const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16);
     const uint32_t leader_empty = kPair ? mapa_shared(smem_u32(&sm->acc_empty[0]), 0) : smem_u32(&sm->acc_empty[0]);
-    const int runs = (kb1 - kb0 + kRunStages - 1) / kRunStages;
-    uint32_t acc = h;
+    const int segs = (2 * (kb1 - kb0) + kSegment - 1) / kSegment;
+    const int runs = h == 0 ? (segs + 1) / 2 : 1 + segs / 2;
+    uint32_t begun = 0;  // runs begun before this tile, in the order in which they take slots
     bool alive = h < kHalves;
-    int sum[128];
+    int sum[kHalf];
     for (int t = unit; t < tiles && alive; t += units) {
 #pragma unroll
-      for (int j = 0; j < 128; ++j) sum[j] = 0;
-      for (int run = 0; run < runs; ++run, acc += kHalves) {
-        const uint32_t a = acc % kAccSlots;
-        if (!warp_wait<kPair>(smem_u32(&sm->acc_full[a]), (acc / kAccSlots) & 1, p.ctl, abort_flag)) {
+      for (int j = 0; j < kHalf; ++j) sum[j] = 0;
+      for (int run = 0; run < runs; ++run) {
+        // two runs begin with a tile's first segment, one with every other
+        const uint32_t g = begun + (kHalves == 1 ? run : run == 0 ? h : 2 * run + 1 - h), a = g % kAccSlots;
+        if (!warp_wait<kPair>(smem_u32(&sm->acc_full[a]), (g / kAccSlots) & 1, p.ctl, abort_flag)) {
           alive = false;
           break;
         }
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (c * 16 >= kHalf) break;
+        for (int c = 0; c < kHalf / 16; ++c) {
           uint32_t r[16];
           tmem_ld_32x32b_x16(t_lane + a * 128 + c * 16, r);
           tmem_ld_wait();
@@ -516,6 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(leader_empty + a * 8);
         }
       }
+      begun += kHalves == 1 ? (segs + 1) / 2 : segs + 1;
       if (!alive) break;
       int64_t m0, n0;
       tile_mn(t, m0, n0);
@@ -532,42 +550,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!kPair && p.splits > 1) {
-      // the cluster's parts of one tile: owner o adds weight rows [o per, (o + 1) per)
-      cluster_barrier_sync();  // no CTA of the cluster uses its stages any more
-      const int per = (kRows + p.splits - 1) / p.splits, pitch = T::width + 4;
-      const int row = q * 32 + lane, owner = row / per;
-      const uint32_t dst = mapa_shared(smem_u32(smem), (uint32_t)owner) +
-                           (uint32_t)(((rank * per + row - owner * per) * pitch + h * kHalf) * 4);
-      if (h < kHalves) {
-#pragma unroll
-        for (int j = 0; j < 128; j += 4)
-          if (j < kHalf)
-            asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + j * 4), "r"(sum[j]), "r"(sum[j + 1]),
-                         "r"(sum[j + 2]), "r"(sum[j + 3])
-                         : "memory");
-      }
-      cluster_barrier_sync();  // every part has landed
+      // the cluster's parts of one tile: owner o adds tokens [o per, (o + 1) per)
       int64_t m0, n0;
       tile_mn(unit, m0, n0);
-      const int rows = min(per, kRows - rank * per), cols = (int)min((int64_t)T::width, p.M - m0);
-      const int* part = reinterpret_cast<const int*>(smem);
-      for (int e = threadIdx.x - kPromWarp0 * 32; e < rows * cols && !*abort_flag; e += kPromWarps * 32) {
-        const int c = e / rows, r = e - c * rows;
-        const int64_t n = n0 + rank * per + r;
-        if (n >= p.N) continue;
-        int v = 0;
-        for (int s = 0; s < p.splits; ++s) v += part[(s * per + r) * pitch + c];
-        const float f = (float)v * __ldg(p.sa + m0 + c) * __ldg(p.sb + n);
-        if (p.c_dtype == Q4_BF16)
-          static_cast<__nv_bfloat16*>(p.C)[(m0 + c) * p.N + n] = __float2bfloat16_rn(f);
-        else
-          static_cast<float*>(p.C)[(m0 + c) * p.N + n] = f;
+      const int cols = (int)min((int64_t)T::width, p.M - m0), per = (cols + p.splits - 1) / p.splits;
+      cluster_barrier_sync();  // no CTA of the cluster uses its stages any more
+      if (h < kHalves) {
+        // part[rank][token - owner * per][weight row] in the owner's shared memory
+        const uint32_t to = smem_u32(smem) + (uint32_t)((rank * per * kRows + q * 32 + lane) * 4);
+        int owner = min(h * kHalf / per, p.splits - 1), at = h * kHalf - owner * per;  // (halves without a token store nothing)
+        uint32_t dst = mapa_shared(to, (uint32_t)owner);
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) {
+          if (h * kHalf + j < cols) {
+            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst + (uint32_t)(at * kRows * 4)), "r"(sum[j]) : "memory");
+            if (++at == per) at = 0, dst = mapa_shared(to, (uint32_t)min(++owner, p.splits - 1));
+          }
+        }
+      }
+      cluster_barrier_sync();  // every part has landed
+      const int mine = min(per, cols - rank * per), row = q * 32 + lane;
+      const int64_t n = n0 + row;
+      const int* part = reinterpret_cast<const int*>(smem) + row;
+      if (n < p.N && !*abort_flag) {
+        const float sb = __ldg(p.sb + n);
+        for (int c = h; c < mine; c += 2) {
+          int v = 0;
+          for (int r = 0; r < p.splits; ++r) v += part[(r * per + c) * kRows];
+          const int64_t m = m0 + rank * per + c;
+          const float f = (float)v * __ldg(p.sa + m) * sb;
+          if (p.c_dtype == Q4_BF16)
+            static_cast<__nv_bfloat16*>(p.C)[m * p.N + n] = __float2bfloat16_rn(f);
+          else
+            static_cast<float*>(p.C)[m * p.N + n] = f;
+        }
       }
     }
   }
   // (the promotion warps of a split tile meet the cluster's others above; what
   // follows is short enough for every warp's registers)
-  if (!kPair && p.splits > 1 && warp < kPromWarp0) {
+  if (!kPair && p.splits > 1 && warp < T::prom_warp0) {
     cluster_barrier_sync();
     cluster_barrier_sync();
   }
@@ -617,7 +639,7 @@ q4_status launch_plan(const Plan& s, const int8_t* qa, const int8_t* qb, const P
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return Q4_ERR_CUDA;
   static int max_pairs[64] = {0}, ready[64] = {0};
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(T::threads, 1, 1);
   cfg.dynamicSmemBytes = kSmemTotal;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
