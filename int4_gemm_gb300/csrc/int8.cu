@@ -25,7 +25,7 @@
 //   last eight   promotion: slot -> 32-bit integers in registers, then scales and
 //                stores.
 // Large products run on CTA pairs (256 weight rows x 256 tokens, cta_group::2),
-// the others on single CTAs (128 weight rows x up to 256 tokens) whose K range is
+// the others on single CTAs (128 weight rows x 16 to 128 tokens) whose K range is
 // split over a cluster where there are few tiles; the integer sums then meet in
 // distributed shared memory.
 #include <algorithm>
@@ -67,11 +67,10 @@ __global__ void __launch_bounds__(kQuantThreads)
 // ------------------------------------------------------------------ product
 constexpr int kRows = 128;        // weight rows of a CTA
 constexpr int kStageK = 128;      // columns per TMA stage
-constexpr int kChunk = 64;        // columns per conversion: 128 bytes of f16
-constexpr int kSegment = 8;       // chunks of half a run: a run's sums, of 1024 columns, are exact in FP32
-constexpr int kConvSlots = 4;     // tensor-memory slots of converted weights, 32 columns each
-constexpr int kAccSlots = 3;      // accumulator slots of up to 128 tokens
-constexpr uint32_t kTmemA = kAccSlots * 128;  // first column of the converted weights
+constexpr int kPanel = 64;        // columns of a row of 128 bytes of f16
+constexpr int kSegmentK = 512;    // columns of half a run: a run's sums, of 1024 columns, are exact in FP32
+constexpr int kConvSlots = 4;     // slots of converted weights and tokens
+constexpr int kAccSlots = 3;      // accumulator slots of kHalf tokens
 constexpr int kMaxStages = 12;
 constexpr uint32_t kWeightBytes = kRows * kStageK;
 constexpr int kConvWarp0 = 4, kPromWarps = 8;
@@ -80,7 +79,6 @@ constexpr int kConvWarp0 = 4, kPromWarps = 8;
 constexpr int kIssueRegs = 48, kConvRegs = 64;
 constexpr uint32_t kSmemTotal = 232448;
 constexpr uint32_t kSmemRing = kSmemTotal - 1024 /*align*/ - 512 /*barriers*/;
-static_assert(kTmemA + kConvSlots * 32 <= 512, "TMEM columns");
 
 struct Smem {
   uint64_t full[kMaxStages];        // the stage's codes landed
@@ -179,20 +177,65 @@ __device__ __forceinline__ uint2 int8x4_to_f16(uint32_t w) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// Up to kCols tokens of one weight row per lane: 32 consecutive outputs of a token
-// per store.  The tokens' scales come from the lanes that loaded them.
-template <typename C, int kCols>
-__device__ __forceinline__ void store_columns(C* out, int64_t N, const float* sa, int cols, float sb, bool in, int lane,
-                                              const int (&v)[kCols]) {
+// Tokens m0 .. m0 + cols - 1 of one weight row n per lane: 32 consecutive outputs
+// of a token per store.  The tokens' scales come from the lanes that loaded them.
+template <int kCols, typename C>
+__device__ __forceinline__ void store_columns_as(C* out, const Params& p, int64_t m0, int64_t n, int cols, int lane,
+                                                 const int (&v)[kCols]) {
+  const float sb = n < p.N ? __ldg(p.sb + n) : 0.f;
   float scale[(kCols + 31) / 32];
 #pragma unroll
-  for (int i = 0; i < (kCols + 31) / 32; ++i) scale[i] = i * 32 + lane < cols ? __ldg(sa + i * 32 + lane) : 0.f;
+  for (int i = 0; i < (kCols + 31) / 32; ++i) scale[i] = i * 32 + lane < cols ? __ldg(p.sa + m0 + i * 32 + lane) : 0.f;
+  out += m0 * p.N + n;
 #pragma unroll
   for (int j = 0; j < kCols; ++j) {
     const float s = __shfl_sync(0xffffffffu, scale[j / 32], j & 31);
-    if (in && j < cols) out[0] = to_elem<C>((float)v[j] * s * sb);
-    out += N;
+    if (n < p.N && j < cols) out[0] = to_elem<C>((float)v[j] * s * sb);
+    out += p.N;
   }
+}
+
+// The same for one CTA's share of a tile whose K parts lie in the shared memory of
+// the cluster's kParts CTAs, part[weight row][token]: groups of four tokens of one
+// weight row per lane, `first`, first + step and so on.  A load from another CTA
+// takes some 1000 clocks, so several are in flight.
+template <int kParts, typename C>
+__device__ __forceinline__ void join_columns_as(const Params& p, uint32_t row_smem, int64_t m0, int64_t n, int cols, int first,
+                                                int step) {
+  constexpr int kFlight = 8 / kParts;
+  const float sb = n < p.N ? __ldg(p.sb + n) : 0.f;
+  C* out = static_cast<C*>(p.C) + m0 * p.N + n;
+  for (int c0 = 4 * first; c0 < cols; c0 += 4 * step * kFlight) {
+    int x[kFlight][kParts][4];
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int c = c0 + 4 * step * f;
+      if (c >= cols) break;
+#pragma unroll
+      for (int r = 0; r < kParts; ++r)
+        asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x[f][r][0]), "=r"(x[f][r][1]), "=r"(x[f][r][2]), "=r"(x[f][r][3])
+                     : "r"(mapa_shared(row_smem + 4 * c, (uint32_t)r)));
+    }
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int v = 0;
+#pragma unroll
+        for (int r = 0; r < kParts; ++r) v += x[f][r][i];
+        const int c = c0 + 4 * step * f + i;
+        if (c < cols && n < p.N) out[c * p.N] = to_elem<C>((float)v * __ldg(p.sa + m0 + c) * sb);
+      }
+  }
+}
+template <int kParts>
+__device__ __forceinline__ void join_columns(const Params& p, uint32_t row_smem, int64_t m0, int64_t n, int cols, int first,
+                                             int step) {
+  if (p.c_dtype == Q4_BF16)
+    join_columns_as<kParts, __nv_bfloat16>(p, row_smem, m0, n, cols, first, step);
+  else
+    join_columns_as<kParts, float>(p, row_smem, m0, n, cols, first, step);
 }
 
 // What a CTA holds of a tile: kHalf tokens per accumulator slot, kHalves slots.
@@ -202,19 +245,34 @@ struct Cut {
   static constexpr int own = kPair ? width / 2 : width;    // of which this CTA holds
   static constexpr int box = kPair ? kHalf / 2 : kHalf;    // tokens of one copy
   static constexpr uint32_t stage_bytes = kWeightBytes + own * kStageK;
-  static constexpr uint32_t f16_bytes = own * kChunk * 2;  // converted tokens per slot
-  static constexpr int conv_slots = own > 128 ? 2 : kConvSlots;
+  // columns per conversion: with few tokens two panels, whose MMAs are short, so
+  // that the waits and commits around them count half (1 token x 8192 x 8192: 21.5
+  // us with one)
+  static constexpr int panels = kHalf <= 64 ? 2 : 1;
+  static constexpr int per_stage = kStageK / (panels * kPanel);  // conversions per stage
+  static constexpr int segment = kSegmentK / (panels * kPanel);  // conversions per half run
+  static constexpr uint32_t panel_bytes = own * 128;
+  static constexpr uint32_t f16_bytes = panels * panel_bytes;  // converted tokens per slot
+  static constexpr uint32_t acc_columns = kHalf <= 64 ? 64 : 128;
+  static constexpr uint32_t tmem_a = kAccSlots * acc_columns;  // first column of the converted weights
+  static constexpr uint32_t a_columns = panels * kPanel / 2;
+  static_assert(tmem_a + kConvSlots * a_columns <= 512, "TMEM columns");
+  // groups of four converter warps: more where small accumulators leave registers
+  // for them, since the weights' way through a group takes 800 clocks per chunk
+  // whatever the tokens, and HBM brings 64 columns in 350
+  static constexpr int groups = kHalf > 64 ? 2 : kHalves == 1 ? 4 : 3;
+  static constexpr int conv_slots = own > 128 ? 2 : groups == 3 ? 3 : kConvSlots;
   static constexpr int fit = (kSmemRing - conv_slots * f16_bytes) / stage_bytes;
   static constexpr int stages = fit < kMaxStages ? fit : kMaxStages;
-  // groups of four converter warps: four where few tokens leave registers for them,
-  // since the weights' way through a group takes 800 clocks per chunk whatever the
-  // tokens, and HBM brings a chunk in 350
-  static constexpr int groups = kHalf <= 64 ? 4 : 2;
   static constexpr int prom_warp0 = kConvWarp0 + 4 * groups;
   static constexpr int threads = (prom_warp0 + kPromWarps) * 32;
   static constexpr int prom_regs = kHalf <= 64 ? 96 : 152;
   static constexpr int launch_regs = 65536 / threads / 8 * 8;
   static_assert(kIssueRegs + groups * kConvRegs + 2 * prom_regs <= (1 + groups + 2) * launch_regs, "registers");
+  // a group that has waited for its conversion slot knows that the chunks up to
+  // conv_slots before its own are done, so that neither of its two waits can take
+  // an older phase of the barrier for its own
+  static_assert(conv_slots >= groups && stages * per_stage >= conv_slots, "phases");
   static_assert(stages >= 3 && f16_bytes % 1024 == 0 && stage_bytes % 1024 == 0, "shared memory");
 };
 
@@ -238,7 +296,7 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(smem_u32(&sm->full[s]), 1);
-      mbar_init(smem_u32(&sm->empty[s]), 8);
+      mbar_init(smem_u32(&sm->empty[s]), 4 * T::per_stage);
     }
     for (int s = 0; s < kConvSlots; ++s) {
       mbar_init(smem_u32(&sm->conv_full[s]), kPair && rank == 0 ? 5 : 4);
@@ -318,39 +376,42 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
     } else if (warp == 1 && (!kPair || rank == 0)) {
       // ---------------------------------------------------------- MMA issuer
       constexpr uint32_t idesc = mma_desc(kPair ? 2 * kRows : kRows, kHalf);
-      constexpr uint32_t half_bytes = T::f16_bytes / kHalves;
+      constexpr uint32_t half_bytes = T::panel_bytes / kHalves;
       const uint64_t desc0 = smem_desc(smem_u32(f16_smem), 16, 1024, 2);  // 128-byte swizzle, 8-row groups 1024 bytes apart
       const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0), bar0 = smem_u32(&sm->conv_full[0]);
       const uint32_t acc_full0 = smem_u32(&sm->acc_full[0]), acc_empty0 = smem_u32(&sm->acc_empty[0]);
       constexpr uint32_t kToEmpty = offsetof(Smem, conv_empty) - offsetof(Smem, conv_full);
-      // the issue path counts: a 64-column chunk's MMAs run for 512 clocks, and every
-      // uniform operation in front of them takes some ten
+      // the issue path counts: a 64-column chunk's MMAs run for 512 clocks (256 x 256),
+      // and every uniform operation in front of them takes some ten
       uint32_t slot = 0, phase = 0;
       uint32_t acc[2] = {0, 0}, next_acc = 0, next_phase = 1;  // each half's slot; the next one, parity of its wait
       bool alive = true;
+      auto chunk_wait = [&]() {
+        alive = warp_wait<kPair>(bar0 + slot * 8, phase, p.ctl, abort_flag);
+        tc_fence_after();
+        return alive;
+      };
       auto next_chunk = [&]() {
+        __syncwarp();
         if (++slot == T::conv_slots) slot = 0, phase ^= 1;
       };
       // one half's MMAs of the chunk in `slot`; the first of a run overwrite
       auto half = [&](int h, bool first) {
         const uint64_t b = desc0 + (slot * T::f16_bytes + h * half_bytes) / 16;
-        const uint32_t d = tmem_u + acc[h] * 128, a = tmem_u + kTmemA + slot * 32;
+        const uint32_t d = tmem_u + acc[h] * T::acc_columns, a = tmem_u + T::tmem_a + slot * T::a_columns;
 #pragma unroll
-        for (uint32_t k = 0; k < kChunk / 16; ++k) mma_f16<kPair>(d, a + k * 8, b + 2 * k, idesc, !first || k != 0 ? 1u : 0u);
+        for (uint32_t k = 0; k < T::panels * kPanel / 16; ++k)
+          mma_f16<kPair>(d, a + k * 8, b + k / 4 * (T::panel_bytes / 16) + k % 4 * 2, idesc, !first || k != 0 ? 1u : 0u);
       };
       for (int t = unit; t < tiles && alive; t += units) {
         int seg = 0;
-        for (int left = 2 * (kb1 - kb0); left > 0 && alive; left -= kSegment, ++seg) {
-          const int n = min(left, kSegment);  // chunks of this segment, an even number
+        for (int left = T::per_stage * (kb1 - kb0); left > 0 && alive; left -= T::segment, ++seg) {
+          const int n = min(left, T::segment);  // chunks of this segment
           // the second half's runs begin one segment apart from the first's, so
           // that their slots are read at different times
           const bool begins[2] = {seg % 2 == 0, seg % 2 == 1 || seg == 0};
-          const bool ends[2] = {seg % 2 == 1 || left <= kSegment, seg % 2 == 0 || left <= kSegment};
-          if (!warp_wait<kPair>(bar0 + slot * 8, phase, p.ctl, abort_flag)) {
-            alive = false;
-            break;
-          }
-          tc_fence_after();
+          const bool ends[2] = {seg % 2 == 1 || left <= T::segment, seg % 2 == 0 || left <= T::segment};
+          if (!chunk_wait()) break;
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) {
             if (begins[h]) {
@@ -364,6 +425,7 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
             }
             if (elect_one()) {
               half(h, begins[h]);
+              if (n == 1 && ends[h]) commit<kPair>(acc_full0 + acc[h] * 8);
               if (h == kHalves - 1) commit<kPair>(bar0 + kToEmpty + slot * 8);
             }
             __syncwarp();
@@ -372,11 +434,7 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
           next_chunk();
 #pragma unroll 1
           for (int i = 1; i < n; ++i) {
-            if (!warp_wait<kPair>(bar0 + slot * 8, phase, p.ctl, abort_flag)) {
-              alive = false;
-              break;
-            }
-            tc_fence_after();
+            if (!chunk_wait()) break;
             if (elect_one()) {
 #pragma unroll
               for (int h = 0; h < kHalves; ++h) {
@@ -385,7 +443,6 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
               }
               commit<kPair>(bar0 + kToEmpty + slot * 8);
             }
-            __syncwarp();
             next_chunk();
           }
         }
@@ -408,7 +465,7 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
       uint32_t slot = 0, phase = 0;
       bool alive = true;
       for (int t = unit; t < tiles && alive; t += units) {
-        for (int i = 0; i < 2 * (kb1 - kb0); ++i) {
+        for (int i = 0; i < T::per_stage * (kb1 - kb0); ++i) {
           if (!warp_wait<false>(smem_u32(&sm->conv_full[slot]), phase, p.ctl, abort_flag)) {
             alive = false;
             break;
@@ -423,63 +480,71 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
     // ------------------------------------------------------------ converters
     registers_down<kConvRegs>();
     const int group = (warp - kConvWarp0) >> 2, q = warp & 3;
-    const int sub = group & 1;  // which 64 columns of a stage
-    uint32_t at_stage = group >> 1;  // stages since the start, of which this group takes every (groups / 2)-th
-    int tile = unit, kb = kb0 + (group >> 1);
+    static_assert(T::groups % T::per_stage == 0, "a group takes the same part of its stages");
+    constexpr int kStep = T::groups / T::per_stage;  // a group takes every kStep-th stage
+    const int sub = group % T::per_stage;            // which of its parts
+    uint32_t at_stage = group / T::per_stage;        // stages since the start
+    int tile = unit, kb = kb0 + group / T::per_stage;
     bool alive = true;
     for (;;) {
       while (kb >= kb1 && tile < tiles) kb -= kb1 - kb0, tile += units;
       if (tile >= tiles || !alive) break;
       {
-        const uint32_t stage = at_stage % T::stages, phase = (at_stage / T::stages) & 1, chunk = 2 * at_stage + sub;
-        const uint32_t slot = chunk % T::conv_slots;
-        if (!warp_wait<false>(smem_u32(&sm->full[stage]), phase, p.ctl, abort_flag) ||
-            !warp_wait<kPair>(smem_u32(&sm->conv_empty[slot]), ((chunk / T::conv_slots) & 1) ^ 1, p.ctl, abort_flag)) {
+        const uint32_t stage = at_stage % T::stages, phase = (at_stage / T::stages) & 1;
+        const uint32_t chunk = T::per_stage * at_stage + sub, slot = chunk % T::conv_slots;
+        if (!warp_wait<kPair>(smem_u32(&sm->conv_empty[slot]), ((chunk / T::conv_slots) & 1) ^ 1, p.ctl, abort_flag) ||
+            !warp_wait<false>(smem_u32(&sm->full[stage]), phase, p.ctl, abort_flag)) {
           alive = false;
           break;
         }
         tc_fence_after();
         const uint8_t* raw = smem + stage * T::stage_bytes;
-        // this thread's weight row: 64 codes, two halves of 16 TMEM columns
+        // this thread's weight row: 64 codes per panel, two halves of 16 TMEM columns
+        constexpr int kPieces = T::panels * 4;  // of 16 codes
         {
           const int r = q * 32 + lane;
-          const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + kTmemA + slot * 32;
-          uint4 v[4];
+          const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + T::tmem_a + slot * T::a_columns;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            v[j] = *reinterpret_cast<const uint4*>(raw + r * kStageK + (((sub * 4 + j) ^ (r & 7)) << 4));
+          for (int j0 = 0; j0 < kPieces; j0 += 4) {
+            uint4 v[4];
 #pragma unroll
-          for (int j = 0; j < 4; j += 2) {
-            uint32_t o[16];
+            for (int j = 0; j < 4; ++j)
+              v[j] = *reinterpret_cast<const uint4*>(raw + r * kStageK + (((sub * kPieces + j0 + j) ^ (r & 7)) << 4));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint4& x = v[j + i / 4];
-              const uint2 f = int8x4_to_f16((i & 3) == 0 ? x.x : (i & 3) == 1 ? x.y : (i & 3) == 2 ? x.z : x.w);
-              o[2 * i] = f.x;
-              o[2 * i + 1] = f.y;
+            for (int j = 0; j < 4; j += 2) {
+              uint32_t o[16];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint4& x = v[j + i / 4];
+                const uint2 f = int8x4_to_f16((i & 3) == 0 ? x.x : (i & 3) == 1 ? x.y : (i & 3) == 2 ? x.z : x.w);
+                o[2 * i] = f.x;
+                o[2 * i + 1] = f.y;
+              }
+              tmem_st_x16(at + (j0 + j) * 8, o);
             }
-            tmem_st_x16(at + j * 8, o);
           }
         }
         // tokens: a warp takes 8 rows of four 16-code pieces at a time, four times
         // in flight
-        uint8_t* f16 = f16_smem + slot * T::f16_bytes;
         const int r0 = q * 8 + (lane & 7), j = lane >> 3;
-        const uint8_t* from = raw + kWeightBytes + r0 * kStageK + (((sub * 4 + j) ^ (lane & 7)) << 4);
-        uint8_t* to = f16 + r0 * 128;
         constexpr int kTurns = (T::own + 31) / 32, kFlight = kTurns < 4 ? kTurns : 4;
 #pragma unroll
-        for (int u = 0; u < kTurns; u += kFlight) {
-          uint4 x[kFlight];
+        for (int pan = 0; pan < T::panels; ++pan) {
+          const uint8_t* from = raw + kWeightBytes + r0 * kStageK + (((sub * kPieces + pan * 4 + j) ^ (lane & 7)) << 4);
+          uint8_t* to = f16_smem + slot * T::f16_bytes + pan * T::panel_bytes + r0 * 128;
 #pragma unroll
-          for (int i = 0; i < kFlight; ++i)
-            if (T::own >= 32 || q * 8 < T::own) x[i] = *reinterpret_cast<const uint4*>(from + (u + i) * 32 * kStageK);
+          for (int u = 0; u < kTurns; u += kFlight) {
+            uint4 x[kFlight];
 #pragma unroll
-          for (int i = 0; i < kFlight; ++i) {
-            if (T::own < 32 && q * 8 >= T::own) continue;
-            const uint2 f0 = int8x4_to_f16(x[i].x), f1 = int8x4_to_f16(x[i].y), f2 = int8x4_to_f16(x[i].z), f3 = int8x4_to_f16(x[i].w);
-            *reinterpret_cast<uint4*>(to + (u + i) * 32 * 128 + (((2 * j) ^ (lane & 7)) << 4)) = make_uint4(f0.x, f0.y, f1.x, f1.y);
-            *reinterpret_cast<uint4*>(to + (u + i) * 32 * 128 + (((2 * j + 1) ^ (lane & 7)) << 4)) = make_uint4(f2.x, f2.y, f3.x, f3.y);
+            for (int i = 0; i < kFlight; ++i)
+              if (T::own >= 32 || q * 8 < T::own) x[i] = *reinterpret_cast<const uint4*>(from + (u + i) * 32 * kStageK);
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+              if (T::own < 32 && q * 8 >= T::own) continue;
+              const uint2 f0 = int8x4_to_f16(x[i].x), f1 = int8x4_to_f16(x[i].y), f2 = int8x4_to_f16(x[i].z), f3 = int8x4_to_f16(x[i].w);
+              *reinterpret_cast<uint4*>(to + (u + i) * 32 * 128 + (((2 * j) ^ (lane & 7)) << 4)) = make_uint4(f0.x, f0.y, f1.x, f1.y);
+              *reinterpret_cast<uint4*>(to + (u + i) * 32 * 128 + (((2 * j + 1) ^ (lane & 7)) << 4)) = make_uint4(f2.x, f2.y, f3.x, f3.y);
+            }
           }
         }
         tmem_st_wait();
@@ -490,7 +555,7 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
           mbar_arrive(smem_u32(&sm->empty[stage]));
           mbar_arrive(smem_u32(&sm->conv_full[slot]));
         }
-        at_stage += T::groups / 2, kb += T::groups / 2;
+        at_stage += kStep, kb += kStep;
       }
     }
   } else {
@@ -500,7 +565,7 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
     const int h = (warp - T::prom_warp0) >> 2;  // half of the tile's tokens
     const uint32_t t_lane = tmem + ((uint32_t)(q * 32) << 16);
     const uint32_t leader_empty = kPair ? mapa_shared(smem_u32(&sm->acc_empty[0]), 0) : smem_u32(&sm->acc_empty[0]);
-    const int segs = (2 * (kb1 - kb0) + kSegment - 1) / kSegment;
+    const int segs = (T::per_stage * (kb1 - kb0) + T::segment - 1) / T::segment;
     const int runs = h == 0 ? (segs + 1) / 2 : 1 + segs / 2;
     uint32_t begun = 0;  // runs begun before this tile, in the order in which they take slots
     bool alive = h < kHalves;
@@ -519,7 +584,7 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
 #pragma unroll
         for (int c = 0; c < kHalf / 16; ++c) {
           uint32_t r[16];
-          tmem_ld_32x32b_x16(t_lane + a * 128 + c * 16, r);
+          tmem_ld_32x32b_x16(t_lane + a * T::acc_columns + c * 16, r);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 16; ++j) sum[c * 16 + j] += __float2int_rn(__uint_as_float(r[j]));
@@ -539,52 +604,38 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
       tile_mn(t, m0, n0);
       if (kPair || p.splits == 1) {
         const int64_t n = n0 + q * 32 + lane;
-        const float sb = n < p.N ? __ldg(p.sb + n) : 0.f;
         m0 += h * kHalf;
         const int cols = (int)min((int64_t)kHalf, p.M - m0);
         if (p.c_dtype == Q4_BF16)
-          store_columns<__nv_bfloat16, kHalf>(static_cast<__nv_bfloat16*>(p.C) + m0 * p.N + n, p.N, p.sa + m0, cols, sb, n < p.N,
-                                              lane, sum);
+          store_columns_as<kHalf>(static_cast<__nv_bfloat16*>(p.C), p, m0, n, cols, lane, sum);
         else
-          store_columns<float, kHalf>(static_cast<float*>(p.C) + m0 * p.N + n, p.N, p.sa + m0, cols, sb, n < p.N, lane, sum);
+          store_columns_as<kHalf>(static_cast<float*>(p.C), p, m0, n, cols, lane, sum);
       }
     }
     if (!kPair && p.splits > 1) {
-      // the cluster's parts of one tile: owner o adds tokens [o per, (o + 1) per)
+      // the cluster's parts of one tile meet in shared memory, which no copy and no
+      // MMA uses any more (this CTA's are complete: the last sums were read)
       int64_t m0, n0;
       tile_mn(unit, m0, n0);
-      const int cols = (int)min((int64_t)T::width, p.M - m0), per = (cols + p.splits - 1) / p.splits;
-      cluster_barrier_sync();  // no CTA of the cluster uses its stages any more
+      constexpr int kPitch = T::width + 4;
+      const uint32_t row = smem_u32(smem) + (uint32_t)((q * 32 + lane) * kPitch * 4);
       if (h < kHalves) {
-        // part[rank][token - owner * per][weight row] in the owner's shared memory
-        const uint32_t to = smem_u32(smem) + (uint32_t)((rank * per * kRows + q * 32 + lane) * 4);
-        int owner = min(h * kHalf / per, p.splits - 1), at = h * kHalf - owner * per;  // (halves without a token store nothing)
-        uint32_t dst = mapa_shared(to, (uint32_t)owner);
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
-          if (h * kHalf + j < cols) {
-            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst + (uint32_t)(at * kRows * 4)), "r"(sum[j]) : "memory");
-            if (++at == per) at = 0, dst = mapa_shared(to, (uint32_t)min(++owner, p.splits - 1));
-          }
-        }
+        for (int j = 0; j < kHalf; j += 4)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (uint32_t)((h * kHalf + j) * 4)), "r"(sum[j]),
+                       "r"(sum[j + 1]), "r"(sum[j + 2]), "r"(sum[j + 3])
+                       : "memory");
       }
-      cluster_barrier_sync();  // every part has landed
-      const int mine = min(per, cols - rank * per), row = q * 32 + lane;
-      const int64_t n = n0 + row;
-      const int* part = reinterpret_cast<const int*>(smem) + row;
-      if (n < p.N && !*abort_flag) {
-        const float sb = __ldg(p.sb + n);
-        for (int c = h; c < mine; c += 2) {
-          int v = 0;
-          for (int r = 0; r < p.splits; ++r) v += part[(r * per + c) * kRows];
-          const int64_t m = m0 + rank * per + c;
-          const float f = (float)v * __ldg(p.sa + m) * sb;
-          if (p.c_dtype == Q4_BF16)
-            static_cast<__nv_bfloat16*>(p.C)[m * p.N + n] = __float2bfloat16_rn(f);
-          else
-            static_cast<float*>(p.C)[m * p.N + n] = f;
-        }
+      cluster_barrier_sync();  // every part is there
+      const int cols = (int)min((int64_t)T::width, p.M - m0);
+      if (!*abort_flag) {
+        const int64_t n = n0 + q * 32 + lane;
+        if (p.splits == 2)
+          join_columns<2>(p, row, m0, n, cols, 2 * rank + h, 4);
+        else
+          join_columns<4>(p, row, m0, n, cols, 2 * rank + h, 8);
       }
+      cluster_barrier_sync();  // no CTA leaves while another reads its part
     }
   }
   // (the promotion warps of a split tile meet the cluster's others above; what
@@ -610,21 +661,31 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
 // How a product is cut: the kernel's form, tiles and K parts.
 struct Plan {
   bool pair;
-  int half, halves, num_m, num_n, splits;
+  int width, num_m, num_n, splits;  // width: tokens of a tile
 };
+// The cut with the least estimated time.  A form costs a fixed time and so much per
+// 64 columns of a tile (measured, ns: 16 x 8192 x 8192 24.3 us with 16-token tiles,
+// 28.9 with 64, 39.7 with 128, 48.3 as pairs; 512 x 512 x 512 5.6, 6.9, 7.9 and 10.5;
+// 8192 x 28672 x 8192, 47 tiles per pair, 2020 us), and joining the parts of a split K
+// takes a time of its own (the same 16 x 8192 x 8192 with two parts: 17.2 us; eight
+// parts were never the best).
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
-  Plan s;
-  const int sms = num_sms();
-  s.pair = M > 256 && ceil_div(M, 256) * ceil_div(N, 256) >= sms / 4;
-  s.half = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  s.halves = M <= 128 ? 1 : 2;
-  s.num_m = (int)ceil_div(M, s.half * s.halves);
-  s.num_n = (int)ceil_div(N, s.pair ? 2 * kRows : kRows);
-  s.splits = 1;
-  if (!s.pair)
-    s.splits = (int)std::max<int64_t>(
-        1, std::min<int64_t>({8, sms / std::max<int64_t>(1, (int64_t)s.num_m * s.num_n), ceil_div(K, kStageK)}));
-  return s;
+  const int64_t sms = num_sms(), chunks = ceil_div(K, kPanel);
+  Plan best = {true, 256, (int)ceil_div(M, 256), (int)ceil_div(N, 256), 1};
+  int64_t least = 8000 + ceil_div((int64_t)best.num_m * best.num_n, sms / 2) * chunks * 318;
+  const struct { int width, fixed, chunk, join; } forms[] = {
+      {16, 4400, 155, 3000}, {32, 4400, 162, 3000}, {64, 5000, 195, 4000}, {128, 5800, 268, 5500}};
+  for (const auto& f : forms) {
+    const int64_t tiles = ceil_div(M, f.width) * ceil_div(N, kRows);
+    for (int splits = 1; splits <= 4 && splits * kStageK < K + kStageK && (splits == 1 || splits * tiles <= sms); splits *= 2) {
+      const int64_t cost = f.fixed + (splits > 1 ? f.join : 0) + ceil_div(tiles * splits, sms) * ceil_div(chunks, splits) * f.chunk;
+      if (cost < least) {
+        least = cost;
+        best = {false, f.width, (int)ceil_div(M, f.width), (int)ceil_div(N, kRows), splits};
+      }
+    }
+  }
+  return best;
 }
 
 template <bool kPair, int kHalf, int kHalves>
@@ -688,11 +749,10 @@ q4_status launch_int8_gemm(const int8_t* qa, const float* sa, const int8_t* qb, 
   p.num_m = s.num_m; p.num_n = s.num_n; p.splits = s.splits;
   p.ctl = KernelCtl{device_status_ptr(), wait_budget_ns()};
   if (s.pair) return launch_plan<true, 128, 2>(s, qa, qb, p, stream);
-  if (s.half == 16) return launch_plan<false, 16, 1>(s, qa, qb, p, stream);
-  if (s.half == 32) return launch_plan<false, 32, 1>(s, qa, qb, p, stream);
-  if (s.half == 64) return launch_plan<false, 64, 1>(s, qa, qb, p, stream);
-  if (s.halves == 1) return launch_plan<false, 128, 1>(s, qa, qb, p, stream);
-  return launch_plan<false, 128, 2>(s, qa, qb, p, stream);
+  if (s.width == 16) return launch_plan<false, 16, 1>(s, qa, qb, p, stream);
+  if (s.width == 32) return launch_plan<false, 32, 1>(s, qa, qb, p, stream);
+  if (s.width == 64) return launch_plan<false, 64, 1>(s, qa, qb, p, stream);
+  return launch_plan<false, 64, 2>(s, qa, qb, p, stream);
 }
 
 }  // namespace q4
