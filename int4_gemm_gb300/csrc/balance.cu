@@ -6,11 +6,14 @@
 //   d_logits[t, e] = d_loss coeff / n * p[t, e] (f[e] - sum over j of p[t, j] f[j])
 // (counts are constants to the gradient).  Softmax and sums are FP32.
 //
-// A warp holds a token's logits, lane l the experts l, l + 32, ..., and adds its
-// tokens' probabilities up in registers; the blocks' sums meet in the workspace
-// and are added in a fixed order by a second kernel (the counts are integers,
-// whose order does not matter).
+// A token's logits are held by 1 to 32 lanes, eight neighbouring experts per load
+// where rows are aligned (Lanes), else by a warp, lane l the experts l, l + 32, ...;
+// its probabilities are added up in registers, token by token.  The blocks' sums
+// meet in the workspace and are added in a fixed order: by the first block of a
+// cluster that has done everything, where there are few tokens, else by a second
+// kernel (the counts are integers, whose order does not matter).
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "elem.cuh"
@@ -19,208 +22,372 @@
 namespace q4 {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxExperts = 1024;
-constexpr int kFinishThreads = 1024;
+constexpr int kCluster = 8;
 
-// A token's softmax in a warp: lane l holds experts l + 32 i.  NaN and +inf mask
-// their expert; all zero (and false) where every expert is masked.
-template <typename T, int kN>
-__device__ __forceinline__ bool token_softmax(const T* __restrict__ row, int E, int lane, float (&p)[kN], bool& bad) {
-  float top = -INFINITY;
+// The lanes that hold a token and their experts: kVec: `lanes` lanes, chunk c of
+// lane l the experts 8 (l + lanes c) ...; otherwise a warp, single experts.
+template <typename T, bool kVec, int kN>
+struct Lanes {
+  static constexpr int n = kVec ? 8 * kN : kN;  // experts of a lane
+  static constexpr int words = kVec ? kN * 2 * (int)sizeof(T) : kN;
+  int lanes, l, sub, per_warp;
+  __device__ __forceinline__ explicit Lanes(int lanes_)
+      : lanes(kVec ? lanes_ : 32), l(threadIdx.x & (lanes - 1)), sub((threadIdx.x & 31) / lanes), per_warp(32 / lanes) {}
+  __device__ __forceinline__ int expert(int i) const { return kVec ? 8 * (l + lanes * (i / 8)) + i % 8 : l + 32 * i; }
+  __device__ __forceinline__ void load(const T* __restrict__ row, int E, bool live, uint32_t (&w)[words]) const {
+    if constexpr (kVec) {
+      constexpr int per = words / kN / 4;  // 128-bit words of a chunk
 #pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    const int e = lane + 32 * i;
-    float v = e < E ? Elem<T>::to_f(row[e]) : -INFINITY;
-    if (!(v < INFINITY)) {
-      bad = true;
-      v = -INFINITY;
+      for (int c = 0; c < kN; ++c)
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+          const int e = 8 * (l + lanes * c);
+          const uint4 v = live && e < E ? __ldg(reinterpret_cast<const uint4*>(row + e) + i) : make_uint4(0u, 0u, 0u, 0u);
+          uint32_t* o = w + 4 * (c * per + i);
+          o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const int e = expert(i);
+        if constexpr (sizeof(T) == 2)
+          w[i] = live && e < E ? __ldg(reinterpret_cast<const unsigned short*>(row) + e) : 0u;
+        else
+          w[i] = live && e < E ? __float_as_uint(__ldg(row + e)) : 0u;
+      }
     }
-    p[i] = v;
-    top = fmaxf(top, v);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (top == -INFINITY) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) p[i] = 0.f;
-    return false;
+  static __device__ __forceinline__ float value(const uint32_t (&w)[words], int i) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else if constexpr (kVec) {
+      const float2 v = unpack2<T>(w[i / 2]);
+      return i & 1 ? v.y : v.x;
+    } else
+      return unpack2<T>(w[i]).x;
   }
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    p[i] = __expf(p[i] - top);
-    sum += p[i];
+  __device__ __forceinline__ float sum(float v) const {
+    for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
   }
+  // Softmax of a token; NaN and +inf mask their expert.  All zero (and false) where
+  // every expert is masked.
+  __device__ __forceinline__ bool softmax(const uint32_t (&w)[words], int E, bool live, float (&p)[n], bool& bad) const {
+    float top = -INFINITY;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float inv = __fdiv_rn(1.f, sum);
+    for (int i = 0; i < n; ++i) {
+      float v = live && expert(i) < E ? value(w, i) : -INFINITY;
+      if (!(v < INFINITY)) {
+        bad = true;
+        v = -INFINITY;
+      }
+      p[i] = v;
+      top = fmaxf(top, v);
+    }
+    for (int o = lanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const bool there = top > -INFINITY;
+    if (!there) top = 0.f;  // the masked experts' exponentials are zero then, too
+    float total = 0.f;
 #pragma unroll
-  for (int i = 0; i < kN; ++i) p[i] *= inv;
-  return true;
-}
-
-template <typename T, int kN>
-__global__ void __launch_bounds__(kThreads)
-    balance_kernel(const T* __restrict__ logits, int64_t tokens, int E, int64_t ld, const int32_t* __restrict__ ids,
-                   int64_t slots, float* __restrict__ part_p, int32_t* __restrict__ part_c, int* status) {
-  pdl_wait();
-  __shared__ float sum[kWarps][32 * kN];
-  __shared__ int32_t count[kMaxExperts + 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int e = threadIdx.x; e <= E; e += kThreads) count[e] = 0;
-  __syncthreads();
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < slots; i += (int64_t)gridDim.x * kThreads) {
-    const int e = __ldg(ids + i);
-    if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+    for (int i = 0; i < n; ++i) {
+      p[i] = __expf(p[i] - top);
+      total += p[i];
+    }
+    total = sum(total);
+    const float inv = there ? __fdiv_rn(1.f, total) : 0.f;
+#pragma unroll
+    for (int i = 0; i < n; ++i) p[i] *= inv;
+    return there;
   }
-  float acc[kN];
-#pragma unroll
-  for (int i = 0; i < kN; ++i) acc[i] = 0.f;
-  int there = 0;
-  bool bad = false;
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < tokens; t += (int64_t)gridDim.x * kWarps) {
-    float p[kN];
-    there += token_softmax<T, kN>(logits + t * ld, E, lane, p, bad);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) acc[i] += p[i];
-  }
-  if (bad) latch_status(status, Q4_ERR_NONFINITE);
-  if (lane == 0) atomicAdd(&count[E], there);
-#pragma unroll
-  for (int i = 0; i < kN; ++i) sum[warp][lane + 32 * i] = acc[i];
-  __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += kThreads) {
-    part_c[(int64_t)blockIdx.x * (E + 1) + e] = count[e];
-    if (e == E) continue;
-    float s = 0.f;
-    for (int w = 0; w < kWarps; ++w) s += sum[w][e];
-    part_p[(int64_t)blockIdx.x * E + e] = s;
-  }
-}
+};
 
 // f[e] from the counts (0 where no token takes part).
 __device__ __forceinline__ float load_factor(int32_t count, int32_t n, int E, int top_k) {
   return n > 0 ? (float)count * ((float)E / ((float)n * (float)top_k)) : 0.f;
 }
 
-__global__ void __launch_bounds__(kFinishThreads)
-    balance_finish_kernel(const float* __restrict__ part_p, const int32_t* __restrict__ part_c, int parts, int E,
-                          int top_k, float coeff, float* __restrict__ loss, int32_t* __restrict__ counts,
-                          float* __restrict__ mean) {
-  pdl_wait();
+struct FinishArgs {
+  int parts, E, top_k;
+  float coeff;
+  float* part_p;    // [parts, E]
+  int32_t* part_c;  // [parts, E + 1]
+  float* loss;
+  int32_t* counts;
+  float* mean;
+};
+
+// One block: counts, means and the loss from the blocks' parts.  Expert e's parts
+// are added by blockDim / E' threads (E' = E rounded up to a power of two) whose
+// sums meet in a fixed order.  `scratch`: 2 * blockDim words.
+__device__ __forceinline__ void finish(const FinishArgs& a, uint32_t* scratch) {
   __shared__ int32_t tokens;
-  __shared__ float warp_sum[kFinishThreads / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float warp_sum[32];
+  const int threads = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int width = 32;  // experts side by side
+  while (width < a.E && width < threads) width *= 2;
+  const int groups = threads / width, at = threadIdx.x & (width - 1), group = threadIdx.x / width;
+  float* sp = reinterpret_cast<float*>(scratch);
+  int32_t* sc = reinterpret_cast<int32_t*>(scratch + threads);
   if (warp == 0) {
     int32_t n = 0;
-    for (int q = lane; q < parts; q += 32) n += part_c[(int64_t)q * (E + 1) + E];
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    if (lane == 0) tokens = n, counts[E] = n;
+    for (int q = lane; q < a.parts; q += 32) n += a.part_c[(int64_t)q * (a.E + 1) + a.E];
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) tokens = n, a.counts[a.E] = n;
   }
-  __syncthreads();
-  const int32_t n = tokens;
   float part = 0.f;
-  for (int e = threadIdx.x; e < E; e += kFinishThreads) {
+  for (int e0 = 0; e0 < a.E; e0 += width) {
+    const int e = e0 + at;
     int32_t c = 0;
     float s = 0.f;
-    for (int q = 0; q < parts; ++q) {
-      c += part_c[(int64_t)q * (E + 1) + e];
-      s += part_p[(int64_t)q * E + e];
+    if (e < a.E) {
+#pragma unroll 8
+      for (int q = group; q < a.parts; q += groups) {
+        c += a.part_c[(int64_t)q * (a.E + 1) + e];
+        s += a.part_p[(int64_t)q * a.E + e];
+      }
     }
-    const float m = n > 0 ? __fdiv_rn(s, (float)n) : 0.f;
-    counts[e] = c;
-    mean[e] = m;
-    part = fmaf(load_factor(c, n, E, top_k), m, part);
+    __syncthreads();  // (the first time round: tokens is there)
+    sp[threadIdx.x] = s;
+    sc[threadIdx.x] = c;
+    __syncthreads();
+    if (group == 0 && e < a.E) {
+      for (int g = 1; g < groups; ++g) s += sp[g * width + at], c += sc[g * width + at];
+      const int32_t n = tokens;
+      const float m = n > 0 ? __fdiv_rn(s, (float)n) : 0.f;
+      a.counts[e] = c;
+      a.mean[e] = m;
+      part = fmaf(load_factor(c, n, a.E, a.top_k), m, part);
+    }
   }
+#pragma unroll
   for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
   if (lane == 0) warp_sum[warp] = part;
   __syncthreads();
   if (threadIdx.x == 0) {
     float s = 0.f;
-    for (int w = 0; w < kFinishThreads / 32; ++w) s += warp_sum[w];
-    *loss = coeff * s;
+    for (int w = 0; w < threads / 32; ++w) s += warp_sum[w];
+    *a.loss = a.coeff * s;
   }
 }
 
-template <typename T, int kN>
+template <typename T, bool kVec, int kN>
 __global__ void __launch_bounds__(kThreads)
-    balance_backward_kernel(const T* __restrict__ logits, int64_t tokens, int E, int64_t ld, const int32_t* __restrict__ counts,
-                            int top_k, const float* __restrict__ d_loss, float coeff, int accumulate, T* __restrict__ d_logits) {
+    balance_kernel(const T* __restrict__ logits, int64_t tokens, int64_t ld, const int32_t* __restrict__ ids, int lanes,
+                   bool all, const FinishArgs f, int* status) {
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  using L = Lanes<T, kVec, kN>;
+  // the warps' sums one after another where all do not fit: 16 warps x 1024 experts
+  constexpr int kSumWarps = 8;
+  __shared__ float sum[kSumWarps * kMaxExperts];
+  __shared__ int32_t count[kMaxExperts + 1];
+  const L lay(lanes);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = f.E;
+  for (int e = threadIdx.x; e <= E; e += kThreads) count[e] = 0;
+  __syncthreads();
+  const int64_t slots = tokens * f.top_k;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < slots; i += (int64_t)gridDim.x * kThreads) {
+    const int e = __ldg(ids + i);
+    if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+  }
+  float acc[L::n];
+#pragma unroll
+  for (int i = 0; i < L::n; ++i) acc[i] = 0.f;
+  int there = 0;
+  bool bad = false;
+  // the next token's logits are on their way while this one's are worked on
+  const int64_t step = (int64_t)gridDim.x * kWarps * lay.per_warp;
+  int64_t t = ((int64_t)blockIdx.x * kWarps + warp) * lay.per_warp + lay.sub;
+  uint32_t w[L::words];
+  lay.load(logits + t * ld, E, t < tokens, w);
+  for (int64_t first = t - lay.sub; first < tokens; first += step, t += step) {
+    uint32_t next[L::words];
+    lay.load(logits + (t + step) * ld, E, t + step < tokens, next);
+    float p[L::n];
+    there += lay.softmax(w, E, t < tokens, p, bad) && lay.l == 0;
+#pragma unroll
+    for (int i = 0; i < L::n; ++i) acc[i] += p[i];
+#pragma unroll
+    for (int i = 0; i < L::words; ++i) w[i] = next[i];
+  }
+  if (bad) latch_status(status, Q4_ERR_NONFINITE);
+  there = __reduce_add_sync(0xffffffffu, there);
+  if (lane == 0) atomicAdd(&count[E], there);
+  // lanes of several tokens hold the same experts
+  for (int o = lay.lanes; o < 32; o <<= 1) {
+#pragma unroll
+    for (int i = 0; i < L::n; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+  }
+#pragma unroll
+  for (int turn = 0; turn < kWarps / kSumWarps; ++turn) {
+    if (warp / kSumWarps == turn && lay.sub == 0) {
+      float* to = sum + warp % kSumWarps * kMaxExperts;
+#pragma unroll
+      for (int i = 0; i < L::n; ++i) {
+        const int e = lay.expert(i);
+        if (e < E) to[e] = turn ? to[e] + acc[i] : acc[i];
+      }
+    }
+    __syncthreads();
+  }
+  for (int e = threadIdx.x; e <= E; e += kThreads) {
+    f.part_c[(int64_t)blockIdx.x * (E + 1) + e] = count[e];
+    if (e == E) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSumWarps; ++i) s += sum[i * kMaxExperts + e];
+    f.part_p[(int64_t)blockIdx.x * E + e] = s;
+  }
+  if (!all) return;
+  cluster_barrier_sync();  // the cluster's parts are written
+  if (blockIdx.x == 0) finish(f, reinterpret_cast<uint32_t*>(sum));
+}
+
+__global__ void __launch_bounds__(1024) balance_finish_kernel(const FinishArgs f) {
+  pdl_wait();
+  __shared__ uint32_t scratch[2 * 1024];
+  finish(f, scratch);
+}
+
+template <typename T, bool kVec, int kN>
+__global__ void __launch_bounds__(256)
+    balance_backward_kernel(const T* __restrict__ logits, int64_t tokens, int E, int64_t ld, const int32_t* __restrict__ counts,
+                            int lanes, int top_k, const float* __restrict__ d_loss, float coeff, int accumulate,
+                            T* __restrict__ d_logits) {
+  pdl_wait();
+  using L = Lanes<T, kVec, kN>;
+  const L lay(lanes);
+  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int32_t n = __ldg(counts + E);
   const float g = n > 0 ? __ldg(d_loss) * __fdiv_rn(coeff, (float)n) : 0.f;
-  float f[kN];
+  float f[L::n];
 #pragma unroll
-  for (int i = 0; i < kN; ++i) f[i] = lane + 32 * i < E ? load_factor(__ldg(counts + lane + 32 * i), n, E, top_k) : 0.f;
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < tokens; t += (int64_t)gridDim.x * kWarps) {
-    float p[kN];
+  for (int i = 0; i < L::n; ++i) f[i] = lay.expert(i) < E ? load_factor(__ldg(counts + lay.expert(i)), n, E, top_k) : 0.f;
+  const int64_t step = (int64_t)gridDim.x * warps * lay.per_warp;
+  int64_t t = ((int64_t)blockIdx.x * warps + warp) * lay.per_warp + lay.sub;
+  uint32_t w[L::words];
+  lay.load(logits + t * ld, E, t < tokens, w);
+  for (int64_t first = t - lay.sub; first < tokens; first += step, t += step) {
+    uint32_t next[L::words];
+    lay.load(logits + (t + step) * ld, E, t + step < tokens, next);
+    const bool live = t < tokens;
+    float p[L::n];
     bool bad = false;
-    token_softmax<T, kN>(logits + t * ld, E, lane, p, bad);
+    lay.softmax(w, E, live, p, bad);
     float dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) dot = fmaf(p[i], f[i], dot);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    for (int i = 0; i < L::n; ++i) dot = fmaf(p[i], f[i], dot);
+    dot = lay.sum(dot);
     T* out = d_logits + t * E;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int e = lane + 32 * i;
-      if (e >= E) continue;
-      float d = g * p[i] * (f[i] - dot);
-      if (accumulate) d += Elem<T>::to_f(out[e]);
-      out[e] = to_elem<T>(d);
+    for (int i = 0; i < L::n; ++i) p[i] = g * p[i] * (f[i] - dot);
+    if constexpr (kVec) {
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        const int e = 8 * (lay.l + lay.lanes * c);
+        if (!live || e >= E) continue;
+        uint4* to = reinterpret_cast<uint4*>(out + e);
+        float* d = p + 8 * c;
+        if (accumulate) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] += Elem<T>::to_f(out[e + i]);
+        }
+        if constexpr (sizeof(T) == 4) {
+          to[0] = make_uint4(__float_as_uint(d[0]), __float_as_uint(d[1]), __float_as_uint(d[2]), __float_as_uint(d[3]));
+          to[1] = make_uint4(__float_as_uint(d[4]), __float_as_uint(d[5]), __float_as_uint(d[6]), __float_as_uint(d[7]));
+        } else {
+          to[0] = make_uint4(pack2<T>(d[0], d[1]), pack2<T>(d[2], d[3]), pack2<T>(d[4], d[5]), pack2<T>(d[6], d[7]));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < L::n; ++i) {
+        const int e = lay.expert(i);
+        if (!live || e >= E) continue;
+        if (accumulate) p[i] += Elem<T>::to_f(out[e]);
+        out[e] = to_elem<T>(p[i]);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < L::words; ++i) w[i] = next[i];
   }
 }
 
+// The kernels' forms: eight experts per load (kVec) with 1, 2 or 4 loads per lane,
+// or single experts, 1 to 32 per lane.
 template <typename F>
-q4_status by_experts(int E, F&& f) {
-  if (E <= 32) return f(std::integral_constant<int, 1>());
-  if (E <= 64) return f(std::integral_constant<int, 2>());
-  if (E <= 128) return f(std::integral_constant<int, 4>());
-  if (E <= 256) return f(std::integral_constant<int, 8>());
-  if (E <= 512) return f(std::integral_constant<int, 16>());
-  return f(std::integral_constant<int, 32>());
+q4_status by_experts(bool vec, int E, F&& f) {
+  if (vec) {
+    if (E <= 256) return f(std::true_type(), std::integral_constant<int, 1>());
+    if (E <= 512) return f(std::true_type(), std::integral_constant<int, 2>());
+    return f(std::true_type(), std::integral_constant<int, 4>());
+  }
+  if (E <= 64) return f(std::false_type(), std::integral_constant<int, 2>());
+  if (E <= 256) return f(std::false_type(), std::integral_constant<int, 8>());
+  return f(std::false_type(), std::integral_constant<int, 32>());
+}
+int lanes_of(bool vec, int E) {
+  int lanes = 1;
+  while (lanes < 32 && 8 * lanes < E) lanes *= 2;
+  return vec ? lanes : 32;
 }
 
-int balance_grid(int64_t tokens) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(tokens, 4 * kWarps), 2 * num_sms()));
-}
+// Blocks: a cluster that finishes by itself where a warp has few tokens (1000 x 64:
+// 4.6 us, with a second kernel 6.1), else one per SM.
+bool one_cluster(int64_t tokens, int64_t E) { return tokens * E <= (int64_t)kCluster * kWarps * 256 * 16; }
+int balance_grid(int64_t tokens, int64_t E) { return one_cluster(tokens, E) ? kCluster : num_sms(); }
 
 }  // namespace
 
 size_t balance_workspace_bytes(int64_t tokens, int64_t E) {
-  return (size_t)balance_grid(tokens) * (size_t)(2 * E + 1) * 4;
+  return (size_t)balance_grid(tokens, E) * (size_t)(2 * E + 1) * 4;
 }
 
 q4_status launch_balance(const void* logits, int dtype, int64_t tokens, int E, int64_t ld, const int32_t* ids, int top_k,
                          float coeff, float* loss, int32_t* counts, float* mean, void* ws, cudaStream_t stream) {
-  const int grid = balance_grid(tokens);
-  float* part_p = static_cast<float*>(ws);
-  int32_t* part_c = reinterpret_cast<int32_t*>(part_p + (size_t)grid * E);
+  const int grid = balance_grid(tokens, E);
+  const bool all = one_cluster(tokens, E);
+  FinishArgs f = {grid, E, top_k, coeff, static_cast<float*>(ws), nullptr, loss, counts, mean};
+  f.part_c = reinterpret_cast<int32_t*>(f.part_p + (size_t)grid * E);
+  const bool vec = E % 8 == 0 && ld * (dtype == Q4_F32 ? 4 : 2) % 16 == 0 && mult(logits, 16);
   const q4_status st = by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
-    return by_experts(E, [&](auto n) {
-      return launch_pdl(balance_kernel<T, decltype(n)::value>, grid, kThreads, 0, stream, static_cast<const T*>(logits), tokens, E,
-                        ld, ids, tokens * top_k, part_p, part_c, device_status_ptr());
+    return by_experts(vec, E, [&](auto v, auto n) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)grid, 1, 1);
+      cfg.blockDim = dim3(kThreads, 1, 1);
+      cfg.stream = stream;
+      cudaLaunchAttribute attr[2];
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      attr[1].id = cudaLaunchAttributeClusterDimension;
+      attr[1].val.clusterDim.x = kCluster;
+      attr[1].val.clusterDim.y = 1;
+      attr[1].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = all ? 2 : 1;
+      return cudaLaunchKernelEx(&cfg, balance_kernel<T, decltype(v)::value, decltype(n)::value>, static_cast<const T*>(logits),
+                                tokens, ld, ids, lanes_of(vec, E), all, f, device_status_ptr()) == cudaSuccess
+                 ? Q4_OK
+                 : Q4_ERR_CUDA;
     });
   });
-  if (st != Q4_OK) return st;
-  return launch_pdl(balance_finish_kernel, 1, kFinishThreads, 0, stream, static_cast<const float*>(part_p),
-                    static_cast<const int32_t*>(part_c), grid, E, top_k, coeff, loss, counts, mean);
+  if (st != Q4_OK || all) return st;
+  return launch_pdl(balance_finish_kernel, 1, 1024, 0, stream, f);
 }
 
 q4_status launch_balance_backward(const void* logits, int dtype, int64_t tokens, int E, int64_t ld, const int32_t* counts,
                                   int top_k, const float* d_loss, float coeff, bool accumulate, void* d_logits,
                                   cudaStream_t stream) {
-  const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(tokens, kWarps), (int64_t)num_sms() * 8);
+  const bool vec = E % 8 == 0 && ld * (dtype == Q4_F32 ? 4 : 2) % 16 == 0 && mult(logits, 16) && mult(d_logits, 16);
+  const int lanes = lanes_of(vec, E), per_block = 8 * (32 / lanes);  // tokens at a time
+  const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(tokens, per_block), (int64_t)num_sms() * 6);
   return by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
-    return by_experts(E, [&](auto n) {
-      return launch_pdl(balance_backward_kernel<T, decltype(n)::value>, grid, kThreads, 0, stream, static_cast<const T*>(logits),
-                        tokens, E, ld, counts, top_k, d_loss, coeff, (int)accumulate, static_cast<T*>(d_logits));
+    return by_experts(vec, E, [&](auto v, auto n) {
+      return launch_pdl(balance_backward_kernel<T, decltype(v)::value, decltype(n)::value>, grid, 256, 0, stream,
+                        static_cast<const T*>(logits), tokens, E, ld, counts, lanes, top_k, d_loss, coeff, (int)accumulate,
+                        static_cast<T*>(d_logits));
     });
   });
 }

@@ -1,0 +1,321 @@
+// What the norm and its gradient share: rows spread over threads, their reduction,
+// and the ring of rows in shared memory.
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "common.cuh"
+#include "elem.cuh"
+#include "internal.h"
+
+namespace q4 {
+namespace {
+
+// 8 of the 128 columns of a block, held by one of 16 lanes: with 128-bit accesses
+// (kVec) columns 8 l .. 8 l + 7 of lane l, otherwise l, l + 16, ..., 16-bit
+// elements one per word.  Columns past the block's end are zero.
+template <typename T, bool kVec>
+struct Piece {
+  static constexpr bool packed = kVec && sizeof(T) == 2;
+  static constexpr int words = packed ? 4 : 8;
+  uint32_t w[words];
+
+  // cols <= 0: no column.
+  __device__ __forceinline__ void load(const T* p, int l, int cols) {
+    if constexpr (kVec) {
+#pragma unroll
+      for (int i = 0; i < words / 4; ++i) {
+        const uint4 v = 8 * l < cols ? reinterpret_cast<const uint4*>(p + 8 * l)[i] : make_uint4(0u, 0u, 0u, 0u);
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = l + 16 * i;
+        if constexpr (sizeof(T) == 2)
+          w[i] = at < cols ? reinterpret_cast<const unsigned short*>(p)[at] : 0u;
+        else
+          w[i] = at < cols ? __float_as_uint(p[at]) : 0u;
+      }
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (packed) {
+      const float2 v = unpack2<T>(w[i / 2]);
+      return i & 1 ? v.y : v.x;
+    } else if constexpr (sizeof(T) == 2) {
+      return unpack2<T>(w[i]).x;
+    } else {
+      return __uint_as_float(w[i]);
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, int l, int cols, const float (&f)[8]) {
+    if constexpr (kVec) {
+      if (8 * l >= cols) return;
+      uint4* out = reinterpret_cast<uint4*>(p + 8 * l);
+      if constexpr (sizeof(T) == 4) {
+        out[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        out[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+      } else {
+        out[0] = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (l + 16 * i < cols) p[l + 16 * i] = to_elem<T>(f[i]);
+    }
+  }
+  // Eight codes: bytes 0..3 in c.x, 4..7 in c.y.
+  static __device__ __forceinline__ void store_codes(uint8_t* p, int l, int cols, uint2 c) {
+    if constexpr (kVec) {
+      if (8 * l < cols) *reinterpret_cast<uint2*>(p + 8 * l) = c;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (l + 16 * i < cols) p[l + 16 * i] = (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+    }
+  }
+};
+
+// The weights of a piece (columns c + ...), T or FP32; all 1 without weights.
+template <typename T, bool kVec>
+__device__ __forceinline__ void load_weights(const void* w, bool w32, int64_t c, int l, int cols, float (&f)[8]) {
+  if (!w) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = 1.f;
+  } else if (w32) {
+    Piece<float, kVec> p;
+    p.load(static_cast<const float*>(w) + c, l, cols);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = p.at(i);
+  } else {
+    Piece<T, kVec> p;
+    p.load(static_cast<const T*>(w) + c, l, cols);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = p.at(i);
+  }
+}
+
+// (sum, largest) over the `group` threads that hold a row, in every one of them.
+// Groups of more than a warp are whole warps of a block that comes here together;
+// buf alternates between two buffers from row to row, so that one barrier per row
+// is enough.
+struct Exchange {
+  float2 part[2][32];
+};
+template <bool kTop>
+__device__ __forceinline__ float2 group_reduce(float sum, float top, int group, Exchange& ex, int buf) {
+  const int width = min(group, 32);
+  for (int o = width / 2; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (kTop) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  }
+  if (group > 32) {
+    const int lane = threadIdx.x & 31, warps = group >> 5, first = (threadIdx.x >> 5) / warps * warps;
+    if (lane == 0) ex.part[buf][threadIdx.x >> 5] = make_float2(sum, top);
+    __syncthreads();
+    if (warps <= 8) {  // few enough for every thread to add them up
+      sum = top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i >= warps) break;
+        const float2 v = ex.part[buf][first + i];
+        sum += v.x;
+        if (kTop) top = fmaxf(top, v.y);
+      }
+    } else {
+      const float2 v = lane < warps ? ex.part[buf][first + lane] : make_float2(0.f, 0.f);
+      sum = v.x, top = v.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (kTop) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
+    }
+  }
+  return make_float2(sum, top);
+}
+
+// Threads of a block for kC pieces per thread.
+constexpr int max_threads(int C) { return C == 1 ? 1024 : 512; }
+
+// Which row and columns a thread holds: `group` threads per row, the block's
+// groups one row each, piece i of thread t the 128-column block t / 16 + i *
+// (group / 16).
+struct Place {
+  int l, t, group, per_block, sub, stride;
+  __device__ __forceinline__ explicit Place(int group_)
+      : l(threadIdx.x & 15), t(threadIdx.x % group_), group(group_), per_block(blockDim.x / group_), sub(threadIdx.x / group_),
+        stride(group_ >> 4) {}
+  __device__ __forceinline__ int block(int i) const { return (t >> 4) + i * stride; }
+  __device__ __forceinline__ int64_t at(int i) const { return (int64_t)block(i) * 128; }
+  __device__ __forceinline__ int cols(int i, int64_t H) const { return (int)min((int64_t)128, H - at(i)); }
+};
+
+// ------------------------------------------------------------------ rows through shared memory
+constexpr int kMaxRing = 8;
+// A ring of stages, each the block's next per_block rows of up to three matrices.
+struct Ring {
+  uint64_t full[kMaxRing];
+  int abort;
+};
+struct RingArgs {
+  int stages;
+  uint32_t stage_bytes, row_bytes;
+  KernelCtl ctl;
+};
+
+__device__ __forceinline__ void ring_init(Ring& ring, const RingArgs& r) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < r.stages; ++s) mbar_init(smem_u32(&ring.full[s]), 1);
+    ring.abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+}
+
+// Bytes of a row in a stage.  Rows that do not lie on 16-byte boundaries (kVec
+// false) are copied with the whole 16-byte words that hold their ends.
+template <bool kVec>
+__host__ __device__ constexpr uint32_t staged_row(uint32_t row_bytes) {
+  return kVec ? row_bytes : (row_bytes + 30) / 16 * 16;
+}
+
+// One thread: rows base .. of the matrices into stage s.  The last row of all is
+// left out where its copy would reach behind it (kVec false); it is read in place.
+template <bool kVec, int kMats>
+__device__ __forceinline__ void ring_fill(Ring& ring, const RingArgs& r, uint32_t smem, int s, const void* const (&mat)[kMats],
+                                          const int64_t (&pitch)[kMats], int64_t base, int64_t rows, int per_block) {
+  if (base >= rows) return;
+  const int n = (int)min((int64_t)per_block, (kVec ? rows : rows - 1) - base);
+  const uint32_t bar = smem_u32(&ring.full[s]), staged = staged_row<kVec>(r.row_bytes);
+  const uint32_t dst = smem + s * r.stage_bytes;
+  if constexpr (kVec) {
+    int mats = 0;
+    for (int m = 0; m < kMats; ++m) mats += mat[m] != nullptr;
+    mbar_arrive_expect_tx(bar, (uint32_t)(mats * n) * staged);
+    for (int m = 0; m < kMats; ++m) {
+      if (!mat[m]) continue;
+      const uint8_t* src = static_cast<const uint8_t*>(mat[m]) + base * pitch[m];
+      const uint32_t to = dst + (uint32_t)(m * per_block) * staged;
+      if (pitch[m] == r.row_bytes)
+        bulk_load(to, src, (uint32_t)n * staged, bar);
+      else
+        for (int i = 0; i < n; ++i) bulk_load(to + i * staged, src + i * pitch[m], staged, bar);
+    }
+  } else {
+    uint32_t bytes = 0;
+    for (int turn = 0; turn < 2; ++turn) {  // the bytes first, then the copies
+      if (turn) mbar_arrive_expect_tx(bar, bytes);
+      for (int m = 0; m < kMats; ++m) {
+        if (!mat[m]) continue;
+        for (int i = 0; i < n; ++i) {
+          const uintptr_t at = reinterpret_cast<uintptr_t>(mat[m]) + (base + i) * pitch[m], begin = at & ~uintptr_t(15);
+          const uint32_t size = (uint32_t)(((at + r.row_bytes + 15) & ~uintptr_t(15)) - begin);
+          if (turn)
+            bulk_load(dst + (uint32_t)(m * per_block + i) * staged, reinterpret_cast<const void*>(begin), size, bar);
+          else
+            bytes += size;
+        }
+      }
+    }
+  }
+}
+
+// A row of a matrix in its stage.
+template <bool kVec, typename T>
+__device__ __forceinline__ const T* ring_row(const uint8_t* stage, const RingArgs& r, int m, const Place& pl, const void* mat,
+                                             int64_t pitch, int64_t row) {
+  const uint8_t* p = stage + (uint32_t)(m * pl.per_block + pl.sub) * staged_row<kVec>(r.row_bytes);
+  if (!kVec) p += (reinterpret_cast<uintptr_t>(mat) + row * pitch) & 15;
+  return reinterpret_cast<const T*>(p);
+}
+
+// The weights of a thread's pieces as they were loaded: 16-bit ones stay packed.
+// FP32 weights of 16-bit rows are read from global memory every time.
+template <typename T, bool kVec, int kC>
+struct HeldWeights {
+  Piece<T, kVec> w[kC];
+  const void* p;
+  bool fp32, held;
+  __device__ __forceinline__ HeldWeights(const void* weight, bool w_fp32, const Place& pl, int64_t H)
+      : p(weight), fp32(w_fp32), held(weight && (!w_fp32 || sizeof(T) == 4)) {
+    if (held) {
+#pragma unroll
+      for (int i = 0; i < kC; ++i) w[i].load(static_cast<const T*>(weight) + pl.at(i), pl.l, pl.cols(i, H));
+    }
+  }
+  __device__ __forceinline__ void get(const Place& pl, int64_t H, int i, float (&f)[8]) const {
+    if (held) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = w[i].at(j);
+    } else {
+      load_weights<T, kVec>(p, fp32, pl.at(i), pl.l, pl.cols(i, H), f);
+    }
+  }
+};
+
+// How rows are spread: kC pieces per thread, threads per row and per block, blocks,
+// and the ring's stages (0: none) and bytes.
+struct Shape {
+  int C, group, threads, grid, stages;
+  uint32_t stage_bytes;
+};
+constexpr uint32_t kRingTotal = 216 * 1024;  // of an SM's shared memory
+Shape shape_of(int64_t rows, int64_t H, int mats, int size, bool vec, int most_resident) {
+  const int blocks = (int)ceil_div(H, 128);
+  auto spread = [&](int C, int most_threads) {
+    Shape s = {};
+    s.C = C;
+    const int halves = (int)ceil_div(blocks, C);  // groups of 16 lanes
+    s.group = halves == 1 ? 16 : (halves + 1) / 2 * 32;
+    s.threads = std::max(1, most_threads / s.group) * s.group;
+    return s;
+  };
+  const int64_t sms = num_sms();
+  if (blocks <= (vec ? 128 : 32)) {
+    Shape s = spread(!vec ? 2 : blocks >= 16 ? 4 : blocks >= 4 ? 2 : 1, 256);
+    const int per_block = s.threads / s.group;
+    const uint32_t row_bytes = (uint32_t)(H * size);
+    s.stage_bytes = (uint32_t)(mats * per_block) * (vec ? staged_row<true>(row_bytes) : staged_row<false>(row_bytes));
+    int resident = s.threads > 256 ? 1 : most_resident;
+    while (resident > 1 && 2 * s.stage_bytes > kRingTotal / resident) --resident;
+    s.stages = (int)std::min<int64_t>(kMaxRing, kRingTotal / resident / s.stage_bytes);
+    s.grid = (int)std::min<int64_t>(ceil_div(rows, per_block), sms * resident);
+    if (s.stages >= 2 && ceil_div(rows, per_block) >= 2 * sms * resident) return s;
+  }
+  int C = 1;
+  const int most = rows <= 2 * sms ? 64 : 16;  // blocks of 128 columns that one piece per thread takes
+  if (blocks > most) C = blocks > 128 ? 8 : 4;
+  Shape s = spread(C, 128);
+  s.grid = (int)std::min<int64_t>(ceil_div(rows, s.threads / s.group), sms * std::max(1, 1024 / s.threads));
+  return s;
+}
+
+template <typename F>
+q4_status by_pieces(int C, F&& f) {
+  if (C == 1) return f(std::integral_constant<int, 1>());
+  if (C == 2) return f(std::integral_constant<int, 2>());
+  if (C == 4) return f(std::integral_constant<int, 4>());
+  return f(std::integral_constant<int, 8>());
+}
+
+// The kernel's shared memory is allowed once per device.
+template <typename Kernel>
+q4_status allow_smem(Kernel kernel, int (&ready)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return Q4_ERR_CUDA;
+  if (!ready[dev]) {
+    Q4_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingTotal));
+    ready[dev] = 1;
+  }
+  return Q4_OK;
+}
+
+RingArgs ring_of(const Shape& s, int64_t row_bytes) {
+  return RingArgs{s.stages, s.stage_bytes, (uint32_t)row_bytes, KernelCtl{device_status_ptr(), wait_budget_ns()}};
+}
+
+}  // namespace
+}  // namespace q4

@@ -1,0 +1,253 @@
+// Gradient of the root-mean-square norm.  With g = d_y w,
+//   d_x = rstd g - h rstd^3 mean(g h) (+ d_h),  d_w = sum over rows of d_y h rstd
+//
+// Each block of threads takes every gridDim.x-th row (or as many rows as it has
+// groups) and adds its rows' part of d_w up in registers, columns fixed to
+// threads; the blocks' sums go to the workspace and are added in their order by
+// a second kernel, so that results do not depend on timing.
+#include "norm.cuh"
+
+namespace q4 {
+namespace {
+
+// The block's part of d_w: the groups' sums one after another.
+template <bool kVec, int kC>
+__device__ __forceinline__ void store_partial(const NormBackwardArgs& a, const Place& pl, const float (&acc)[kC][8]) {
+  if (!a.partial) return;
+  float* out = a.partial + (int64_t)blockIdx.x * a.H;
+  for (int s = 0; s < pl.per_block; ++s) {
+    if (s) __syncthreads();
+    if (pl.sub != s) continue;
+#pragma unroll
+    for (int i = 0; i < kC; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = kVec ? 8 * pl.l + j : pl.l + 16 * j;
+        if (c < pl.cols(i, a.H)) out[pl.at(i) + c] = s ? out[pl.at(i) + c] + acc[i][j] : acc[i][j];
+      }
+  }
+}
+
+template <typename T, bool kVec, int kC>
+__global__ void __launch_bounds__(max_threads(kC))
+    norm_backward_kernel(const NormBackwardArgs a, int group) {
+  pdl_wait();
+  using P = Piece<T, kVec>;
+  __shared__ Exchange ex;
+  const Place pl(group);
+  float acc[kC][8];
+#pragma unroll
+  for (int i = 0; i < kC; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+  int buf = 0;
+  for (int64_t base = (int64_t)blockIdx.x * pl.per_block; base < a.rows; base += (int64_t)gridDim.x * pl.per_block, buf ^= 1) {
+    const int64_t row = base + pl.sub;
+    const bool live = row < a.rows;
+    P dy[kC], h[kC], dh[kC];
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      const int n = live ? pl.cols(i, a.H) : 0;
+      dy[i].load(static_cast<const T*>(a.d_y) + row * a.ld_d_y + pl.at(i), pl.l, n);
+      h[i].load(static_cast<const T*>(a.h) + row * a.ld_h + pl.at(i), pl.l, n);
+      if (a.d_h) dh[i].load(static_cast<const T*>(a.d_h) + row * a.ld_d_h + pl.at(i), pl.l, n);
+    }
+    const float rstd = live ? a.rstd[row] : 0.f;
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      float w[8];
+      load_weights<T, kVec>(a.weight, a.w_fp32, pl.at(i), pl.l, pl.cols(i, a.H), w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float hj = h[i].at(j);
+        dot = fmaf(dy[i].at(j) * w[j], hj, dot);
+        acc[i][j] = fmaf(dy[i].at(j), hj * rstd, acc[i][j]);
+      }
+    }
+    const float2 r = group_reduce<false>(dot, 0.f, group, ex, buf);
+    const float c = rstd * rstd * (r.x / (float)a.H);  // mean(g h) rstd^2
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      float w[8], d[8];
+      load_weights<T, kVec>(a.weight, a.w_fp32, pl.at(i), pl.l, pl.cols(i, a.H), w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        d[j] = rstd * fmaf(-h[i].at(j), c, dy[i].at(j) * w[j]);
+        if (a.d_h) d[j] += dh[i].at(j);
+      }
+      P::store(static_cast<T*>(a.d_x) + row * a.H + pl.at(i), pl.l, live ? pl.cols(i, a.H) : 0, d);
+    }
+  }
+  store_partial<kVec, kC>(a, pl, acc);
+}
+
+// The same with the rows in shared memory, which are read twice there; a stage is
+// refilled after the next row's exchange, when every thread has left it.
+template <typename T, bool kVec, int kC, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
+    norm_backward_ring_kernel(const NormBackwardArgs a, int group, const RingArgs r) {
+  extern __shared__ __align__(128) uint8_t stage_smem[];
+  using P = Piece<T, kVec>;
+  __shared__ Ring ring;
+  __shared__ Exchange ex;
+  ring_init(ring, r);
+  pdl_wait();
+  const Place pl(group);
+  const void* const mat[3] = {a.d_y, a.h, a.d_h};
+  const int64_t size = sizeof(T), pitch[3] = {a.ld_d_y * size, a.ld_h * size, a.ld_d_h * size};
+  const int64_t step = (int64_t)gridDim.x * pl.per_block, base0 = (int64_t)blockIdx.x * pl.per_block;
+  if (threadIdx.x == 0)
+    for (int s = 0; s < r.stages; ++s)
+      ring_fill<kVec>(ring, r, smem_u32(stage_smem), s, mat, pitch, base0 + s * step, a.rows, pl.per_block);
+  const HeldWeights<T, kVec, kC> w(a.weight, a.w_fp32, pl, a.H);
+  float acc[kC][8];
+#pragma unroll
+  for (int i = 0; i < kC; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+  int stage = 0, buf = 0;
+  uint32_t phase = 0;
+  const float inv_H = 1.f / (float)a.H;
+  for (int64_t base = base0; base < a.rows; base += step, buf ^= 1) {
+    const int64_t row = base + pl.sub;
+    const bool live = row < a.rows;
+    const float rstd = live ? __ldg(a.rstd + row) : 0.f;
+    mbar_wait(smem_u32(&ring.full[stage]), phase, r.ctl, &ring.abort);
+    const uint8_t* st = stage_smem + stage * r.stage_bytes;
+    const T* sdy = ring_row<kVec, T>(st, r, 0, pl, a.d_y, pitch[0], row);
+    const T* sh = ring_row<kVec, T>(st, r, 1, pl, a.h, pitch[1], row);
+    const T* sdh = ring_row<kVec, T>(st, r, 2, pl, a.d_h, pitch[2], row);
+    const bool in_place = !kVec && row == a.rows - 1;
+    const T* gdy = static_cast<const T*>(a.d_y) + row * a.ld_d_y;
+    const T* gh = static_cast<const T*>(a.h) + row * a.ld_h;
+    const T* gdh = static_cast<const T*>(a.d_h) + row * a.ld_d_h;
+    auto load = [&](P& p, const T* staged, const T* global, int i, int n) {
+      if (in_place)
+        p.load(global + pl.at(i), pl.l, n);
+      else
+        p.load(staged + pl.at(i), pl.l, n);
+    };
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      const int n = live ? pl.cols(i, a.H) : 0;
+      P dy, h;
+      load(dy, sdy, gdy, i, n);
+      load(h, sh, gh, i, n);
+      float f[8];
+      w.get(pl, a.H, i, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float t = dy.at(j) * h.at(j);
+        dot = fmaf(t, f[j], dot);
+        acc[i][j] = fmaf(t, rstd, acc[i][j]);
+      }
+    }
+    const float2 q = group_reduce<false>(dot, 0.f, group, ex, buf);
+    if (pl.group <= 32) __syncthreads();
+    if (threadIdx.x == 0 && base != base0) {  // every thread has left the stage of the row before
+      const int64_t next = base + (r.stages - 1) * step;
+      ring_fill<kVec>(ring, r, smem_u32(stage_smem), stage ? stage - 1 : r.stages - 1, mat, pitch, next, a.rows, pl.per_block);
+    }
+    const float c = rstd * rstd * rstd * (q.x * inv_H);
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      const int n = live ? pl.cols(i, a.H) : 0;
+      P dy, h, dh;
+      load(dy, sdy, gdy, i, n);
+      load(h, sh, gh, i, n);
+      if (a.d_h) load(dh, sdh, gdh, i, n);
+      float f[8], d[8];
+      w.get(pl, a.H, i, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        d[j] = fmaf(-h.at(j), c, dy.at(j) * (f[j] * rstd));
+        if (a.d_h) d[j] += dh.at(j);
+      }
+      P::store(static_cast<T*>(a.d_x) + row * a.H + pl.at(i), pl.l, n, d);
+    }
+    if (++stage == r.stages) stage = 0, phase ^= 1;
+  }
+  store_partial<kVec, kC>(a, pl, acc);
+}
+
+// d_w[c] = sum of the `parts` partial sums of column c.  32 columns per block, 32
+// warps of partial sums each, which meet in a fixed order (8 warps: 10 us instead
+// of 3 for 304 parts of 7168).
+constexpr int kWeightWarps = 32;
+__global__ void __launch_bounds__(32 * kWeightWarps) norm_weight_kernel(const float* __restrict__ partial, int parts, int64_t H,
+                                                                        float* __restrict__ d_w) {
+  pdl_wait();
+  __shared__ float s[kWeightWarps][33];
+  const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  float sum = 0.f;
+  if (c < H) {
+#pragma unroll 8
+    for (int p = threadIdx.y; p < parts; p += kWeightWarps) sum += partial[(int64_t)p * H + c];
+  }
+  s[threadIdx.y][threadIdx.x] = sum;
+  __syncthreads();
+  // warp y adds the parts of column y up
+  sum = s[threadIdx.x][threadIdx.y];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const int64_t mine = (int64_t)blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && mine < H) d_w[mine] = sum;
+}
+
+template <typename T, bool kVec, int kC, int kThreads>
+q4_status launch_norm_backward_ring(const NormBackwardArgs& a, const Shape& s, cudaStream_t stream) {
+  static int ready[64] = {0};
+  const auto kernel = norm_backward_ring_kernel<T, kVec, kC, kThreads>;
+  const q4_status st = allow_smem(kernel, ready);
+  if (st != Q4_OK) return st;
+  return launch_pdl(kernel, s.grid, s.threads, (size_t)s.stages * s.stage_bytes, stream, a, s.group,
+                    ring_of(s, a.H * (int64_t)sizeof(T)));
+}
+
+template <typename T, int kC>
+q4_status launch_norm_backward_form(const NormBackwardArgs& a, const Shape& s, bool vec, cudaStream_t stream) {
+  if (s.stages) {
+    if constexpr (kC == 2)
+      if (!vec) return launch_norm_backward_ring<T, false, kC, 256>(a, s, stream);
+    if constexpr (kC == 4)
+      if (s.threads > 256) return launch_norm_backward_ring<T, true, kC, 512>(a, s, stream);
+    if constexpr (kC <= 4) return launch_norm_backward_ring<T, true, kC, 256>(a, s, stream);
+  }
+  if constexpr (kC != 2)
+    return launch_pdl(vec ? norm_backward_kernel<T, true, kC> : norm_backward_kernel<T, false, kC>, s.grid, s.threads, 0, stream, a,
+                      s.group);
+  return Q4_ERR_UNSUPPORTED_SHAPE;  // not reached: two pieces are for rings
+}
+
+}  // namespace
+
+// Room for the largest grid that these sizes can have.
+size_t norm_backward_workspace_bytes(int64_t rows, int64_t H) {
+  if (rows == 0 || H == 0) return 0;
+  int grid = 0;
+  for (int mats : {2, 3})
+    for (int size : {2, 4})
+      for (bool vec : {false, true}) grid = std::max(grid, shape_of(rows, H, mats, size, vec, 2).grid);
+  return (size_t)grid * (size_t)H * sizeof(float);
+}
+
+q4_status launch_norm_backward(NormBackwardArgs a, int dtype, float* d_weight, void* ws, cudaStream_t stream) {
+  a.partial = d_weight ? static_cast<float*>(ws) : nullptr;
+  const int size = dtype == Q4_F32 ? 4 : 2;
+  const bool vec = a.H % 8 == 0 && a.ld_d_y * size % 16 == 0 && a.ld_h * size % 16 == 0 && (!a.d_h || a.ld_d_h * size % 16 == 0) &&
+                   mult(a.d_y, 16) && mult(a.h, 16) && mult(a.d_h, 16) && mult(a.d_x, 16) && mult(a.weight, 16);
+  const Shape s = shape_of(a.rows, a.H, a.d_h ? 3 : 2, size, vec, 2);
+  const q4_status st = by_dtype(dtype, [&](auto tag) {
+    using T = decltype(tag);
+    return by_pieces(s.C, [&](auto c) {
+      return launch_norm_backward_form<T, decltype(c)::value>(a, s, vec, stream);
+    });
+  });
+  if (st != Q4_OK || !d_weight) return st;
+  return launch_pdl(norm_weight_kernel, (unsigned)ceil_div(a.H, 32), dim3(32, kWeightWarps), 0, stream, static_cast<const float*>(ws), s.grid,
+                    a.H, d_weight);
+}
+
+}  // namespace q4
