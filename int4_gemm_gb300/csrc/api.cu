@@ -949,7 +949,7 @@ q4_status norm_common(int form, const void* x, int dtype, int64_t rows, int64_t 
   NormArgs a = {};
   a.x = x; a.residual = residual; a.weight = weight;
   a.rows = rows; a.H = H; a.ldx = ldx; a.ld_residual = ld_residual;
-  a.w_fp32 = w_dtype == Q4_F32; a.eps = eps;
+  a.w_dtype = w_dtype; a.eps = eps;
   a.h = h; a.y = y; a.codes = static_cast<uint8_t*>(codes); a.scales = scales; a.rstd = rstd;
   return launch_norm(a, dtype, form, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -1000,7 +1000,7 @@ q4_status rms_norm_backward(const void* d_y, int dtype, int64_t rows, int64_t H,
   NormBackwardArgs a = {};
   a.d_y = d_y; a.h = h; a.d_h = d_h; a.weight = weight;
   a.rows = rows; a.H = H; a.ld_d_y = ld_d_y; a.ld_h = ld_h; a.ld_d_h = ld_d_h;
-  a.rstd = rstd; a.w_fp32 = w_dtype == Q4_F32; a.d_x = d_x;
+  a.rstd = rstd; a.w_dtype = w_dtype; a.d_x = d_x;
   return launch_norm_backward(a, dtype, d_weight, ws, s);
 }
 

@@ -9,9 +9,9 @@
 // A token's logits are held by 1 to 32 lanes, eight neighbouring experts per load
 // where rows are aligned (Lanes), else by a warp, lane l the experts l, l + 32, ...;
 // its probabilities are added up in registers, token by token.  The blocks' sums
-// meet in the workspace and are added in a fixed order: by the first block of a
-// cluster that has done everything, where there are few tokens, else by a second
-// kernel (the counts are integers, whose order does not matter).
+// meet in the workspace and are added in a fixed order: by the same blocks, one
+// cluster, where there are few tokens, else by a second kernel (the counts are
+// integers, whose order does not matter).
 #include <algorithm>
 #include <type_traits>
 
@@ -26,12 +26,21 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kCluster = 8;
 
+// 2^x within 2^-22 relative (0 below 2^-126).
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The lanes that hold a token and their experts: kVec: `lanes` lanes, chunk c of
 // lane l the experts 8 (l + lanes c) ...; otherwise a warp, single experts.
 template <typename T, bool kVec, int kN>
 struct Lanes {
   static constexpr int n = kVec ? 8 * kN : kN;  // experts of a lane
   static constexpr int words = kVec ? kN * 2 * (int)sizeof(T) : kN;
+  // -inf, twice in a word of 16-bit elements: what experts behind the last have
+  static constexpr uint32_t kMasked = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
   int lanes, l, sub, per_warp;
   __device__ __forceinline__ explicit Lanes(int lanes_)
       : lanes(kVec ? lanes_ : 32), l(threadIdx.x & (lanes - 1)), sub((threadIdx.x & 31) / lanes), per_warp(32 / lanes) {}
@@ -44,7 +53,7 @@ struct Lanes {
 #pragma unroll
         for (int i = 0; i < per; ++i) {
           const int e = 8 * (l + lanes * c);
-          const uint4 v = live && e < E ? __ldg(reinterpret_cast<const uint4*>(row + e) + i) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 v = live && e < E ? __ldg(reinterpret_cast<const uint4*>(row + e) + i) : make_uint4(kMasked, kMasked, kMasked, kMasked);
           uint32_t* o = w + 4 * (c * per + i);
           o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
         }
@@ -53,9 +62,9 @@ struct Lanes {
       for (int i = 0; i < kN; ++i) {
         const int e = expert(i);
         if constexpr (sizeof(T) == 2)
-          w[i] = live && e < E ? __ldg(reinterpret_cast<const unsigned short*>(row) + e) : 0u;
+          w[i] = live && e < E ? __ldg(reinterpret_cast<const unsigned short*>(row) + e) : kMasked;
         else
-          w[i] = live && e < E ? __float_as_uint(__ldg(row + e)) : 0u;
+          w[i] = live && e < E ? __float_as_uint(__ldg(row + e)) : kMasked;
       }
     }
   }
@@ -71,34 +80,35 @@ struct Lanes {
     for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   }
-  // Softmax of a token; NaN and +inf mask their expert.  All zero (and false) where
-  // every expert is masked.
-  __device__ __forceinline__ bool softmax(const uint32_t (&w)[words], int E, bool live, float (&p)[n], bool& bad) const {
-    float top = -INFINITY;
+  // exp of a token's logits over the largest, and 1 over their sum (0 and false where
+  // every expert is masked).  NaN and +inf mask their expert; they are looked for
+  // where the sum shows them.
+  __device__ __forceinline__ bool softmax(uint32_t (&w)[words], float (&p)[n], float& inv, bool& bad) const {
+    constexpr float kLog2e = 1.4426950408889634f;
+    for (int turn = 0;; ++turn) {
+      float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      float v = live && expert(i) < E ? value(w, i) : -INFINITY;
-      if (!(v < INFINITY)) {
-        bad = true;
-        v = -INFINITY;
+      for (int i = 0; i < n; ++i) {
+        p[i] = value(w, i);
+        if (turn && !(p[i] < INFINITY)) {
+          bad = true;
+          p[i] = -INFINITY;
+        }
+        top = fmaxf(top, p[i]);
       }
-      p[i] = v;
-      top = fmaxf(top, v);
-    }
-    for (int o = lanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bool there = top > -INFINITY;
-    if (!there) top = 0.f;  // the masked experts' exponentials are zero then, too
-    float total = 0.f;
+      for (int o = lanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool there = top > -INFINITY;
+      if (!there) top = 0.f;  // the exponentials are zero then
+      float total = 0.f;
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      p[i] = __expf(p[i] - top);
-      total += p[i];
+      for (int i = 0; i < n; ++i) {
+        p[i] = exp2_fast((p[i] - top) * kLog2e);
+        total += p[i];
+      }
+      total = sum(total);
+      inv = there ? __fdividef(1.f, total) : 0.f;
+      if (turn || __all_sync(0xffffffffu, total < INFINITY)) return there;
     }
-    total = sum(total);
-    const float inv = there ? __fdiv_rn(1.f, total) : 0.f;
-#pragma unroll
-    for (int i = 0; i < n; ++i) p[i] *= inv;
-    return there;
   }
 };
 
@@ -117,58 +127,75 @@ struct FinishArgs {
   float* mean;
 };
 
-// One block: counts, means and the loss from the blocks' parts.  Expert e's parts
-// are added by blockDim / E' threads (E' = E rounded up to a power of two) whose
-// sums meet in a fixed order.  `scratch`: 2 * blockDim words.
+// A cluster's blocks: counts, means and the loss from the parts.  Each block takes
+// an eighth of the experts, the threads of an expert every so many-th part; their
+// sums meet in a fixed order, and so do the blocks' parts of the loss.
+// `scratch`: 2 * blockDim words.
 __device__ __forceinline__ void finish(const FinishArgs& a, uint32_t* scratch) {
   __shared__ int32_t tokens;
-  __shared__ float warp_sum[32];
-  const int threads = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int width = 32;  // experts side by side
-  while (width < a.E && width < threads) width *= 2;
-  const int groups = threads / width, at = threadIdx.x & (width - 1), group = threadIdx.x / width;
+  __shared__ float warp_sum[32], block_sum;
+  const int threads = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = (int)cluster_ctarank();
+  const int per = (a.E + kCluster - 1) / kCluster, begin = rank * per, end = min(a.E, begin + per);
+  int width = 1;  // experts side by side: at most 128
+  while (width < per) width *= 2;
+  const int groups = threads / width, at = threadIdx.x & (width - 1), group = threadIdx.x / width, e = begin + at;
   float* sp = reinterpret_cast<float*>(scratch);
   int32_t* sc = reinterpret_cast<int32_t*>(scratch + threads);
   if (warp == 0) {
     int32_t n = 0;
     for (int q = lane; q < a.parts; q += 32) n += a.part_c[(int64_t)q * (a.E + 1) + a.E];
     n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) tokens = n, a.counts[a.E] = n;
+    if (lane == 0) tokens = n;
+    if (lane == 0 && rank == 0) a.counts[a.E] = n;
   }
-  float part = 0.f;
-  for (int e0 = 0; e0 < a.E; e0 += width) {
-    const int e = e0 + at;
-    int32_t c = 0;
-    float s = 0.f;
-    if (e < a.E) {
-#pragma unroll 8
-      for (int q = group; q < a.parts; q += groups) {
-        c += a.part_c[(int64_t)q * (a.E + 1) + e];
-        s += a.part_p[(int64_t)q * a.E + e];
-      }
+  int32_t c = 0;
+  float s = 0.f;
+  if (e < end) {
+#pragma unroll 4
+    for (int q = group; q < a.parts; q += groups) {
+      c += a.part_c[(int64_t)q * (a.E + 1) + e];
+      s += a.part_p[(int64_t)q * a.E + e];
     }
-    __syncthreads();  // (the first time round: tokens is there)
-    sp[threadIdx.x] = s;
-    sc[threadIdx.x] = c;
+  }
+  sp[threadIdx.x] = s;
+  sc[threadIdx.x] = c;
+  // the groups meet in pairs
+  for (int g = groups / 2; g > 0; g /= 2) {
     __syncthreads();
-    if (group == 0 && e < a.E) {
-      for (int g = 1; g < groups; ++g) s += sp[g * width + at], c += sc[g * width + at];
-      const int32_t n = tokens;
-      const float m = n > 0 ? __fdiv_rn(s, (float)n) : 0.f;
-      a.counts[e] = c;
-      a.mean[e] = m;
-      part = fmaf(load_factor(c, n, a.E, a.top_k), m, part);
+    if (group < g) {
+      sp[threadIdx.x] += sp[threadIdx.x + g * width];
+      sc[threadIdx.x] += sc[threadIdx.x + g * width];
     }
+  }
+  __syncthreads();
+  float part = 0.f;
+  if (group == 0 && e < end) {
+    const int32_t n = tokens;
+    const float m = n > 0 ? __fdiv_rn(sp[threadIdx.x], (float)n) : 0.f;
+    a.counts[e] = sc[threadIdx.x];
+    a.mean[e] = m;
+    part = load_factor(sc[threadIdx.x], n, a.E, a.top_k) * m;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
   if (lane == 0) warp_sum[warp] = part;
   __syncthreads();
   if (threadIdx.x == 0) {
-    float s = 0.f;
-    for (int w = 0; w < threads / 32; ++w) s += warp_sum[w];
-    *a.loss = a.coeff * s;
+    float sum = 0.f;
+    for (int w = 0; w < (width + 31) / 32; ++w) sum += warp_sum[w];  // group 0's warps
+    block_sum = sum;
   }
+  cluster_barrier_sync();  // every block's part of the loss is there
+  if (rank == 0 && threadIdx.x == 0) {
+    float sum = 0.f;
+    for (int b = 0; b < kCluster; ++b) {
+      float v;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(&block_sum), (uint32_t)b)));
+      sum += v;
+    }
+    *a.loss = a.coeff * sum;
+  }
+  cluster_barrier_sync();  // no block leaves before its part was read
 }
 
 template <typename T, bool kVec, int kN>
@@ -203,10 +230,10 @@ __global__ void __launch_bounds__(kThreads)
   for (int64_t first = t - lay.sub; first < tokens; first += step, t += step) {
     uint32_t next[L::words];
     lay.load(logits + (t + step) * ld, E, t + step < tokens, next);
-    float p[L::n];
-    there += lay.softmax(w, E, t < tokens, p, bad) && lay.l == 0;
+    float p[L::n], inv;
+    there += lay.softmax(w, p, inv, bad) && lay.l == 0;
 #pragma unroll
-    for (int i = 0; i < L::n; ++i) acc[i] += p[i];
+    for (int i = 0; i < L::n; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
 #pragma unroll
     for (int i = 0; i < L::words; ++i) w[i] = next[i];
   }
@@ -240,7 +267,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   if (!all) return;
   cluster_barrier_sync();  // the cluster's parts are written
-  if (blockIdx.x == 0) finish(f, reinterpret_cast<uint32_t*>(sum));
+  finish(f, reinterpret_cast<uint32_t*>(sum));
 }
 
 __global__ void __launch_bounds__(1024) balance_finish_kernel(const FinishArgs f) {
@@ -271,16 +298,17 @@ __global__ void __launch_bounds__(256)
     uint32_t next[L::words];
     lay.load(logits + (t + step) * ld, E, t + step < tokens, next);
     const bool live = t < tokens;
-    float p[L::n];
+    float p[L::n], inv;
     bool bad = false;
-    lay.softmax(w, E, live, p, bad);
+    lay.softmax(w, p, inv, bad);
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < L::n; ++i) dot = fmaf(p[i], f[i], dot);
-    dot = lay.sum(dot);
+    dot = lay.sum(dot) * inv;
+    inv *= g;
     T* out = d_logits + t * E;
 #pragma unroll
-    for (int i = 0; i < L::n; ++i) p[i] = g * p[i] * (f[i] - dot);
+    for (int i = 0; i < L::n; ++i) p[i] = inv * p[i] * (f[i] - dot);
     if constexpr (kVec) {
 #pragma unroll
       for (int c = 0; c < kN; ++c) {
@@ -337,6 +365,16 @@ int lanes_of(bool vec, int E) {
 bool one_cluster(int64_t tokens, int64_t E) { return tokens * E <= (int64_t)kCluster * kWarps * 256 * 16; }
 int balance_grid(int64_t tokens, int64_t E) { return one_cluster(tokens, E) ? kCluster : num_sms(); }
 
+// Programmatic dependent launch, and clusters of kCluster blocks.
+void cluster_attributes(cudaLaunchAttribute (&attr)[2]) {
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+}
+
 }  // namespace
 
 size_t balance_workspace_bytes(int64_t tokens, int64_t E) {
@@ -358,12 +396,7 @@ q4_status launch_balance(const void* logits, int dtype, int64_t tokens, int E, i
       cfg.blockDim = dim3(kThreads, 1, 1);
       cfg.stream = stream;
       cudaLaunchAttribute attr[2];
-      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      attr[0].val.programmaticStreamSerializationAllowed = 1;
-      attr[1].id = cudaLaunchAttributeClusterDimension;
-      attr[1].val.clusterDim.x = kCluster;
-      attr[1].val.clusterDim.y = 1;
-      attr[1].val.clusterDim.z = 1;
+      cluster_attributes(attr);
       cfg.attrs = attr;
       cfg.numAttrs = all ? 2 : 1;
       return cudaLaunchKernelEx(&cfg, balance_kernel<T, decltype(v)::value, decltype(n)::value>, static_cast<const T*>(logits),
@@ -373,7 +406,16 @@ q4_status launch_balance(const void* logits, int dtype, int64_t tokens, int E, i
     });
   });
   if (st != Q4_OK || all) return st;
-  return launch_pdl(balance_finish_kernel, 1, 1024, 0, stream, f);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCluster, 1, 1);
+  cfg.blockDim = dim3(1024, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  cluster_attributes(attr);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  Q4_CUDA_TRY(cudaLaunchKernelEx(&cfg, balance_finish_kernel, f));
+  return Q4_OK;
 }
 
 q4_status launch_balance_backward(const void* logits, int dtype, int64_t tokens, int E, int64_t ld, const int32_t* counts,

@@ -163,7 +163,7 @@ enum { Q4_NORM_PLAIN = 0, Q4_NORM_FP8 = 1, Q4_NORM_INT8 = 2 };
 struct NormArgs {
   const void *x, *residual, *weight;  // residual, weight: may be null
   int64_t rows, H, ldx, ld_residual;
-  bool w_fp32;
+  int w_dtype;
   float eps;
   void *h, *y;  // may be null
   uint8_t* codes;
@@ -174,7 +174,7 @@ struct NormBackwardArgs {
   const void *d_y, *h, *d_h, *weight;  // d_h, weight: may be null
   int64_t rows, H, ld_d_y, ld_h, ld_d_h;
   const float* rstd;
-  bool w_fp32;
+  int w_dtype;
   void* d_x;
   float* partial;  // [grid, H], set by the launcher
 };

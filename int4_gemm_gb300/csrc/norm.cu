@@ -38,16 +38,21 @@ __device__ __forceinline__ uint2 int8x8(const float (&v)[8], float f) {
   return make_uint2(o[0], o[1]);
 }
 
-// A row of h = x + residual in v: reduced, scaled by the weights and written.
+// A row of h = x + residual in v: reduced, scaled by the weights and written.  H is
+// 0 for a row that is not there.
 template <typename T, bool kVec, int kC, int kForm, typename Weights, typename AfterReduce>
-__device__ __forceinline__ void norm_row(const NormArgs& a, const Place& pl, int64_t row, bool live, float (&v)[kC][8], Exchange& ex,
-                                         int buf, int* status, Weights&& weights, AfterReduce&& after_reduce) {
+__device__ __forceinline__ void norm_row(const NormArgs& a, const Place& pl, int64_t row, int H, float inv_H, float (&v)[kC][8],
+                                         Exchange& ex, int buf, int* status, Weights&& weights, AfterReduce&& after_reduce) {
   using P = Piece<T, kVec>;
-  auto cols = [&](int i) { return live ? pl.cols(i, a.H) : 0; };
+  const int64_t start = row * a.H;
   float sum = 0.f, top = 0.f;
+  if (a.h) {
+    T* h = static_cast<T*>(a.h) + start;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) P::store(h + pl.at(i), pl.l, pl.cols(i, H), v[i]);
+  }
 #pragma unroll
   for (int i = 0; i < kC; ++i) {
-    if (a.h) P::store(static_cast<T*>(a.h) + row * a.H + pl.at(i), pl.l, cols(i), v[i]);
     float w[8];
     weights(i, w);
 #pragma unroll
@@ -59,24 +64,26 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const Place& pl, int
   }
   const float2 r = group_reduce<kForm == Q4_NORM_INT8>(sum, top, pl.group, ex, buf);
   after_reduce();
-  const float rstd = __frsqrt_rn(r.x / (float)a.H + a.eps);
-  if (pl.t == 0 && live) {
+  const float rstd = rsqrtf(fmaf(r.x, inv_H, a.eps));  // within 2 ulp
+  if (pl.t == 0 && H) {
     if (a.rstd) a.rstd[row] = rstd;
     if (nonfinite(r.x)) latch_status(status, Q4_ERR_NONFINITE);
   }
   // the codes' factor rstd / s may be off by 2 ulp, as rstd may
   if constexpr (kForm == Q4_NORM_INT8) {
     const float s = fmaxf(r.y * rstd, 1e-12f) * (1.f / 127.f);
-    if (pl.t == 0 && live) {
+    if (pl.t == 0 && H) {
       a.scales[row] = s;
       if (nonfinite(s)) latch_status(status, Q4_ERR_NONFINITE);
     }
     const float f = __fdividef(rstd, s);
+    uint8_t* codes = a.codes + start;
 #pragma unroll
-    for (int i = 0; i < kC; ++i) P::store_codes(a.codes + row * a.H + pl.at(i), pl.l, cols(i), int8x8(v[i], f));
+    for (int i = 0; i < kC; ++i) P::store_codes(codes + pl.at(i), pl.l, pl.cols(i, H), int8x8(v[i], f));
   }
   if constexpr (kForm == Q4_NORM_FP8) {
-    const int blocks = (int)((a.H + 127) / 128);
+    uint8_t* codes = a.codes + start;
+    float* scales = a.scales + row * ((a.H + 127) / 128);
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       float m = 0.f;
@@ -85,21 +92,43 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const Place& pl, int
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       const float s = fmaxf(m * rstd, 1e-12f) * (1.f / 448.f);
-      P::store_codes(a.codes + row * a.H + pl.at(i), pl.l, cols(i), e4m3x8(v[i], __fdividef(rstd, s)));
-      if (pl.l == 0 && cols(i) > 0) {
-        a.scales[row * blocks + pl.block(i)] = s;
+      P::store_codes(codes + pl.at(i), pl.l, pl.cols(i, H), e4m3x8(v[i], __fdividef(rstd, s)));
+      if (pl.l == 0 && pl.cols(i, H) > 0) {
+        scales[pl.block(i)] = s;
         if (nonfinite(s)) latch_status(status, Q4_ERR_NONFINITE);
       }
     }
   }
   if (a.y) {
+    T* out = static_cast<T*>(a.y) + start;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       float y[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] = v[i][j] * rstd;
-      P::store(static_cast<T*>(a.y) + row * a.H + pl.at(i), pl.l, cols(i), y);
+      P::store(out + pl.at(i), pl.l, pl.cols(i, H), y);
     }
+  }
+}
+
+// A row's pieces x (+ res) into v.
+template <typename T, bool kVec, int kC>
+__device__ __forceinline__ void load_row(const T* x, const T* res, bool add, const Place& pl, int H, float (&v)[kC][8]) {
+  using P = Piece<T, kVec>;
+#pragma unroll
+  for (int i = 0; i < kC; ++i) {
+    P px;
+    px.load(x + pl.at(i), pl.l, pl.cols(i, H));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = px.at(j);
+  }
+  if (!add) return;
+#pragma unroll
+  for (int i = 0; i < kC; ++i) {
+    P pr;
+    pr.load(res + pl.at(i), pl.l, pl.cols(i, H));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] += pr.at(j);
   }
 }
 
@@ -109,86 +138,59 @@ template <typename T, bool kVec, int kC, int kForm>
 __global__ void __launch_bounds__(max_threads(kC))
     norm_kernel(const NormArgs a, int group, int* status) {
   pdl_wait();
-  using P = Piece<T, kVec>;
   __shared__ Exchange ex;
   const Place pl(group);
+  const int width = (int)a.H;
+  const float inv_H = 1.f / (float)width;
   auto weights = [&](int i, float (&f)[8]) {
-    load_weights<T, kVec>(a.weight, a.w_fp32, pl.at(i), pl.l, pl.cols(i, a.H), f);
+    load_weights<T, kVec>(a.weight, a.w_dtype == Q4_F32, pl.at(i), pl.l, pl.cols(i, width), f);
   };
   int buf = 0;
   for (int64_t base = (int64_t)blockIdx.x * pl.per_block; base < a.rows; base += (int64_t)gridDim.x * pl.per_block, buf ^= 1) {
     const int64_t row = base + pl.sub;
-    const bool live = row < a.rows;
+    const int H = row < a.rows ? width : 0;
     float v[kC][8];
-    {
-      P px[kC], pr[kC];
-#pragma unroll
-      for (int i = 0; i < kC; ++i)
-        px[i].load(static_cast<const T*>(a.x) + row * a.ldx + pl.at(i), pl.l, live ? pl.cols(i, a.H) : 0);
-      if (a.residual) {
-#pragma unroll
-        for (int i = 0; i < kC; ++i)
-          pr[i].load(static_cast<const T*>(a.residual) + row * a.ld_residual + pl.at(i), pl.l, live ? pl.cols(i, a.H) : 0);
-      }
-#pragma unroll
-      for (int i = 0; i < kC; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = a.residual ? px[i].at(j) + pr[i].at(j) : px[i].at(j);
-    }
-    norm_row<T, kVec, kC, kForm>(a, pl, row, live, v, ex, buf, status, weights, [] {});
+    load_row<T, kVec, kC>(static_cast<const T*>(a.x) + row * a.ldx, static_cast<const T*>(a.residual) + row * a.ld_residual,
+                          a.residual != nullptr, pl, H, v);
+    norm_row<T, kVec, kC, kForm>(a, pl, row, H, inv_H, v, ex, buf, status, weights, [] {});
   }
 }
 
-// Blocks per SM that a kernel of kThreads threads is compiled for.
-template <typename T, bool kVec>
-constexpr int resident_blocks(int threads) { return threads > 256 ? 1 : kVec && sizeof(T) == 2 ? 3 : 2; }
-
 template <typename T, bool kVec, int kC, int kForm, int kThreads>
-__global__ void __launch_bounds__(kThreads, resident_blocks<T, kVec>(kThreads)) norm_ring_kernel(const NormArgs a, int group, const RingArgs r) {
+__global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2) norm_ring_kernel(const NormArgs a, int group, const RingArgs r) {
   extern __shared__ __align__(128) uint8_t stage_smem[];
-  using P = Piece<T, kVec>;
   __shared__ Ring ring;
   __shared__ Exchange ex;
   ring_init(ring, r);
   pdl_wait();
   const Place pl(group);
+  const int width = (int)a.H;
+  const float inv_H = 1.f / (float)width;
   const void* const mat[2] = {a.x, a.residual};
   const int64_t pitch[2] = {a.ldx * (int64_t)sizeof(T), a.ld_residual * (int64_t)sizeof(T)};
   const int64_t step = (int64_t)gridDim.x * pl.per_block, base0 = (int64_t)blockIdx.x * pl.per_block;
   if (threadIdx.x == 0)
     for (int s = 0; s < r.stages; ++s)
       ring_fill<kVec>(ring, r, smem_u32(stage_smem), s, mat, pitch, base0 + s * step, a.rows, pl.per_block);
-  const HeldWeights<T, kVec, kC> w(a.weight, a.w_fp32, pl, a.H);
+  const HeldWeights<T, kVec, kC> w(a.weight, a.w_dtype, pl, width);
+  auto weights = [&](int i, float (&f)[8]) { w.get(pl, width, i, f); };
   int stage = 0, buf = 0;
   uint32_t phase = 0;
   for (int64_t base = base0; base < a.rows; base += step, buf ^= 1) {
     const int64_t row = base + pl.sub;
-    const bool live = row < a.rows;
+    const int H = row < a.rows ? width : 0;
     mbar_wait(smem_u32(&ring.full[stage]), phase, r.ctl, &ring.abort);
     float v[kC][8];
-    auto load = [&](const T* x, const T* res) {
-#pragma unroll
-      for (int i = 0; i < kC; ++i) {
-        P px;
-        px.load(x + pl.at(i), pl.l, live ? pl.cols(i, a.H) : 0);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = px.at(j);
-        if (a.residual) {
-          P pr;
-          pr.load(res + pl.at(i), pl.l, live ? pl.cols(i, a.H) : 0);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] += pr.at(j);
-        }
-      }
-    };
     if (!kVec && row == a.rows - 1) {
-      load(static_cast<const T*>(a.x) + row * a.ldx, static_cast<const T*>(a.residual) + row * a.ld_residual);
+      load_row<T, kVec, kC>(static_cast<const T*>(a.x) + row * a.ldx, static_cast<const T*>(a.residual) + row * a.ld_residual,
+                            a.residual != nullptr, pl, H, v);
     } else {
       const uint8_t* st = stage_smem + stage * r.stage_bytes;
-      load(ring_row<kVec, T>(st, r, 0, pl, a.x, pitch[0], row), ring_row<kVec, T>(st, r, 1, pl, a.residual, pitch[1], row));
+      load_row<T, kVec, kC>(ring_row<kVec, T>(st, r, 0, pl, a.x, pitch[0], row),
+                            ring_row<kVec, T>(st, r, 1, pl, a.residual, pitch[1], row), a.residual != nullptr, pl, H, v);
     }
     norm_row<T, kVec, kC, kForm>(
-        a, pl, row, live, v, ex, buf, r.ctl.status, [&](int i, float (&f)[8]) { w.get(pl, a.H, i, f); },
+        a, pl, row, H, inv_H, v, ex, buf, r.ctl.status, weights,
         [&] {  // every thread has read the stage: the next rows may come
           if (pl.group <= 32) __syncthreads();
           if (threadIdx.x == 0)
@@ -229,7 +231,7 @@ q4_status launch_norm(const NormArgs& a, int dtype, int form, cudaStream_t strea
   const int size = dtype == Q4_F32 ? 4 : 2;
   const bool vec = a.H % 8 == 0 && a.ldx * size % 16 == 0 && (!a.residual || a.ld_residual * size % 16 == 0) && mult(a.x, 16) &&
                    mult(a.residual, 16) && mult(a.h, 16) && mult(a.y, 16) && mult(a.codes, 8) && mult(a.weight, 16);
-  const Shape s = shape_of(a.rows, a.H, a.residual ? 2 : 1, size, vec, vec && size == 2 ? 3 : 2);
+  const Shape s = shape_of(a.rows, a.H, a.residual ? 2 : 1, size, vec);
   return by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
     return by_pieces(s.C, [&](auto c) {

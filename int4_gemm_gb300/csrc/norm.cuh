@@ -29,16 +29,19 @@ struct Piece {
         const uint4 v = 8 * l < cols ? reinterpret_cast<const uint4*>(p + 8 * l)[i] : make_uint4(0u, 0u, 0u, 0u);
         w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
       }
+    } else if (cols >= 128) {  // no test per element
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = one(p + l + 16 * i);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int at = l + 16 * i;
-        if constexpr (sizeof(T) == 2)
-          w[i] = at < cols ? reinterpret_cast<const unsigned short*>(p)[at] : 0u;
-        else
-          w[i] = at < cols ? __float_as_uint(p[at]) : 0u;
-      }
+      for (int i = 0; i < 8; ++i) w[i] = l + 16 * i < cols ? one(p + l + 16 * i) : 0u;
     }
+  }
+  static __device__ __forceinline__ uint32_t one(const T* p) {
+    if constexpr (sizeof(T) == 2)
+      return *reinterpret_cast<const unsigned short*>(p);
+    else
+      return __float_as_uint(*p);
   }
   __device__ __forceinline__ float at(int i) const {
     if constexpr (packed) {
@@ -60,6 +63,9 @@ struct Piece {
       } else {
         out[0] = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
       }
+    } else if (cols >= 128) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[l + 16 * i] = to_elem<T>(f[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -70,6 +76,9 @@ struct Piece {
   static __device__ __forceinline__ void store_codes(uint8_t* p, int l, int cols, uint2 c) {
     if constexpr (kVec) {
       if (8 * l < cols) *reinterpret_cast<uint2*>(p + 8 * l) = c;
+    } else if (cols >= 128) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[l + 16 * i] = (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -80,7 +89,7 @@ struct Piece {
 
 // The weights of a piece (columns c + ...), T or FP32; all 1 without weights.
 template <typename T, bool kVec>
-__device__ __forceinline__ void load_weights(const void* w, bool w32, int64_t c, int l, int cols, float (&f)[8]) {
+__device__ __forceinline__ void load_weights(const void* w, bool w32, int c, int l, int cols, float (&f)[8]) {
   if (!w) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = 1.f;
@@ -149,8 +158,9 @@ struct Place {
       : l(threadIdx.x & 15), t(threadIdx.x % group_), group(group_), per_block(blockDim.x / group_), sub(threadIdx.x / group_),
         stride(group_ >> 4) {}
   __device__ __forceinline__ int block(int i) const { return (t >> 4) + i * stride; }
-  __device__ __forceinline__ int64_t at(int i) const { return (int64_t)block(i) * 128; }
-  __device__ __forceinline__ int cols(int i, int64_t H) const { return (int)min((int64_t)128, H - at(i)); }
+  __device__ __forceinline__ int at(int i) const { return block(i) * 128; }
+  // columns of piece i of a row of H (0: a row that is not there)
+  __device__ __forceinline__ int cols(int i, int H) const { return min(128, H - at(i)); }
 };
 
 // ------------------------------------------------------------------ rows through shared memory
@@ -232,27 +242,31 @@ __device__ __forceinline__ const T* ring_row(const uint8_t* stage, const RingArg
   return reinterpret_cast<const T*>(p);
 }
 
-// The weights of a thread's pieces as they were loaded: 16-bit ones stay packed.
-// FP32 weights of 16-bit rows are read from global memory every time.
+// The weights of a thread's pieces as they were loaded, 16-bit ones packed (as
+// FP32 in shared memory, from where every row took them, 20 to 30% slower).  FP32
+// weights of 16-bit rows are read from global memory every time.
 template <typename T, bool kVec, int kC>
 struct HeldWeights {
   Piece<T, kVec> w[kC];
   const void* p;
-  bool fp32, held;
-  __device__ __forceinline__ HeldWeights(const void* weight, bool w_fp32, const Place& pl, int64_t H)
-      : p(weight), fp32(w_fp32), held(weight && (!w_fp32 || sizeof(T) == 4)) {
-    if (held) {
+  bool held;
+  __device__ __forceinline__ HeldWeights(const void* weight, int w_dtype, const Place& pl, int H)
+      : p(weight), held(!weight || sizeof(T) == 4 || w_dtype != Q4_F32) {
+    constexpr uint32_t kOne = sizeof(T) == 4 ? 0x3f800000u : std::is_same<T, __half>::value ? 0x3c003c00u : 0x3f803f80u;
 #pragma unroll
-      for (int i = 0; i < kC; ++i) w[i].load(static_cast<const T*>(weight) + pl.at(i), pl.l, pl.cols(i, H));
+    for (int i = 0; i < kC; ++i) {
+      if (weight && held) {
+        w[i].load(static_cast<const T*>(weight) + pl.at(i), pl.l, pl.cols(i, H));
+      } else {
+#pragma unroll
+        for (int j = 0; j < Piece<T, kVec>::words; ++j) w[i].w[j] = kOne;
+      }
     }
   }
-  __device__ __forceinline__ void get(const Place& pl, int64_t H, int i, float (&f)[8]) const {
-    if (held) {
+  __device__ __forceinline__ void get(const Place& pl, int H, int i, float (&f)[8]) const {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = w[i].at(j);
-    } else {
-      load_weights<T, kVec>(p, fp32, pl.at(i), pl.l, pl.cols(i, H), f);
-    }
+    for (int j = 0; j < 8; ++j) f[j] = w[i].at(j);
+    if (!held) load_weights<T, kVec>(p, true, pl.at(i), pl.l, pl.cols(i, H), f);
   }
 };
 
@@ -263,7 +277,7 @@ struct Shape {
   uint32_t stage_bytes;
 };
 constexpr uint32_t kRingTotal = 216 * 1024;  // of an SM's shared memory
-Shape shape_of(int64_t rows, int64_t H, int mats, int size, bool vec, int most_resident) {
+Shape shape_of(int64_t rows, int64_t H, int mats, int size, bool vec) {
   const int blocks = (int)ceil_div(H, 128);
   auto spread = [&](int C, int most_threads) {
     Shape s = {};
@@ -279,8 +293,9 @@ Shape shape_of(int64_t rows, int64_t H, int mats, int size, bool vec, int most_r
     const int per_block = s.threads / s.group;
     const uint32_t row_bytes = (uint32_t)(H * size);
     s.stage_bytes = (uint32_t)(mats * per_block) * (vec ? staged_row<true>(row_bytes) : staged_row<false>(row_bytes));
-    int resident = s.threads > 256 ? 1 : most_resident;
-    while (resident > 1 && 2 * s.stage_bytes > kRingTotal / resident) --resident;
+    // (three blocks per SM of the registers that are left then: 34 us instead of 26
+    // for 4096 x 7168 to INT8)
+    const int resident = s.threads <= 256 && 2 * s.stage_bytes <= kRingTotal / 2 ? 2 : 1;
     s.stages = (int)std::min<int64_t>(kMaxRing, kRingTotal / resident / s.stage_bytes);
     s.grid = (int)std::min<int64_t>(ceil_div(rows, per_block), sms * resident);
     if (s.stages >= 2 && ceil_div(rows, per_block) >= 2 * sms * resident) return s;

@@ -23,7 +23,7 @@ __device__ __forceinline__ void store_partial(const NormBackwardArgs& a, const P
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int c = kVec ? 8 * pl.l + j : pl.l + 16 * j;
-        if (c < pl.cols(i, a.H)) out[pl.at(i) + c] = s ? out[pl.at(i) + c] + acc[i][j] : acc[i][j];
+        if (c < pl.cols(i, (int)a.H)) out[pl.at(i) + c] = s ? out[pl.at(i) + c] + acc[i][j] : acc[i][j];
       }
   }
 }
@@ -35,6 +35,8 @@ __global__ void __launch_bounds__(max_threads(kC))
   using P = Piece<T, kVec>;
   __shared__ Exchange ex;
   const Place pl(group);
+  const int width = (int)a.H;
+  const float inv_H = 1.f / (float)width;
   float acc[kC][8];
 #pragma unroll
   for (int i = 0; i < kC; ++i)
@@ -43,40 +45,40 @@ __global__ void __launch_bounds__(max_threads(kC))
   int buf = 0;
   for (int64_t base = (int64_t)blockIdx.x * pl.per_block; base < a.rows; base += (int64_t)gridDim.x * pl.per_block, buf ^= 1) {
     const int64_t row = base + pl.sub;
-    const bool live = row < a.rows;
+    const int H = row < a.rows ? width : 0;
     P dy[kC], h[kC], dh[kC];
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
-      const int n = live ? pl.cols(i, a.H) : 0;
+      const int n = pl.cols(i, H);
       dy[i].load(static_cast<const T*>(a.d_y) + row * a.ld_d_y + pl.at(i), pl.l, n);
       h[i].load(static_cast<const T*>(a.h) + row * a.ld_h + pl.at(i), pl.l, n);
       if (a.d_h) dh[i].load(static_cast<const T*>(a.d_h) + row * a.ld_d_h + pl.at(i), pl.l, n);
     }
-    const float rstd = live ? a.rstd[row] : 0.f;
+    const float rstd = H ? a.rstd[row] : 0.f;
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       float w[8];
-      load_weights<T, kVec>(a.weight, a.w_fp32, pl.at(i), pl.l, pl.cols(i, a.H), w);
+      load_weights<T, kVec>(a.weight, a.w_dtype == Q4_F32, pl.at(i), pl.l, pl.cols(i, width), w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float hj = h[i].at(j);
-        dot = fmaf(dy[i].at(j) * w[j], hj, dot);
-        acc[i][j] = fmaf(dy[i].at(j), hj * rstd, acc[i][j]);
+        const float t = dy[i].at(j) * h[i].at(j);
+        dot = fmaf(t, w[j], dot);
+        acc[i][j] = fmaf(t, rstd, acc[i][j]);
       }
     }
     const float2 r = group_reduce<false>(dot, 0.f, group, ex, buf);
-    const float c = rstd * rstd * (r.x / (float)a.H);  // mean(g h) rstd^2
+    const float c = rstd * rstd * rstd * (r.x * inv_H);
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       float w[8], d[8];
-      load_weights<T, kVec>(a.weight, a.w_fp32, pl.at(i), pl.l, pl.cols(i, a.H), w);
+      load_weights<T, kVec>(a.weight, a.w_dtype == Q4_F32, pl.at(i), pl.l, pl.cols(i, width), w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        d[j] = rstd * fmaf(-h[i].at(j), c, dy[i].at(j) * w[j]);
+        d[j] = fmaf(-h[i].at(j), c, dy[i].at(j) * (w[j] * rstd));
         if (a.d_h) d[j] += dh[i].at(j);
       }
-      P::store(static_cast<T*>(a.d_x) + row * a.H + pl.at(i), pl.l, live ? pl.cols(i, a.H) : 0, d);
+      P::store(static_cast<T*>(a.d_x) + row * a.H + pl.at(i), pl.l, pl.cols(i, H), d);
     }
   }
   store_partial<kVec, kC>(a, pl, acc);
@@ -94,13 +96,15 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
   ring_init(ring, r);
   pdl_wait();
   const Place pl(group);
+  const int width = (int)a.H;
+  const float inv_H = 1.f / (float)width;
   const void* const mat[3] = {a.d_y, a.h, a.d_h};
   const int64_t size = sizeof(T), pitch[3] = {a.ld_d_y * size, a.ld_h * size, a.ld_d_h * size};
   const int64_t step = (int64_t)gridDim.x * pl.per_block, base0 = (int64_t)blockIdx.x * pl.per_block;
   if (threadIdx.x == 0)
     for (int s = 0; s < r.stages; ++s)
       ring_fill<kVec>(ring, r, smem_u32(stage_smem), s, mat, pitch, base0 + s * step, a.rows, pl.per_block);
-  const HeldWeights<T, kVec, kC> w(a.weight, a.w_fp32, pl, a.H);
+  const HeldWeights<T, kVec, kC> w(a.weight, a.w_dtype, pl, width);
   float acc[kC][8];
 #pragma unroll
   for (int i = 0; i < kC; ++i)
@@ -108,35 +112,29 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
   int stage = 0, buf = 0;
   uint32_t phase = 0;
-  const float inv_H = 1.f / (float)a.H;
   for (int64_t base = base0; base < a.rows; base += step, buf ^= 1) {
     const int64_t row = base + pl.sub;
-    const bool live = row < a.rows;
-    const float rstd = live ? __ldg(a.rstd + row) : 0.f;
+    const int H = row < a.rows ? width : 0;
+    const float rstd = H ? __ldg(a.rstd + row) : 0.f;
     mbar_wait(smem_u32(&ring.full[stage]), phase, r.ctl, &ring.abort);
     const uint8_t* st = stage_smem + stage * r.stage_bytes;
-    const T* sdy = ring_row<kVec, T>(st, r, 0, pl, a.d_y, pitch[0], row);
-    const T* sh = ring_row<kVec, T>(st, r, 1, pl, a.h, pitch[1], row);
-    const T* sdh = ring_row<kVec, T>(st, r, 2, pl, a.d_h, pitch[2], row);
-    const bool in_place = !kVec && row == a.rows - 1;
-    const T* gdy = static_cast<const T*>(a.d_y) + row * a.ld_d_y;
-    const T* gh = static_cast<const T*>(a.h) + row * a.ld_h;
-    const T* gdh = static_cast<const T*>(a.d_h) + row * a.ld_d_h;
-    auto load = [&](P& p, const T* staged, const T* global, int i, int n) {
-      if (in_place)
-        p.load(global + pl.at(i), pl.l, n);
-      else
-        p.load(staged + pl.at(i), pl.l, n);
-    };
+    const T* dy_row = ring_row<kVec, T>(st, r, 0, pl, a.d_y, pitch[0], row);
+    const T* h_row = ring_row<kVec, T>(st, r, 1, pl, a.h, pitch[1], row);
+    const T* dh_row = ring_row<kVec, T>(st, r, 2, pl, a.d_h, pitch[2], row);
+    if (!kVec && row == a.rows - 1) {  // in place
+      dy_row = static_cast<const T*>(a.d_y) + row * a.ld_d_y;
+      h_row = static_cast<const T*>(a.h) + row * a.ld_h;
+      dh_row = static_cast<const T*>(a.d_h) + row * a.ld_d_h;
+    }
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
-      const int n = live ? pl.cols(i, a.H) : 0;
+      const int n = pl.cols(i, H);
       P dy, h;
-      load(dy, sdy, gdy, i, n);
-      load(h, sh, gh, i, n);
       float f[8];
-      w.get(pl, a.H, i, f);
+      dy.load(dy_row + pl.at(i), pl.l, n);
+      h.load(h_row + pl.at(i), pl.l, n);
+      w.get(pl, width, i, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float t = dy.at(j) * h.at(j);
@@ -151,21 +149,25 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
       ring_fill<kVec>(ring, r, smem_u32(stage_smem), stage ? stage - 1 : r.stages - 1, mat, pitch, next, a.rows, pl.per_block);
     }
     const float c = rstd * rstd * rstd * (q.x * inv_H);
+    T* out = static_cast<T*>(a.d_x) + row * a.H;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
-      const int n = live ? pl.cols(i, a.H) : 0;
-      P dy, h, dh;
-      load(dy, sdy, gdy, i, n);
-      load(h, sh, gh, i, n);
-      if (a.d_h) load(dh, sdh, gdh, i, n);
-      float f[8], d[8];
-      w.get(pl, a.H, i, f);
+      const int n = pl.cols(i, H);
+      P dy, h;
+      float f[8];
+      dy.load(dy_row + pl.at(i), pl.l, n);
+      h.load(h_row + pl.at(i), pl.l, n);
+      w.get(pl, width, i, f);
+      float d[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        d[j] = fmaf(-h.at(j), c, dy.at(j) * (f[j] * rstd));
-        if (a.d_h) d[j] += dh.at(j);
+      for (int j = 0; j < 8; ++j) d[j] = fmaf(-h.at(j), c, dy.at(j) * (f[j] * rstd));
+      if (a.d_h) {
+        P dh;
+        dh.load(dh_row + pl.at(i), pl.l, n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] += dh.at(j);
       }
-      P::store(static_cast<T*>(a.d_x) + row * a.H + pl.at(i), pl.l, n, d);
+      P::store(out + pl.at(i), pl.l, n, d);
     }
     if (++stage == r.stages) stage = 0, phase ^= 1;
   }
@@ -229,7 +231,7 @@ size_t norm_backward_workspace_bytes(int64_t rows, int64_t H) {
   int grid = 0;
   for (int mats : {2, 3})
     for (int size : {2, 4})
-      for (bool vec : {false, true}) grid = std::max(grid, shape_of(rows, H, mats, size, vec, 2).grid);
+      for (bool vec : {false, true}) grid = std::max(grid, shape_of(rows, H, mats, size, vec).grid);
   return (size_t)grid * (size_t)H * sizeof(float);
 }
 
@@ -238,7 +240,7 @@ q4_status launch_norm_backward(NormBackwardArgs a, int dtype, float* d_weight, v
   const int size = dtype == Q4_F32 ? 4 : 2;
   const bool vec = a.H % 8 == 0 && a.ld_d_y * size % 16 == 0 && a.ld_h * size % 16 == 0 && (!a.d_h || a.ld_d_h * size % 16 == 0) &&
                    mult(a.d_y, 16) && mult(a.h, 16) && mult(a.d_h, 16) && mult(a.d_x, 16) && mult(a.weight, 16);
-  const Shape s = shape_of(a.rows, a.H, a.d_h ? 3 : 2, size, vec, 2);
+  const Shape s = shape_of(a.rows, a.H, a.d_h ? 3 : 2, size, vec);
   const q4_status st = by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
     return by_pieces(s.C, [&](auto c) {
