@@ -174,6 +174,13 @@ def _new(shape, dtype: torch.dtype, device, stream=None, result: bool = True) ->
     return t
 
 
+def _maker(stream):
+    """torch.empty, or what makes a call's results on ``stream`` (see _new)."""
+    if stream is None:
+        return torch.empty
+    return lambda shape, dtype, device: _new(shape, dtype, device, stream)
+
+
 def _given(t: torch.Tensor, stream) -> torch.Tensor:
     """The caller's tensor, not reused before ``stream`` is done with it."""
     if stream is not None:
@@ -782,25 +789,47 @@ def gemm_w8a8_int8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: tor
 
 # --------------------------------------------------------------------------- norm
 
-def _norm_operands(x, weight, residual, h_out, stream):
-    """(row pitches of x and residual, weight's dtype code, h)."""
-    ldx, (rows, H), dev = _pitched(x, "x"), x.shape, x.device
-    ldr = 0
-    if residual is not None:
-        if residual.shape != x.shape or residual.dtype != x.dtype or residual.device != dev:
-            raise ValueError(f"residual must be a {x.dtype} tensor of shape ({rows}, {H}) on {dev}")
-        ldr = _pitched(residual, "residual")
-    elif h_out is not None:
-        raise ValueError("h_out needs a residual (without one h is x)")
-    h = None if residual is None else _out(h_out, rows, H, x.dtype, dev, stream)
-    return ldx, ldr, _norm_weight(weight, x), h
-
-
 def _norm_weight(weight, x) -> int:
     if weight is None:
         return F32
-    return _DTYPE[_exact(weight, "weight", (x.shape[1],), torch.float32 if weight.dtype == torch.float32 else x.dtype,
-                         x.device).dtype]
+    dtype = weight.dtype
+    _exact(weight, "weight", (x.shape[1],), dtype if dtype is torch.float32 else x.dtype, x.device)
+    return _DTYPE[dtype]
+
+
+def _norm(fn, x, weight, residual, eps, out, h_out, stream, codes=None, blocks=0, need_y=True):
+    """The three forms' call: -> (codes, scales, y, h, rstd), without codes (their
+    type, with `blocks` scales per row) the first two None."""
+    ldx = _pitched(x, "x")
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    rows, H = shape
+    wd = _norm_weight(weight, x)
+    new = _maker(stream)
+    h, ldr, res = None, 0, None
+    if residual is not None:
+        if residual.shape != shape or residual.dtype != dtype or residual.device != dev:
+            raise ValueError(f"residual must be a {dtype} tensor of shape ({rows}, {H}) on {dev}")
+        ldr, res = _pitched(residual, "residual"), residual.data_ptr()
+        h = new(shape, dtype=dtype, device=dev) if h_out is None else _out(h_out, rows, H, dtype, dev, stream)
+    elif h_out is not None:
+        raise ValueError("h_out needs a residual (without one h is x)")
+    rstd = new(rows, dtype=torch.float32, device=dev)
+    y = None
+    if need_y:
+        y = new(shape, dtype=dtype, device=dev) if out is None else _out(out, rows, H, dtype, dev, stream)
+    args = (x.data_ptr(), _DTYPE[dtype], rows, H, ldx, res, ldr, None if weight is None else weight.data_ptr(), wd, eps)
+    tail = (None if y is None else y.data_ptr(), None if h is None else h.data_ptr(), rstd.data_ptr(), _stream(stream))
+    scales = None
+    call = getattr(_lib or load(), fn)
+    if codes is None:
+        status = call(*args, *tail)
+    else:
+        codes = new(shape, dtype=codes, device=dev)
+        scales = new((rows, blocks) if blocks else rows, dtype=torch.float32, device=dev)
+        status = call(*args, codes.data_ptr(), scales.data_ptr(), *tail)
+    if status:
+        _check(fn, status)
+    return codes, scales, y, h, rstd
 
 
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
@@ -809,25 +838,7 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: O
     residual: h = x) -> (y [rows, H] = h * rstd * weight, h [rows, H] or None
     without a residual, rstd float32 [rows]).  weight [H] in x's type or
     float32, None: all 1.  ``h_out`` may be residual itself."""
-    ldx, ldr, wd, h = _norm_operands(x, weight, residual, h_out, stream)
-    rows, H = x.shape
-    y = _out(out, rows, H, x.dtype, x.device, stream)
-    rstd = _new(rows, torch.float32, x.device, stream)
-    _check("rms_norm", lib().rms_norm(x.data_ptr(), _DTYPE[x.dtype], rows, H, ldx, _ptr(residual), ldr, _ptr(weight), wd,
-                                      eps, y.data_ptr(), _ptr(h), rstd.data_ptr(), _stream(stream)))
-    return y, h, rstd
-
-
-def _norm_8bit(fn, code_dtype, scales_shape, x, weight, residual, eps, need_y, h_out, stream):
-    ldx, ldr, wd, h = _norm_operands(x, weight, residual, h_out, stream)
-    (rows, H), dev = x.shape, x.device
-    codes = _new((rows, H), code_dtype, dev, stream)
-    scales = _new(scales_shape, torch.float32, dev, stream)
-    y = _new((rows, H), x.dtype, dev, stream) if need_y else None
-    rstd = _new(rows, torch.float32, dev, stream)
-    _check(fn, getattr(lib(), fn)(x.data_ptr(), _DTYPE[x.dtype], rows, H, ldx, _ptr(residual), ldr, _ptr(weight), wd, eps,
-                                  codes.data_ptr(), scales.data_ptr(), _ptr(y), _ptr(h), rstd.data_ptr(), _stream(stream)))
-    return codes, scales, y, h, rstd
+    return _norm("rms_norm", x, weight, residual, eps, out, h_out, stream)[2:]
 
 
 def rms_norm_fp8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
@@ -836,8 +847,7 @@ def rms_norm_fp8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residua
     float32 [rows, ceil(H/128)], y or None without ``need_y``, h or None without
     a residual, rstd): the activations of gemm_fp8_blockwise and gemm_w4a8, and
     an 8-bit checkpoint for grouped_wgrad_fp8."""
-    return _norm_8bit("rms_norm_fp8", torch.uint8, (x.shape[0], -(-x.shape[-1] // 128)), x, weight, residual, eps, need_y,
-                      h_out, stream)
+    return _norm("rms_norm_fp8", x, weight, residual, eps, None, h_out, stream, torch.uint8, -(-x.shape[-1] // 128), need_y)
 
 
 def rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
@@ -845,7 +855,7 @@ def rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residu
     """rms_norm with its result in 8-bit integers -> (codes int8 [rows, H],
     scales float32 [rows], y or None without ``need_y``, h or None without a
     residual, rstd): gemm_w8a8_int8's activations."""
-    return _norm_8bit("rms_norm_int8", torch.int8, (x.shape[0],), x, weight, residual, eps, need_y, h_out, stream)
+    return _norm("rms_norm_int8", x, weight, residual, eps, None, h_out, stream, torch.int8, 0, need_y)
 
 
 def rms_norm_backward(d_y: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -895,18 +905,22 @@ def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, coeff: float = 1.0
         raise ValueError("ids must be a [T, top_k] tensor")
     k = ids.shape[1]
     _exact(ids, "ids", (T, k), torch.int32, dev)
-    loss = _new(1, torch.float32, dev, stream)
-    counts = _new(E + 1, torch.int32, dev, stream)
-    mean = _new(E, torch.float32, dev, stream)
-    L = lib()
+    new, L = _maker(stream), _lib or load()
+    loss = new(1, dtype=torch.float32, device=dev)
+    counts = new(E + 1, dtype=torch.int32, device=dev)
+    mean = new(E, dtype=torch.float32, device=dev)
+    n = 0
     if ws is None:
         n = L.q4_workspace_size(OP_MOE_BALANCE_LOSS, T, E, 0)
-        ws = _empty(n, dev, stream) if n else None
+        if n:
+            ws = _empty(n, dev, stream)
     else:
-        _given(ws, stream)
-    _check("moe_balance_loss", L.moe_balance_loss(
+        n = _given(ws, stream).numel()
+    status = L.moe_balance_loss(
         logits.data_ptr(), _DTYPE[logits.dtype], T, E, ld, ids.data_ptr(), k, coeff, loss.data_ptr(), counts.data_ptr(),
-        mean.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+        mean.data_ptr(), None if ws is None else ws.data_ptr(), n, _stream(stream))
+    if status:
+        _check("moe_balance_loss", status)
     return loss, counts, mean
 
 

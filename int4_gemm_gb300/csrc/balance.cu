@@ -9,9 +9,9 @@
 // A token's logits are held by 1 to 32 lanes, eight neighbouring experts per load
 // where rows are aligned (Lanes), else by a warp, lane l the experts l, l + 32, ...;
 // its probabilities are added up in registers, token by token.  The blocks' sums
-// meet in the workspace and are added in a fixed order: by the same blocks, one
-// cluster, where there are few tokens, else by a second kernel (the counts are
-// integers, whose order does not matter).
+// meet in a fixed order: in distributed shared memory of the same blocks, one
+// cluster, where there are few tokens, else in the workspace, from where a second
+// kernel adds them (the counts are integers, whose order does not matter).
 #include <algorithm>
 #include <type_traits>
 
@@ -120,18 +120,24 @@ __device__ __forceinline__ float load_factor(int32_t count, int32_t n, int E, in
 struct FinishArgs {
   int parts, E, top_k;
   float coeff;
-  float* part_p;    // [parts, E]
+  float* part_p;    // [parts, E]; null: the parts are the cluster's, in its shared memory
   int32_t* part_c;  // [parts, E + 1]
   float* loss;
   int32_t* counts;
   float* mean;
 };
 
+__device__ __forceinline__ int32_t load_peer(uint32_t addr, uint32_t rank) {
+  int32_t v;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(addr, rank)));
+  return v;
+}
+
 // A cluster's blocks: counts, means and the loss from the parts.  Each block takes
 // an eighth of the experts, the threads of an expert every so many-th part; their
 // sums meet in a fixed order, and so do the blocks' parts of the loss.
-// `scratch`: 2 * blockDim words.
-__device__ __forceinline__ void finish(const FinishArgs& a, uint32_t* scratch) {
+// `scratch`: 2 * blockDim words; own_p, own_c: this block's parts in shared memory.
+__device__ __forceinline__ void finish(const FinishArgs& a, uint32_t* scratch, uint32_t own_p, uint32_t own_c) {
   __shared__ int32_t tokens;
   __shared__ float warp_sum[32], block_sum;
   const int threads = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = (int)cluster_ctarank();
@@ -141,9 +147,12 @@ __device__ __forceinline__ void finish(const FinishArgs& a, uint32_t* scratch) {
   const int groups = threads / width, at = threadIdx.x & (width - 1), group = threadIdx.x / width, e = begin + at;
   float* sp = reinterpret_cast<float*>(scratch);
   int32_t* sc = reinterpret_cast<int32_t*>(scratch + threads);
+  auto part_c = [&](int q, int i) {
+    return a.part_p ? a.part_c[(int64_t)q * (a.E + 1) + i] : load_peer(own_c + 4 * i, (uint32_t)q);
+  };
   if (warp == 0) {
     int32_t n = 0;
-    for (int q = lane; q < a.parts; q += 32) n += a.part_c[(int64_t)q * (a.E + 1) + a.E];
+    for (int q = lane; q < a.parts; q += 32) n += part_c(q, a.E);
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0) tokens = n;
     if (lane == 0 && rank == 0) a.counts[a.E] = n;
@@ -153,8 +162,8 @@ __device__ __forceinline__ void finish(const FinishArgs& a, uint32_t* scratch) {
   if (e < end) {
 #pragma unroll 4
     for (int q = group; q < a.parts; q += groups) {
-      c += a.part_c[(int64_t)q * (a.E + 1) + e];
-      s += a.part_p[(int64_t)q * a.E + e];
+      c += part_c(q, e);
+      s += a.part_p ? a.part_p[(int64_t)q * a.E + e] : __int_as_float(load_peer(own_p + 4 * e, (uint32_t)q));
     }
   }
   sp[threadIdx.x] = s;
@@ -188,11 +197,8 @@ __device__ __forceinline__ void finish(const FinishArgs& a, uint32_t* scratch) {
   cluster_barrier_sync();  // every block's part of the loss is there
   if (rank == 0 && threadIdx.x == 0) {
     float sum = 0.f;
-    for (int b = 0; b < kCluster; ++b) {
-      float v;
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(&block_sum), (uint32_t)b)));
-      sum += v;
-    }
+    for (int b = 0; b < kCluster; ++b)
+      sum += __int_as_float(load_peer(smem_u32(&block_sum), (uint32_t)b));
     *a.loss = a.coeff * sum;
   }
   cluster_barrier_sync();  // no block leaves before its part was read
@@ -201,12 +207,13 @@ __device__ __forceinline__ void finish(const FinishArgs& a, uint32_t* scratch) {
 template <typename T, bool kVec, int kN>
 __global__ void __launch_bounds__(kThreads)
     balance_kernel(const T* __restrict__ logits, int64_t tokens, int64_t ld, const int32_t* __restrict__ ids, int lanes,
-                   bool all, const FinishArgs f, int* status) {
+                   const FinishArgs f, int* status) {
   pdl_wait();
   using L = Lanes<T, kVec, kN>;
   // the warps' sums one after another where all do not fit: 16 warps x 1024 experts
   constexpr int kSumWarps = 8;
   __shared__ float sum[kSumWarps * kMaxExperts];
+  __shared__ float total[kMaxExperts];
   __shared__ int32_t count[kMaxExperts + 1];
   const L lay(lanes);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = f.E;
@@ -258,22 +265,27 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
   }
   for (int e = threadIdx.x; e <= E; e += kThreads) {
-    f.part_c[(int64_t)blockIdx.x * (E + 1) + e] = count[e];
-    if (e == E) continue;
     float s = 0.f;
+    if (e < E) {
 #pragma unroll
-    for (int i = 0; i < kSumWarps; ++i) s += sum[i * kMaxExperts + e];
-    f.part_p[(int64_t)blockIdx.x * E + e] = s;
+      for (int i = 0; i < kSumWarps; ++i) s += sum[i * kMaxExperts + e];
+    }
+    if (f.part_p) {
+      f.part_c[(int64_t)blockIdx.x * (E + 1) + e] = count[e];
+      if (e < E) f.part_p[(int64_t)blockIdx.x * E + e] = s;
+    } else if (e < E) {
+      total[e] = s;
+    }
   }
-  if (!all) return;
-  cluster_barrier_sync();  // the cluster's parts are written
-  finish(f, reinterpret_cast<uint32_t*>(sum));
+  if (f.part_p) return;
+  cluster_barrier_sync();  // the cluster's parts are there
+  finish(f, reinterpret_cast<uint32_t*>(sum), smem_u32(total), smem_u32(count));
 }
 
 __global__ void __launch_bounds__(1024) balance_finish_kernel(const FinishArgs f) {
   pdl_wait();
   __shared__ uint32_t scratch[2 * 1024];
-  finish(f, scratch);
+  finish(f, scratch, 0, 0);
 }
 
 template <typename T, bool kVec, int kN>
@@ -378,15 +390,15 @@ void cluster_attributes(cudaLaunchAttribute (&attr)[2]) {
 }  // namespace
 
 size_t balance_workspace_bytes(int64_t tokens, int64_t E) {
-  return (size_t)balance_grid(tokens, E) * (size_t)(2 * E + 1) * 4;
+  return one_cluster(tokens, E) ? 0 : (size_t)balance_grid(tokens, E) * (size_t)(2 * E + 1) * 4;
 }
 
 q4_status launch_balance(const void* logits, int dtype, int64_t tokens, int E, int64_t ld, const int32_t* ids, int top_k,
                          float coeff, float* loss, int32_t* counts, float* mean, void* ws, cudaStream_t stream) {
   const int grid = balance_grid(tokens, E);
   const bool all = one_cluster(tokens, E);
-  FinishArgs f = {grid, E, top_k, coeff, static_cast<float*>(ws), nullptr, loss, counts, mean};
-  f.part_c = reinterpret_cast<int32_t*>(f.part_p + (size_t)grid * E);
+  FinishArgs f = {grid, E, top_k, coeff, all ? nullptr : static_cast<float*>(ws), nullptr, loss, counts, mean};
+  if (!all) f.part_c = reinterpret_cast<int32_t*>(f.part_p + (size_t)grid * E);
   const bool vec = E % 8 == 0 && ld * (dtype == Q4_F32 ? 4 : 2) % 16 == 0 && mult(logits, 16);
   const q4_status st = by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
@@ -400,7 +412,7 @@ q4_status launch_balance(const void* logits, int dtype, int64_t tokens, int E, i
       cfg.attrs = attr;
       cfg.numAttrs = all ? 2 : 1;
       return cudaLaunchKernelEx(&cfg, balance_kernel<T, decltype(v)::value, decltype(n)::value>, static_cast<const T*>(logits),
-                                tokens, ld, ids, lanes_of(vec, E), all, f, device_status_ptr()) == cudaSuccess
+                                tokens, ld, ids, lanes_of(vec, E), f, device_status_ptr()) == cudaSuccess
                  ? Q4_OK
                  : Q4_ERR_CUDA;
     });

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(max_threads(kC))
 }
 
 template <typename T, bool kVec, int kC, int kForm, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2) norm_ring_kernel(const NormArgs a, int group, const RingArgs r) {
+__global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads)) norm_ring_kernel(const NormArgs a, int group, const RingArgs r) {
   extern __shared__ __align__(128) uint8_t stage_smem[];
   __shared__ Ring ring;
   __shared__ Exchange ex;

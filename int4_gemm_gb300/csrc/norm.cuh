@@ -277,6 +277,11 @@ struct Shape {
   uint32_t stage_bytes;
 };
 constexpr uint32_t kRingTotal = 216 * 1024;  // of an SM's shared memory
+// Blocks per SM that the ring kernels are compiled for: single elements need few
+// registers and many warps; of aligned rows, whose threads hold 32 elements, three
+// blocks would spill (34 us instead of 26 for 4096 x 7168 to INT8).
+__host__ __device__ constexpr int resident_blocks(bool vec, int threads) { return threads > 256 ? 1 : vec ? 2 : 3; }
+
 Shape shape_of(int64_t rows, int64_t H, int mats, int size, bool vec) {
   const int blocks = (int)ceil_div(H, 128);
   auto spread = [&](int C, int most_threads) {
@@ -293,9 +298,8 @@ Shape shape_of(int64_t rows, int64_t H, int mats, int size, bool vec) {
     const int per_block = s.threads / s.group;
     const uint32_t row_bytes = (uint32_t)(H * size);
     s.stage_bytes = (uint32_t)(mats * per_block) * (vec ? staged_row<true>(row_bytes) : staged_row<false>(row_bytes));
-    // (three blocks per SM of the registers that are left then: 34 us instead of 26
-    // for 4096 x 7168 to INT8)
-    const int resident = s.threads <= 256 && 2 * s.stage_bytes <= kRingTotal / 2 ? 2 : 1;
+    int resident = resident_blocks(vec, s.threads);
+    while (resident > 1 && 2 * s.stage_bytes > kRingTotal / resident) --resident;
     s.stages = (int)std::min<int64_t>(kMaxRing, kRingTotal / resident / s.stage_bytes);
     s.grid = (int)std::min<int64_t>(ceil_div(rows, per_block), sms * resident);
     if (s.stages >= 2 && ceil_div(rows, per_block) >= 2 * sms * resident) return s;

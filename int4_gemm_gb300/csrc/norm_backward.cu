@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(max_threads(kC))
 // The same with the rows in shared memory, which are read twice there; a stage is
 // refilled after the next row's exchange, when every thread has left it.
 template <typename T, bool kVec, int kC, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads))
     norm_backward_ring_kernel(const NormBackwardArgs a, int group, const RingArgs r) {
   extern __shared__ __align__(128) uint8_t stage_smem[];
   using P = Piece<T, kVec>;
@@ -225,13 +225,23 @@ q4_status launch_norm_backward_form(const NormBackwardArgs& a, const Shape& s, b
 
 }  // namespace
 
+namespace {
+// The gradient's spread: where rows are few, at most a block per SM, since each
+// writes a row of d_w's parts (512 x 4096: 19 us with a block per row).
+Shape backward_shape(int64_t rows, int64_t H, int mats, int size, bool vec) {
+  Shape s = shape_of(rows, H, mats, size, vec);
+  if (!s.stages) s.grid = std::min(s.grid, num_sms());
+  return s;
+}
+}  // namespace
+
 // Room for the largest grid that these sizes can have.
 size_t norm_backward_workspace_bytes(int64_t rows, int64_t H) {
   if (rows == 0 || H == 0) return 0;
   int grid = 0;
   for (int mats : {2, 3})
     for (int size : {2, 4})
-      for (bool vec : {false, true}) grid = std::max(grid, shape_of(rows, H, mats, size, vec).grid);
+      for (bool vec : {false, true}) grid = std::max(grid, backward_shape(rows, H, mats, size, vec).grid);
   return (size_t)grid * (size_t)H * sizeof(float);
 }
 
@@ -240,7 +250,7 @@ q4_status launch_norm_backward(NormBackwardArgs a, int dtype, float* d_weight, v
   const int size = dtype == Q4_F32 ? 4 : 2;
   const bool vec = a.H % 8 == 0 && a.ld_d_y * size % 16 == 0 && a.ld_h * size % 16 == 0 && (!a.d_h || a.ld_d_h * size % 16 == 0) &&
                    mult(a.d_y, 16) && mult(a.h, 16) && mult(a.d_h, 16) && mult(a.d_x, 16) && mult(a.weight, 16);
-  const Shape s = shape_of(a.rows, a.H, a.d_h ? 3 : 2, size, vec);
+  const Shape s = backward_shape(a.rows, a.H, a.d_h ? 3 : 2, size, vec);
   const q4_status st = by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
     return by_pieces(s.C, [&](auto c) {

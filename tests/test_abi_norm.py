@@ -94,12 +94,15 @@ def test_balance(clib):
             assert f(**bad) == -1, bad
         assert f(E=1025, ld=1025) == -2 and f(E=64, ld=64, k=33) == -2 and f(T=1 << 40) == -2
     for bad in (dict(ids=None), dict(loss=None), dict(mean=None), dict(loss=FAR[0]), dict(counts=FAR[1] + 4),
-                dict(mean=FAR[3] + 32), dict(ws=FAR[0]), dict(ws=FAR[3])):
+                dict(mean=FAR[3] + 32)):
         assert fwd(**bad) == -1, bad
-    need = clib.q4_workspace_size(14, 4, 8, 0)
+    far = dict(T=1 << 20, x=FAR[8], ids=FAR[8] + (1 << 28))
+    for bad in (dict(ws=FAR[8]), dict(ws=FAR[8] + (1 << 28)), dict(ws=FAR[3])):
+        assert fwd(**far, **bad) == -1, bad
+    need = clib.q4_workspace_size(14, 1 << 20, 8, 0)
     assert need > 0 and clib.q4_workspace_size(14, 4, 1025, 0) == 0 and clib.q4_workspace_size(14, -4, 8, 0) == 0
     for ws, nb in ((None, need), (FAR[5] + 16, need), (FAR[5], need - 1)):
-        assert fwd(ws=ws, nb=nb) == -6
+        assert fwd(T=1 << 20, x=FAR[8], ids=FAR[8] + (1 << 28), ws=ws, nb=nb) == -6
     for bad in (dict(d=None), dict(out=None), dict(out=FAR[0] + 16), dict(out=FAR[2]), dict(out=FAR[1])):
         assert bwd(**bad) == -1, bad
     assert bwd(T=0, x=None) == 0

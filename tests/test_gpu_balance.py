@@ -171,7 +171,8 @@ def test_refusals(lib):
             call()
     for call in (lambda: lib.moe_balance_loss(x, ids, float("nan")), lambda: lib.moe_balance_loss_backward(x, counts, 9, one),
                  lambda: lib.moe_balance_loss_backward(x, counts, 2, one, out=x),
-                 lambda: lib.moe_balance_loss(x, ids, ws=torch.empty(16, dtype=torch.uint8, device="cuda")),
+                 lambda: lib.moe_balance_loss(x.repeat(1 << 17, 1), ids.repeat(1 << 17, 1),
+                                              ws=torch.empty(16, dtype=torch.uint8, device="cuda")),
                  lambda: lib.moe_balance_loss(torch.zeros((2, 1025), device="cuda"), ids[:2])):
         with pytest.raises(lib.Q4Error):
             call()
