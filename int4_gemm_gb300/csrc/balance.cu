@@ -25,6 +25,10 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kCluster = 8;
+// Loads per lane where there are many logits: fewer lanes share a token and its
+// reductions (65536 x 256 bf16: 25.9 us with one, 20.6 with two, 19.5 with four, the
+// gradient 21.0, 17.7 and 31.8); elsewhere one (16384 x 64 FP32: 8.2, 8.5 and 11.4).
+int loads_of(int64_t tokens, int64_t E) { return tokens * E >= (int64_t)1 << 22 ? 2 : 1; }
 
 // 2^x within 2^-22 relative (0 below 2^-126).
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -77,38 +81,57 @@ struct Lanes {
       return unpack2<T>(w[i]).x;
   }
   __device__ __forceinline__ float sum(float v) const {
-    for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  __device__ __forceinline__ float largest(float v) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o < lanes) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
   }
   // exp of a token's logits over the largest, and 1 over their sum (0 and false where
   // every expert is masked).  NaN and +inf mask their expert; they are looked for
   // where the sum shows them.
-  __device__ __forceinline__ bool softmax(uint32_t (&w)[words], float (&p)[n], float& inv, bool& bad) const {
-    constexpr float kLog2e = 1.4426950408889634f;
-    for (int turn = 0;; ++turn) {
-      float top = -INFINITY;
+  __device__ __forceinline__ bool softmax(const uint32_t (&w)[words], float (&p)[n], float& inv, bool& bad) const {
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      p[i] = value(w, i);
+      top = fmaxf(top, p[i]);
+    }
+    top = largest(top);
+    float total = exponentials(p, top);
+    if (!__all_sync(0xffffffffu, total < INFINITY)) {
+      top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < n; ++i) {
         p[i] = value(w, i);
-        if (turn && !(p[i] < INFINITY)) {
+        if (!(p[i] < INFINITY)) {
           bad = true;
           p[i] = -INFINITY;
         }
         top = fmaxf(top, p[i]);
       }
-      for (int o = lanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const bool there = top > -INFINITY;
-      if (!there) top = 0.f;  // the exponentials are zero then
-      float total = 0.f;
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        p[i] = exp2_fast((p[i] - top) * kLog2e);
-        total += p[i];
-      }
-      total = sum(total);
-      inv = there ? __fdividef(1.f, total) : 0.f;
-      if (turn || __all_sync(0xffffffffu, total < INFINITY)) return there;
+      top = largest(top);
+      total = exponentials(p, top);
     }
+    const bool there = top > -INFINITY;
+    inv = there ? __fdividef(1.f, total) : 0.f;
+    return there;
+  }
+  __device__ __forceinline__ float exponentials(float (&p)[n], float top) const {
+    constexpr float kLog2e = 1.4426950408889634f;
+    if (top == -INFINITY) top = 0.f;  // the exponentials are zero then
+    float total = 0.f;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      p[i] = exp2_fast((p[i] - top) * kLog2e);
+      total += p[i];
+    }
+    return sum(total);
   }
 };
 
@@ -353,22 +376,23 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// The kernels' forms: eight experts per load (kVec) with 1, 2 or 4 loads per lane,
-// or single experts, 1 to 32 per lane.
+// The kernels' forms: eight experts per load (kVec) with 1, 2 or 4 loads per lane, at
+// least `loads` where there are as many, or single experts, 2 to 32 per lane.
 template <typename F>
-q4_status by_experts(bool vec, int E, F&& f) {
+q4_status by_experts(bool vec, int E, int loads, F&& f) {
   if (vec) {
-    if (E <= 256) return f(std::true_type(), std::integral_constant<int, 1>());
-    if (E <= 512) return f(std::true_type(), std::integral_constant<int, 2>());
+    if (E <= 256 && (loads == 1 || E <= 8)) return f(std::true_type(), std::integral_constant<int, 1>());
+    if (E <= 512 && (loads <= 2 || E <= 16)) return f(std::true_type(), std::integral_constant<int, 2>());
     return f(std::true_type(), std::integral_constant<int, 4>());
   }
   if (E <= 64) return f(std::false_type(), std::integral_constant<int, 2>());
   if (E <= 256) return f(std::false_type(), std::integral_constant<int, 8>());
   return f(std::false_type(), std::integral_constant<int, 32>());
 }
-int lanes_of(bool vec, int E) {
+// Lanes of a token with `loads` loads each.
+int lanes_of(bool vec, int E, int loads) {
   int lanes = 1;
-  while (lanes < 32 && 8 * lanes < E) lanes *= 2;
+  while (lanes < 32 && 8 * loads * lanes < E) lanes *= 2;
   return vec ? lanes : 32;
 }
 
@@ -402,7 +426,7 @@ q4_status launch_balance(const void* logits, int dtype, int64_t tokens, int E, i
   const bool vec = E % 8 == 0 && ld * (dtype == Q4_F32 ? 4 : 2) % 16 == 0 && mult(logits, 16);
   const q4_status st = by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
-    return by_experts(vec, E, [&](auto v, auto n) {
+    return by_experts(vec, E, all ? 1 : loads_of(tokens, E), [&](auto v, auto n) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3((unsigned)grid, 1, 1);
       cfg.blockDim = dim3(kThreads, 1, 1);
@@ -412,7 +436,7 @@ q4_status launch_balance(const void* logits, int dtype, int64_t tokens, int E, i
       cfg.attrs = attr;
       cfg.numAttrs = all ? 2 : 1;
       return cudaLaunchKernelEx(&cfg, balance_kernel<T, decltype(v)::value, decltype(n)::value>, static_cast<const T*>(logits),
-                                tokens, ld, ids, lanes_of(vec, E), f, device_status_ptr()) == cudaSuccess
+                                tokens, ld, ids, lanes_of(vec, E, decltype(n)::value), f, device_status_ptr()) == cudaSuccess
                  ? Q4_OK
                  : Q4_ERR_CUDA;
     });
@@ -434,11 +458,11 @@ q4_status launch_balance_backward(const void* logits, int dtype, int64_t tokens,
                                   int top_k, const float* d_loss, float coeff, bool accumulate, void* d_logits,
                                   cudaStream_t stream) {
   const bool vec = E % 8 == 0 && ld * (dtype == Q4_F32 ? 4 : 2) % 16 == 0 && mult(logits, 16) && mult(d_logits, 16);
-  const int lanes = lanes_of(vec, E), per_block = 8 * (32 / lanes);  // tokens at a time
-  const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(tokens, per_block), (int64_t)num_sms() * 6);
   return by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
-    return by_experts(vec, E, [&](auto v, auto n) {
+    return by_experts(vec, E, loads_of(tokens, E), [&](auto v, auto n) {
+      const int lanes = lanes_of(vec, E, decltype(n)::value), per_block = 8 * (32 / lanes);  // tokens at a time
+      const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(tokens, per_block), (int64_t)num_sms() * 6);
       return launch_pdl(balance_backward_kernel<T, decltype(v)::value, decltype(n)::value>, grid, 256, 0, stream,
                         static_cast<const T*>(logits), tokens, E, ld, counts, lanes, top_k, d_loss, coeff, (int)accumulate,
                         static_cast<T*>(d_logits));

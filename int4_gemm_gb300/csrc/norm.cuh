@@ -111,30 +111,38 @@ __device__ __forceinline__ void load_weights(const void* w, bool w32, int c, int
 // buf alternates between two buffers from row to row, so that one barrier per row
 // is enough.
 struct Exchange {
-  float2 part[2][32];
+  __align__(16) float2 part[2][32];
 };
+// Before the first row: parts that no warp writes are zero.
+__device__ __forceinline__ void exchange_init(Exchange& ex) {
+  if (threadIdx.x < 64) ex.part[threadIdx.x >> 5][threadIdx.x & 31] = make_float2(0.f, 0.f);
+}
 template <bool kTop>
 __device__ __forceinline__ float2 group_reduce(float sum, float top, int group, Exchange& ex, int buf) {
-  const int width = min(group, 32);
-  for (int o = width / 2; o > 0; o >>= 1) {
+  if (group >= 32) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+    if (kTop) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
     sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (kTop) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   }
   if (group > 32) {
-    const int lane = threadIdx.x & 31, warps = group >> 5, first = (threadIdx.x >> 5) / warps * warps;
-    if (lane == 0) ex.part[buf][threadIdx.x >> 5] = make_float2(sum, top);
+    const int lane = threadIdx.x & 31, warps = group >> 5, warp = threadIdx.x >> 5;
+    const bool few = warps <= 4;  // four slots per group, else all for the only one
+    if (lane == 0) ex.part[buf][few ? warp / warps * 4 + warp % warps : warp] = make_float2(sum, top);
     __syncthreads();
     if (warps <= 8) {  // few enough for every thread to add them up
-      sum = top = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (i >= warps) break;
-        const float2 v = ex.part[buf][first + i];
-        sum += v.x;
-        if (kTop) top = fmaxf(top, v.y);
-      }
+      const float4* part = reinterpret_cast<const float4*>(ex.part[buf] + (few ? warp / warps * 4 : warp / warps * warps));
+      float4 v[4];
+      v[0] = part[0], v[1] = part[1];
+      v[2] = v[3] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!few) v[2] = part[2], v[3] = part[3];
+      sum = ((v[0].x + v[0].z) + (v[1].x + v[1].z)) + ((v[2].x + v[2].z) + (v[3].x + v[3].z));
+      if (kTop) top = fmaxf(fmaxf(fmaxf(v[0].y, v[0].w), fmaxf(v[1].y, v[1].w)), fmaxf(fmaxf(v[2].y, v[2].w), fmaxf(v[3].y, v[3].w)));
     } else {
-      const float2 v = lane < warps ? ex.part[buf][first + lane] : make_float2(0.f, 0.f);
+      const float2 v = ex.part[buf][lane];
       sum = v.x, top = v.y;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
@@ -161,6 +169,8 @@ struct Place {
   __device__ __forceinline__ int at(int i) const { return block(i) * 128; }
   // columns of piece i of a row of H (0: a row that is not there)
   __device__ __forceinline__ int cols(int i, int H) const { return min(128, H - at(i)); }
+  // Whether C pieces of every thread lie inside a row of H.
+  __device__ __forceinline__ bool whole(int C, int H) const { return C * stride * 128 == H; }
 };
 
 // ------------------------------------------------------------------ rows through shared memory
@@ -176,12 +186,13 @@ struct RingArgs {
   KernelCtl ctl;
 };
 
-__device__ __forceinline__ void ring_init(Ring& ring, const RingArgs& r) {
+__device__ __forceinline__ void ring_init(Ring& ring, const RingArgs& r, Exchange& ex) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < r.stages; ++s) mbar_init(smem_u32(&ring.full[s]), 1);
     ring.abort = 0;
     fence_mbar_init();
   }
+  exchange_init(ex);
   __syncthreads();
 }
 
@@ -263,10 +274,11 @@ struct HeldWeights {
       }
     }
   }
+  template <bool kHeld>
   __device__ __forceinline__ void get(const Place& pl, int H, int i, float (&f)[8]) const {
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = w[i].at(j);
-    if (!held) load_weights<T, kVec>(p, true, pl.at(i), pl.l, pl.cols(i, H), f);
+    if (!kHeld && !held) load_weights<T, kVec>(p, true, pl.at(i), pl.l, pl.cols(i, H), f);
   }
 };
 

@@ -34,6 +34,8 @@ __global__ void __launch_bounds__(max_threads(kC))
   pdl_wait();
   using P = Piece<T, kVec>;
   __shared__ Exchange ex;
+  exchange_init(ex);
+  __syncthreads();
   const Place pl(group);
   const int width = (int)a.H;
   const float inv_H = 1.f / (float)width;
@@ -93,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads))
   using P = Piece<T, kVec>;
   __shared__ Ring ring;
   __shared__ Exchange ex;
-  ring_init(ring, r);
+  ring_init(ring, r, ex);
   pdl_wait();
   const Place pl(group);
   const int width = (int)a.H;
@@ -112,64 +114,75 @@ __global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads))
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
   int stage = 0, buf = 0;
   uint32_t phase = 0;
-  for (int64_t base = base0; base < a.rows; base += step, buf ^= 1) {
-    const int64_t row = base + pl.sub;
-    const int H = row < a.rows ? width : 0;
-    const float rstd = H ? __ldg(a.rstd + row) : 0.f;
-    mbar_wait(smem_u32(&ring.full[stage]), phase, r.ctl, &ring.abort);
-    const uint8_t* st = stage_smem + stage * r.stage_bytes;
-    const T* dy_row = ring_row<kVec, T>(st, r, 0, pl, a.d_y, pitch[0], row);
-    const T* h_row = ring_row<kVec, T>(st, r, 1, pl, a.h, pitch[1], row);
-    const T* dh_row = ring_row<kVec, T>(st, r, 2, pl, a.d_h, pitch[2], row);
-    if (!kVec && row == a.rows - 1) {  // in place
-      dy_row = static_cast<const T*>(a.d_y) + row * a.ld_d_y;
-      h_row = static_cast<const T*>(a.h) + row * a.ld_h;
-      dh_row = static_cast<const T*>(a.d_h) + row * a.ld_d_h;
-    }
-    float dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < kC; ++i) {
-      const int n = pl.cols(i, H);
-      P dy, h;
-      float f[8];
-      dy.load(dy_row + pl.at(i), pl.l, n);
-      h.load(h_row + pl.at(i), pl.l, n);
-      w.get(pl, width, i, f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float t = dy.at(j) * h.at(j);
-        dot = fmaf(t, f[j], dot);
-        acc[i][j] = fmaf(t, rstd, acc[i][j]);
+  auto rows = [&](auto tag) {
+    constexpr bool kWhole = decltype(tag)::value;  // as in the forward kernel
+    for (int64_t base = base0; base < a.rows; base += step, buf ^= 1) {
+      const int64_t row = base + pl.sub;
+      const int H = kWhole || row < a.rows ? width : 0;
+      const float rstd = kWhole || H ? __ldg(a.rstd + row) : 0.f;
+      mbar_wait(smem_u32(&ring.full[stage]), phase, r.ctl, &ring.abort);
+      const uint8_t* st = stage_smem + stage * r.stage_bytes;
+      const T* dy_row = ring_row<kVec, T>(st, r, 0, pl, a.d_y, pitch[0], row);
+      const T* h_row = ring_row<kVec, T>(st, r, 1, pl, a.h, pitch[1], row);
+      const T* dh_row = ring_row<kVec, T>(st, r, 2, pl, a.d_h, pitch[2], row);
+      if (!kVec && row == a.rows - 1) {  // in place
+        dy_row = static_cast<const T*>(a.d_y) + row * a.ld_d_y;
+        h_row = static_cast<const T*>(a.h) + row * a.ld_h;
+        dh_row = static_cast<const T*>(a.d_h) + row * a.ld_d_h;
       }
-    }
-    const float2 q = group_reduce<false>(dot, 0.f, group, ex, buf);
-    if (pl.group <= 32) __syncthreads();
-    if (threadIdx.x == 0 && base != base0) {  // every thread has left the stage of the row before
-      const int64_t next = base + (r.stages - 1) * step;
-      ring_fill<kVec>(ring, r, smem_u32(stage_smem), stage ? stage - 1 : r.stages - 1, mat, pitch, next, a.rows, pl.per_block);
-    }
-    const float c = rstd * rstd * rstd * (q.x * inv_H);
-    T* out = static_cast<T*>(a.d_x) + row * a.H;
+      float dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < kC; ++i) {
-      const int n = pl.cols(i, H);
-      P dy, h;
-      float f[8];
-      dy.load(dy_row + pl.at(i), pl.l, n);
-      h.load(h_row + pl.at(i), pl.l, n);
-      w.get(pl, width, i, f);
-      float d[8];
+      for (int i = 0; i < kC; ++i) {
+        const int n = kWhole ? 128 : pl.cols(i, H);
+        P dy, h;
+        float f[8];
+        dy.load(dy_row + pl.at(i), pl.l, n);
+        h.load(h_row + pl.at(i), pl.l, n);
+        w.template get<kWhole>(pl, width, i, f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = fmaf(-h.at(j), c, dy.at(j) * (f[j] * rstd));
-      if (a.d_h) {
-        P dh;
-        dh.load(dh_row + pl.at(i), pl.l, n);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] += dh.at(j);
+        for (int j = 0; j < 8; ++j) {
+          const float t = dy.at(j) * h.at(j);
+          dot = fmaf(t, f[j], dot);
+          acc[i][j] = fmaf(t, rstd, acc[i][j]);
+        }
       }
-      P::store(out + pl.at(i), pl.l, n, d);
+      const float2 q = group_reduce<false>(dot, 0.f, group, ex, buf);
+      if (pl.group <= 32) __syncthreads();
+      if (threadIdx.x == 0 && base != base0) {  // every thread has left the stage of the row before
+        const int64_t next = base + (r.stages - 1) * step;
+        ring_fill<kVec>(ring, r, smem_u32(stage_smem), stage ? stage - 1 : r.stages - 1, mat, pitch, next, a.rows, pl.per_block);
+      }
+      const float c = rstd * rstd * rstd * (q.x * inv_H);
+      T* out = static_cast<T*>(a.d_x) + row * a.H;
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        const int n = kWhole ? 128 : pl.cols(i, H);
+        P dy, h;
+        float f[8];
+        dy.load(dy_row + pl.at(i), pl.l, n);
+        h.load(h_row + pl.at(i), pl.l, n);
+        w.template get<kWhole>(pl, width, i, f);
+        float d[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = fmaf(-h.at(j), c, dy.at(j) * (f[j] * rstd));
+        if (a.d_h) {
+          P dh;
+          dh.load(dh_row + pl.at(i), pl.l, n);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] += dh.at(j);
+        }
+        P::store(out + pl.at(i), pl.l, n, d);
+      }
+      if (++stage == r.stages) stage = 0, phase ^= 1;
     }
-    if (++stage == r.stages) stage = 0, phase ^= 1;
+  };
+  if constexpr (kVec && kC == 4) {
+    if (w.held && pl.whole(kC, width) && a.rows % pl.per_block == 0)
+      rows(std::true_type());
+    else
+      rows(std::false_type());
+  } else {
+    rows(std::false_type());
   }
   store_partial<kVec, kC>(a, pl, acc);
 }
