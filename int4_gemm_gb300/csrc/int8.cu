@@ -1,11 +1,8 @@
-// 8-bit integers with one scale per row: the quantizer and the product
+// Product of 8-bit integers with one scale per row of either operand:
 //   C[m, n] = sa[m] sb[n] sum over k of qa[m, k] qb[n, k]
 // with exact 32-bit integer sums.
 //
-// The quantizer follows the oracle step by step in FP32 with IEEE rounding:
-//   s = max(amax, 1e-12) * RN(1 / 127),  q = rint(x / s)  (ties to even)
-//
-// The product on this GPU's f16 tensor cores, which are far faster than its
+// It runs on this GPU's f16 tensor cores, which are far faster than its
 // integer ones: an 8-bit integer is an f16 number, a product of two (at most
 // 2^14) and the FP32 sum of 1024 of them (at most 2^24) are exact, and every
 // 1024 columns the sum is added to a 32-bit integer.  The weights are the M
@@ -37,32 +34,6 @@
 
 namespace q4 {
 namespace {
-
-constexpr int kQuantThreads = 256;
-
-// One block of threads per row: the largest magnitude, then the codes (the row
-// comes from L1 or L2 the second time).
-template <typename T>
-__global__ void __launch_bounds__(kQuantThreads)
-    quantize_int8_kernel(const T* __restrict__ x, int64_t K, int64_t ld, int8_t* __restrict__ codes, float* __restrict__ scales,
-                         int* status) {
-  pdl_wait();
-  __shared__ uint32_t part[kQuantThreads / 32];
-  const T* row = x + (int64_t)blockIdx.x * ld;
-  uint32_t top = 0;  // as bits: NaN and infinities come out on top
-  for (int64_t k = threadIdx.x; k < K; k += kQuantThreads) top = max(top, __float_as_uint(Elem<T>::to_f(row[k])) & 0x7fffffffu);
-  top = __reduce_max_sync(0xffffffffu, top);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
-  __syncthreads();
-  for (int w = 0; w < kQuantThreads / 32; ++w) top = max(top, part[w]);
-  const float s = fmaxf(__uint_as_float(top), 1e-12f) * (1.f / 127.f);
-  if (threadIdx.x == 0) {
-    scales[blockIdx.x] = s;
-    if (nonfinite(__uint_as_float(top))) latch_status(status, Q4_ERR_NONFINITE);
-  }
-  for (int64_t k = threadIdx.x; k < K; k += kQuantThreads)
-    codes[(int64_t)blockIdx.x * K + k] = (int8_t)min(max(__float2int_rn(__fdiv_rn(Elem<T>::to_f(row[k]), s)), -127), 127);
-}
 
 // ------------------------------------------------------------------ product
 constexpr int kRows = 128;        // weight rows of a CTA
@@ -730,15 +701,6 @@ q4_status launch_plan(const Plan& s, const int8_t* qa, const int8_t* qb, const P
 }
 
 }  // namespace
-
-q4_status launch_quantize_int8(const void* x, int dtype, int64_t rows, int64_t K, int64_t ld, int8_t* codes, float* scales,
-                               cudaStream_t stream) {
-  return by_dtype(dtype, [&](auto tag) {
-    using T = decltype(tag);
-    return launch_pdl(quantize_int8_kernel<T>, (unsigned)rows, kQuantThreads, 0, stream, static_cast<const T*>(x), K, ld, codes,
-                      scales, device_status_ptr());
-  });
-}
 
 q4_status launch_int8_gemm(const int8_t* qa, const float* sa, const int8_t* qb, const float* sb, int64_t M, int64_t N, int64_t K,
                            void* C, int c_dtype, cudaStream_t stream) {

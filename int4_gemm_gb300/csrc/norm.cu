@@ -14,7 +14,7 @@
 // pieces each.  What registers can hold in flight (32 KB per SM) is too little for
 // HBM, so where there are many aligned rows they come through a ring in shared
 // memory, filled by bulk copies some rows ahead.
-#include "norm.cuh"
+#include "rows.cuh"
 
 namespace q4 {
 namespace {
@@ -22,20 +22,6 @@ namespace {
 __device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float f) {
   return make_uint2(e4m3x2(v[0] * f, v[1] * f) | e4m3x2(v[2] * f, v[3] * f) << 16,
                     e4m3x2(v[4] * f, v[5] * f) | e4m3x2(v[6] * f, v[7] * f) << 16);
-}
-
-// The low byte of v f rounded to the nearest integer (even at ties), |v f| < 2^22:
-// adding 1.5 * 2^23 leaves the integer in the low bits of the sum.
-__device__ __forceinline__ uint32_t int8_bits(float v, float f) { return __float_as_uint(fmaf(v, f, 12582912.f)); }
-__device__ __forceinline__ uint2 int8x8(const float (&v)[8], float f) {
-  uint32_t o[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t lo = __byte_perm(int8_bits(v[4 * i], f), int8_bits(v[4 * i + 1], f), 0x0040);
-    const uint32_t hi = __byte_perm(int8_bits(v[4 * i + 2], f), int8_bits(v[4 * i + 3], f), 0x0040);
-    o[i] = __byte_perm(lo, hi, 0x5410);
-  }
-  return make_uint2(o[0], o[1]);
 }
 
 // A row of h = x + residual in v: reduced, scaled by the weights and written.  H is
@@ -71,14 +57,15 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const Place& pl, int
     if (a.rstd) a.rstd[row] = rstd;
     if (nonfinite(r.x)) latch_status(status, Q4_ERR_NONFINITE);
   }
-  // the codes' factor rstd / s may be off by 2 ulp, as rstd may
   if constexpr (kForm == Q4_NORM_INT8) {
+    // the codes are rint(h w f); where the scale is not the least one, f = rstd / s =
+    // 127 / amax |h w| needs neither rstd nor s and their roundings
     const float s = fmaxf(r.y * rstd, 1e-12f) * (1.f / 127.f);
+    const float f = r.y * rstd > 1e-12f ? __fdiv_rn(127.f, r.y) : __fdiv_rn(rstd, s);
     if (pl.t == 0 && H) {
       a.scales[row] = s;
       if (nonfinite(s)) latch_status(status, Q4_ERR_NONFINITE);
     }
-    const float f = __fdividef(rstd, s);
     uint8_t* codes = a.codes + start;
 #pragma unroll
     for (int i = 0; i < kC; ++i) P::store_codes(codes + pl.at(i), pl.l, cols(i), int8x8(v[i], f));
@@ -94,7 +81,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const Place& pl, int
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       const float s = fmaxf(m * rstd, 1e-12f) * (1.f / 448.f);
-      P::store_codes(codes + pl.at(i), pl.l, cols(i), e4m3x8(v[i], __fdividef(rstd, s)));
+      P::store_codes(codes + pl.at(i), pl.l, cols(i), e4m3x8(v[i], m * rstd > 1e-12f ? __fdividef(448.f, m) : __fdividef(rstd, s)));
       if (pl.l == 0 && cols(i) > 0) {
         scales[pl.block(i)] = s;
         if (nonfinite(s)) latch_status(status, Q4_ERR_NONFINITE);

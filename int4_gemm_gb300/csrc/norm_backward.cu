@@ -5,7 +5,7 @@
 // groups) and adds its rows' part of d_w up in registers, columns fixed to
 // threads; the blocks' sums go to the workspace and are added in their order by
 // a second kernel, so that results do not depend on timing.
-#include "norm.cuh"
+#include "rows.cuh"
 
 namespace q4 {
 namespace {

@@ -1,5 +1,6 @@
-// What the norm and its gradient share: rows spread over threads, their reduction,
-// and the ring of rows in shared memory.
+// What kernels that hold whole rows share (the norm, its gradient, the INT8
+// quantizer): rows spread over threads, their reduction, and a ring of rows in
+// shared memory.
 #pragma once
 
 #include <algorithm>
@@ -86,6 +87,20 @@ struct Piece {
     }
   }
 };
+
+// The low byte of v f rounded to the nearest integer (even at ties), |v f| < 2^22:
+// adding 1.5 * 2^23 leaves the integer in the low bits of the sum.
+__device__ __forceinline__ uint32_t int8_bits(float v, float f) { return __float_as_uint(fmaf(v, f, 12582912.f)); }
+__device__ __forceinline__ uint2 int8x8(const float (&v)[8], float f) {
+  uint32_t o[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = __byte_perm(int8_bits(v[4 * i], f), int8_bits(v[4 * i + 1], f), 0x0040);
+    const uint32_t hi = __byte_perm(int8_bits(v[4 * i + 2], f), int8_bits(v[4 * i + 3], f), 0x0040);
+    o[i] = __byte_perm(lo, hi, 0x5410);
+  }
+  return make_uint2(o[0], o[1]);
+}
 
 // The weights of a piece (columns c + ...), T or FP32; all 1 without weights.
 template <typename T, bool kVec>
@@ -289,24 +304,27 @@ struct Shape {
   uint32_t stage_bytes;
 };
 constexpr uint32_t kRingTotal = 216 * 1024;  // of an SM's shared memory
+// Rows of `blocks` 128-column blocks, C pieces per thread, at most (where a row
+// takes no more) most_threads threads.
+inline Shape spread(int blocks, int C, int most_threads) {
+  Shape s = {};
+  s.C = C;
+  const int halves = (int)ceil_div(blocks, C);  // groups of 16 lanes
+  s.group = halves == 1 ? 16 : (halves + 1) / 2 * 32;
+  s.threads = std::max(1, most_threads / s.group) * s.group;
+  return s;
+}
+
 // Blocks per SM that the ring kernels are compiled for: single elements need few
 // registers and many warps; of aligned rows, whose threads hold 32 elements, three
 // blocks would spill (34 us instead of 26 for 4096 x 7168 to INT8).
 __host__ __device__ constexpr int resident_blocks(bool vec, int threads) { return threads > 256 ? 1 : vec ? 2 : 3; }
 
-Shape shape_of(int64_t rows, int64_t H, int mats, int size, bool vec) {
+inline Shape shape_of(int64_t rows, int64_t H, int mats, int size, bool vec) {
   const int blocks = (int)ceil_div(H, 128);
-  auto spread = [&](int C, int most_threads) {
-    Shape s = {};
-    s.C = C;
-    const int halves = (int)ceil_div(blocks, C);  // groups of 16 lanes
-    s.group = halves == 1 ? 16 : (halves + 1) / 2 * 32;
-    s.threads = std::max(1, most_threads / s.group) * s.group;
-    return s;
-  };
   const int64_t sms = num_sms();
   if (blocks <= (vec ? 128 : 32)) {
-    Shape s = spread(!vec ? 2 : blocks >= 16 ? 4 : blocks >= 4 ? 2 : 1, 256);
+    Shape s = spread(blocks, !vec ? 2 : blocks >= 16 ? 4 : blocks >= 4 ? 2 : 1, 256);
     const int per_block = s.threads / s.group;
     const uint32_t row_bytes = (uint32_t)(H * size);
     s.stage_bytes = (uint32_t)(mats * per_block) * (vec ? staged_row<true>(row_bytes) : staged_row<false>(row_bytes));
@@ -319,7 +337,7 @@ Shape shape_of(int64_t rows, int64_t H, int mats, int size, bool vec) {
   int C = 1;
   const int most = rows <= 2 * sms ? 64 : 16;  // blocks of 128 columns that one piece per thread takes
   if (blocks > most) C = blocks > 128 ? 8 : 4;
-  Shape s = spread(C, 128);
+  Shape s = spread(blocks, C, 128);
   s.grid = (int)std::min<int64_t>(ceil_div(rows, s.threads / s.group), sms * std::max(1, 1024 / s.threads));
   return s;
 }
