@@ -81,7 +81,9 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const Place& pl, int
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       const float s = fmaxf(m * rstd, 1e-12f) * (1.f / 448.f);
-      P::store_codes(codes + pl.at(i), pl.l, cols(i), e4m3x8(v[i], m * rstd > 1e-12f ? __fdividef(448.f, m) : __fdividef(rstd, s)));
+      // 448 / m, as 7 / (m / 64): __fdividef gives 0 for divisors above 2^126
+      const float f = m * rstd > 1e-12f ? __fdividef(7.f, m * 0x1p-6f) : __fdividef(rstd, s);
+      P::store_codes(codes + pl.at(i), pl.l, cols(i), e4m3x8(v[i], f));
       if (pl.l == 0 && cols(i) > 0) {
         scales[pl.block(i)] = s;
         if (nonfinite(s)) latch_status(status, Q4_ERR_NONFINITE);

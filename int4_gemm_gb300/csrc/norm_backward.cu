@@ -10,6 +10,10 @@
 namespace q4 {
 namespace {
 
+// rstd^3 mean, by factors that stay in range: rstd mean is as large as g (rstd^3 by
+// itself is below the least number for h above 2^49).
+__device__ __forceinline__ float h_factor(float rstd, float mean) { return rstd * (rstd * (rstd * mean)); }
+
 // The block's part of d_w: the groups' sums one after another.
 template <bool kVec, int kC>
 __device__ __forceinline__ void store_partial(const NormBackwardArgs& a, const Place& pl, const float (&acc)[kC][8]) {
@@ -70,7 +74,7 @@ __global__ void __launch_bounds__(max_threads(kC))
       }
     }
     const float2 r = group_reduce<false>(dot, 0.f, group, ex, buf);
-    const float c = rstd * rstd * rstd * (r.x * inv_H);
+    const float c = h_factor(rstd, r.x * inv_H);
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       float w[8], d[8];
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads))
         const int64_t next = base + (r.stages - 1) * step;
         ring_fill<kVec>(ring, r, smem_u32(stage_smem), stage ? stage - 1 : r.stages - 1, mat, pitch, next, a.rows, pl.per_block);
       }
-      const float c = rstd * rstd * rstd * (q.x * inv_H);
+      const float c = h_factor(rstd, q.x * inv_H);
       T* out = static_cast<T*>(a.d_x) + row * a.H;
 #pragma unroll
       for (int i = 0; i < kC; ++i) {
