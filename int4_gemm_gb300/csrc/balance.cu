@@ -10,7 +10,7 @@
 // where rows are aligned (Lanes), else by a warp, lane l the experts l, l + 32, ...;
 // its probabilities are added up in registers, token by token.  The blocks' sums
 // meet in a fixed order: in distributed shared memory of the same blocks, one
-// cluster, where there are few tokens, else in the workspace, from where a second
+// cluster, where there are few tokens (one_cluster), else in the workspace, from where a second
 // kernel adds them (the counts are integers, whose order does not matter).
 #include <algorithm>
 #include <type_traits>
@@ -396,9 +396,14 @@ int lanes_of(bool vec, int E, int loads) {
   return vec ? lanes : 32;
 }
 
-// Blocks: a cluster that finishes by itself where a warp has few tokens (1000 x 64:
-// 4.6 us, with a second kernel 6.1), else one per SM.
-bool one_cluster(int64_t tokens, int64_t E) { return tokens * E <= (int64_t)kCluster * kWarps * 256 * 16; }
+// Blocks: a cluster that finishes by itself where a warp has few tokens, four turns of
+// 256 experts or (more of them, or widths that eight do not divide) of a token, else
+// one per SM and a second launch.  FP32, cluster and grid: 1000 x 64 6.1 and 7.5 us,
+// 2000 x 64 7.2 and 7.5, 8192 x 64 12.0 and 7.6, 256 x 256 6.3 and 8.7, 1000 x 256 9.2
+// and 8.7, 512 x 1024 14.3 and 16.9, 500 x 60 5.8 and 7.0, 2000 x 60 9.2 and 7.0.
+bool one_cluster(int64_t tokens, int64_t E) {
+  return tokens * (E % 8 ? 256 : std::min<int64_t>(E, 256)) <= (int64_t)kCluster * kWarps * 4 * 256;
+}
 int balance_grid(int64_t tokens, int64_t E) { return one_cluster(tokens, E) ? kCluster : num_sms(); }
 
 // Programmatic dependent launch, and clusters of kCluster blocks.
