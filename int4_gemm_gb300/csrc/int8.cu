@@ -148,35 +148,45 @@ __device__ __forceinline__ uint2 int8x4_to_f16(uint32_t w) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
+// A lane's scales of a tile: its weight row's, and those of the tokens lane, lane +
+// 32, ...  Single CTAs load them when the tile begins, behind whose sums their way
+// from memory hides (256 x 8192 x 8192 40.1 -> 38.6 us, 1 x 128 x 128 4.35 -> 4.10);
+// pairs, which have no registers for them until the sums are complete, then.
+template <int kCols>
+struct Scales {
+  float weight, token[(kCols + 31) / 32];
+  __device__ __forceinline__ void load(const Params& p, int64_t m0, int64_t n, int cols, int lane) {
+    weight = n < p.N ? __ldg(p.sb + n) : 0.f;
+#pragma unroll
+    for (int i = 0; i < (kCols + 31) / 32; ++i) token[i] = i * 32 + lane < cols ? __ldg(p.sa + m0 + i * 32 + lane) : 0.f;
+  }
+};
+
 // Tokens m0 .. m0 + cols - 1 of one weight row n per lane: 32 consecutive outputs
 // of a token per store.  The tokens' scales come from the lanes that loaded them.
 template <int kCols, typename C>
-__device__ __forceinline__ void store_columns_as(C* out, const Params& p, int64_t m0, int64_t n, int cols, int lane,
+__device__ __forceinline__ void store_columns_as(C* out, const Params& p, int64_t m0, int64_t n, int cols, const Scales<kCols>& scales,
                                                  const int (&v)[kCols]) {
-  const float sb = n < p.N ? __ldg(p.sb + n) : 0.f;
-  float scale[(kCols + 31) / 32];
-#pragma unroll
-  for (int i = 0; i < (kCols + 31) / 32; ++i) scale[i] = i * 32 + lane < cols ? __ldg(p.sa + m0 + i * 32 + lane) : 0.f;
   out += m0 * p.N + n;
 #pragma unroll
   for (int j = 0; j < kCols; ++j) {
-    const float s = __shfl_sync(0xffffffffu, scale[j / 32], j & 31);
-    if (n < p.N && j < cols) out[0] = to_elem<C>((float)v[j] * s * sb);
+    const float s = __shfl_sync(0xffffffffu, scales.token[j / 32], j & 31);
+    if (n < p.N && j < cols) out[0] = to_elem<C>((float)v[j] * s * scales.weight);
     out += p.N;
   }
 }
 
 // The same for one CTA's share of a tile whose K parts lie in the shared memory of
 // the cluster's kParts CTAs, part[weight row][token]: groups of four tokens of one
-// weight row per lane, `first`, first + step and so on.  A load from another CTA
-// takes some 1000 clocks, so several are in flight.
+// weight row per lane, `first`, first + step and so on (a warp's at most 32 tokens;
+// lane l has the scale of the l-th).  A load from another CTA takes some 1000
+// clocks, so several are in flight.
 template <int kParts, typename C>
 __device__ __forceinline__ void join_columns_as(const Params& p, uint32_t row_smem, int64_t m0, int64_t n, int cols, int first,
-                                                int step) {
+                                                int step, float token_scale, float weight_scale) {
   constexpr int kFlight = 8 / kParts;
-  const float sb = n < p.N ? __ldg(p.sb + n) : 0.f;
   C* out = static_cast<C*>(p.C) + m0 * p.N + n;
-  for (int c0 = 4 * first; c0 < cols; c0 += 4 * step * kFlight) {
+  for (int c0 = 4 * first, at = 0; c0 < cols; c0 += 4 * step * kFlight, at += 4 * kFlight) {
     int x[kFlight][kParts][4];
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
@@ -196,17 +206,18 @@ __device__ __forceinline__ void join_columns_as(const Params& p, uint32_t row_sm
 #pragma unroll
         for (int r = 0; r < kParts; ++r) v += x[f][r][i];
         const int c = c0 + 4 * step * f + i;
-        if (c < cols && n < p.N) out[c * p.N] = to_elem<C>((float)v * __ldg(p.sa + m0 + c) * sb);
+        const float s = __shfl_sync(0xffffffffu, token_scale, at + 4 * f + i);
+        if (c < cols && n < p.N) out[c * p.N] = to_elem<C>((float)v * s * weight_scale);
       }
   }
 }
 template <int kParts>
 __device__ __forceinline__ void join_columns(const Params& p, uint32_t row_smem, int64_t m0, int64_t n, int cols, int first,
-                                             int step) {
+                                             int step, float token_scale, float weight_scale) {
   if (p.c_dtype == Q4_BF16)
-    join_columns_as<kParts, __nv_bfloat16>(p, row_smem, m0, n, cols, first, step);
+    join_columns_as<kParts, __nv_bfloat16>(p, row_smem, m0, n, cols, first, step, token_scale, weight_scale);
   else
-    join_columns_as<kParts, float>(p, row_smem, m0, n, cols, first, step);
+    join_columns_as<kParts, float>(p, row_smem, m0, n, cols, first, step, token_scale, weight_scale);
 }
 
 // What a CTA holds of a tile: kHalf tokens per accumulator slot, kHalves slots.
@@ -540,8 +551,26 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
     const int runs = h == 0 ? (segs + 1) / 2 : 1 + segs / 2;
     uint32_t begun = 0;  // runs begun before this tile, in the order in which they take slots
     bool alive = h < kHalves;
+    const bool split = !kPair && p.splits > 1;
+    // of a split tile: its weight row's scale, and one of the tokens that the warp joins
+    const int join_first = 2 * rank + h, join_step = 2 * p.splits;
+    float token_scale = 0.f, weight_scale = 0.f;
+    if (split) {
+      int64_t m0, n0;
+      tile_mn(unit, m0, n0);
+      const int64_t n = n0 + q * 32 + lane, m = m0 + 4 * (join_first + join_step * (lane >> 2)) + (lane & 3);
+      weight_scale = n < p.N ? __ldg(p.sb + n) : 0.f;
+      token_scale = m < p.M ? __ldg(p.sa + m) : 0.f;
+    }
     int sum[kHalf];
     for (int t = unit; t < tiles && alive; t += units) {
+      int64_t m0, n0;
+      tile_mn(t, m0, n0);
+      m0 += h * kHalf;
+      const int64_t n = n0 + q * 32 + lane;
+      const int cols = (int)min((int64_t)kHalf, p.M - m0);
+      Scales<kHalf> scales;
+      if (!kPair && !split) scales.load(p, m0, n, cols, lane);
 #pragma unroll
       for (int j = 0; j < kHalf; ++j) sum[j] = 0;
       for (int run = 0; run < runs; ++run) {
@@ -571,19 +600,15 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
       }
       begun += kHalves == 1 ? (segs + 1) / 2 : segs + 1;
       if (!alive) break;
-      int64_t m0, n0;
-      tile_mn(t, m0, n0);
-      if (kPair || p.splits == 1) {
-        const int64_t n = n0 + q * 32 + lane;
-        m0 += h * kHalf;
-        const int cols = (int)min((int64_t)kHalf, p.M - m0);
+      if (!split) {
+        if (kPair) scales.load(p, m0, n, cols, lane);
         if (p.c_dtype == Q4_BF16)
-          store_columns_as<kHalf>(static_cast<__nv_bfloat16*>(p.C), p, m0, n, cols, lane, sum);
+          store_columns_as<kHalf>(static_cast<__nv_bfloat16*>(p.C), p, m0, n, cols, scales, sum);
         else
-          store_columns_as<kHalf>(static_cast<float*>(p.C), p, m0, n, cols, lane, sum);
+          store_columns_as<kHalf>(static_cast<float*>(p.C), p, m0, n, cols, scales, sum);
       }
     }
-    if (!kPair && p.splits > 1) {
+    if (split) {
       // the cluster's parts of one tile meet in shared memory, which no copy and no
       // MMA uses any more (this CTA's are complete: the last sums were read)
       int64_t m0, n0;
@@ -602,9 +627,9 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
       if (!*abort_flag) {
         const int64_t n = n0 + q * 32 + lane;
         if (p.splits == 2)
-          join_columns<2>(p, row, m0, n, cols, 2 * rank + h, 4);
+          join_columns<2>(p, row, m0, n, cols, join_first, join_step, token_scale, weight_scale);
         else
-          join_columns<4>(p, row, m0, n, cols, 2 * rank + h, 8);
+          join_columns<4>(p, row, m0, n, cols, join_first, join_step, token_scale, weight_scale);
       }
       cluster_barrier_sync();  // no CTA leaves while another reads its part
     }
@@ -638,7 +663,7 @@ struct Plan {
 // 64 columns of a tile (measured, ns: 16 x 8192 x 8192 24.3 us with 16-token tiles,
 // 28.9 with 64, 39.7 with 128, 48.3 as pairs; 512 x 512 x 512 5.6, 6.9, 7.9 and 10.5;
 // 8192 x 28672 x 8192, 47 tiles per pair, 2020 us), and joining the parts of a split K
-// takes a time of its own (the same 16 x 8192 x 8192 with two parts: 17.2 us; eight
+// takes a time of its own (the same 16 x 8192 x 8192 with two parts: 17.7 us; eight
 // parts were never the best).
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
   const int64_t sms = num_sms(), chunks = ceil_div(K, kPanel);
