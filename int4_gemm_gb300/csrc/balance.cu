@@ -25,6 +25,7 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxExperts = 1024;
 constexpr int kCluster = 8;
+constexpr int kFlight = 8;  // loads of a thread on their way at a time: ids, the blocks' parts
 // Loads per lane where there are many logits: fewer lanes share a token and its
 // reductions (65536 x 256 bf16: 25.9 us with one, 20.6 with two, 19.5 with four, the
 // gradient 21.0, 17.7 and 31.8); elsewhere one (16384 x 64 FP32: 8.2, 8.5 and 11.4).
@@ -175,7 +176,13 @@ __device__ __forceinline__ void finish(const FinishArgs& a, uint32_t* scratch, u
   };
   if (warp == 0) {
     int32_t n = 0;
-    for (int q = lane; q < a.parts; q += 32) n += part_c(q, a.E);
+    for (int q = lane; q < a.parts; q += 32 * kFlight) {
+      int32_t v[kFlight];
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) v[u] = q + 32 * u < a.parts ? part_c(q + 32 * u, a.E) : 0;
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) n += v[u];
+    }
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0) tokens = n;
     if (lane == 0 && rank == 0) a.counts[a.E] = n;
@@ -183,10 +190,18 @@ __device__ __forceinline__ void finish(const FinishArgs& a, uint32_t* scratch, u
   int32_t c = 0;
   float s = 0.f;
   if (e < end) {
-#pragma unroll 4
-    for (int q = group; q < a.parts; q += groups) {
-      c += part_c(q, e);
-      s += a.part_p ? a.part_p[(int64_t)q * a.E + e] : __int_as_float(load_peer(own_p + 4 * e, (uint32_t)q));
+    for (int first = group; first < a.parts; first += groups * kFlight) {
+      int32_t vc[kFlight];
+      float vp[kFlight];
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        const int q = first + u * groups;
+        const bool there = q < a.parts;
+        vc[u] = there ? part_c(q, e) : 0;
+        vp[u] = !there ? 0.f : a.part_p ? a.part_p[(int64_t)q * a.E + e] : __int_as_float(load_peer(own_p + 4 * e, (uint32_t)q));
+      }
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) c += vc[u], s += vp[u];
     }
   }
   sp[threadIdx.x] = s;
@@ -242,21 +257,25 @@ __global__ void __launch_bounds__(kThreads)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = f.E;
   for (int e = threadIdx.x; e <= E; e += kThreads) count[e] = 0;
   __syncthreads();
-  const int64_t slots = tokens * f.top_k;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < slots; i += (int64_t)gridDim.x * kThreads) {
-    const int e = __ldg(ids + i);
-    if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+  // the next token's logits are on their way while this one's are worked on
+  const int64_t step = (int64_t)gridDim.x * kWarps * lay.per_warp;
+  int64_t t = ((int64_t)blockIdx.x * kWarps + warp) * lay.per_warp + lay.sub;
+  uint32_t w[L::words];
+  lay.load(logits + t * ld, E, t < tokens, w);
+  const int64_t slots = tokens * f.top_k, stride = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < slots; i += kFlight * stride) {
+    int id[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) id[u] = i + u * stride < slots ? __ldg(ids + i + u * stride) : -1;
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+      if (id[u] >= 0 && id[u] < E) atomicAdd(&count[id[u]], 1);
   }
   float acc[L::n];
 #pragma unroll
   for (int i = 0; i < L::n; ++i) acc[i] = 0.f;
   int there = 0;
   bool bad = false;
-  // the next token's logits are on their way while this one's are worked on
-  const int64_t step = (int64_t)gridDim.x * kWarps * lay.per_warp;
-  int64_t t = ((int64_t)blockIdx.x * kWarps + warp) * lay.per_warp + lay.sub;
-  uint32_t w[L::words];
-  lay.load(logits + t * ld, E, t < tokens, w);
   for (int64_t first = t - lay.sub; first < tokens; first += step, t += step) {
     uint32_t next[L::words];
     lay.load(logits + (t + step) * ld, E, t + step < tokens, next);
@@ -311,8 +330,13 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const FinishArgs f
   finish(f, scratch, 0, 0);
 }
 
+// Blocks of the gradient per SM, all resident: a second wave repeats the counts' way
+// from memory (six blocks for all: 65536 x 256 bf16 17.7 us instead of 15.7, 8192 x
+// 1024 25.9 instead of 18.9, 32768 x 64 5.8 instead of 4.6).
+constexpr int gradient_blocks(bool vec, int n) { return vec ? (n == 1 ? 4 : n == 2 ? 3 : 2) : n <= 8 ? 4 : 2; }
+
 template <typename T, bool kVec, int kN>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, gradient_blocks(kVec, kN))
     balance_backward_kernel(const T* __restrict__ logits, int64_t tokens, int E, int64_t ld, const int32_t* __restrict__ counts,
                             int lanes, int top_k, const float* __restrict__ d_loss, float coeff, int accumulate,
                             T* __restrict__ d_logits) {
@@ -320,15 +344,15 @@ __global__ void __launch_bounds__(256)
   using L = Lanes<T, kVec, kN>;
   const L lay(lanes);
   const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int64_t step = (int64_t)gridDim.x * warps * lay.per_warp;
+  int64_t t = ((int64_t)blockIdx.x * warps + warp) * lay.per_warp + lay.sub;
+  uint32_t w[L::words];
+  lay.load(logits + t * ld, E, t < tokens, w);
   const int32_t n = __ldg(counts + E);
   const float g = n > 0 ? __ldg(d_loss) * __fdiv_rn(coeff, (float)n) : 0.f;
   float f[L::n];
 #pragma unroll
   for (int i = 0; i < L::n; ++i) f[i] = lay.expert(i) < E ? load_factor(__ldg(counts + lay.expert(i)), n, E, top_k) : 0.f;
-  const int64_t step = (int64_t)gridDim.x * warps * lay.per_warp;
-  int64_t t = ((int64_t)blockIdx.x * warps + warp) * lay.per_warp + lay.sub;
-  uint32_t w[L::words];
-  lay.load(logits + t * ld, E, t < tokens, w);
   for (int64_t first = t - lay.sub; first < tokens; first += step, t += step) {
     uint32_t next[L::words];
     lay.load(logits + (t + step) * ld, E, t + step < tokens, next);
@@ -467,7 +491,7 @@ q4_status launch_balance_backward(const void* logits, int dtype, int64_t tokens,
     using T = decltype(tag);
     return by_experts(vec, E, loads_of(tokens, E), [&](auto v, auto n) {
       const int lanes = lanes_of(vec, E, decltype(n)::value), per_block = 8 * (32 / lanes);  // tokens at a time
-      const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(tokens, per_block), (int64_t)num_sms() * 6);
+      const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(tokens, per_block), (int64_t)num_sms() * gradient_blocks(vec, decltype(n)::value));
       return launch_pdl(balance_backward_kernel<T, decltype(v)::value, decltype(n)::value>, grid, 256, 0, stream,
                         static_cast<const T*>(logits), tokens, E, ld, counts, lanes, top_k, d_loss, coeff, (int)accumulate,
                         static_cast<T*>(d_logits));
