@@ -149,8 +149,10 @@ __global__ void __launch_bounds__(max_threads(kC))
   }
 }
 
+constexpr int kSingles = 3;  // blocks per SM for single elements, which need few registers
+
 template <typename T, bool kVec, int kC, int kForm, int kThreads>
-__global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads)) norm_ring_kernel(const NormArgs a, int group, const RingArgs r) {
+__global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads, kSingles)) norm_ring_kernel(const NormArgs a, int group, const RingArgs r) {
   extern __shared__ __align__(128) uint8_t stage_smem[];
   __shared__ Ring ring;
   __shared__ Exchange ex;
@@ -237,7 +239,7 @@ q4_status launch_norm(const NormArgs& a, int dtype, int form, cudaStream_t strea
   const int size = dtype == Q4_F32 ? 4 : 2;
   const bool vec = a.H % 8 == 0 && a.ldx * size % 16 == 0 && (!a.residual || a.ld_residual * size % 16 == 0) && mult(a.x, 16) &&
                    mult(a.residual, 16) && mult(a.h, 16) && mult(a.y, 16) && mult(a.codes, 8) && mult(a.weight, 16);
-  const Shape s = shape_of(a.rows, a.H, a.residual ? 2 : 1, size, vec);
+  const Shape s = shape_of(a.rows, a.H, a.residual ? 2 : 1, size, vec, kSingles);
   return by_dtype(dtype, [&](auto tag) {
     using T = decltype(tag);
     return by_pieces(s.C, [&](auto c) {

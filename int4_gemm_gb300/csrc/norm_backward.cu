@@ -90,13 +90,21 @@ __global__ void __launch_bounds__(max_threads(kC))
   store_partial<kVec, kC>(a, pl, acc);
 }
 
-// The same with the rows in shared memory, which are read twice there; a stage is
-// refilled after the next row's exchange, when every thread has left it.
+// Blocks per SM for single elements, which keep their rows in registers (9973 x 1411
+// bf16 42.3 us; three blocks, for which registers are too few, 58.7, or 46.2 with two
+// reads from shared memory; one block 67.5).
+constexpr int kSingles = 2;
+
+// The same with the rows in shared memory, which aligned ones are read from twice;
+// a stage is refilled after the next row's exchange, when every thread has left it.
 template <typename T, bool kVec, int kC, int kThreads>
-__global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads))
+__global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads, kSingles))
     norm_backward_ring_kernel(const NormBackwardArgs a, int group, const RingArgs r) {
   extern __shared__ __align__(128) uint8_t stage_smem[];
   using P = Piece<T, kVec>;
+  // between the two passes in registers (aligned rows, of 32 elements per thread, have
+  // none for it: 16384 x 7168 bf16 154 us without, 201 with)
+  constexpr bool kHold = !kVec;
   __shared__ Ring ring;
   __shared__ Exchange ex;
   ring_init(ring, r, ex);
@@ -135,10 +143,12 @@ __global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads))
         dh_row = static_cast<const T*>(a.d_h) + row * a.ld_d_h;
       }
       float dot = 0.f;
+      P held_dy[kHold ? kC : 1], held_h[kHold ? kC : 1];
 #pragma unroll
       for (int i = 0; i < kC; ++i) {
         const int n = kWhole ? 128 : pl.cols(i, H);
-        P dy, h;
+        P& dy = held_dy[kHold ? i : 0];
+        P& h = held_h[kHold ? i : 0];
         float f[8];
         dy.load(dy_row + pl.at(i), pl.l, n);
         h.load(h_row + pl.at(i), pl.l, n);
@@ -161,10 +171,13 @@ __global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads))
 #pragma unroll
       for (int i = 0; i < kC; ++i) {
         const int n = kWhole ? 128 : pl.cols(i, H);
-        P dy, h;
+        P& dy = held_dy[kHold ? i : 0];
+        P& h = held_h[kHold ? i : 0];
         float f[8];
-        dy.load(dy_row + pl.at(i), pl.l, n);
-        h.load(h_row + pl.at(i), pl.l, n);
+        if (!kHold) {
+          dy.load(dy_row + pl.at(i), pl.l, n);
+          h.load(h_row + pl.at(i), pl.l, n);
+        }
         w.template get<kWhole>(pl, width, i, f);
         float d[8];
 #pragma unroll
@@ -246,7 +259,7 @@ namespace {
 // The gradient's spread: where rows are few, at most a block per SM, since each
 // writes a row of d_w's parts (512 x 4096: 19 us with a block per row).
 Shape backward_shape(int64_t rows, int64_t H, int mats, int size, bool vec) {
-  Shape s = shape_of(rows, H, mats, size, vec);
+  Shape s = shape_of(rows, H, mats, size, vec, kSingles);
   if (!s.stages) s.grid = std::min(s.grid, num_sms());
   return s;
 }

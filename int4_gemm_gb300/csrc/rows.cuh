@@ -315,12 +315,14 @@ inline Shape spread(int blocks, int C, int most_threads) {
   return s;
 }
 
-// Blocks per SM that the ring kernels are compiled for: single elements need few
-// registers and many warps; of aligned rows, whose threads hold 32 elements, three
+// Blocks per SM that the ring kernels are compiled for: single elements need many
+// warps (`singles` blocks); of aligned rows, whose threads hold 32 elements, three
 // blocks would spill (34 us instead of 26 for 4096 x 7168 to INT8).
-__host__ __device__ constexpr int resident_blocks(bool vec, int threads) { return threads > 256 ? 1 : vec ? 2 : 3; }
+__host__ __device__ constexpr int resident_blocks(bool vec, int threads, int singles) {
+  return threads > 256 ? 1 : vec ? 2 : singles;
+}
 
-inline Shape shape_of(int64_t rows, int64_t H, int mats, int size, bool vec) {
+inline Shape shape_of(int64_t rows, int64_t H, int mats, int size, bool vec, int singles) {
   const int blocks = (int)ceil_div(H, 128);
   const int64_t sms = num_sms();
   if (blocks <= (vec ? 128 : 32)) {
@@ -328,7 +330,7 @@ inline Shape shape_of(int64_t rows, int64_t H, int mats, int size, bool vec) {
     const int per_block = s.threads / s.group;
     const uint32_t row_bytes = (uint32_t)(H * size);
     s.stage_bytes = (uint32_t)(mats * per_block) * (vec ? staged_row<true>(row_bytes) : staged_row<false>(row_bytes));
-    int resident = resident_blocks(vec, s.threads);
+    int resident = resident_blocks(vec, s.threads, singles);
     while (resident > 1 && 2 * s.stage_bytes > kRingTotal / resident) --resident;
     s.stages = (int)std::min<int64_t>(kMaxRing, kRingTotal / resident / s.stage_bytes);
     s.grid = (int)std::min<int64_t>(ceil_div(rows, per_block), sms * resident);
