@@ -27,8 +27,9 @@ constexpr int kMaxExperts = 1024;
 constexpr int kCluster = 8;
 constexpr int kFlight = 8;  // loads of a thread on their way at a time: ids, the blocks' parts
 // Loads per lane where there are many logits: fewer lanes share a token and its
-// reductions (65536 x 256 bf16: 25.9 us with one, 20.6 with two, 19.5 with four, the
-// gradient 21.0, 17.7 and 31.8); elsewhere one (16384 x 64 FP32: 8.2, 8.5 and 11.4).
+// reductions (65536 x 256 bf16, before later steps: 25.9 us with one, 20.6 with two, 19.5
+// with four, the gradient 21.0, 17.7 and 31.8; now 18.9 and 15.6 with two); elsewhere
+// one (16384 x 64 FP32: 8.2, 8.5 and 11.4).
 int loads_of(int64_t tokens, int64_t E) { return tokens * E >= (int64_t)1 << 22 ? 2 : 1; }
 
 // 2^x within 2^-22 relative (0 below 2^-126).
@@ -324,9 +325,14 @@ __global__ void __launch_bounds__(kThreads)
   finish(f, reinterpret_cast<uint32_t*>(sum), smem_u32(total), smem_u32(count));
 }
 
-__global__ void __launch_bounds__(1024) balance_finish_kernel(const FinishArgs f) {
+// Threads of its blocks: more where they have parts of many experts to add up (16384 x
+// 64 FP32: 7.3 us with 512 threads, 7.9 with 1024; 8192 x 1024 bf16 19.8 and 18.4;
+// starting it early, to wait beside the first kernel's blocks, changed nothing).
+constexpr int kFinishThreads = 1024;
+int finish_threads(int E) { return E <= 256 ? kFinishThreads / 2 : kFinishThreads; }
+__global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const FinishArgs f) {
   pdl_wait();
-  __shared__ uint32_t scratch[2 * 1024];
+  __shared__ uint32_t scratch[2 * kFinishThreads];
   finish(f, scratch, 0, 0);
 }
 
@@ -473,7 +479,7 @@ q4_status launch_balance(const void* logits, int dtype, int64_t tokens, int E, i
   if (st != Q4_OK || all) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kCluster, 1, 1);
-  cfg.blockDim = dim3(1024, 1, 1);
+  cfg.blockDim = dim3((unsigned)finish_threads(E), 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   cluster_attributes(attr);
