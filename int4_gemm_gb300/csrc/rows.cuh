@@ -128,6 +128,9 @@ __device__ __forceinline__ void load_weights(const void* w, bool w32, int c, int
 struct Exchange {
   __align__(16) float2 part[2][32];
 };
+// Groups of a block that the exchange has room for: up to four warps each take four
+// slots, larger ones all of them; within a warp there is no exchange.
+constexpr int most_groups(int group) { return group <= 32 ? 64 : group <= 128 ? 8 : 1; }
 // Before the first row: parts that no warp writes are zero.
 __device__ __forceinline__ void exchange_init(Exchange& ex) {
   if (threadIdx.x < 64) ex.part[threadIdx.x >> 5][threadIdx.x & 31] = make_float2(0.f, 0.f);
