@@ -6,7 +6,8 @@
 // threads; the blocks' sums go to the workspace and are added in their order by
 // a second kernel, so that results do not depend on timing.
 //
-// HBM-bound where rows are aligned: 16384 x 7168 bf16 with d_h 150.5 us (6.2 TB/s), 8192 x 4096 50.6 us (5.3 TB/s); single elements wait for
+// HBM-bound where rows are aligned: 16384 x 7168 bf16 with d_h 150.5 us (6.2 TB/s),
+// 8192 x 4096 50.6 us (5.3 TB/s); single elements wait for
 // their latencies: 9973 x 1411 bf16 37.9 us (2.2 TB/s).  512 x 4096 11.7 us, 64 x 16384
 // 16.0: latencies of two dependent kernels.
 #include "rows.cuh"
