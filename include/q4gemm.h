@@ -532,7 +532,8 @@ q4_status gemm_w8a8_int8(const int8_t* qa, const float* sa, const int8_t* qb, co
  *   rms_norm_fp8   E4M3 codes [rows, H] of y, one FP32 scale per row and 128
  *                  columns, max(amax, 1e-12) / 448, scales [rows, ceil(H / 128)]:
  *                  the activations of gemm_fp8_blockwise and gemm_w4a8 (where
- *                  H % 128 == 0) and an 8-bit checkpoint for grouped_wgrad_fp8;
+ *                  H % 128 == 0) and an 8-bit checkpoint for grouped_wgrad_fp8
+ *                  (which rounds code * scale to bf16 once);
  *   rms_norm_int8  integers int8 [rows, H], one FP32 scale per row, max(amax,
  *                  1e-12) / 127, scales [rows]: gemm_w8a8_int8's activations.
  * The 8-bit forms write y too where y is not NULL.  h [rows, H] (NULL: not

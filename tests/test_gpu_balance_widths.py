@@ -8,7 +8,8 @@ from oracle import norm as o
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("tokens,E", [(2048, 6), (2049, 6), (5000, 60), (80000, 6)])
+@pytest.mark.parametrize("tokens,E", [(2048, 6), (2049, 6), (5000, 60), (80000, 6), (512, 60), (513, 60), (2048, 64), (2049, 64), (512, 1000), (513, 1000),
+                                      (700, 1024), (512, 256), (513, 264)])
 def test_balance_of_few_unaligned_experts(lib, tokens, E):
     g = torch.Generator("cuda").manual_seed(E)
     logits = torch.randn((tokens, E), device="cuda", generator=g)

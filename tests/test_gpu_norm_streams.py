@@ -113,6 +113,46 @@ def test_graphs(lib):
     assert lib.sync_status() == 0
 
 
+def test_two_graphs_with_one_workspace(lib):
+    """Captured with the same workspace and replayed in turn: a call leaves nothing
+    in it that the next one needs."""
+    g = torch.Generator("cuda").manual_seed(9)
+
+    def normal(*shape):
+        return torch.randn(shape, device="cuda", generator=g)
+    sizes = ((700, 1024), (5000, 512))
+    n = max(lib.lib().q4_workspace_size(lib.OP_RMS_NORM_BACKWARD, r, 0, H) for r, H in sizes)
+    ws = torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")
+    logits = [normal(40000, 64), normal(9000, 256)]
+    ids = [lib.moe_route_topk(t, 4)[0] for t in logits]
+    m = max(lib.lib().q4_workspace_size(lib.OP_MOE_BALANCE_LOSS, *t.shape, 0) for t in logits)
+    assert m
+    ws_balance = torch.full((m,), 0xff, dtype=torch.uint8, device="cuda")
+    calls = []
+    for r, H in sizes:
+        d_y, h, w = normal(r, H), normal(r, H), normal(H)
+        _, _, rstd = lib.rms_norm(h)
+        calls.append(lambda ws, a=(d_y, h, rstd, w): lib.rms_norm_backward(*a, ws=ws))
+    for t, i in zip(logits, ids):
+        calls.append(lambda ws, a=(t, i): lib.moe_balance_loss(*a, ws=ws))
+    want = [[t.clone() for t in call(None)] for call in calls]
+    graphs = []
+    for k, call in enumerate(calls):
+        shared = ws if k < 2 else ws_balance
+        call(shared)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            graphs.append((graph, call(shared)))
+    for order in ((0, 1, 2, 3), (3, 2, 1, 0), (1, 1, 0, 3, 3, 2)):
+        for k in order:
+            for t in graphs[k][1]:
+                t.zero_()
+            graphs[k][0].replay()
+            for t, u in zip(graphs[k][1], want[k]):
+                assert torch.equal(t, u)
+    assert lib.sync_status() == 0
+
+
 def test_two_streams_at_once(lib):
     """The same call on two streams at the same time, with outputs and workspaces of
     their own."""
