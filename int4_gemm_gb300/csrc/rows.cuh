@@ -129,8 +129,8 @@ struct Exchange {
   __align__(16) float2 part[2][32];
 };
 // Groups of a block that the exchange has room for: up to four warps each take four
-// slots, larger ones all of them; within a warp there is no exchange.
-constexpr int most_groups(int group) { return group <= 32 ? 64 : group <= 128 ? 8 : 1; }
+// slots, up to eight eight, larger ones all of them; within a warp there is no exchange.
+constexpr int most_groups(int group) { return group <= 32 ? 64 : group <= 128 ? 8 : group <= 256 ? 4 : 1; }
 // Before the first row: parts that no warp writes are zero.
 __device__ __forceinline__ void exchange_init(Exchange& ex) {
   if (threadIdx.x < 64) ex.part[threadIdx.x >> 5][threadIdx.x & 31] = make_float2(0.f, 0.f);
@@ -148,15 +148,15 @@ __device__ __forceinline__ float2 group_reduce(float sum, float top, int group, 
   }
   if (group > 32) {
     const int lane = threadIdx.x & 31, warps = group >> 5, warp = threadIdx.x >> 5;
-    const bool few = warps <= 4;  // four slots per group, else all for the only one
-    if (lane == 0) ex.part[buf][few ? warp / warps * 4 + warp % warps : warp] = make_float2(sum, top);
+    const int slots = warps <= 4 ? 4 : 8, first = warp / warps * slots;
+    if (lane == 0) ex.part[buf][warps <= 8 ? first + warp % warps : warp] = make_float2(sum, top);
     __syncthreads();
     if (warps <= 8) {  // few enough for every thread to add them up
-      const float4* part = reinterpret_cast<const float4*>(ex.part[buf] + (few ? warp / warps * 4 : warp / warps * warps));
+      const float4* part = reinterpret_cast<const float4*>(ex.part[buf] + first);
       float4 v[4];
       v[0] = part[0], v[1] = part[1];
       v[2] = v[3] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (!few) v[2] = part[2], v[3] = part[3];
+      if (slots == 8) v[2] = part[2], v[3] = part[3];
       sum = ((v[0].x + v[0].z) + (v[1].x + v[1].z)) + ((v[2].x + v[2].z) + (v[3].x + v[3].z));
       if (kTop) top = fmaxf(fmaxf(fmaxf(v[0].y, v[0].w), fmaxf(v[1].y, v[1].w)), fmaxf(fmaxf(v[2].y, v[2].w), fmaxf(v[3].y, v[3].w)));
     } else {
