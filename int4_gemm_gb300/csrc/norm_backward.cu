@@ -8,7 +8,7 @@
 //
 // HBM-bound where rows are aligned: 16384 x 7168 bf16 with d_h 150.5 us (6.2 TB/s),
 // 8192 x 4096 50.6 us (5.3 TB/s); single elements wait for
-// their latencies: 9973 x 1411 bf16 37.9 us (2.2 TB/s).  512 x 4096 11.7 us, 64 x 16384
+// their latencies: 9973 x 1411 bf16 36.8 us (2.3 TB/s).  512 x 4096 11.6 us, 64 x 16384
 // 16.0: latencies of two dependent kernels.
 #include "rows.cuh"
 
@@ -122,15 +122,10 @@ __global__ void __launch_bounds__(max_threads(kC))
   store_partial<kVec, kC>(a, pl, acc, scratch);
 }
 
-// Blocks per SM for single elements, which keep their rows in registers (9973 x 1411
-// bf16, before the groups' sums met in shared memory, 42.3 us; three blocks, for which registers are too few, 58.7, or 46.2 with two
-// reads from shared memory; one block 67.5).
-constexpr int kSingles = 2;
-
 // The same with the rows in shared memory, which aligned ones are read from twice;
 // a stage is refilled after the next row's exchange, when every thread has left it.
 template <typename T, bool kVec, int kC, int kThreads>
-__global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads, kSingles))
+__global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads, true))
     norm_backward_ring_kernel(const NormBackwardArgs a, int group, const RingArgs r) {
   extern __shared__ __align__(128) uint8_t stage_smem[];
   using P = Piece<T, kVec>;
@@ -293,7 +288,7 @@ namespace {
 // writes a row of d_w's parts (512 x 4096: 19 us with a block per row), and as many
 // rows at a time in it (11.7 us, one after another 17.0).
 Shape backward_shape(int64_t rows, int64_t H, int mats, int size, bool vec) {
-  Shape s = shape_of(rows, H, mats, size, vec, kSingles);
+  Shape s = shape_of(rows, H, mats, size, vec, true);
   if (s.stages) return s;
   const int64_t most = std::min(max_threads(s.C) / s.group, most_groups(s.group));
   const int64_t side = std::min<int64_t>(ceil_div(rows, num_sms()), most);

@@ -319,13 +319,20 @@ inline Shape spread(int blocks, int C, int most_threads) {
 }
 
 // Blocks per SM that the ring kernels are compiled for: single elements need many
-// warps (`singles` blocks); of aligned rows, whose threads hold 32 elements, three
-// blocks would spill (34 us instead of 26 for 4096 x 7168 to INT8).
-__host__ __device__ constexpr int resident_blocks(bool vec, int threads, int singles) {
-  return threads > 256 ? 1 : vec ? 2 : singles;
+// warps (the norm; the gradient keeps its rows in registers instead: 9973 x 1411 bf16,
+// at the time, 42.3 us with two blocks, 58.7 with three, 46.2 with three that read
+// their rows twice, 67.5 with one); of aligned rows, whose threads hold 32 elements,
+// three blocks would spill (34 us instead of 26 for 4096 x 7168 to INT8).
+__host__ __device__ constexpr int resident_blocks(bool vec, int threads, bool gradient) {
+  return threads > 256 ? 1 : vec || gradient ? 2 : 3;
 }
 
-inline Shape shape_of(int64_t rows, int64_t H, int mats, int size, bool vec, int singles) {
+// Rows go through the ring where its blocks have a turn each, aligned ones of the norm
+// where every other block has (bf16, ring and straight: norm 256 x 8192 6.1 and 7.1 us,
+// 600 x 8192 10.1 and 14.2, 1000 x 4096 7.5 and 12.1, but of one turn in four 256 x 4096
+// 4.0 and 3.4; single elements 500 x 2047 4.8 and 4.1, 1500 x 2047 10.0 and 10.8;
+// gradient 700 x 4096 13.8 and 15.7, 2000 x 2048 12.0 and 15.6, 400 x 4096 12.9 and 11.0).
+inline Shape shape_of(int64_t rows, int64_t H, int mats, int size, bool vec, bool gradient) {
   const int blocks = (int)ceil_div(H, 128);
   const int64_t sms = num_sms();
   if (blocks <= (vec ? 128 : 32)) {
@@ -333,11 +340,11 @@ inline Shape shape_of(int64_t rows, int64_t H, int mats, int size, bool vec, int
     const int per_block = s.threads / s.group;
     const uint32_t row_bytes = (uint32_t)(H * size);
     s.stage_bytes = (uint32_t)(mats * per_block) * (vec ? staged_row<true>(row_bytes) : staged_row<false>(row_bytes));
-    int resident = resident_blocks(vec, s.threads, singles);
+    int resident = resident_blocks(vec, s.threads, gradient);
     while (resident > 1 && 2 * s.stage_bytes > kRingTotal / resident) --resident;
     s.stages = (int)std::min<int64_t>(kMaxRing, kRingTotal / resident / s.stage_bytes);
     s.grid = (int)std::min<int64_t>(ceil_div(rows, per_block), sms * resident);
-    if (s.stages >= 2 && ceil_div(rows, per_block) >= 2 * sms * resident) return s;
+    if (s.stages >= 2 && ceil_div(rows, per_block) * (vec && !gradient ? 2 : 1) >= sms * resident) return s;
   }
   int C = 1;
   const int most = rows <= 2 * sms ? 64 : 16;  // blocks of 128 columns that one piece per thread takes
