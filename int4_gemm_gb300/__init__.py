@@ -867,26 +867,34 @@ def rms_norm_backward(d_y: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, we
     gradient that reaches h by other ways, is added to it, and ``out`` may be
     d_h itself.  ``ws`` from ``workspace(OP_RMS_NORM_BACKWARD, rows, 0, H, device)``."""
     ldy, ldh = _pitched(d_y, "d_y"), _pitched(h, "h")
-    (rows, H), dev = d_y.shape, d_y.device
-    ldd = 0
-    for name, t in (("h", h), ("d_h", d_h)):
-        if t is not None and (t.shape != d_y.shape or t.dtype != d_y.dtype or t.device != dev):
-            raise ValueError(f"{name} must be a {d_y.dtype} tensor of shape ({rows}, {H}) on {dev}")
+    shape, dtype, dev = d_y.shape, d_y.dtype, d_y.device
+    rows, H = shape
+    if h.shape != shape or h.dtype != dtype or h.device != dev:
+        raise ValueError(f"h must be a {dtype} tensor of shape ({rows}, {H}) on {dev}")
+    ldd, joined = 0, None
     if d_h is not None:
-        ldd = _pitched(d_h, "d_h")
+        if d_h.shape != shape or d_h.dtype != dtype or d_h.device != dev:
+            raise ValueError(f"d_h must be a {dtype} tensor of shape ({rows}, {H}) on {dev}")
+        ldd, joined = _pitched(d_h, "d_h"), d_h.data_ptr()
     _exact(rstd, "rstd", (rows,), torch.float32, dev)
     wd = _norm_weight(weight, d_y)
-    d_x = _out(out, rows, H, d_y.dtype, dev, stream)
-    dw = _new(H, torch.float32, dev, stream) if need_d_weight else None
-    L = lib()
-    if ws is None:
-        n = L.q4_workspace_size(OP_RMS_NORM_BACKWARD, rows, 0, H) if need_d_weight else 0
-        ws = _empty(n, dev, stream) if n else None
-    else:
-        _given(ws, stream)
-    _check("rms_norm_backward", L.rms_norm_backward(
-        d_y.data_ptr(), _DTYPE[d_y.dtype], rows, H, ldy, h.data_ptr(), ldh, rstd.data_ptr(), _ptr(weight), wd, _ptr(d_h), ldd,
-        d_x.data_ptr(), _ptr(dw), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+    new, L = _maker(stream), _lib or load()
+    d_x = new(shape, dtype=dtype, device=dev) if out is None else _out(out, rows, H, dtype, dev, stream)
+    dw, n = None, 0
+    if need_d_weight:
+        dw = new(H, dtype=torch.float32, device=dev)
+        if ws is None:
+            n = L.q4_workspace_size(OP_RMS_NORM_BACKWARD, rows, 0, H)
+            if n:
+                ws = _empty(n, dev, stream)
+    if ws is not None and not n:
+        n = _given(ws, stream).numel()
+    status = L.rms_norm_backward(
+        d_y.data_ptr(), _DTYPE[dtype], rows, H, ldy, h.data_ptr(), ldh, rstd.data_ptr(),
+        None if weight is None else weight.data_ptr(), wd, joined, ldd, d_x.data_ptr(), None if dw is None else dw.data_ptr(),
+        None if ws is None else ws.data_ptr(), n, _stream(stream))
+    if status:
+        _check("rms_norm_backward", status)
     return d_x, dw
 
 

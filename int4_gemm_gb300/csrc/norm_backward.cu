@@ -298,14 +298,10 @@ Shape backward_shape(int64_t rows, int64_t H, int mats, int size, bool vec) {
 }
 }  // namespace
 
-// Room for the largest grid that these sizes can have.
+// Room for the largest grid: at most two blocks per SM, a row or more each.
 size_t norm_backward_workspace_bytes(int64_t rows, int64_t H) {
   if (rows == 0 || H == 0) return 0;
-  int grid = 0;
-  for (int mats : {2, 3})
-    for (int size : {2, 4})
-      for (bool vec : {false, true}) grid = std::max(grid, backward_shape(rows, H, mats, size, vec).grid);
-  return (size_t)grid * (size_t)H * sizeof(float);
+  return (size_t)std::min<int64_t>(rows, 2 * num_sms()) * (size_t)H * sizeof(float);
 }
 
 q4_status launch_norm_backward(NormBackwardArgs a, int dtype, float* d_weight, void* ws, cudaStream_t stream) {
