@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads, fals
           a, pl, row, H, inv_H, v, ex, buf, r.ctl.status, weights,
           [&] {  // every thread has read the stage: the next rows may come
             if (pl.group <= 32) __syncthreads();
-            if (threadIdx.x == 0)
+            if (threadIdx.x == 0 && ring_over(ring, stage, phase))
               ring_fill<kVec>(ring, r, smem_u32(stage_smem), stage, mat, pitch, base + r.stages * step, a.rows, pl.per_block);
           });
       if (++stage == r.stages) stage = 0, phase ^= 1;
@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads, fals
   } else {
     rows(std::false_type());
   }
+  ring_end(ring, r);
 }
 
 template <typename T, bool kVec, int kC, int kForm, int kThreads>

@@ -191,7 +191,9 @@ __global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads, true
       if (pl.group <= 32) __syncthreads();
       if (threadIdx.x == 0 && base != base0) {  // every thread has left the stage of the row before
         const int64_t next = base + (r.stages - 1) * step;
-        ring_fill<kVec>(ring, r, smem_u32(stage_smem), stage ? stage - 1 : r.stages - 1, mat, pitch, next, a.rows, pl.per_block);
+        const int left = stage ? stage - 1 : r.stages - 1;
+        if (ring_over(ring, left, stage ? phase : phase ^ 1))
+          ring_fill<kVec>(ring, r, smem_u32(stage_smem), left, mat, pitch, next, a.rows, pl.per_block);
       }
       const float c = h_factor(rstd, q.x * inv_H);
       T* out = static_cast<T*>(a.d_x) + row * a.H;
@@ -228,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads, true
   } else {
     rows(std::false_type());
   }
+  ring_end(ring, r);
   store_partial<kVec, kC>(a, pl, acc, reinterpret_cast<float*>(stage_smem));
 }
 

@@ -262,6 +262,21 @@ __device__ __forceinline__ void ring_fill(Ring& ring, const RingArgs& r, uint32_
   }
 }
 
+// Whether a stage's phase is over, so that it may be filled again (it is not where a
+// wait ran out).
+__device__ __forceinline__ bool ring_over(Ring& ring, int stage, uint32_t phase) {
+  return mbar_try_wait(smem_u32(&ring.full[stage]), phase);
+}
+// After the last row: where a wait ran out, the block stays for as long again, so that
+// copies still on their way end before its memory is another's.
+__device__ __forceinline__ void ring_end(Ring& ring, const RingArgs& r) {
+  if (threadIdx.x == 0 && *static_cast<volatile int*>(&ring.abort)) {
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 <= r.ctl.wait_ns) {
+    }
+  }
+}
+
 // A row of a matrix in its stage.
 template <bool kVec, typename T>
 __device__ __forceinline__ const T* ring_row(const uint8_t* stage, const RingArgs& r, int m, const Place& pl, const void* mat,
