@@ -375,6 +375,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
+// The same where the arrival hands over what lies in this CTA's shared memory (a
+// relay: what it has acquired from this CTA's barrier goes along), for a wait with
+// cluster-scope acquire.  The release is a fence at cluster scope for shared memory
+// alone; an arrival that releases at cluster scope waits for global memory, too.
+__device__ __forceinline__ void mbar_arrive_cluster_smem(uint32_t cluster_addr) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+      : "memory");
+}
 
 // 32 lanes x 4 columns of 32 bits from registers into TMEM (the warp's lane quarter)
 __device__ __forceinline__ void tmem_st_32x32b_x4(uint32_t taddr, const uint4& v) {

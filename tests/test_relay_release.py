@@ -1,0 +1,32 @@
+"""CTA pairs: what the odd CTA's relay hands to the even CTA lies in shared memory,
+so its arrival releases at cluster scope.  No run shows the difference (the memory
+model asks for it, the hardware may order the stores anyway), so the source is read."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "int4_gemm_gb300", "csrc")
+
+
+def _source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return f.read()
+
+
+def _releases_at_cluster_scope(helper):
+    """The arrival's own release, or one of shared memory by a fence in front of it."""
+    body = re.search(r"void %s\(uint32_t \w+\) \{(.*?)\n\}" % helper, _source("common.cuh"), re.S).group(1)
+    fence = body.find("fence.release.sync_restrict::shared::cta.cluster;")
+    arrive = re.search(r"mbarrier\.arrive\.(\w+)\.cluster\.shared::cluster", body)
+    return bool(arrive) and (arrive.group(1) == "release" or 0 <= fence < arrive.start())
+
+
+@pytest.mark.parametrize("name", ["int8.cu"])
+def test_relay_releases_at_cluster_scope(name):
+    parts = _source(name).split("relay (odd CTA)\n")
+    assert len(parts) == 2
+    relay = parts[1][:parts[1].index("// ----")]
+    arrivals = re.findall(r"\b(mbar_arrive\w*)\(", relay)
+    assert len(arrivals) == 1
+    assert _releases_at_cluster_scope(arrivals[0])
