@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
             alive = false;
             break;
           }
-          mbar_arrive_cluster(leader_pair_full + stage * 8);
+          mbar_arrive_cluster_smem(leader_pair_full + stage * 8);
           if (++stage == kPStages) stage = 0, phase ^= 1;
         }
       }

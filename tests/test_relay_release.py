@@ -22,7 +22,7 @@ def _releases_at_cluster_scope(helper):
     return bool(arrive) and (arrive.group(1) == "release" or 0 <= fence < arrive.start())
 
 
-@pytest.mark.parametrize("name", ["int8.cu", "w4a8.cu"])
+@pytest.mark.parametrize("name", ["int8.cu", "w4a8.cu", "fp8.cu"])
 def test_relay_releases_at_cluster_scope(name):
     parts = _source(name).split("relay (odd CTA)\n")
     assert len(parts) == 2
