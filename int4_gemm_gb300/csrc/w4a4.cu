@@ -366,6 +366,11 @@ __global__ void __launch_bounds__(block_threads<GROUPED>(), 1)
     if constexpr (P2) mbar_arrive_cluster(mapa_shared(smem_u32(bar), 0));
     else mbar_arrive(smem_u32(bar));
   };
+  // the same where the stage's codes in this CTA's shared memory go along
+  auto hand_to_leader = [&](uint64_t* bar) {
+    if constexpr (P2) mbar_arrive_cluster_smem(mapa_shared(smem_u32(bar), 0));
+    else mbar_arrive(smem_u32(bar));
+  };
   auto tile_at = [&](int t) -> TileInfo {
     if constexpr (GROUPED) return grouped_tile(p, s_sched, t);
     else return dense_tile<TM>(p, t, crank);
@@ -528,7 +533,7 @@ __global__ void __launch_bounds__(block_threads<GROUPED>(), 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader(&sm->sf_full[stage]);
+        if (lane == 0) hand_to_leader(&sm->sf_full[stage]);
         if (++stage == kStages) stage = 0, phase ^= 1;
       }
     }
