@@ -36,7 +36,7 @@ def test_scale_writers_hand_the_stage_over_at_cluster_scope():
     """The FP4 product has no relay: its scale writers tell the even CTA that the odd
     one's stage, codes in shared memory among it, is there."""
     source = _source("w4a4.cu")
-    handing = re.findall(r"(\w+)\(&sm->sf_full\[stage\]\)", source)
+    handing = re.findall(r"if \(lane == 0\) (\w+)\(&sm->sf_full\[stage\]\)", source)
     assert len(handing) == 1
     helper = re.search(r"auto %s = \[&\]\(uint64_t\* bar\) \{\s*if constexpr \(P2\) (\w+)\(" % handing[0], source).group(1)
     assert _releases_at_cluster_scope(helper)
