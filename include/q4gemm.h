@@ -539,7 +539,8 @@ q4_status gemm_w8a8_int8(const int8_t* qa, const float* sa, const int8_t* qb, co
  * The 8-bit forms write y too where y is not NULL.  h [rows, H] (NULL: not
  * written) may be residual itself (the same address, ld_residual = H); rstd
  * [rows] FP32 (NULL: not written) is what the gradient needs.  A row whose
- * input, sum of squares or scale is not finite latches Q4_ERR_NONFINITE.
+ * input, sum of squares or scale is not finite latches Q4_ERR_NONFINITE; a NaN in
+ * h * weight makes its 8-bit scale NaN.
  *
  * rms_norm_backward: from d_y [rows, H] (the gradient of y), h and rstd, with
  * g = d_y * weight,

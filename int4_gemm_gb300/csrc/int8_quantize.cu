@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(max_threads(kC))
     else
       top = __uint_as_float(bits);
     const float2 r = group_reduce<true>(nonfinite(top) ? 1.f : 0.f, top, group, ex, buf);
-    const float s = fmaxf(r.y, 1e-12f) * (1.f / 127.f);
+    const float s = max_nan(r.y, 1e-12f) * (1.f / 127.f);
     if (pl.t == 0 && H) {
       scales[row] = s;
       if (r.x != 0.f) latch_status(status, Q4_ERR_NONFINITE);
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kLongThreads)
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
   __syncthreads();
   for (int w = 0; w < kLongThreads / 32; ++w) top = max(top, part[w]);
-  const float s = fmaxf(__uint_as_float(top), 1e-12f) * (1.f / 127.f);
+  const float s = max_nan(__uint_as_float(top), 1e-12f) * (1.f / 127.f);
   if (threadIdx.x == 0) {
     scales[blockIdx.x] = s;
     if (nonfinite(__uint_as_float(top))) latch_status(status, Q4_ERR_NONFINITE);

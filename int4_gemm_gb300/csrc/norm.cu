@@ -54,7 +54,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const Place& pl, int
     for (int j = 0; j < 8; ++j) {
       sum = fmaf(v[i][j], v[i][j], sum);
       v[i][j] *= w[j];
-      if (kForm == Q4_NORM_INT8) top = fmaxf(top, fabsf(v[i][j]));
+      if (kForm == Q4_NORM_INT8) top = max_nan(top, fabsf(v[i][j]));
     }
   }
   const float2 r = group_reduce<kForm == Q4_NORM_INT8>(sum, top, pl.group, ex, buf);
@@ -67,7 +67,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const Place& pl, int
   if constexpr (kForm == Q4_NORM_INT8) {
     // the codes are rint(h w f); where the scale is not the least one, f = rstd / s =
     // 127 / amax |h w| needs neither rstd nor s and their roundings
-    const float s = fmaxf(r.y * rstd, 1e-12f) * (1.f / 127.f);
+    const float s = max_nan(r.y * rstd, 1e-12f) * (1.f / 127.f);
     const float f = r.y * rstd > 1e-12f ? __fdiv_rn(127.f, r.y) : __fdiv_rn(rstd, s);
     if (pl.t == 0 && H) {
       a.scales[row] = s;
@@ -84,10 +84,10 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, const Place& pl, int
     for (int i = 0; i < kC; ++i) {
       float m = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[i][j]));
+      for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[i][j]));
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float s = fmaxf(m * rstd, 1e-12f) * (1.f / 448.f);
+      for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float s = max_nan(m * rstd, 1e-12f) * (1.f / 448.f);
       // 448 / m, as 7 / (m / 64): __fdividef gives 0 for divisors above 2^126
       const float f = m * rstd > 1e-12f ? __fdividef(7.f, m * 0x1p-6f) : __fdividef(rstd, s);
       P::store_codes(codes + pl.at(i), pl.l, cols(i), e4m3x8(v[i], f));

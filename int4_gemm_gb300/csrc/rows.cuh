@@ -121,6 +121,14 @@ __device__ __forceinline__ void load_weights(const void* w, bool w32, int c, int
   }
 }
 
+// The larger of two, and NaN where one of them is (fmaxf drops it): a NaN among a
+// row's values reaches its scale.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // (sum, largest) over the `group` threads that hold a row, in every one of them.
 // Groups of more than a warp are whole warps of a block that comes here together;
 // buf alternates between two buffers from row to row, so that one barrier per row
@@ -139,12 +147,12 @@ template <bool kTop>
 __device__ __forceinline__ float2 group_reduce(float sum, float top, int group, Exchange& ex, int buf) {
   if (group >= 32) {
     sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-    if (kTop) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+    if (kTop) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 16));
   }
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) {
     sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (kTop) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (kTop) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
   }
   if (group > 32) {
     const int lane = threadIdx.x & 31, warps = group >> 5, warp = threadIdx.x >> 5;
@@ -158,14 +166,14 @@ __device__ __forceinline__ float2 group_reduce(float sum, float top, int group, 
       v[2] = v[3] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (slots == 8) v[2] = part[2], v[3] = part[3];
       sum = ((v[0].x + v[0].z) + (v[1].x + v[1].z)) + ((v[2].x + v[2].z) + (v[3].x + v[3].z));
-      if (kTop) top = fmaxf(fmaxf(fmaxf(v[0].y, v[0].w), fmaxf(v[1].y, v[1].w)), fmaxf(fmaxf(v[2].y, v[2].w), fmaxf(v[3].y, v[3].w)));
+      if (kTop) top = max_nan(max_nan(max_nan(v[0].y, v[0].w), max_nan(v[1].y, v[1].w)), max_nan(max_nan(v[2].y, v[2].w), max_nan(v[3].y, v[3].w)));
     } else {
       const float2 v = ex.part[buf][lane];
       sum = v.x, top = v.y;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (kTop) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (kTop) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
       }
     }
   }
