@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads, fals
       const int H = kWhole || row < a.rows ? width : 0;
       mbar_wait(smem_u32(&ring.full[stage]), phase, r.ctl, &ring.abort);
       float v[kC][8];
-      if (!kVec && row == a.rows - 1) {
+      if (!kVec && read_in_place(row, a.rows, r.edge)) {
         load_row<T, kVec, kC, kWhole>(static_cast<const T*>(a.x) + row * a.ldx,
                                       static_cast<const T*>(a.residual) + row * a.ld_residual, a.residual != nullptr, pl, H, v);
       } else {
@@ -220,7 +220,7 @@ q4_status launch_norm_ring(const NormArgs& a, const Shape& s, cudaStream_t strea
   const q4_status st = allow_smem(kernel, ready);
   if (st != Q4_OK) return st;
   return launch_pdl(kernel, s.grid, s.threads, (size_t)s.stages * s.stage_bytes, stream, a, s.group,
-                    ring_of(s, a.H * (int64_t)sizeof(T)));
+                    ring_of(s, kVec, a.H * (int64_t)sizeof(T)));
 }
 
 template <typename T, int kC, int kForm>

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads, true
       const T* dy_row = ring_row<kVec, T>(st, r, 0, pl, a.d_y, pitch[0], row);
       const T* h_row = ring_row<kVec, T>(st, r, 1, pl, a.h, pitch[1], row);
       const T* dh_row = ring_row<kVec, T>(st, r, 2, pl, a.d_h, pitch[2], row);
-      if (!kVec && row == a.rows - 1) {  // in place
+      if (!kVec && read_in_place(row, a.rows, r.edge)) {
         dy_row = static_cast<const T*>(a.d_y) + row * a.ld_d_y;
         h_row = static_cast<const T*>(a.h) + row * a.ld_h;
         dh_row = static_cast<const T*>(a.d_h) + row * a.ld_d_h;
@@ -266,7 +266,7 @@ q4_status launch_norm_backward_ring(const NormBackwardArgs& a, const Shape& s, c
   if (st != Q4_OK) return st;
   const uint32_t scratch = s.threads > s.group ? 32 * (uint32_t)s.threads : 0;
   return launch_pdl(kernel, s.grid, s.threads, std::max(s.stages * s.stage_bytes, scratch), stream, a, s.group,
-                    ring_of(s, a.H * (int64_t)sizeof(T)));
+                    ring_of(s, kVec, a.H * (int64_t)sizeof(T)));
 }
 
 template <typename T, int kC>

@@ -9,6 +9,7 @@
 #include "common.cuh"
 #include "elem.cuh"
 #include "internal.h"
+#include "ring_rows.h"
 
 namespace q4 {
 namespace {
@@ -207,7 +208,7 @@ struct Ring {
   int abort;
 };
 struct RingArgs {
-  int stages;
+  int stages, edge;  // edge: rows at either end that are read in place
   uint32_t stage_bytes, row_bytes;
   KernelCtl ctl;
 };
@@ -222,23 +223,22 @@ __device__ __forceinline__ void ring_init(Ring& ring, const RingArgs& r, Exchang
   __syncthreads();
 }
 
-// Bytes of a row in a stage.  Rows that do not lie on 16-byte boundaries (kVec
-// false) are copied with the whole 16-byte words that hold their ends.
+// Bytes of a row in a stage.
 template <bool kVec>
 __host__ __device__ constexpr uint32_t staged_row(uint32_t row_bytes) {
-  return kVec ? row_bytes : (row_bytes + 30) / 16 * 16;
+  return kVec ? row_bytes : window_bytes(row_bytes);
 }
 
-// One thread: rows base .. of the matrices into stage s.  The last row of all is
-// left out where its copy would reach behind it (kVec false); it is read in place.
+// One thread: rows base .. of the matrices into stage s, but for those that are read
+// in place.
 template <bool kVec, int kMats>
 __device__ __forceinline__ void ring_fill(Ring& ring, const RingArgs& r, uint32_t smem, int s, const void* const (&mat)[kMats],
                                           const int64_t (&pitch)[kMats], int64_t base, int64_t rows, int per_block) {
   if (base >= rows) return;
-  const int n = (int)min((int64_t)per_block, (kVec ? rows : rows - 1) - base);
   const uint32_t bar = smem_u32(&ring.full[s]), staged = staged_row<kVec>(r.row_bytes);
   const uint32_t dst = smem + s * r.stage_bytes;
   if constexpr (kVec) {
+    const int n = (int)min((int64_t)per_block, rows - base);
     int mats = 0;
     for (int m = 0; m < kMats; ++m) mats += mat[m] != nullptr;
     mbar_arrive_expect_tx(bar, (uint32_t)(mats * n) * staged);
@@ -252,18 +252,21 @@ __device__ __forceinline__ void ring_fill(Ring& ring, const RingArgs& r, uint32_
         for (int i = 0; i < n; ++i) bulk_load(to + i * staged, src + i * pitch[m], staged, bar);
     }
   } else {
+    const CopiedRows c = copied_rows(base, per_block, rows, r.edge);
+    const int n = c.end - c.begin;
+    const uint32_t first = dst + (uint32_t)c.begin * staged;
+    base += c.begin;
     uint32_t bytes = 0;
     for (int turn = 0; turn < 2; ++turn) {  // the bytes first, then the copies
       if (turn) mbar_arrive_expect_tx(bar, bytes);
       for (int m = 0; m < kMats; ++m) {
         if (!mat[m]) continue;
         for (int i = 0; i < n; ++i) {
-          const uintptr_t at = reinterpret_cast<uintptr_t>(mat[m]) + (base + i) * pitch[m], begin = at & ~uintptr_t(15);
-          const uint32_t size = (uint32_t)(((at + r.row_bytes + 15) & ~uintptr_t(15)) - begin);
+          const Window w = window_of(reinterpret_cast<uintptr_t>(mat[m]) + (base + i) * pitch[m], r.row_bytes);
           if (turn)
-            bulk_load(dst + (uint32_t)(m * per_block + i) * staged, reinterpret_cast<const void*>(begin), size, bar);
+            bulk_load(first + (uint32_t)(m * per_block + i) * staged, reinterpret_cast<const void*>(w.begin), w.size, bar);
           else
-            bytes += size;
+            bytes += w.size;
         }
       }
     }
@@ -397,8 +400,9 @@ q4_status allow_smem(Kernel kernel, int (&ready)[64]) {
   return Q4_OK;
 }
 
-RingArgs ring_of(const Shape& s, int64_t row_bytes) {
-  return RingArgs{s.stages, s.stage_bytes, (uint32_t)row_bytes, KernelCtl{device_status_ptr(), wait_budget_ns()}};
+RingArgs ring_of(const Shape& s, bool vec, int64_t row_bytes) {
+  return RingArgs{s.stages, vec ? 0 : edge_rows((uint32_t)row_bytes), s.stage_bytes, (uint32_t)row_bytes,
+                  KernelCtl{device_status_ptr(), wait_budget_ns()}};
 }
 
 }  // namespace
