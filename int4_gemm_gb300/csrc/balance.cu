@@ -129,6 +129,9 @@ struct Lanes {
     inv = there ? __fdividef(1.f, total) : 0.f;
     return there;
   }
+  // exp(-d), d = top - x, as 2^(-d log2 e): the difference, the constant (2^-26 off) and
+  // the product put the exponent off by 2.25 * 2^-24 of itself, which is that times d
+  // relative to the result, and the instruction 2^-22 more: 2^-18 at d = 25.
   __device__ __forceinline__ float exponentials(float (&p)[n], float top) const {
     constexpr float kLog2e = 1.4426950408889634f;
     if (top == -INFINITY) top = 0.f;  // the exponentials are zero then
