@@ -7,11 +7,12 @@ allocated here, on the caller's side of the ABI) and streams.  There is no
 fallback: if ``libq4gemm.so`` is missing or a call fails, an exception is
 raised.
 
-A call runs on the current stream, or on ``stream``, whose memory its own outputs
-and workspaces then are: work that is pending elsewhere does not touch them, and
-the current stream may read them (after waiting for ``stream``) and let them go.
-Ordering ``stream`` with the inputs, and with an ``out`` or ``ws`` that is given,
-is the caller's part, as under ``torch.cuda.stream``.
+A call runs on the current device, where its tensors are, and on the current
+stream, or on ``stream``, whose memory its own outputs and workspaces then are: work
+that is pending elsewhere does not touch them, and the current stream may read them
+(after waiting for ``stream``) and let them go.  Ordering ``stream`` with the inputs,
+and with an ``out`` or ``ws`` that is given, is the caller's part, as under
+``torch.cuda.stream``.
 """
 from __future__ import annotations
 
@@ -502,11 +503,18 @@ def grouped_gemm_moe(tokens: torch.Tensor, expert_offsets: torch.Tensor, row_tok
 
 # --------------------------------------------------------------------------- routed experts
 
+def _here(x: torch.Tensor, name: str):
+    """Kernels run on the current device: a tensor of another one is refused."""
+    if x.get_device() != _device():
+        raise ValueError(f"{name} is on {x.device}, not on the current device (torch.cuda.device)")
+
+
 def _pitched(x: torch.Tensor, name: str) -> int:
     """The row pitch (at least the width) of a 2-D CUDA matrix whose rows are
     contiguous and do not overlap."""
     if not x.is_cuda or x.dtype not in _DTYPE or x.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor of float32, bfloat16 or float16")
+    _here(x, name)
     (rows, cols), (pitch, step) = x.shape, x.stride()
     if cols > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
@@ -774,6 +782,7 @@ def gemm_w8a8_int8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: tor
     rms_norm_int8).  K % 16 == 0, K < 131072; out float32 or bfloat16."""
     if qa.dim() != 2 or qb.dim() != 2 or not qa.is_cuda:
         raise ValueError("qa and qb must be 2-D CUDA tensors")
+    _here(qa, "qa")
     (M, K), N, dev = qa.shape, qb.shape[0], qa.device
     _exact(qa, "qa", (M, K), torch.int8, dev)
     _exact(qb, "qb", (N, K), torch.int8, dev)
