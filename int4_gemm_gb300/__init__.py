@@ -189,6 +189,13 @@ def _given(t: torch.Tensor, stream) -> torch.Tensor:
     return t
 
 
+def _given_ws(ws: torch.Tensor, device, stream) -> int:
+    """The caller's workspace, checked: its bytes."""
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {device}")
+    return _given(ws, stream).numel() * ws.element_size()
+
+
 def _out(out: Optional[torch.Tensor], M: int, N: int, dtype: torch.dtype, device, stream=None) -> torch.Tensor:
     """A new [M, N] output, or the caller's, checked against the call."""
     if out is None:
@@ -596,10 +603,10 @@ def moe_sort_tokens(ids: torch.Tensor, E: int, ws: Optional[torch.Tensor] = None
         n = L.q4_workspace_size(OP_MOE_SORT, T * k, E, 0)
         ws = _empty(n, dev, stream) if n else None
     else:
-        _given(ws, stream)
+        _given_ws(ws, dev, stream)
     _check("moe_sort_tokens", L.moe_sort_tokens(
         ids.data_ptr(), T, k, E, offsets.data_ptr(), row_token.data_ptr(), slot_row.data_ptr(),
-        _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+        _ptr(ws), 0 if ws is None else ws.nbytes, _stream(stream)))
     return offsets, row_token, slot_row
 
 
@@ -753,11 +760,11 @@ def grouped_wgrad_fp8(d_y: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
     if ws is None:
         ws = wgrad_workspace(R, N, K, E, dev, stream)
     else:
-        _given(ws, stream)
+        _given_ws(ws, dev, stream)
     _check("grouped_wgrad_fp8", lib().grouped_wgrad_fp8(
         d_y.data_ptr(), R, N, ldy, codes.data_ptr(), scales.data_ptr(), T, K, _ptr(row_token),
         expert_offsets.data_ptr(), E, out.data_ptr(), _DTYPE[out.dtype], int(accumulate),
-        ws.data_ptr(), ws.numel(), _stream(stream)))
+        ws.data_ptr(), ws.nbytes, _stream(stream)))
     return out
 
 
@@ -897,7 +904,7 @@ def rms_norm_backward(d_y: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, we
             if n:
                 ws = _empty(n, dev, stream)
     if ws is not None and not n:
-        n = _given(ws, stream).numel()
+        n = _given_ws(ws, dev, stream)
     status = L.rms_norm_backward(
         d_y.data_ptr(), _DTYPE[dtype], rows, H, ldy, h.data_ptr(), ldh, rstd.data_ptr(),
         None if weight is None else weight.data_ptr(), wd, joined, ldd, d_x.data_ptr(), None if dw is None else dw.data_ptr(),
@@ -932,7 +939,7 @@ def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, coeff: float = 1.0
         if n:
             ws = _empty(n, dev, stream)
     else:
-        n = _given(ws, stream).numel()
+        n = _given_ws(ws, dev, stream)
     status = L.moe_balance_loss(
         logits.data_ptr(), _DTYPE[logits.dtype], T, E, ld, ids.data_ptr(), k, coeff, loss.data_ptr(), counts.data_ptr(),
         mean.data_ptr(), None if ws is None else ws.data_ptr(), n, _stream(stream))
