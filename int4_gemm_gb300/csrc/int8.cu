@@ -32,6 +32,7 @@
 // 8192 x 8192 17.6 us (3.8 TB/s: 9.9 us of reading at the copy rate, the rest start, join
 // and stores).
 #include <algorithm>
+#include <atomic>
 #include <cstddef>
 
 #include "common.cuh"
@@ -671,7 +672,9 @@ q4_status launch_plan(const Plan& s, const int8_t* qa, const int8_t* qb, const P
   if ((st = make_tmap_2d_u8(&tt, qa, p.K, p.M, p.K, kStageK, T::box, true)) != Q4_OK) return st;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return Q4_ERR_CUDA;
-  static int max_pairs[64] = {0}, ready[64] = {0};
+  // CTAs that are resident at once (single CTAs: one per SM), 0 before the device's
+  // first call; written once all is set up, since calls come from several threads
+  static std::atomic<int> resident[64];
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(T::threads, 1, 1);
   cfg.dynamicSmemBytes = kSmemTotal;
@@ -685,18 +688,20 @@ q4_status launch_plan(const Plan& s, const int8_t* qa, const int8_t* qb, const P
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (!ready[dev]) {
+  int ctas = resident[dev].load(std::memory_order_acquire);
+  if (!ctas) {
     Q4_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTotal));
+    ctas = num_sms();
     if (kPair) {  // persistent: as many pairs as are resident at once
       int n = 0;
-      cfg.gridDim = dim3((unsigned)(num_sms() / 2 * 2), 1, 1);
-      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) n = num_sms() / 2;
-      max_pairs[dev] = std::min(n, num_sms() / 2);
+      cfg.gridDim = dim3((unsigned)(ctas / 2 * 2), 1, 1);
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) n = ctas / 2;
+      ctas = 2 * std::min(n, ctas / 2);
     }
-    ready[dev] = 1;
+    resident[dev].store(ctas, std::memory_order_release);
   }
   const int tiles = s.num_m * s.num_n;
-  const int grid = kPair ? 2 * std::min(tiles, max_pairs[dev]) : s.splits > 1 ? tiles * s.splits : std::min(tiles, num_sms());
+  const int grid = kPair ? 2 * std::min(tiles, ctas / 2) : s.splits > 1 ? tiles * s.splits : std::min(tiles, ctas);
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
   Q4_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, tw, tt, p));
   return Q4_OK;

@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, resident_blocks(kVec, kThreads, fals
 
 template <typename T, bool kVec, int kC, int kForm, int kThreads>
 q4_status launch_norm_ring(const NormArgs& a, const Shape& s, cudaStream_t stream) {
-  static int ready[64] = {0};
+  static std::atomic<int> ready[64];
   const auto kernel = norm_ring_kernel<T, kVec, kC, kForm, kThreads>;
   const q4_status st = allow_smem(kernel, ready);
   if (st != Q4_OK) return st;

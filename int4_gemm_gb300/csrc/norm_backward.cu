@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(32 * kWeightWarps) norm_weight_kernel(const fl
 
 template <typename T, bool kVec, int kC, int kThreads>
 q4_status launch_norm_backward_ring(const NormBackwardArgs& a, const Shape& s, cudaStream_t stream) {
-  static int ready[64] = {0};
+  static std::atomic<int> ready[64];
   const auto kernel = norm_backward_ring_kernel<T, kVec, kC, kThreads>;
   const q4_status st = allow_smem(kernel, ready);
   if (st != Q4_OK) return st;

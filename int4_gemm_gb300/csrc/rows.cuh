@@ -4,6 +4,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -388,14 +389,15 @@ q4_status by_pieces(int C, F&& f) {
   return f(std::integral_constant<int, 8>());
 }
 
-// The kernel's shared memory is allowed once per device.
+// The kernel's shared memory is allowed once per device (calls come from several
+// threads).
 template <typename Kernel>
-q4_status allow_smem(Kernel kernel, int (&ready)[64]) {
+q4_status allow_smem(Kernel kernel, std::atomic<int> (&ready)[64]) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return Q4_ERR_CUDA;
-  if (!ready[dev]) {
+  if (!ready[dev].load(std::memory_order_acquire)) {
     Q4_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingTotal));
-    ready[dev] = 1;
+    ready[dev].store(1, std::memory_order_release);
   }
   return Q4_OK;
 }
