@@ -315,14 +315,10 @@ __global__ void __launch_bounds__((Cut<kPair, kHalf, kHalves>::threads), 1)
   pdl_wait();  // from here on global memory: operands come from the previous kernel
   const uint32_t tmem = sm->tmem_base;
   volatile int* abort_flag = &sm->abort;
-  // bands of 4096 tokens, whose codes stay in L2; within a band tokens first
   auto tile_mn = [&](int t, int64_t& m0, int64_t& n0) {
-    constexpr int band_m = 4096 / T::width;
-    const int band_tiles = band_m * p.num_n;
-    const int band = t / band_tiles, r = t - band * band_tiles;
-    const int gm = min(band_m, p.num_m - band * band_m);
-    m0 = (int64_t)(band * band_m + r % gm) * T::width;
-    n0 = (int64_t)(r / gm) * (kPair ? 2 * kRows : kRows) + (kPair ? rank * kRows : 0);
+    const Tile at = tile_at(t, T::width, p.num_m, p.num_n);
+    m0 = (int64_t)at.m * T::width;
+    n0 = (int64_t)at.n * (kPair ? 2 * kRows : kRows) + (kPair ? rank * kRows : 0);
   };
 
   if (warp < kConvWarp0) {

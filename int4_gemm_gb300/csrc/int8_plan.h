@@ -4,6 +4,14 @@
 
 #include <stdint.h>
 
+#ifndef Q4_HOST_DEVICE
+#ifdef __CUDACC__
+#define Q4_HOST_DEVICE __host__ __device__ __forceinline__
+#else
+#define Q4_HOST_DEVICE inline
+#endif
+#endif
+
 namespace q4 {
 namespace {
 
@@ -40,6 +48,19 @@ inline Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t sms) {
     }
   }
   return best;
+}
+
+// The t-th tile: bands of 4096 tokens, whose codes stay in L2; within a band tokens
+// first.
+struct Tile {
+  int m, n;  // of the tiles of tokens and of weight rows
+};
+Q4_HOST_DEVICE Tile tile_at(int t, int width, int num_m, int num_n) {
+  const int band_m = num_m < 4096 / width ? num_m : 4096 / width;  // (a band has no more tiles than there are)
+  const int band_tiles = band_m * num_n;
+  const int band = t / band_tiles, r = t - band * band_tiles;
+  const int left = num_m - band * band_m, rows = left < band_m ? left : band_m;
+  return {band * band_m + r % rows, r / rows};
 }
 
 }  // namespace

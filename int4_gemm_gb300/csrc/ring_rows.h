@@ -9,10 +9,12 @@
 
 #include <stdint.h>
 
+#ifndef Q4_HOST_DEVICE
 #ifdef __CUDACC__
 #define Q4_HOST_DEVICE __host__ __device__ __forceinline__
 #else
 #define Q4_HOST_DEVICE inline
+#endif
 #endif
 
 namespace q4 {

@@ -38,3 +38,19 @@ def test_product(lib, size, dtype):
     C = lib.gemm_w8a8_int8(*ops, out_dtype=dtype)
     assert torch.equal(C, _want(*ops, dtype))
     assert lib.sync_status() == 0
+
+
+def test_most_weight_rows(lib):
+    """2^30 - 1 of them, the most that a call takes."""
+    N, K = 2 ** 30 - 1, 16
+    g = torch.Generator("cuda").manual_seed(8)
+    qa = torch.randint(-128, 128, (1, K), dtype=torch.int8, device="cuda", generator=g)
+    qb = torch.zeros((N, K), dtype=torch.int8, device="cuda")
+    parts = [slice(0, 1000), slice(N // 2, N // 2 + 1000), slice(N - 1000, N)]
+    for at in parts:
+        qb[at] = torch.randint(-128, 128, (1000, K), dtype=torch.int8, device="cuda", generator=g)
+    sa, sb = torch.rand(1, device="cuda", generator=g), torch.ones(N, device="cuda")
+    C = lib.gemm_w8a8_int8(qa, sa, qb, sb)
+    for at in parts:
+        assert torch.equal(C[:, at], _want(qa, sa, qb[at], sb[at], torch.bfloat16))
+    assert int(torch.count_nonzero(C)) <= 3000 and lib.sync_status() == 0

@@ -9,6 +9,35 @@ import pytest
 from test_gpu_int8_forms import SIZES
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "int4_gemm_gb300", "csrc")
+TILES = r"""
+#include <cstdio>
+#include <vector>
+#include "int8_plan.h"
+int main() {
+  // every tile once
+  for (int width : {16, 32, 64, 128, 256})
+    for (int num_m : {1, 2, 15, 16, 17, 63, 64, 65, 300})
+      for (int num_n : {1, 3, 40}) {
+        std::vector<int> seen(num_m * num_n, 0);
+        for (int t = 0; t < num_m * num_n; ++t) {
+          const q4::Tile at = q4::tile_at(t, width, num_m, num_n);
+          if (at.m < 0 || at.m >= num_m || at.n < 0 || at.n >= num_n || seen[at.m * num_n + at.n]++) return 1;
+        }
+      }
+  // the most weight rows: 2^30 - 1, and the most tokens
+  for (int width : {16, 32, 64, 128}) {
+    const int num_n = 1 << 23;
+    for (int t : {0, 1, num_n / 2, num_n - 1})
+      if (q4::tile_at(t, width, 1, num_n).n != t || q4::tile_at(t, width, 1, num_n).m != 0) return 2;
+  }
+  const int num_m = 1 << 22;
+  for (int t : {0, num_m - 1, 2 * num_m, 3 * num_m - 1}) {
+    const q4::Tile at = q4::tile_at(t, 256, num_m, 3);
+    if (at.m != t / 48 * 16 + t % 48 % 16 || at.n != t % 48 / 16) return 3;
+  }
+  puts("tiles");
+}
+"""
 PROGRAM = r"""
 #include <cstdio>
 #include "int8_plan.h"
@@ -22,18 +51,22 @@ int main() {
 """
 
 
-@pytest.fixture(scope="module")
-def plans(tmp_path_factory):
+def _compile(at, text, *flags):
     cc = shutil.which("g++") or shutil.which("c++")
     if cc is None:
         pytest.skip("no C++ compiler")
-    at = tmp_path_factory.mktemp("plan")
-    (at / "plan.cc").write_text(PROGRAM)
-    subprocess.run([cc, "-std=c++17", "-O1", "-I", CSRC, "-o", str(at / "plan"), str(at / "plan.cc")], check=True)
+    (at / "program.cc").write_text(text)
+    subprocess.run([cc, "-std=c++17", "-O1", *flags, "-I", CSRC, "-o", str(at / "program"), str(at / "program.cc")], check=True)
+    return str(at / "program")
+
+
+@pytest.fixture(scope="module")
+def plans(tmp_path_factory):
+    program = _compile(tmp_path_factory.mktemp("plan"), PROGRAM)
 
     def ask(sizes, sms=152):
         text = "".join(f"{m} {n} {k} {sms}\n" for m, n, k in sizes)
-        out = subprocess.run([str(at / "plan")], input=text, capture_output=True, text=True, check=True).stdout
+        out = subprocess.run([program], input=text, capture_output=True, text=True, check=True).stdout
         return [tuple(int(v) for v in line.split()) for line in out.splitlines()]
     return ask
 
@@ -74,3 +107,10 @@ def test_parts_and_tiles_stay_in_range(plans):
     for (m, n, k), (pair, width, splits, num_m, num_n) in zip(sizes, plans(sizes)):
         assert num_m == -(-m // width) and num_n == -(-n // (256 if pair else 128)) and num_m * num_n < 2 ** 31
         assert splits == 1 or (not pair and splits <= -(-k // 128) and splits * num_m * num_n <= 152)
+
+
+def test_tiles(tmp_path):
+    """Each tile once, and no step of the way to it beyond 32 bits."""
+    program = _compile(tmp_path, TILES, "-fsanitize=signed-integer-overflow", "-fsanitize-undefined-trap-on-error")
+    r = subprocess.run([program], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "tiles", (r.returncode, r.stderr)
