@@ -28,7 +28,7 @@
 //
 // Measured: 8192 x 28672 x 8192 2030 us (1895 TFLOP/s: the tensor pipe, at the rate of
 // a library product in bf16), 4096 x 4864 x 4096 98.8 us (1653 TFLOP/s), 256 x 8192 x 8192
-// 38.5 us (891 TFLOP/s: the conversion, 195 ns per 64 columns of a 64-token tile), 1 x
+// 38.5 us (891 TFLOP/s: the conversion, 268 ns per 64 columns of a 128-token tile), 1 x
 // 8192 x 8192 17.6 us (3.8 TB/s: 9.9 us of reading at the copy rate, the rest start, join
 // and stores).
 #include <algorithm>

@@ -8,7 +8,8 @@
 // 2^-12 of a half-integer (a quotient below 128 is off by less than 2^-14), where it
 // is divided.  8192 x 8192 bf16 49.1 us (4.1 TB/s: instruction issue, 58%; with a division
 // for every element, single loads and two passes 62.6), 28672 x 8192 FP32 175 us (6.7
-// TB/s), 100 x 7168 bf16 2.9 us.
+// TB/s), 100 x 7168 bf16 2.9 us.  Above 16384 columns, with single loads, the second
+// pass and the division: 8192 x 28672 bf16 261 us (2.7 TB/s), FP32 323 (3.6 TB/s).
 #include "rows.cuh"
 
 namespace q4 {

@@ -17,10 +17,12 @@
 //
 // Measured: 8192 x 8192 bf16 with residual to FP8 75.6 us (6.2 TB/s), to bf16 87.5
 // (6.1 TB/s); 8192 x 4096 to INT8 41.6 (5.7 TB/s); 4096 x 7168 f16 without residual to
-// INT8 22.5 (3.9 TB/s: instruction issue, 49% of the slots with two blocks per SM, and
-// latencies of a row's reduction that so few warps do not cover); 3001 x 2047 FP32
-// 18.2 (5.4 TB/s); 8192 x 1411 bf16 to FP8 32.2 (2.5 TB/s: single elements); 4 x 7168
-// 2.9 (launch and one row's latency); 256 x 8192 6.1, 1000 x 4096 to INT8 7.5.
+// INT8 22.6 (3.9 TB/s: latency of a row's chain, wait to codes, of which 16 warps per SM
+// have one each under way; half of the issue slots are free); 3001 x 2047 FP32
+// 18.2 (5.4 TB/s); 8192 x 1411 bf16 to FP8 31.5 (2.6 TB/s: single elements); 4 x 7168
+// 3.1 (launch and one row's latency); 256 x 8192 to FP8 6.1, 1000 x 4096 to INT8 7.8;
+// 2048 x 32768 112 (4.8 TB/s, no ring).  FP32 weights of 16-bit rows are read for every
+// row: 8192 x 8192 to FP8 86.0, 4096 x 7168 to INT8 34.5.
 #include "rows.cuh"
 
 namespace q4 {

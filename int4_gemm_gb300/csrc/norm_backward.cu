@@ -6,10 +6,11 @@
 // threads; the blocks' sums go to the workspace and are added in their order by
 // a second kernel, so that results do not depend on timing.
 //
-// HBM-bound where rows are aligned: 16384 x 7168 bf16 with d_h 150.5 us (6.2 TB/s),
-// 8192 x 4096 50.6 us (5.3 TB/s); single elements wait for
-// their latencies: 9973 x 1411 bf16 36.8 us (2.3 TB/s).  512 x 4096 11.6 us, 64 x 16384
-// 16.0: latencies of two dependent kernels.
+// HBM-bound where rows are aligned: 16384 x 7168 bf16 with d_h 150.9 us (6.2 TB/s; with
+// FP32 weights, read for every row, 182), 8192 x 4096 50.6 us (5.3 TB/s); single elements
+// wait for their latencies: 9973 x 1411 bf16 36.2 us (2.3 TB/s), FP32 36.6 (4.6 TB/s).
+// 512 x 4096 11.8 us, 64 x 16384 16.2: latencies of two dependent kernels; 65536 x 128
+// without d_h 18.6 (2.7 TB/s): the same of short rows.
 #include "rows.cuh"
 
 namespace q4 {
