@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(block_threads<GROUPED>(), 1)
         for (int kb = kb_begin; kb < kb_end; ++kb) {
           // sf_full implies full in both CTAs: every scale-writer warp waits
           // for its own CTA's copies of the stage before it arrives
-          if (!mbar_wait(smem_u32(&sm->sf_full[stage]), phase, p.ctl, abort_flag)) {
+          if (!mbar_wait<P2>(smem_u32(&sm->sf_full[stage]), phase, p.ctl, abort_flag)) {
             alive = false;
             break;
           }

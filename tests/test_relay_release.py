@@ -40,3 +40,12 @@ def test_scale_writers_hand_the_stage_over_at_cluster_scope():
     assert len(handing) == 1
     helper = re.search(r"auto %s = \[&\]\(uint64_t\* bar\) \{\s*if constexpr \(P2\) (\w+)\(" % handing[0], source).group(1)
     assert _releases_at_cluster_scope(helper)
+    # and the wait for it acquires at cluster scope
+    assert len(re.findall(r"mbar_wait<P2>\(smem_u32\(&sm->sf_full\[stage\]\)", source)) == 1
+
+
+@pytest.mark.parametrize("name,wait", [("w4a8.cu", r"mbar_wait<true>\(smem_u32\(&sm->pair_full\[stage\]\)"),
+                                       ("fp8.cu", r"mbar_wait<true>\(smem_u32\(&sm->pair_full\[stage\]\)"),
+                                       ("int8.cu", r"warp_wait<kPair>\(bar0 \+ slot \* 8")])
+def test_issuer_acquires_at_cluster_scope(name, wait):
+    assert len(re.findall(wait, _source(name))) == 1
