@@ -590,6 +590,7 @@ def moe_sort_tokens(ids: torch.Tensor, E: int, ws: Optional[torch.Tensor] = None
     ``workspace(OP_MOE_SORT, T * top_k, E, 0, device)``."""
     if not ids.is_cuda or ids.dim() != 2:
         raise ValueError("ids must be a [T, top_k] CUDA tensor")
+    _here(ids, "ids")
     T, k = ids.shape
     dev = ids.device
     _exact(ids, "ids", (T, k), torch.int32, dev)

@@ -18,6 +18,7 @@ def calls(lib):
         "rms_norm": lambda: lib.rms_norm(x), "rms_norm_fp8": lambda: lib.rms_norm_fp8(x, residual=x),
         "rms_norm_int8": lambda: lib.rms_norm_int8(x), "rms_norm_backward": lambda: lib.rms_norm_backward(x, x, rstd),
         "quantize_int8": lambda: lib.quantize_int8(x), "gemm_w8a8_int8": lambda: lib.gemm_w8a8_int8(q, s, q, s),
+        "moe_sort_tokens": lambda: lib.moe_sort_tokens(ids, 8), "moe_route_topk": lambda: lib.moe_route_topk(logits, 2),
         "moe_balance_loss": lambda: lib.moe_balance_loss(logits, ids),
         "moe_balance_loss_backward": lambda: lib.moe_balance_loss_backward(logits, counts, 2, one),
     }
